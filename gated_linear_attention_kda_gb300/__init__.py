@@ -457,3 +457,7 @@ def version() -> int:
 def library():
     """The loaded ctypes handle of libkda.so (for direct C-ABI calls)."""
     return _lib
+
+
+from .block import (conv, conv_step, gated_norm, residual_norm, ssm, ssm_step,  # noqa: E402
+                    ssm_workspace_bytes)

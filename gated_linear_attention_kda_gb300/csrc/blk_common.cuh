@@ -1,0 +1,72 @@
+// blk_common.cuh -- pieces shared by the operators around the mixer (convolution, state-space
+// scan, norms): 8-channel bf16 vectors, the activations, varlen lookups.
+#pragma once
+#include "kda_common.cuh"
+
+namespace kda {
+namespace blk {
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + 2^(-z log2 e)). The exponential and the reciprocal are the hardware approximations
+// (relative error below 2^-20 together for |z| < 88, far under the bf16 rounding that follows);
+// z -> -inf gives 0, z -> +inf gives 1. The tanh form would lose the lower tail's relative precision.
+__device__ __forceinline__ float sigmoid_fast(float z) { return rcp_approx(1.f + ex2_approx(-LOG2E * z)); }
+
+__device__ __forceinline__ float apply_act(float z, int act)
+{
+    if (act == KDA_ACT_NONE) return z;
+    const float s = sigmoid_fast(z);
+    return act == KDA_ACT_SILU ? z * s : s;
+}
+
+// eight consecutive bf16 channels
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8])
+{
+    f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
+    f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+__device__ __forceinline__ void load8f(const float *p, float (&f)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Bounds of the packed sequence that holds token t: the last i with cu[i] <= t (for rising bounds
+// that skips empty sequences). ok only where the bounds really enclose t inside [0, total].
+struct Enclosing {
+    int seq;
+    long long b, e;
+    bool ok;
+};
+__device__ __forceinline__ Enclosing find_sequence(const int64_t *cu, int nseq, long long total, long long t)
+{
+    int lo = 0, hi = nseq;
+    while (hi - lo > 1) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+    }
+    const long long b = __ldg(cu + lo), e = __ldg(cu + lo + 1);
+    return {lo, b, e, b >= 0 && b <= t && t < e && e <= total};
+}
+
+// One block looks every bound over: they rise from 0 to total, or the device error word says so.
+__device__ __forceinline__ void check_bounds(const int64_t *cu, int nseq, long long total)
+{
+    bool bad = false;
+    for (int i = threadIdx.x; i < nseq; i += blockDim.x) bad |= cu[i] > cu[i + 1];
+    if (threadIdx.x == 0) bad |= cu[0] != 0 || cu[nseq] != total;
+    if (bad) atomicOr(&g_dev_error, DEVERR_SEQLENS);
+}
+
+}  // namespace blk
+}  // namespace kda

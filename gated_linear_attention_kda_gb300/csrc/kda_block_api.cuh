@@ -1,0 +1,474 @@
+// kda_block_api.cuh -- host side of the operators around the mixer (include/kda.h): argument
+// checks, launch shapes and launches. Included by kda_fwd.cu, whose error reporting it uses.
+#pragma once
+#include "kda_conv.cuh"
+#include "kda_norm.cuh"
+#include "kda_ssm_step.cuh"
+
+namespace kda {
+namespace blk {
+
+// A tensor of `tokens` rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+    const void *base;
+    int64_t stride, width, tokens;
+};
+
+// Whether two strided tensors share an element. Rows of one stride may interleave (slices of one
+// wider row); of different strides, overlapping ranges count as shared.
+static bool share(const Rows &a, const Rows &b)
+{
+    if (!a.base || !b.base || a.tokens < 1 || b.tokens < 1) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.base), b0 = reinterpret_cast<uintptr_t>(b.base);
+    const uintptr_t a1 = a0 + static_cast<uintptr_t>((a.tokens - 1) * a.stride + a.width);
+    const uintptr_t b1 = b0 + static_cast<uintptr_t>((b.tokens - 1) * b.stride + b.width);
+    if (a1 <= b0 || b1 <= a0) return false;
+    if (a.stride != b.stride) return true;
+    const int64_t d = static_cast<int64_t>(b0 - a0) % a.stride, off = d < 0 ? d + a.stride : d;
+    return !(off >= a.width && off + b.width <= a.stride);
+}
+// The same elements in the same places (an element-wise kernel may write over its input).
+static bool same(const Rows &a, const Rows &b) { return a.base == b.base && (a.stride == b.stride || a.tokens <= 1); }
+
+static bool stride_ok(int64_t stride, int64_t elems, int64_t multiple)
+{
+    return stride >= elems && stride % multiple == 0 && stride <= (int64_t(1) << 32);
+}
+
+struct Device {
+    int id, sms;
+};
+static kda_status device(Device *d)
+{
+    cudaError_t e = cudaGetDevice(&d->id);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id);
+    if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "CUDA device query failed: %s", cudaGetErrorString(e));
+    return KDA_OK;
+}
+
+static kda_status launched(const char *what)
+{
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "%s launch failed: %s", what, cudaGetErrorString(e));
+    return KDA_OK;
+}
+
+static kda_status check_varlen(const int64_t *cu, int64_t N, int64_t B, int64_t T, int64_t *nseq, int64_t *total)
+{
+    if (B < 1 || T < 0 || T > (int64_t(1) << 31) || B > (int64_t(1) << 31))
+        return fail(KDA_ERR_SHAPE, "bad sizes B=%lld T=%lld", (long long)B, (long long)T);
+    if (cu && (B != 1 || N < 1 || N > (int64_t(1) << 28)))
+        return fail(KDA_ERR_SHAPE, "varlen mode needs B == 1 and N >= 1 (B=%lld N=%lld)", (long long)B, (long long)N);
+    if (cu && !aligned(cu, 8)) return fail(KDA_ERR_ALIGN, "cu_seqlens must be 8-byte aligned");
+    *nseq = cu ? N : B;
+    *total = B * T;
+    if (*total > (int64_t(1) << 31) - 256) return fail(KDA_ERR_SHAPE, "too many tokens (%lld)", (long long)*total);
+    return KDA_OK;
+}
+
+// A state pair: the same buffer or disjoint ones.
+static bool partial_overlap(const void *a, const void *b, int64_t bytes)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x != y && x < y + bytes && y < x + bytes;
+}
+
+template <int W>
+static kda_status launch_conv(const conv::ConvParams &q, cudaStream_t s)
+{
+    conv::ConvParams p = q;
+    const int nc8 = p.C / 8;
+    const int64_t states = p.fin ? (static_cast<int64_t>(p.nseq) * nc8 + conv::THREADS - 1) / conv::THREADS : 0;
+    const int64_t per = static_cast<int64_t>(conv::THREADS / p.cg) * conv::RUN;
+    p.tiles = (p.total + per - 1) / per;
+    // in place, the final states are written once every block has read the initial ones
+    const bool after = p.fin && p.fin == p.init && p.tiles > 0;
+    int64_t gx = p.tiles + (after ? 0 : states);
+    if (gx == 0 && p.cu) gx = 1;  // nothing to write, but the bounds are looked over
+    if (gx > 0x7fffffff || states > 0x7fffffff || (nc8 + p.cg - 1) / p.cg > 65535)
+        return fail(KDA_ERR_SHAPE, "problem too large");
+    if (gx > 0)
+        conv::kda_conv_kernel<W><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>((nc8 + p.cg - 1) / p.cg)), conv::THREADS, 0, s>>>(p);
+    if (after) {
+        p.tiles = 0;
+        conv::kda_conv_kernel<W><<<dim3(static_cast<unsigned>(states)), conv::THREADS, 0, s>>>(p);
+    }
+    return launched("convolution");
+}
+
+template <int W>
+static kda_status launch_conv_step(const conv::ConvParams &p, uint16_t *state, cudaStream_t s)
+{
+    const int64_t n = static_cast<int64_t>(p.nseq) * (p.C / 8), grid = (n + conv::THREADS - 1) / conv::THREADS;
+    if (grid > 0x7fffffff) return fail(KDA_ERR_SHAPE, "problem too large");
+    conv::kda_conv_step_kernel<W><<<static_cast<unsigned>(grid), conv::THREADS, 0, s>>>(p, state);
+    return launched("convolution step");
+}
+
+static kda_status check_conv(const void *x, int64_t xs, const float *weight, const float *bias, kda_act act, const void *out,
+                             int64_t os, int64_t C, int64_t W, bool tokens)
+{
+    if (W < 2 || W > 4) return fail(KDA_ERR_SHAPE, "W must be 2, 3 or 4 (got %lld)", (long long)W);
+    if (C < 8 || C % 8 || C > (int64_t(1) << 24)) return fail(KDA_ERR_SHAPE, "C must be a positive multiple of 8 (got %lld)", (long long)C);
+    if (act != KDA_ACT_NONE && act != KDA_ACT_SILU) return fail(KDA_ERR_RANGE, "act must be KDA_ACT_NONE or KDA_ACT_SILU");
+    if (!weight || (tokens && (!x || !out))) return fail(KDA_ERR_NULL, "x, weight and out are required");
+    if (tokens && (!stride_ok(xs, C, 8) || !stride_ok(os, C, 8)))
+        return fail(KDA_ERR_ALIGN, "token strides must be multiples of 8 elements and at least C (x %lld, out %lld)", (long long)xs, (long long)os);
+    if ((tokens && (!aligned(x, 16) || !aligned(out, 16))) || !aligned(weight, 4) || !aligned(bias, 4))
+        return fail(KDA_ERR_ALIGN, "x and out must be 16-byte, weight and bias 4-byte aligned");
+    return KDA_OK;
+}
+
+static kda_status check_ssm(const void *x, int64_t xs, const void *dt, int64_t dts, const void *b, int64_t bs, const void *c,
+                            int64_t cs, const float *A_log, const float *D, const float *dt_bias, const void *out, int64_t os,
+                            int64_t H, int64_t P, int64_t G, int64_t K, bool tokens)
+{
+    if (P != 64 && P != 128) return fail(KDA_ERR_SHAPE, "P must be 64 or 128 (got %lld)", (long long)P);
+    if (K != ssm::NS) return fail(KDA_ERR_SHAPE, "K must be 128 (got %lld)", (long long)K);
+    if (H < 1 || H > (1 << 20) || G < 1 || H % G) return fail(KDA_ERR_SHAPE, "G must divide H (H=%lld G=%lld)", (long long)H, (long long)G);
+    if (!A_log || (tokens && (!x || !dt || !b || !c || !out))) return fail(KDA_ERR_NULL, "x, dt, b, c, A_log and out are required");
+    if (!aligned(A_log, 4) || !aligned(D, 4) || !aligned(dt_bias, 4)) return fail(KDA_ERR_ALIGN, "A_log, D and dt_bias must be 4-byte aligned");
+    if (!tokens) return KDA_OK;
+    if (!stride_ok(xs, H * P, 8) || !stride_ok(os, H * P, 8) || !stride_ok(bs, G * K, 8) || !stride_ok(cs, G * K, 8) || !stride_ok(dts, H, 1))
+        return fail(KDA_ERR_ALIGN, "token strides must cover a token's elements and, but for dt's, be multiples of 8 elements");
+    if (!aligned(x, 16) || !aligned(b, 16) || !aligned(c, 16) || !aligned(out, 16) || !aligned(dt, 2))
+        return fail(KDA_ERR_ALIGN, "x, b, c and out must be 16-byte, dt 2-byte aligned");
+    return KDA_OK;
+}
+
+static kda_status launch_ssm_steps(const ssm::SsmParams &p, cudaStream_t s)
+{
+    const int64_t warps = static_cast<int64_t>(p.nseq) * p.H * (p.P / ssm::ROWS);
+    const int64_t grid = (warps + ssm::STEP_THREADS / 32 - 1) / (ssm::STEP_THREADS / 32);
+    ssm::kda_ssm_step_kernel<<<static_cast<unsigned>(grid), ssm::STEP_THREADS, 0, s>>>(p, warps);
+    return launched("state-space step");
+}
+
+// Threads along a row of D channels: a power of two of lanes up to a warp (then one, two or four
+// vectors each), or a CTA of one or two vectors per thread.
+struct RowShape {
+    bool cta;
+    int threads, vpt;
+};
+static RowShape row_shape(int64_t D)
+{
+    const int v = static_cast<int>((D + 7) / 8);
+    if (v <= 128) {
+        int t = 1;
+        while (t < v && t < 32) t <<= 1;
+        const int n = (v + t - 1) / t;
+        return {false, t, n <= 1 ? 1 : n <= 2 ? 2 : 4};
+    }
+    const int vpt = v <= 1024 ? 1 : 2;
+    return {true, (((v + vpt - 1) / vpt) + 31) / 32 * 32, vpt};
+}
+
+// Blocks that fill the machine at the kernel's occupancy, no more than there are row groups.
+template <typename Kern>
+static unsigned row_grid(Kern kern, const RowShape &sh, int64_t rows, const Device &d)
+{
+    const int threads = sh.cta ? sh.threads : norm::WARP_THREADS;
+    int occ = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, 0) != cudaSuccess || occ < 1) occ = 1;
+    const int64_t per = sh.cta ? 1 : norm::WARP_THREADS / sh.threads;
+    return static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(d.sms) * occ, (rows + per - 1) / per));
+}
+
+template <int VPT, bool CTA>
+static kda_status launch_gated(norm::GatedParams p, const RowShape &sh, const Device &d, cudaStream_t s)
+{
+    p.tpr = sh.threads;
+    const unsigned grid = row_grid(norm::kda_gated_norm_kernel<VPT, CTA>, sh, p.rows, d);
+    norm::kda_gated_norm_kernel<VPT, CTA><<<grid, CTA ? sh.threads : norm::WARP_THREADS, 0, s>>>(p);
+    return launched("gated norm");
+}
+
+template <int VPT, bool CTA>
+static kda_status launch_residual(norm::ResidualParams p, bool f32, const RowShape &sh, const Device &d, cudaStream_t s)
+{
+    p.tpr = sh.threads;
+    const int threads = CTA ? sh.threads : norm::WARP_THREADS;
+    if (f32)
+        norm::kda_residual_norm_kernel<VPT, CTA, true><<<row_grid(norm::kda_residual_norm_kernel<VPT, CTA, true>, sh, p.rows, d), threads, 0, s>>>(p);
+    else
+        norm::kda_residual_norm_kernel<VPT, CTA, false><<<row_grid(norm::kda_residual_norm_kernel<VPT, CTA, false>, sh, p.rows, d), threads, 0, s>>>(p);
+    return launched("residual norm");
+}
+
+static bool act_ok(kda_act a) { return a == KDA_ACT_NONE || a == KDA_ACT_SIGMOID || a == KDA_ACT_SILU; }
+
+}  // namespace blk
+}  // namespace kda
+
+extern "C" {
+
+KDA_API kda_status kda_conv(const void *x, int64_t x_stride, const float *weight, const float *bias, kda_act act, void *out,
+                            int64_t out_stride, const void *initial_state, void *final_state, const int64_t *cu_seqlens,
+                            int64_t N, int64_t B, int64_t T, int64_t C, int64_t W, void *stream)
+{
+    t_last_error.clear();
+    int64_t nseq = 0, total = 0;
+    if (const kda_status st = blk::check_varlen(cu_seqlens, N, B, T, &nseq, &total); st != KDA_OK) return st;
+    if (const kda_status st = blk::check_conv(x, x_stride, weight, bias, act, out, out_stride, C, W, total > 0); st != KDA_OK) return st;
+    if (!aligned(initial_state, 16) || !aligned(final_state, 16)) return fail(KDA_ERR_ALIGN, "state buffers must be 16-byte aligned");
+    if (blk::share({x, 2 * x_stride, 2 * C, total}, {out, 2 * out_stride, 2 * C, total}))
+        return fail(KDA_ERR_STATE_MISMATCH, "out must not share memory with x");
+    if (blk::partial_overlap(initial_state, final_state, nseq * (W - 1) * C * 2))
+        return fail(KDA_ERR_STATE_MISMATCH, "initial_state and final_state overlap partially");
+    conv::ConvParams p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.init = static_cast<const uint16_t *>(initial_state);
+    p.out = static_cast<uint16_t *>(out);
+    p.fin = static_cast<uint16_t *>(final_state);
+    p.weight = weight;
+    p.bias = bias;
+    p.cu = cu_seqlens;
+    p.xs = x_stride;
+    p.os = out_stride;
+    p.total = total;
+    p.T = T;
+    p.nseq = static_cast<int>(nseq);
+    p.C = static_cast<int>(C);
+    p.act = act;
+    p.cg = 1;
+    while (p.cg < conv::THREADS && p.cg < C / 8) p.cg <<= 1;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return W == 2 ? blk::launch_conv<2>(p, s) : W == 3 ? blk::launch_conv<3>(p, s) : blk::launch_conv<4>(p, s);
+}
+
+KDA_API kda_status kda_conv_step(const void *x, int64_t x_stride, const float *weight, const float *bias, kda_act act,
+                                 void *out, int64_t out_stride, void *state, int64_t S, int64_t C, int64_t W, void *stream)
+{
+    t_last_error.clear();
+    if (S < 1 || S > (int64_t(1) << 28)) return fail(KDA_ERR_SHAPE, "bad size S=%lld", (long long)S);
+    if (const kda_status st = blk::check_conv(x, x_stride, weight, bias, act, out, out_stride, C, W, true); st != KDA_OK) return st;
+    if (!state) return fail(KDA_ERR_NULL, "state is required");
+    if (!aligned(state, 16)) return fail(KDA_ERR_ALIGN, "state must be 16-byte aligned");
+    const blk::Rows xr{x, 2 * x_stride, 2 * C, S}, orow{out, 2 * out_stride, 2 * C, S};
+    if (!blk::same(xr, orow) && blk::share(xr, orow)) return fail(KDA_ERR_STATE_MISMATCH, "out must be x or share no memory with it");
+    conv::ConvParams p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.out = static_cast<uint16_t *>(out);
+    p.weight = weight;
+    p.bias = bias;
+    p.xs = x_stride;
+    p.os = out_stride;
+    p.nseq = static_cast<int>(S);
+    p.C = static_cast<int>(C);
+    p.act = act;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint16_t *st = static_cast<uint16_t *>(state);
+    return W == 2 ? blk::launch_conv_step<2>(p, st, s) : W == 3 ? blk::launch_conv_step<3>(p, st, s) : blk::launch_conv_step<4>(p, st, s);
+}
+
+KDA_API kda_status kda_ssm_workspace_bytes(int64_t states, int64_t tokens, int64_t H, int64_t P, size_t *bytes)
+{
+    t_last_error.clear();
+    if (!bytes) return fail(KDA_ERR_NULL, "kda_ssm_workspace_bytes: bytes is required");
+    if (states < 0 || tokens < 0 || H < 1 || (P != 64 && P != 128))
+        return fail(KDA_ERR_SHAPE, "bad sizes states=%lld tokens=%lld H=%lld P=%lld", (long long)states, (long long)tokens, (long long)H, (long long)P);
+    *bytes = 0;
+    return KDA_OK;
+}
+
+KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const void *b, int64_t b_stride,
+                           const void *c, int64_t c_stride, const float *A_log, const float *D, const float *dt_bias, void *out,
+                           int64_t out_stride, const void *initial_state, kda_dtype initial_dtype, void *final_state,
+                           kda_dtype final_dtype, const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t H,
+                           int64_t P, int64_t G, int64_t K, void *workspace, size_t workspace_bytes, void *stream)
+{
+    t_last_error.clear();
+    int64_t nseq = 0, total = 0;
+    if (const kda_status st = blk::check_varlen(cu_seqlens, N, B, T, &nseq, &total); st != KDA_OK) return st;
+    if (const kda_status st = blk::check_ssm(x, x_stride, dt, dt_stride, b, b_stride, c, c_stride, A_log, D, dt_bias, out,
+                                             out_stride, H, P, G, K, total > 0); st != KDA_OK)
+        return st;
+    if (nseq * H > (int64_t(1) << 26)) return fail(KDA_ERR_SHAPE, "too many (sequence, head) pairs");
+    auto dt_ok = [](const void *ptr, kda_dtype d) {
+        return ptr ? (d == KDA_DTYPE_BF16 || d == KDA_DTYPE_FP32) : d == KDA_DTYPE_NONE;
+    };
+    if (!dt_ok(initial_state, initial_dtype) || !dt_ok(final_state, final_dtype))
+        return fail(KDA_ERR_DTYPE, "state dtype codes must be BF16/FP32 for a given buffer and NONE for an absent one");
+    if (!aligned(initial_state, 16) || !aligned(final_state, 16)) return fail(KDA_ERR_ALIGN, "state buffers must be 16-byte aligned");
+    if (workspace && !aligned(workspace, 16)) return fail(KDA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if (initial_state && final_state) {
+        if (initial_dtype != final_dtype) return fail(KDA_ERR_STATE_MISMATCH, "final_state must match initial_state's dtype");
+        if (blk::partial_overlap(initial_state, final_state, nseq * H * P * K * (initial_dtype == KDA_DTYPE_FP32 ? 4 : 2)))
+            return fail(KDA_ERR_STATE_MISMATCH, "initial_state and final_state overlap partially");
+    }
+    const blk::Rows orow{out, 2 * out_stride, 2 * H * P, total};
+    if (blk::share(orow, {x, 2 * x_stride, 2 * H * P, total}) || blk::share(orow, {b, 2 * b_stride, 2 * G * K, total}) ||
+        blk::share(orow, {c, 2 * c_stride, 2 * G * K, total}) || blk::share(orow, {dt, 2 * dt_stride, 2 * H, total}))
+        return fail(KDA_ERR_STATE_MISMATCH, "out must not share memory with x, b, c or dt");
+    ssm::SsmParams p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.dt = static_cast<const uint16_t *>(dt);
+    p.b = static_cast<const uint16_t *>(b);
+    p.c = static_cast<const uint16_t *>(c);
+    p.out = static_cast<uint16_t *>(out);
+    p.xs = x_stride;
+    p.dts = dt_stride;
+    p.bs = b_stride;
+    p.cs = c_stride;
+    p.os = out_stride;
+    p.A_log = A_log;
+    p.D = D;
+    p.dt_bias = dt_bias;
+    p.init = initial_state;
+    p.fin = final_state;
+    p.cu = cu_seqlens;
+    p.init_dtype = initial_dtype;
+    p.fin_dtype = final_dtype;
+    p.T = static_cast<int>(T);
+    p.H = static_cast<int>(H);
+    p.P = static_cast<int>(P);
+    p.G = static_cast<int>(G);
+    p.nseq = static_cast<int>(nseq);
+    p.total = static_cast<int>(total);
+    (void)workspace_bytes;
+    return blk::launch_ssm_steps(p, static_cast<cudaStream_t>(stream));
+}
+
+KDA_API kda_status kda_ssm_step(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const void *b,
+                                int64_t b_stride, const void *c, int64_t c_stride, const float *A_log, const float *D,
+                                const float *dt_bias, void *out, int64_t out_stride, void *state, kda_dtype state_dtype,
+                                int64_t S, int64_t H, int64_t P, int64_t G, int64_t K, void *stream)
+{
+    t_last_error.clear();
+    if (S < 1 || S > (int64_t(1) << 26) || S * H > (int64_t(1) << 26)) return fail(KDA_ERR_SHAPE, "bad sizes S=%lld H=%lld", (long long)S, (long long)H);
+    if (const kda_status st = blk::check_ssm(x, x_stride, dt, dt_stride, b, b_stride, c, c_stride, A_log, D, dt_bias, out,
+                                             out_stride, H, P, G, K, true); st != KDA_OK)
+        return st;
+    if (!state) return fail(KDA_ERR_NULL, "state is required");
+    if (state_dtype != KDA_DTYPE_BF16 && state_dtype != KDA_DTYPE_FP32) return fail(KDA_ERR_DTYPE, "state dtype must be BF16 or FP32");
+    if (!aligned(state, 16)) return fail(KDA_ERR_ALIGN, "state must be 16-byte aligned");
+    const blk::Rows orow{out, 2 * out_stride, 2 * H * P, S};
+    if (blk::share(orow, {x, 2 * x_stride, 2 * H * P, S}) || blk::share(orow, {b, 2 * b_stride, 2 * G * K, S}) ||
+        blk::share(orow, {c, 2 * c_stride, 2 * G * K, S}) || blk::share(orow, {dt, 2 * dt_stride, 2 * H, S}))
+        return fail(KDA_ERR_STATE_MISMATCH, "out must not share memory with x, b, c or dt");
+    ssm::SsmParams p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.dt = static_cast<const uint16_t *>(dt);
+    p.b = static_cast<const uint16_t *>(b);
+    p.c = static_cast<const uint16_t *>(c);
+    p.out = static_cast<uint16_t *>(out);
+    p.xs = x_stride;
+    p.dts = dt_stride;
+    p.bs = b_stride;
+    p.cs = c_stride;
+    p.os = out_stride;
+    p.A_log = A_log;
+    p.D = D;
+    p.dt_bias = dt_bias;
+    p.init = p.fin = state;
+    p.init_dtype = p.fin_dtype = state_dtype;
+    p.T = 1;
+    p.H = static_cast<int>(H);
+    p.P = static_cast<int>(P);
+    p.G = static_cast<int>(G);
+    p.nseq = static_cast<int>(S);
+    p.total = static_cast<int>(S);
+    return blk::launch_ssm_steps(p, static_cast<cudaStream_t>(stream));
+}
+
+KDA_API kda_status kda_gated_norm(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, const float *weight,
+                                  int64_t weight_rows, void *out, int64_t out_stride, float eps, kda_act act, int gate_first,
+                                  int64_t M, int64_t R, int64_t D, void *stream)
+{
+    t_last_error.clear();
+    if (D < 8 || D % 8 || D > norm::MAX_D) return fail(KDA_ERR_SHAPE, "D must be a multiple of 8 in 8..%d (got %lld)", norm::MAX_D, (long long)D);
+    if (M < 0 || M > (int64_t(1) << 31) || R < 1 || R > (1 << 20) || M * R > (int64_t(1) << 40)) return fail(KDA_ERR_SHAPE, "bad sizes M=%lld R=%lld", (long long)M, (long long)R);
+    if (weight && weight_rows != 1 && weight_rows != R) return fail(KDA_ERR_SHAPE, "weight_rows must be 1 or R (got %lld)", (long long)weight_rows);
+    if (!blk::act_ok(act)) return fail(KDA_ERR_RANGE, "unknown act %d", static_cast<int>(act));
+    if (!std::isfinite(eps) || eps < 0.f) return fail(KDA_ERR_RANGE, "eps must be finite and not negative");
+    if (M == 0) return KDA_OK;
+    if (!x || !gate || !out) return fail(KDA_ERR_NULL, "x, gate and out are required");
+    if (!blk::stride_ok(x_stride, R * D, 8) || !blk::stride_ok(gate_stride, R * D, 8) || !blk::stride_ok(out_stride, R * D, 8))
+        return fail(KDA_ERR_ALIGN, "token strides must be multiples of 8 elements and at least R * D");
+    if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(out, 16) || !aligned(weight, 16))
+        return fail(KDA_ERR_ALIGN, "x, gate, out and weight must be 16-byte aligned");
+    const blk::Rows orow{out, 2 * out_stride, 2 * R * D, M}, xr{x, 2 * x_stride, 2 * R * D, M}, zr{gate, 2 * gate_stride, 2 * R * D, M};
+    if ((!blk::same(orow, xr) && blk::share(orow, xr)) || (!blk::same(orow, zr) && blk::share(orow, zr)))
+        return fail(KDA_ERR_STATE_MISMATCH, "out must be x, gate, or share no memory with them");
+    blk::Device d;
+    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+    norm::GatedParams p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.z = static_cast<const uint16_t *>(gate);
+    p.out = static_cast<uint16_t *>(out);
+    p.w = weight;
+    p.xs = x_stride;
+    p.zs = gate_stride;
+    p.os = out_stride;
+    p.rows = M * R;
+    p.R = static_cast<int>(R);
+    p.D = static_cast<int>(D);
+    p.act = act;
+    p.gate_first = gate_first != 0;
+    p.w_rows = weight_rows == 1 ? 1 : static_cast<int>(R);
+    p.eps = eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const blk::RowShape sh = blk::row_shape(D);
+    if (sh.cta) return sh.vpt == 1 ? blk::launch_gated<1, true>(p, sh, d, s) : blk::launch_gated<2, true>(p, sh, d, s);
+    return sh.vpt == 1 ? blk::launch_gated<1, false>(p, sh, d, s) : sh.vpt == 2 ? blk::launch_gated<2, false>(p, sh, d, s) : blk::launch_gated<4, false>(p, sh, d, s);
+}
+
+KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                                     void *residual_out, int64_t residual_out_stride, kda_dtype residual_dtype,
+                                     const void *gate, int64_t gate_stride, kda_act act, const float *post_weight,
+                                     const float *channel_scale, float alpha, const float *weight, void *out,
+                                     int64_t out_stride, float eps, int64_t M, int64_t D, void *stream)
+{
+    t_last_error.clear();
+    if (D < 8 || D % 8 || D > norm::MAX_D) return fail(KDA_ERR_SHAPE, "D must be a multiple of 8 in 8..%d (got %lld)", norm::MAX_D, (long long)D);
+    if (M < 0 || M > (int64_t(1) << 31)) return fail(KDA_ERR_SHAPE, "bad size M=%lld", (long long)M);
+    if (residual_dtype != KDA_DTYPE_BF16 && residual_dtype != KDA_DTYPE_FP32) return fail(KDA_ERR_DTYPE, "residual dtype must be BF16 or FP32");
+    if (!blk::act_ok(act)) return fail(KDA_ERR_RANGE, "unknown act %d", static_cast<int>(act));
+    if (!std::isfinite(eps) || eps < 0.f) return fail(KDA_ERR_RANGE, "eps must be finite and not negative");
+    if (!std::isfinite(alpha)) return fail(KDA_ERR_RANGE, "alpha must be finite");
+    if (M == 0) return KDA_OK;
+    if (!x || !residual || (!residual_out && !out)) return fail(KDA_ERR_NULL, "x, residual and one of residual_out and out are required");
+    const int64_t rb = residual_dtype == KDA_DTYPE_FP32 ? 4 : 2, rm = 16 / rb;
+    if (!blk::stride_ok(x_stride, D, 8) || !blk::stride_ok(residual_stride, D, rm) || (residual_out && !blk::stride_ok(residual_out_stride, D, rm)) ||
+        (gate && !blk::stride_ok(gate_stride, D, 8)) || (out && !blk::stride_ok(out_stride, D, 8)))
+        return fail(KDA_ERR_ALIGN, "row strides must be multiples of 16 bytes and at least D");
+    const void *need16[] = {x, residual, residual_out, gate, out, post_weight, channel_scale, weight};
+    for (const void *ptr : need16)
+        if (!aligned(ptr, 16)) return fail(KDA_ERR_ALIGN, "every buffer must be 16-byte aligned");
+    const blk::Rows xr{x, 2 * x_stride, 2 * D, M}, rr{residual, rb * residual_stride, rb * D, M}, zr{gate, 2 * gate_stride, 2 * D, M};
+    const blk::Rows orow{out, 2 * out_stride, 2 * D, M}, ror{residual_out, rb * residual_out_stride, rb * D, M};
+    auto clash = [](const blk::Rows &w, const blk::Rows &r) { return !blk::same(w, r) && blk::share(w, r); };
+    if (clash(orow, xr) || clash(orow, zr) || blk::share(orow, rr) || blk::share(orow, ror) || clash(ror, rr) ||
+        blk::share(ror, xr) || blk::share(ror, zr))
+        return fail(KDA_ERR_STATE_MISMATCH, "out may be x or gate and residual_out may be residual; no other buffers share memory");
+    blk::Device d;
+    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+    norm::ResidualParams p = {};
+    p.x = static_cast<const uint16_t *>(x);
+    p.z = static_cast<const uint16_t *>(gate);
+    p.r = residual;
+    p.ro = residual_out;
+    p.out = static_cast<uint16_t *>(out);
+    p.post = post_weight;
+    p.chan = channel_scale;
+    p.w = weight;
+    p.xs = x_stride;
+    p.zs = gate_stride;
+    p.rs = residual_stride;
+    p.ros = residual_out_stride;
+    p.os = out_stride;
+    p.rows = M;
+    p.D = static_cast<int>(D);
+    p.act = act;
+    p.alpha = alpha;
+    p.eps = eps;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool f32 = residual_dtype == KDA_DTYPE_FP32;
+    const blk::RowShape sh = blk::row_shape(D);
+    if (sh.cta) return sh.vpt == 1 ? blk::launch_residual<1, true>(p, f32, sh, d, s) : blk::launch_residual<2, true>(p, f32, sh, d, s);
+    return sh.vpt == 1   ? blk::launch_residual<1, false>(p, f32, sh, d, s)
+           : sh.vpt == 2 ? blk::launch_residual<2, false>(p, f32, sh, d, s)
+                         : blk::launch_residual<4, false>(p, f32, sh, d, s);
+}
+
+}  // extern "C"

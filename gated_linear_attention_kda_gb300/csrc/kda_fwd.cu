@@ -895,3 +895,5 @@ KDA_API kda_status kda_fwd_host(const void *q, const void *k, const void *v, con
 }
 
 }  // extern "C"
+
+#include "kda_block_api.cuh"

@@ -1,0 +1,246 @@
+// kda_norm.cuh -- the norms around a mixer or block, fused with what stands next to them:
+//   gated norm     out = x rsqrt(mean x^2 + eps) w act(z), or the gate before the norm
+//   residual norm  r' = r + alpha ch act(z) n(x),  out = r' rsqrt(mean r'^2 + eps) w
+// HBM-bound: every row is read once into registers, reduced there, and written once. A group of
+// threads owns a row, eight channels per 16-byte access: up to 32 lanes for D <= 1024 (sums by
+// shuffles), a whole CTA above (sums through shared memory). Groups walk the rows of a grid that
+// fills the machine and load the next row before reducing the present one. Sums and the norm are fp32.
+#pragma once
+#include "blk_common.cuh"
+
+namespace kda {
+namespace norm {
+
+constexpr int WARP_THREADS = 128;  // CTA of the warp-group form
+constexpr int MAX_D = 16384;       // 1024 threads x 2 vectors of 8
+
+// Threads that share a row, and where this thread stands among them. CTA: the whole block, with
+// two alternating rows of partial sums so that one barrier per sum is enough.
+template <bool CTA>
+struct Group {
+    int tpr;                // threads per row
+    int rank;
+    float (*part)[32];
+    int flip;
+    __device__ __forceinline__ float sum(float v)
+    {
+        if constexpr (!CTA) {
+            for (int m = tpr >> 1; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+            return v;
+        } else {
+#pragma unroll
+            for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+            const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+            if (lane == 0) part[flip][threadIdx.x >> 5] = v;
+            __syncthreads();
+            v = lane < nw ? part[flip][lane] : 0.f;
+            flip ^= 1;
+#pragma unroll
+            for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+            return v;
+        }
+    }
+};
+
+struct GatedParams {
+    const uint16_t *x, *z;
+    uint16_t *out;
+    const float *w;
+    long long xs, zs, os;   // elements between tokens
+    long long rows;         // M * R
+    int R, D, act, gate_first, w_rows;
+    float eps;
+    int tpr;                // threads per row (warp-group form; a power of two)
+};
+
+template <int VPT, bool CTA>
+__global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_gated_norm_kernel(const GatedParams p)
+{
+    __shared__ float part[2][32];
+    Group<CTA> gr{CTA ? static_cast<int>(blockDim.x) : p.tpr, CTA ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (p.tpr - 1), part, 0};
+    const long long per = CTA ? 1 : WARP_THREADS / p.tpr, step = static_cast<long long>(gridDim.x) * per;
+    const long long first = static_cast<long long>(blockIdx.x) * per + (CTA ? 0 : threadIdx.x / p.tpr);
+    const float inv_d = 1.f / static_cast<float>(p.D);
+    int c[VPT];
+    bool live[VPT];
+    float w[VPT][8];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        c[v] = 8 * (gr.rank + v * gr.tpr);
+        live[v] = c[v] < p.D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[v][i] = 1.f;
+        if (live[v] && p.w && p.w_rows == 1) blk::load8f(p.w + c[v], w[v]);
+    }
+    uint4 xn[VPT], zn[VPT];
+    auto fetch = [&](long long row) {
+        const long long m = row / p.R;
+        const int r = static_cast<int>(row - m * p.R);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            xn[v] = zn[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < p.rows && live[v]) {
+                xn[v] = *reinterpret_cast<const uint4 *>(p.x + m * p.xs + static_cast<long long>(r) * p.D + c[v]);
+                zn[v] = *reinterpret_cast<const uint4 *>(p.z + m * p.zs + static_cast<long long>(r) * p.D + c[v]);
+            }
+        }
+    };
+    fetch(first);
+    // every group of a warp makes the same number of steps (the shuffles need all lanes)
+    for (long long base = static_cast<long long>(blockIdx.x) * per; base < p.rows; base += step) {
+        const long long row = base + (first - static_cast<long long>(blockIdx.x) * per);
+        float x[VPT][8], z[VPT][8], ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            blk::unpack8(xn[v], x[v]);
+            blk::unpack8(zn[v], z[v]);
+        }
+        fetch(row + step);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                z[v][i] = blk::apply_act(z[v][i], p.act);
+                if (p.gate_first) x[v][i] = live[v] ? x[v][i] * z[v][i] : 0.f;
+                ss = fmaf(x[v][i], x[v][i], ss);
+            }
+        const float inv = rsqrtf(fmaf(gr.sum(ss), inv_d, p.eps));
+        if (row < p.rows) {
+            const long long m = row / p.R;
+            const int r = static_cast<int>(row - m * p.R);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                if (!live[v]) continue;
+                if (p.w && p.w_rows != 1) blk::load8f(p.w + static_cast<size_t>(r) * p.D + c[v], w[v]);
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    o[i] = x[v][i] * inv * w[v][i];
+                    if (!p.gate_first) o[i] *= z[v][i];
+                }
+                *reinterpret_cast<uint4 *>(p.out + m * p.os + static_cast<long long>(r) * p.D + c[v]) = blk::pack8(o);
+            }
+        }
+    }
+}
+
+struct ResidualParams {
+    const uint16_t *x, *z;
+    const void *r;
+    void *ro;
+    uint16_t *out;
+    const float *post, *chan, *w;
+    long long xs, zs, rs, ros, os;
+    long long rows;
+    int D, act;
+    float alpha, eps;
+    int tpr;
+};
+
+// F32: the residual stream is fp32 (else bf16).
+template <int VPT, bool CTA, bool F32>
+__global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_residual_norm_kernel(const ResidualParams p)
+{
+    __shared__ float part[2][32];
+    Group<CTA> gr{CTA ? static_cast<int>(blockDim.x) : p.tpr, CTA ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (p.tpr - 1), part, 0};
+    const long long per = CTA ? 1 : WARP_THREADS / p.tpr, step = static_cast<long long>(gridDim.x) * per;
+    const long long sub = CTA ? 0 : threadIdx.x / p.tpr;
+    const float inv_d = 1.f / static_cast<float>(p.D);
+    constexpr int RV = F32 ? 2 : 1;  // 16-byte vectors of eight residual channels
+    int c[VPT];
+    bool live[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        c[v] = 8 * (gr.rank + v * gr.tpr);
+        live[v] = c[v] < p.D;
+    }
+    uint4 xn[VPT], zn[VPT], rn[VPT][RV];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            xn[v] = zn[v] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < RV; ++k) rn[v][k] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < p.rows && live[v]) {
+                xn[v] = *reinterpret_cast<const uint4 *>(p.x + row * p.xs + c[v]);
+                if (p.z) zn[v] = *reinterpret_cast<const uint4 *>(p.z + row * p.zs + c[v]);
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.r) + (row * p.rs + c[v]) * (F32 ? 4 : 2));
+#pragma unroll
+                for (int k = 0; k < RV; ++k) rn[v][k] = src[k];
+            }
+        }
+    };
+    fetch(static_cast<long long>(blockIdx.x) * per + sub);
+    for (long long base = static_cast<long long>(blockIdx.x) * per; base < p.rows; base += step) {
+        const long long row = base + sub;
+        float x[VPT][8], z[VPT][8], r[VPT][8], ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            blk::unpack8(xn[v], x[v]);
+            blk::unpack8(zn[v], z[v]);
+            if constexpr (F32) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    r[v][4 * k] = __uint_as_float(rn[v][k].x);
+                    r[v][4 * k + 1] = __uint_as_float(rn[v][k].y);
+                    r[v][4 * k + 2] = __uint_as_float(rn[v][k].z);
+                    r[v][4 * k + 3] = __uint_as_float(rn[v][k].w);
+                }
+            } else {
+                blk::unpack8(rn[v][0], r[v]);
+            }
+        }
+        fetch(row + step);
+        if (p.post) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[v][i], x[v][i], ss);
+            const float inv = rsqrtf(fmaf(gr.sum(ss), inv_d, p.eps));
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                float w[8];
+                if (live[v]) blk::load8f(p.post + c[v], w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[v][i] = live[v] ? x[v][i] * inv * w[i] : 0.f;
+            }
+        }
+        ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            float ch[8];
+            if (p.chan && live[v]) blk::load8f(p.chan + c[v], ch);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float u = x[v][i];
+                if (p.z) u *= blk::apply_act(z[v][i], p.act);
+                if (p.chan) u *= ch[i];
+                r[v][i] = live[v] ? fmaf(p.alpha, u, r[v][i]) : 0.f;
+                ss = fmaf(r[v][i], r[v][i], ss);
+            }
+            if (p.ro && live[v] && row < p.rows) {
+                if constexpr (F32) {
+                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.ro) + row * p.ros + c[v]);
+                    dst[0] = make_float4(r[v][0], r[v][1], r[v][2], r[v][3]);
+                    dst[1] = make_float4(r[v][4], r[v][5], r[v][6], r[v][7]);
+                } else {
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.ro) + row * p.ros + c[v]) = blk::pack8(r[v]);
+                }
+            }
+        }
+        if (!p.out) continue;
+        const float inv = rsqrtf(fmaf(gr.sum(ss), inv_d, p.eps));
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            if (!live[v] || row >= p.rows) continue;
+            float o[8], w[8];
+            if (p.w) blk::load8f(p.w + c[v], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = p.w ? r[v][i] * inv * w[i] : r[v][i] * inv;
+            *reinterpret_cast<uint4 *>(p.out + row * p.os + c[v]) = blk::pack8(o);
+        }
+    }
+}
+
+}  // namespace norm
+}  // namespace kda

@@ -1,0 +1,140 @@
+// kda_ssm_step.cuh -- the selective state-space recurrence token by token: single tokens against a
+// state kept in place, and short prompts.
+//   delta = softplus(dt + dt_bias[h]),  a = -exp(A_log[h]) delta
+//   S <- exp(a) S + delta x b^T,  out = S c + D[h] x          (S: P x 128 per head)
+// A warp owns ROWS rows of one head's state, four of the 128 state channels per lane (16 bytes of
+// fp32 state per row and lane), in fp32 registers from the first token to the last; the row sums
+// S c go through a reduce-scatter butterfly (nine exchanges for eight rows). One token reads and
+// writes the state once, so the step is bound by HBM; a prompt walks its tokens one after another
+// and is bound by the latency of one token's chain.
+#pragma once
+#include "blk_common.cuh"
+
+namespace kda {
+namespace ssm {
+
+constexpr int NS = 128;        // state channels
+constexpr int ROWS = 8;        // state rows per warp
+constexpr int STEP_THREADS = 128;
+// The log2 decay of one token is held at or above this: 2^-160 is zero in fp32 either way, and the
+// running sums of a chunk stay small enough for their differences to be exact to 2^-11.
+constexpr float MIN_LOG2_DECAY = -160.f;
+
+struct SsmParams {
+    const uint16_t *x, *dt, *b, *c;
+    uint16_t *out;
+    long long xs, dts, bs, cs, os;   // elements between tokens
+    const float *A_log, *D, *dt_bias;
+    const void *init;
+    void *fin;
+    const int64_t *cu;
+    int init_dtype, fin_dtype;
+    int T, H, P, G, nseq, total;
+};
+
+__device__ __forceinline__ float softplus(float u) { return u > 20.f ? u : log1pf(expf(u)); }
+
+__device__ __forceinline__ Span ssm_span(const SsmParams &p, int seq)
+{
+    if (p.cu) {
+        const long long b = p.cu[seq], e = p.cu[seq + 1];
+        if (b < 0 || e < b || e > p.total) return {0, 0, false};
+        return {static_cast<int>(b), static_cast<int>(e - b), true};
+    }
+    return {seq * p.T, p.T, true};
+}
+
+__global__ void __launch_bounds__(STEP_THREADS) kda_ssm_step_kernel(const SsmParams p, long long nwarps)
+{
+    const int lane = threadIdx.x & 31;
+    const long long w = static_cast<long long>(blockIdx.x) * (STEP_THREADS / 32) + (threadIdx.x >> 5);
+    if (p.cu && blockIdx.x == 0) blk::check_bounds(p.cu, p.nseq, p.total);
+    if (w >= nwarps) return;
+    const int rb = p.P / ROWS;                       // row blocks per head
+    const long long unit = w / rb;                   // (sequence, head)
+    const int r0 = static_cast<int>(w % rb) * ROWS;
+    const int h = static_cast<int>(unit % p.H), seq = static_cast<int>(unit / p.H);
+    const int g = h / (p.H / p.G);
+    const Span sp = ssm_span(p, seq);
+    if (!sp.ok) return;  // flagged by check_bounds
+    const size_t st = (static_cast<size_t>(unit) * p.P + r0) * NS + 4 * lane;
+    const size_t st_elems = static_cast<size_t>(p.nseq) * p.H * p.P * NS;
+    float s[ROWS][4];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
+        if (p.init && gmem_ok(st + r * NS, 4, st_elems)) {
+            if (p.init_dtype == KDA_DTYPE_FP32) {
+                const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.init) + st + r * NS);
+                s[r][0] = v.x; s[r][1] = v.y; s[r][2] = v.z; s[r][3] = v.w;
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.init) + st + r * NS);
+                s[r][0] = bf16_lo(v.x); s[r][1] = bf16_hi(v.x); s[r][2] = bf16_lo(v.y); s[r][3] = bf16_hi(v.y);
+            }
+        }
+    }
+    const float A2 = -expf(__ldg(p.A_log + h)) * LOG2E;
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f, Dh = p.D ? __ldg(p.D + h) : 0.f;
+    const uint16_t *xp = p.x + static_cast<long long>(sp.bos) * p.xs + static_cast<long long>(h) * p.P + r0;
+    const uint16_t *dp = p.dt + static_cast<long long>(sp.bos) * p.dts + h;
+    const uint16_t *bp = p.b + static_cast<long long>(sp.bos) * p.bs + static_cast<long long>(g) * NS + 4 * lane;
+    const uint16_t *cp = p.c + static_cast<long long>(sp.bos) * p.cs + static_cast<long long>(g) * NS + 4 * lane;
+    uint16_t *op = p.out + static_cast<long long>(sp.bos) * p.os + static_cast<long long>(h) * p.P + r0 + (lane >> 2);
+    uint4 xn = make_uint4(0u, 0u, 0u, 0u);
+    uint2 bn = make_uint2(0u, 0u), cn = bn;
+    uint32_t dn = 0u;
+    auto fetch = [&](int t) {  // token t's inputs, one token ahead of their use
+        xn = *reinterpret_cast<const uint4 *>(xp + t * p.xs);
+        bn = *reinterpret_cast<const uint2 *>(bp + t * p.bs);
+        cn = *reinterpret_cast<const uint2 *>(cp + t * p.cs);
+        dn = dp[t * p.dts];
+    };
+    if (sp.len > 0) fetch(0);
+    for (int t = 0; t < sp.len; ++t) {
+        float x[8];
+        blk::unpack8(xn, x);
+        const float bf[4] = {bf16_lo(bn.x), bf16_hi(bn.x), bf16_lo(bn.y), bf16_hi(bn.y)};
+        const float cf[4] = {bf16_lo(cn.x), bf16_hi(cn.x), bf16_lo(cn.y), bf16_hi(cn.y)};
+        const float delta = softplus(__uint_as_float(dn << 16) + bias);
+        if (t + 1 < sp.len) fetch(t + 1);
+        const float keep = exp2f(A2 * delta);
+        float y[8];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const float dx = delta * x[r];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[r][j] = fmaf(keep, s[r][j], dx * bf[j]);
+            y[r] = fmaf(s[r][0], cf[0], fmaf(s[r][1], cf[1], fmaf(s[r][2], cf[2], s[r][3] * cf[3])));
+        }
+        // reduce-scatter: lane l ends with the sum of row l >> 2
+        float xr[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) xr[r] = x[r];
+#pragma unroll
+        for (int m = 16, n = 4; m >= 4; m >>= 1, n >>= 1) {
+            const bool up = lane & m;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keepv = up ? y[i + n] : y[i], send = up ? y[i] : y[i + n];
+                y[i] = keepv + __shfl_xor_sync(0xffffffffu, send, m);
+                xr[i] = up ? xr[i + n] : xr[i];
+            }
+        }
+        y[0] += __shfl_xor_sync(0xffffffffu, y[0], 2);
+        y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
+        if ((lane & 3) == 0) op[t * p.os] = f2bf_bits(fmaf(Dh, xr[0], y[0]));
+    }
+    if (!p.fin) return;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+        if (gmem_ok(st + r * NS, 4, st_elems)) {
+            if (p.fin_dtype == KDA_DTYPE_FP32)
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.fin) + st + r * NS) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.fin) + st + r * NS) =
+                    make_uint2(pack_bf16(s[r][0], s[r][1]), pack_bf16(s[r][2], s[r][3]));
+        }
+}
+
+}  // namespace ssm
+}  // namespace kda

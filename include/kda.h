@@ -344,6 +344,153 @@ KDA_API kda_status kda_decode_ex(const void *q, const void *k, const void *v, co
                                  void *stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Operators around the mixer. A layer of a recurrent model runs
+ *   kda_residual_norm -> projection -> kda_conv -> kda_fwd or kda_ssm
+ *   -> kda_gated_norm -> projection -> kda_residual_norm,
+ * for prompts and, with kda_conv_step / kda_decode / kda_ssm_step, for single
+ * tokens. The pages have no counterpart for these; each formula stands at its
+ * entry point. All of them allocate nothing, keep no per-call state, are
+ * asynchronous on `stream`, leave their inputs unmodified and can be captured
+ * into a CUDA graph once the entry point has run eagerly on the device.
+ * Activations are bf16, parameters fp32, sums, norms and running states fp32.
+ * Token axes may be strided: `x_stride` (and the like) is the distance in
+ * elements between consecutive tokens of x, so that a slice of a projection's
+ * row can be passed as it stands; the elements of one token are contiguous,
+ * and the tokens of batch row b follow those of row b - 1 at the same
+ * distance. Strides are >= the elements of one token and, like base pointers,
+ * multiples of 16 bytes (dt: any stride).
+ */
+typedef enum kda_act {
+    KDA_ACT_NONE = 0,            /* z */
+    KDA_ACT_SIGMOID = 1,         /* 1 / (1 + exp(-z)) */
+    KDA_ACT_SILU = 2             /* z / (1 + exp(-z)) */
+} kda_act;
+
+/*
+ * kda_conv -- short causal convolution along the tokens, one filter per
+ * channel, in front of a mixer:
+ *   u[t, c] = bias[c] + sum_{j < W} weight[c, j] x[t - (W - 1) + j, c]
+ *   out = act(u),   act KDA_ACT_NONE or KDA_ACT_SILU
+ * where rows before a sequence's first token are the rows of initial_state
+ * (oldest first), or zero.
+ *   x, out   bf16 [B, T, C], token strides x_stride, out_stride; C a multiple
+ *            of 8. out must not share an element with x (KDA_ERR_STATE_MISMATCH).
+ *   weight   fp32 [C, W], W = 2, 3 or 4;  bias fp32 [C] or NULL.
+ *   initial_state, final_state  bf16 [S, W - 1, C] or NULL (S = B, or N in
+ *            varlen mode), contiguous; final_state receives the last W - 1
+ *            rows of [initial_state ; x]. They may be the same buffer;
+ *            partial overlap is rejected (KDA_ERR_STATE_MISMATCH).
+ *   cu_seqlens, N  as kda_fwd's varlen mode (B == 1). Bounds are read on the
+ *            device; where they do not rise from 0 to T, KDA_ERR_DEVICE is
+ *            flagged, nothing outside the buffers is touched, and tokens and
+ *            states of the sequences with bad bounds are unspecified.
+ * T == 0 writes final_state only.
+ */
+KDA_API kda_status kda_conv(const void *x, int64_t x_stride, const float *weight, const float *bias, kda_act act,
+                            void *out, int64_t out_stride, const void *initial_state, void *final_state,
+                            const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t C, int64_t W,
+                            void *stream);
+
+/*
+ * kda_conv_step -- kda_conv for one token of S sequences: x, out bf16 [S, C]
+ * (row strides x_stride, out_stride), state bf16 [S, W - 1, C] read and
+ * written in place (the row of the new token enters at the end). out may be x.
+ */
+KDA_API kda_status kda_conv_step(const void *x, int64_t x_stride, const float *weight, const float *bias, kda_act act,
+                                 void *out, int64_t out_stride, void *state, int64_t S, int64_t C, int64_t W,
+                                 void *stream);
+
+/*
+ * kda_ssm -- selective state-space scan with a scalar decay per head: for
+ * every sequence and head h, with state S (P x K, stored [p][k]) and per token
+ *   delta = softplus(dt + dt_bias[h]),   a = -exp(A_log[h]) delta
+ *   S <- exp(a) S + delta x b^T,   out = S c + D[h] x
+ * where head h reads group h / (H / G) of b and c.
+ *   x, out   bf16 [B, T, H, P], P = 64 or 128, token strides x_stride, out_stride.
+ *            out must not share an element with x, b, c or dt (KDA_ERR_STATE_MISMATCH).
+ *   dt       bf16 [B, T, H] before dt_bias and softplus, token stride dt_stride.
+ *   b, c     bf16 [B, T, G, K], K = 128, G divides H, token strides b_stride, c_stride.
+ *   A_log    fp32 [H];  D, dt_bias  fp32 [H] or NULL (0).
+ *   initial_state, final_state  [S, H, P, K], bf16 or fp32, or NULL, as kda_fwd's
+ *            (same buffer allowed; the running state is held in fp32).
+ *   cu_seqlens, N  as kda_fwd's varlen mode (B == 1).
+ *   workspace  16-byte aligned device buffer or NULL. With at least the
+ *            kda_ssm_workspace_bytes bytes, calls with too few (sequence, head)
+ *            pairs to fill the machine split the time axis: the states that the
+ *            pieces leave are formed first, joined, and the pieces then run side
+ *            by side. Without it such a call runs one piece per pair. Scratch
+ *            after the call; calls that overlap in time must not share it.
+ *            Too small: KDA_ERR_RANGE. Misaligned: KDA_ERR_ALIGN.
+ * A NaN or infinity in x at one token can reach the outputs of up to 127
+ * earlier tokens of the same sequence, head and channel (the tokens of a
+ * chunk are one matrix product); it never reaches another sequence.
+ */
+KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const void *b,
+                           int64_t b_stride, const void *c, int64_t c_stride, const float *A_log, const float *D,
+                           const float *dt_bias, void *out, int64_t out_stride, const void *initial_state,
+                           kda_dtype initial_dtype, void *final_state, kda_dtype final_dtype,
+                           const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t H, int64_t P,
+                           int64_t G, int64_t K, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_ssm_workspace_bytes -- the workspace with which kda_ssm may split the
+ * time axis of a call with `states` sequences (N in varlen mode, else B),
+ * `tokens` tokens in all (B * T) and H heads of P channels on the current
+ * device; 0 when it would not split. Needs a CUDA device.
+ */
+KDA_API kda_status kda_ssm_workspace_bytes(int64_t states, int64_t tokens, int64_t H, int64_t P, size_t *bytes);
+
+/*
+ * kda_ssm_step -- kda_ssm for one token of S sequences against a state updated
+ * in place: x, out bf16 [S, H, P], dt bf16 [S, H], b, c bf16 [S, G, K] (row
+ * strides as above), state [S, H, P, K] in state_dtype (BF16 or FP32).
+ * All arithmetic is fp32; a bf16 state is rounded to nearest even when stored.
+ */
+KDA_API kda_status kda_ssm_step(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const void *b,
+                                int64_t b_stride, const void *c, int64_t c_stride, const float *A_log,
+                                const float *D, const float *dt_bias, void *out, int64_t out_stride, void *state,
+                                kda_dtype state_dtype, int64_t S, int64_t H, int64_t P, int64_t G, int64_t K,
+                                void *stream);
+
+/*
+ * kda_gated_norm -- RMS norm of a mixer's output rows with its output gate:
+ *   gate_first == 0:  out = x rsqrt(mean(x^2) + eps) weight act(gate)
+ *   gate_first != 0:  u = x act(gate),  out = u rsqrt(mean(u^2) + eps) weight
+ * over rows of D channels, R rows per token, M tokens.
+ *   x, gate, out  bf16 [M, R, D], token strides x_stride, gate_stride,
+ *                 out_stride; D a multiple of 8, D <= 16384. out may be x or gate.
+ *   weight        fp32 [weight_rows, D] with weight_rows 1 (shared by the R
+ *                 rows) or R; NULL: 1.
+ *   act           KDA_ACT_NONE, _SIGMOID or _SILU.   eps >= 0 and finite.
+ */
+KDA_API kda_status kda_gated_norm(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride,
+                                  const float *weight, int64_t weight_rows, void *out, int64_t out_stride, float eps,
+                                  kda_act act, int gate_first, int64_t M, int64_t R, int64_t D, void *stream);
+
+/*
+ * kda_residual_norm -- between two blocks: the norm after a block, its gate and
+ * residual scale, the residual sum and the next block's norm in one pass:
+ *   n = x rsqrt(mean(x^2) + eps) post_weight          (post_weight NULL: n = x)
+ *   r' = residual + alpha channel_scale act(gate) n   (NULL: factor 1)
+ *   out = r' rsqrt(mean(r'^2) + eps) weight           (of the fp32 sum, before it is rounded)
+ *   x, gate, out  bf16 [M, D], row strides x_stride, gate_stride, out_stride;
+ *                 gate NULL: no gate. out NULL: the sum alone.
+ *   residual, residual_out  bf16 or fp32 (both residual_dtype) [M, D], row
+ *                 strides residual_stride, residual_out_stride; residual_out
+ *                 may be residual. residual_out NULL: the sum is not written
+ *                 (the norm after the last block); one of the two outputs is
+ *                 required. out may be x or gate; no other buffers may share
+ *                 memory (KDA_ERR_STATE_MISMATCH).
+ *   post_weight, channel_scale, weight  fp32 [D] or NULL.  D as kda_gated_norm's.
+ */
+KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                                     void *residual_out, int64_t residual_out_stride, kda_dtype residual_dtype,
+                                     const void *gate, int64_t gate_stride, kda_act act, const float *post_weight,
+                                     const float *channel_scale, float alpha, const float *weight, void *out,
+                                     int64_t out_stride, float eps, int64_t M, int64_t D, void *stream);
+
+/*
  * kda_probe_chunk -- test hook: one 16-token chunk of one head through the
  * forward pass's per-chunk steps, built from the same device code as the
  * kernels, so that each step can be checked on its own.
