@@ -4,6 +4,7 @@
 #include "kda_conv.cuh"
 #include "kda_norm.cuh"
 #include "kda_ssm_step.cuh"
+#include "kda_ssm_tc.cuh"
 
 namespace kda {
 namespace blk {
@@ -136,12 +137,108 @@ static kda_status check_ssm(const void *x, int64_t xs, const void *dt, int64_t d
     return KDA_OK;
 }
 
+// Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one.
+constexpr int64_t STEP_TOKENS = 16;
+
 static kda_status launch_ssm_steps(const ssm::SsmParams &p, cudaStream_t s)
 {
     const int64_t warps = static_cast<int64_t>(p.nseq) * p.H * (p.P / ssm::ROWS);
     const int64_t grid = (warps + ssm::STEP_THREADS / 32 - 1) / (ssm::STEP_THREADS / 32);
     ssm::kda_ssm_step_kernel<<<static_cast<unsigned>(grid), ssm::STEP_THREADS, 0, s>>>(p, warps);
     return launched("state-space step");
+}
+
+// [tokens, groups, width] bf16 tensor with `stride` elements between tokens, boxes of 64 channels x 1
+// group x 128 tokens, 128-byte swizzle.
+static bool rows_map(CUtensorMap *m, const void *base, int64_t tokens, int64_t groups, int64_t width, int64_t stride)
+{
+    std::memset(m, 0, sizeof *m);
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(groups), static_cast<cuuint64_t>(tokens)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(width * 2), static_cast<cuuint64_t>(stride * 2)};
+    cuuint32_t box[3] = {64, 1, ssmtc::L};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pieces of the time axis. One CTA walks a piece, so a call of fewer (sequence, head) pairs than SMs
+// leaves SMs idle unless sequences are cut. A cut call walks every chunk twice (states first, without
+// the score and output products: about 0.45 of a full walk) and pays two more launches (about three
+// chunks' time together). Chosen: the piece length with the least modelled time, 0 for no cut. Packed
+// sequences are modelled by their mean length; a longer one is cut into more pieces.
+struct SsmPlan {
+    int seg_chunks, seg_per_seq;
+    int64_t slots;
+    size_t bytes;
+};
+static SsmPlan ssm_plan(int64_t states, int64_t tokens, int64_t H, int64_t P, int sms)
+{
+    SsmPlan best = {0, 1, states, 0};
+    if (states < 1 || tokens < 1) return best;
+    const int64_t units = states * H, mean = (tokens + states - 1) / states, nc = (mean + ssmtc::L - 1) / ssmtc::L;
+    auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
+    double cost = static_cast<double>(waves(units)) * nc;
+    for (int64_t s = 2; s <= nc && units * s <= 4 * static_cast<int64_t>(sms); ++s) {
+        const int64_t seg = (nc + s - 1) / s, pieces = (nc + seg - 1) / seg;
+        const double c = static_cast<double>(waves(units * pieces)) * seg + 0.45 * waves(units * (pieces - 1)) * seg + 3.0;
+        if (c < cost) {
+            cost = c;
+            best.seg_chunks = static_cast<int>(seg);
+            best.seg_per_seq = static_cast<int>(pieces);
+        }
+    }
+    if (best.seg_chunks) {
+        best.slots = tokens / (static_cast<int64_t>(ssmtc::L) * best.seg_chunks) + states;
+        best.bytes = static_cast<size_t>(best.slots) * H * (P * ssm::NS + 1) * sizeof(float);
+    }
+    return best;
+}
+
+template <int P, int PARTS, bool FULL>
+static kda_status launch_ssm_tc(int64_t grid, const CUtensorMap &mx, const CUtensorMap &mb, const CUtensorMap &mc,
+                                const CUtensorMap &mo, const ssmtc::TcParams &t, cudaStream_t s)
+{
+    using Lay = ssmtc::Layout<P, PARTS, FULL>;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        const cudaError_t e = cudaFuncSetAttribute(ssmtc::kda_ssm_tc_kernel<P, PARTS, FULL>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC);
+        if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "scan set-up failed: %s", cudaGetErrorString(e));
+        configured_dev = dev;
+    }
+    ssmtc::kda_ssm_tc_kernel<P, PARTS, FULL><<<static_cast<unsigned>(grid), ssmtc::NTHREADS, Lay::ALLOC, s>>>(mx, mb, mc, mo, t);
+    return launched("scan");
+}
+
+template <int P>
+static kda_status launch_ssm(const ssm::SsmParams &p, const SsmPlan &plan, float *ws, cudaStream_t s)
+{
+    CUtensorMap mx, mb, mc, mo;
+    if (!rows_map(&mx, p.x, p.total, p.H, P, p.xs) || !rows_map(&mb, p.b, p.total, p.G, ssm::NS, p.bs) ||
+        !rows_map(&mc, p.c, p.total, p.G, ssm::NS, p.cs) || !rows_map(&mo, p.out, p.total, p.H, P, p.os))
+        return fail(KDA_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad geometry)");
+    ssmtc::TcParams t = {};
+    t.p = p;
+    const bool split = plan.seg_chunks && ws;
+    t.seg_chunks = split ? plan.seg_chunks : 0;
+    t.seg_per_seq = plan.seg_per_seq;
+    t.slots = static_cast<int>(split ? (p.cu ? plan.slots : static_cast<int64_t>(p.nseq) * plan.seg_per_seq) : p.nseq);
+    t.ws = ws;
+    const int64_t grid = static_cast<int64_t>(t.slots) * p.H;
+    if (split) {
+        if (const kda_status st = launch_ssm_tc<P, 3, false>(grid, mx, mb, mc, mo, t, s); st != KDA_OK) return st;
+        ssmtc::kda_ssm_join_kernel<P><<<static_cast<unsigned>(static_cast<int64_t>(p.nseq) * p.H * (P * ssm::NS / (4 * ssmtc::JOIN_THREADS))),
+                                       ssmtc::JOIN_THREADS, 0, s>>>(t);
+        if (const kda_status st = launched("join"); st != KDA_OK) return st;
+    }
+    // an fp32 final state keeps three parts of w b, otherwise two are enough
+    return p.fin && p.fin_dtype == KDA_DTYPE_FP32 ? launch_ssm_tc<P, 3, true>(grid, mx, mb, mc, mo, t, s)
+                                                  : launch_ssm_tc<P, 2, true>(grid, mx, mb, mc, mo, t, s);
 }
 
 // Threads along a row of D channels: a power of two of lanes up to a warp (then one, two or four
@@ -267,7 +364,9 @@ KDA_API kda_status kda_ssm_workspace_bytes(int64_t states, int64_t tokens, int64
     if (!bytes) return fail(KDA_ERR_NULL, "kda_ssm_workspace_bytes: bytes is required");
     if (states < 0 || tokens < 0 || H < 1 || (P != 64 && P != 128))
         return fail(KDA_ERR_SHAPE, "bad sizes states=%lld tokens=%lld H=%lld P=%lld", (long long)states, (long long)tokens, (long long)H, (long long)P);
-    *bytes = 0;
+    blk::Device d;
+    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+    *bytes = blk::ssm_plan(states, tokens, H, P, d.sms).bytes;
     return KDA_OK;
 }
 
@@ -325,8 +424,15 @@ KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int6
     p.G = static_cast<int>(G);
     p.nseq = static_cast<int>(nseq);
     p.total = static_cast<int>(total);
-    (void)workspace_bytes;
-    return blk::launch_ssm_steps(p, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (total <= (cu_seqlens ? 1 : nseq) * blk::STEP_TOKENS) return blk::launch_ssm_steps(p, s);
+    blk::Device d;
+    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+    const blk::SsmPlan plan = blk::ssm_plan(nseq, total, H, P, d.sms);
+    if (workspace && workspace_bytes < plan.bytes)
+        return fail(KDA_ERR_RANGE, "workspace of %zu bytes is smaller than the %zu this call needs", workspace_bytes, plan.bytes);
+    float *ws = static_cast<float *>(workspace);
+    return P == 64 ? blk::launch_ssm<64>(p, plan, ws, s) : blk::launch_ssm<128>(p, plan, ws, s);
 }
 
 KDA_API kda_status kda_ssm_step(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const void *b,

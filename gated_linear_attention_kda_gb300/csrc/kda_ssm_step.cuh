@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(STEP_THREADS) kda_ssm_step_kernel(const SsmPar
         }
         y[0] += __shfl_xor_sync(0xffffffffu, y[0], 2);
         y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
-        if ((lane & 3) == 0) op[t * p.os] = f2bf_bits(fmaf(Dh, xr[0], y[0]));
+        if ((lane & 3) == 0) op[t * p.os] = f2bf_bits(p.D ? fmaf(Dh, xr[0], y[0]) : y[0]);
     }
     if (!p.fin) return;
 #pragma unroll

@@ -1,0 +1,721 @@
+// kda_ssm_tc.cuh -- the selective state-space scan over prompts on the 5th-generation tensor core,
+// 128 tokens at a time.
+//
+// Chunk algebra. With a_t = -exp(A_log) delta_t, the recurrence S <- exp(a) S + delta x b^T,
+// out = S c + D x over a chunk of tokens j = 0..127 that starts from S0 is
+//   G[i, j] = c_i . b_j                                                    (per group)
+//   M[i, j] = G[i, j] delta_j exp(a_{j+1} + ... + a_i)        for j <= i, else 0
+//   out_i   = sum_j M[i, j] x_j + exp(a_0 + ... + a_i) S0 c_i + D x_i
+//   S1      = exp(a_0 + ... + a_127) S0 + sum_j w_j x_j b_j^T,   w_j = delta_j exp(a_{j+1} + ... + a_127)
+// Every exponent is a sum of terms of one sign taken directly: a chunk is four blocks of 32 tokens;
+// between blocks the decay is the product of 2^(sum to the end of j's block) and 2^(sum from there to
+// i), each at most 1, and only inside a block are two running sums subtracted (at most 32 terms, each
+// held at or above -160). So nothing overflows, and the score matrix costs one exponential per token
+// and block instead of one per entry away from the diagonal blocks.
+//
+// One CTA owns the state of one (sequence, head), or of one piece of its time axis, and walks its
+// chunks. The state lives in tensor memory, fp32, transposed (lane = state channel n, column = head
+// channel p), so that
+//   G   [128 x 128]  = C B^T                        A, B straight from the TMA tiles (K-major)
+//   Yx  [128 x P]    = C S0^T                       S0 rounded to bf16 in shared memory
+//   Yi  [128 x P]    = M X                          M bf16 in tensor memory, X straight from its tile
+//   S  += (w B)^T X                                 w B split into bf16 parts, X straight from its tile
+// Roundings: M and S0 to bf16 as operands (the output is bf16; the carried state itself is not
+// rounded); w B into PARTS bf16 parts, 3 where an fp32 state is returned (2^-25 of a term) and 2
+// where it is returned in bf16 or not at all (2^-17). Sums are fp32.
+//
+// Warp roles (512 threads):
+//   warp 0      TMA producer (lane 0): x and b tiles two deep, c one; tensor memory allocation
+//   warp 1      MMA issuer
+//   warp 2      step sizes, running sums and decays of a chunk, one chunk ahead
+//   warp 3      stores the output tile (written over the x tile) by TMA
+//   warps 4-7   scores G -> M, then the output rows (thread = token)
+//   warps 8-11  state: bf16 copy for Yx, decay in place (thread = state channel)
+//   warps 12-15 w B: 16 tokens at a time, first part over the b tile, the others into a ring
+// Tensor memory columns: G (M over it) [0, 128), Yi [128, 128 + P), Yx, S.
+#pragma once
+#include "kda_ssm_step.cuh"
+#include "tcgen05.cuh"
+
+namespace kda {
+namespace ssmtc {
+
+using ssm::MIN_LOG2_DECAY;
+using ssm::NS;
+
+constexpr int L = 128;          // tokens per chunk
+constexpr int SUB = 16;         // tokens per w B block (one MMA step)
+constexpr int NTHREADS = 512;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t T_G = 0, T_YI = 128;
+
+struct TcParams {
+    ssm::SsmParams p;
+    int seg_chunks;             // chunks per piece; 0: sequences are not split
+    int seg_per_seq;            // pieces per batch row (batched mode)
+    int slots;                  // pieces in all
+    float *ws;                  // [slots, H, P, NS] states, then [slots, H] log2 decays
+};
+
+// per-chunk scalars, two buffers: running log2 sums inside 32-token blocks, delta, delta 2^(rest of
+// the block), w, block totals
+constexpr int SC_LOC = 0, SC_DELTA = 512, SC_ES = 1024, SC_W = 1536, SC_TOT = 2048, SC_BYTES = 2112;
+
+template <int P, int PARTS, bool FULL>
+struct Layout {
+    static constexpr int BOX = L * 128;            // 64 channels x 128 rows, 128-byte swizzle
+    static constexpr int XT = P / 64 * BOX, BT = 2 * BOX;
+    static constexpr int SLOT = (PARTS - 1) * SUB * NS * 2;
+    static constexpr int NSLOT = FULL && P == 128 ? 3 : 4;
+    static constexpr int X = 0;                    // two stages
+    static constexpr int B = X + 2 * XT;           // two stages
+    static constexpr int C = B + 2 * BT;
+    static constexpr int H = C + (FULL ? BT : 0);  // bf16 state, [n][p]
+    static constexpr int RING = H + (FULL ? XT : 0);
+    static constexpr int SC = RING + NSLOT * SLOT;
+    static constexpr int BAR = SC + 2 * SC_BYTES;
+    static constexpr int X_FULL = 0, X_EMPTY = 2, B_FULL = 4, B_EMPTY = 6, C_FULL = 8, C_EMPTY = 9, SC_FULL = 10, SC_EMPTY = 12,
+                         G_DONE = 14, M_DONE = 15, Y_DONE = 16, Y_FREE = 17, H_READY = 18, S_DONE = 19, OUT_FULL = 20,
+                         END = 21, W_FULL = 22, W_EMPTY = 26, NBARS = 30;
+    static constexpr int TMEMPTR = BAR + NBARS * 8;
+    static constexpr int FLAGS = TMEMPTR + 16;
+    static constexpr int ALLOC = FLAGS + 16 + 1024;
+    static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+    static_assert(SC % 16 == 0 && BAR % 8 == 0 && TMEMPTR % 16 == 0, "alignment");
+};
+
+struct Piece {
+    int seq, bos, len;      // tokens of the piece
+    bool ok, last;          // last piece of its sequence
+};
+
+__device__ __forceinline__ int pieces_of(int len, int seg_chunks)
+{
+    return len <= L * seg_chunks ? 1 : (len + L * seg_chunks - 1) / (L * seg_chunks);
+}
+
+// Piece `slot` of a split call: the pieces of the sequences one after another, every lane of a warp
+// together (32 sequences per step in varlen mode). Slots past the last piece are not ok.
+__device__ __forceinline__ Piece locate(const TcParams &t, int slot)
+{
+    const ssm::SsmParams &p = t.p;
+    int seq, seg;
+    if (!p.cu) {
+        seq = slot / t.seg_per_seq;
+        seg = slot % t.seg_per_seq;
+    } else {
+        const int lane = threadIdx.x & 31;
+        int base = 0;
+        seq = -1;
+        seg = 0;
+        for (int s0 = 0; s0 < p.nseq && seq < 0; s0 += 32) {
+            int n = 0;
+            if (s0 + lane < p.nseq) {
+                const Span sp = ssm::ssm_span(p, s0 + lane);
+                n = sp.ok ? pieces_of(sp.len, t.seg_chunks) : 0;
+            }
+            int inc = n;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, m);
+                if (lane >= m) inc += v;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, slot >= base + inc - n && slot < base + inc);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                seq = s0 + src;
+                seg = slot - base - __shfl_sync(0xffffffffu, inc - n, src);
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (seq < 0) return {0, 0, 0, false, false};
+    }
+    const Span sp = ssm::ssm_span(p, seq);
+    const int span = L * t.seg_chunks;
+    const long long at = static_cast<long long>(seg) * span;
+    if (at >= sp.len) return {seq, sp.bos, 0, sp.ok && seg == 0, true};  // an empty sequence has one empty piece
+    const int len = min(span, sp.len - static_cast<int>(at));
+    return {seq, sp.bos + static_cast<int>(at), len, sp.ok, at + len == sp.len};
+}
+
+// Varlen order, longest sequences first (up to LPT_MAX_SEQS sequences), so that the long chains start
+// in the first wave.
+__device__ __forceinline__ int longest_first(const ssm::SsmParams &p, int rank)
+{
+    const int lane = threadIdx.x & 31;
+    int found = rank;
+    for (int base = 0; base < p.nseq; base += 32) {
+        const int i = base + lane;
+        const long long li = i < p.nseq ? p.cu[i + 1] - p.cu[i] : -1;
+        int r = 0;
+        for (int j = 0; j < p.nseq; ++j) {
+            const long long lj = p.cu[j + 1] - p.cu[j];
+            r += (lj > li) || (lj == li && j < i);
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, i < p.nseq && r == rank);
+        if (m) found = base + __ffs(m) - 1;
+    }
+    return found;
+}
+
+// FULL: outputs and states; else only the state that the piece leaves when it starts from zero (to
+// the workspace, with its decay), for the pieces that another one follows.
+template <int P, int PARTS, bool FULL>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
+                      const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap to, const TcParams t)
+{
+    using Lay = Layout<P, PARTS, FULL>;
+    constexpr uint32_t T_YX = T_YI + P, T_S = T_YI + 2 * P;
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+#define SM_AT(T, a) (*reinterpret_cast<T *>(smem + (smem_checked((a), sizeof(T), sb) - sb)))
+    const ssm::SsmParams &p = t.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H;
+    Piece pc;
+    if (t.seg_chunks) {
+        pc = locate(t, slot);
+    } else {
+        const int seq = p.cu && p.nseq <= LPT_MAX_SEQS ? longest_first(p, slot) : slot;
+        const Span sp = ssm::ssm_span(p, seq);
+        pc = {seq, sp.bos, sp.len, sp.ok, true};
+    }
+    if (FULL && p.cu && blockIdx.x == 0) blk::check_bounds(p.cu, p.nseq, p.total);
+    if (!pc.ok || (!FULL && pc.last)) return;  // CTA-uniform, before any tensor memory is taken
+    const int nch = (pc.len + L - 1) / L;
+    const int grp = h / (p.H / p.G);
+
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
+    auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
+    auto xt = [&](int n) { return sb + Lay::X + (n & 1) * Lay::XT; };
+    auto bt = [&](int n) { return sb + Lay::B + (n & 1) * Lay::BT; };
+    auto sc = [&](int n) { return sb + Lay::SC + (n & 1) * SC_BYTES; };
+    auto live_of = [&](int n) { return min(L, pc.len - n * L); };
+
+    if (warp == 0) {
+        tc::alloc(sb + Lay::TMEMPTR, TMEM_COLS);
+        tc::relinquish();
+    }
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(Lay::X_FULL + i), 1);
+            mbar_init(bar(Lay::X_EMPTY + i), 1);
+            mbar_init(bar(Lay::B_FULL + i), 1);
+            mbar_init(bar(Lay::B_EMPTY + i), 1);
+            mbar_init(bar(Lay::SC_FULL + i), 1);
+            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 12 : 8);
+        }
+        mbar_init(bar(Lay::C_FULL), 1);
+        mbar_init(bar(Lay::C_EMPTY), 1);
+        mbar_init(bar(Lay::G_DONE), 1);
+        mbar_init(bar(Lay::M_DONE), 4);
+        mbar_init(bar(Lay::Y_DONE), 1);
+        mbar_init(bar(Lay::Y_FREE), 4);
+        mbar_init(bar(Lay::H_READY), 4);
+        mbar_init(bar(Lay::S_DONE), 1);
+        mbar_init(bar(Lay::OUT_FULL), 4);
+        mbar_init(bar(Lay::END), 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(Lay::W_FULL + i), 4);
+            mbar_init(bar(Lay::W_EMPTY + i), 1);
+        }
+        flags[0] = 0;
+        fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR);
+    // the whole warp goes on only when every lane saw the phase
+    auto wait_w = [&](int b, uint32_t par) {
+        const bool ok = __all_sync(0xffffffffu, wait_bar(bar(b), par, flags));
+        __syncwarp();
+        return ok;
+    };
+    auto arrive_w = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tx);
+            tma_prefetch_desc(&tb);
+            if (FULL) tma_prefetch_desc(&tcm);
+            int nb = 0, nx = 0, ncc = 0;  // tiles issued
+            for (int n = 0; n < nch; ++n) {
+                const int s = n & 1, tok = pc.bos + n * L;
+                const uint32_t par = ((n >> 1) & 1) ^ 1;
+                if (!wait_bar(bar(Lay::B_EMPTY + s), par, flags)) break;
+                mbar_arrive_expect_tx(bar(Lay::B_FULL + s), Lay::BT);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) tma_load_3d(bt(n) + k * Lay::BOX, &tb, 64 * k, grp, tok, bar(Lay::B_FULL + s));
+                ++nb;
+                if (!wait_bar(bar(Lay::X_EMPTY + s), par, flags)) break;
+                mbar_arrive_expect_tx(bar(Lay::X_FULL + s), Lay::XT);
+#pragma unroll
+                for (int k = 0; k < P / 64; ++k) tma_load_3d(xt(n) + k * Lay::BOX, &tx, 64 * k, h, tok, bar(Lay::X_FULL + s));
+                ++nx;
+                if constexpr (FULL) {
+                    if (n > 0 && !wait_bar(bar(Lay::C_EMPTY), (n - 1) & 1, flags)) break;
+                    mbar_arrive_expect_tx(bar(Lay::C_FULL), Lay::BT);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) tma_load_3d(sb + Lay::C + k * Lay::BOX, &tcm, 64 * k, grp, tok, bar(Lay::C_FULL));
+                    ++ncc;
+                }
+            }
+            // no copy is in flight when the CTA ends, whichever way the loop was left
+            for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) drain_bar(bar(Lay::B_FULL + (m & 1)), (m >> 1) & 1);
+            for (int m = nx > 2 ? nx - 2 : 0; m < nx; ++m) drain_bar(bar(Lay::X_FULL + (m & 1)), (m >> 1) & 1);
+            if (ncc > 0) drain_bar(bar(Lay::C_FULL), (ncc - 1) & 1);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer (whole warp)
+        if (nch > 0) {
+            constexpr uint32_t id_g = tc::idesc(tc::BF16, 128, 128, 0, 0);
+            constexpr uint32_t id_y = tc::idesc(tc::BF16, 128, P, 0, 1);
+            constexpr uint32_t id_s = tc::idesc(tc::BF16, 128, P, 1, 1);
+            const uint64_t dc = tc::sdesc(sb + Lay::C, 16, 1024, tc::SWZ_128B);
+            const uint64_t dh = tc::sdesc(sb + Lay::H, Lay::BOX, 1024, tc::SWZ_128B);
+            auto kstep = [](int i) { return static_cast<uint64_t>(((i >> 2) * Lay::BOX + (i & 3) * 32) >> 4); };
+            auto issue_g = [&](int n) {
+                if (!wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::C_FULL, n & 1)) return false;
+                if (n > 0 && !wait_w(Lay::Y_DONE, (n - 1) & 1)) return false;  // M of the last chunk has been read
+                tc::fence_after();
+                const uint64_t db = tc::sdesc(bt(n), 16, 1024, tc::SWZ_128B);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_G, dc + kstep(i), db + kstep(i), id_g, i > 0);
+                tc::commit_w(bar(Lay::G_DONE));
+                return true;
+            };
+            int k = 0;  // w B blocks so far
+            bool ok = true;
+            if constexpr (FULL) ok = issue_g(0);
+            for (int n = 0; ok && n < nch; ++n) {
+                const int nsub = (live_of(n) + SUB - 1) / SUB;
+                const uint64_t dx = tc::sdesc(xt(n), Lay::BOX, 1024, tc::SWZ_128B);
+                const uint64_t dhi = tc::sdesc(bt(n), Lay::BOX, 1024, tc::SWZ_128B);
+                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::H_READY, n & 1);
+                for (int s = 0; ok && s < nsub; ++s, ++k) {
+                    const int sl = k % Lay::NSLOT;
+                    ok = wait_w(Lay::W_FULL + sl, (k / Lay::NSLOT) & 1);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint64_t step = static_cast<uint64_t>((SUB * 128 * s) >> 4);
+                    const uint64_t dr = tc::sdesc(sb + Lay::RING + sl * Lay::SLOT, SUB * 128, 1024, tc::SWZ_128B);
+                    tc::mma_ss_w(tmem + T_S, dhi + step, dx + step, id_s, 1);
+#pragma unroll
+                    for (int i = 0; i < PARTS - 1; ++i)
+                        tc::mma_ss_w(tmem + T_S, dr + ((i * SUB * NS * 2) >> 4), dx + step, id_s, 1);
+                    tc::commit_w(bar(Lay::W_EMPTY + sl));
+                    if constexpr (FULL) {
+                        if (s == 0) {  // Yx = C S0^T, over the accumulator whose last values have been read
+                            ok = n == 0 || wait_w(Lay::Y_FREE, (n - 1) & 1);
+                            if (!ok) break;
+                            tc::fence_after();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                tc::mma_ss_w(tmem + T_YX, dc + kstep(i), dh + ((i * 16 * 128) >> 4), id_y, i > 0);
+                            tc::commit_w(bar(Lay::C_EMPTY));
+                        }
+                        if (s == min(3, nsub - 1)) {  // Yi = M X
+                            ok = wait_w(Lay::M_DONE, n & 1);
+                            if (!ok) break;
+                            tc::fence_after();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                tc::mma_ts_w(tmem + T_YI, tmem + T_G + 8 * i, dx + ((i * 16 * 128) >> 4), id_y, i > 0);
+                            tc::commit_w(bar(Lay::Y_DONE));
+                        }
+                    }
+                }
+                if (!ok) break;
+                tc::commit_w(bar(Lay::S_DONE));
+                tc::commit_w(bar(Lay::B_EMPTY + (n & 1)));
+                if constexpr (!FULL) tc::commit_w(bar(Lay::X_EMPTY + (n & 1)));
+                if constexpr (FULL)
+                    if (n + 1 < nch) ok = issue_g(n + 1);
+            }
+            tc::commit_w(bar(Lay::END));
+            if (lane == 0) drain_bar(bar(Lay::END), 0);
+            __syncwarp();
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- step sizes and decays
+        const float A2 = -expf(__ldg(p.A_log + h)) * LOG2E, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
+        const uint16_t *dp = p.dt + static_cast<long long>(pc.bos) * p.dts + h;
+        const int j0 = 4 * lane;
+        uint32_t raw[4] = {0u, 0u, 0u, 0u};
+        auto fetch = [&](int n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n * L + j0 + i < pc.len) raw[i] = dp[static_cast<long long>(n * L + j0 + i) * p.dts];
+        };
+        fetch(0);
+        float seg = 0.f;
+        for (int n = 0; n < nch; ++n) {
+            const int Lv = live_of(n);
+            float d[4], a[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool live = j0 + i < Lv;
+                d[i] = live ? ssm::softplus(__uint_as_float(raw[i] << 16) + bias) : 0.f;
+                a[i] = live ? fmaxf(A2 * d[i], MIN_LOG2_DECAY) : 0.f;
+            }
+            fetch(n + 1);
+            // running sums inside the lane, then over the eight lanes of a block, from both ends
+            const float l0 = a[0], l1 = l0 + a[1], l2 = l1 + a[2], l3 = l2 + a[3];
+            const float r3 = 0.f, r2 = a[3], r1 = a[2] + r2, r0 = a[1] + r1;
+            float pre = l3, post = l3;
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, pre, m, 8), v = __shfl_down_sync(0xffffffffu, post, m, 8);
+                if ((lane & 7) >= m) pre += u;
+                if ((lane & 7) + m < 8) post += v;
+            }
+            float before = __shfl_up_sync(0xffffffffu, pre, 1, 8), after = __shfl_down_sync(0xffffffffu, post, 1, 8);
+            if ((lane & 7) == 0) before = 0.f;
+            if ((lane & 7) == 7) after = 0.f;
+            const float t0 = __shfl_sync(0xffffffffu, pre, 7), t1 = __shfl_sync(0xffffffffu, pre, 15);
+            const float t2 = __shfl_sync(0xffffffffu, pre, 23), t3 = __shfl_sync(0xffffffffu, pre, 31);
+            const int blkq = lane >> 3;
+            const float rest = blkq == 0 ? t1 + (t2 + t3) : blkq == 1 ? t2 + t3 : blkq == 2 ? t3 : 0.f;
+            seg += (t0 + t1) + (t2 + t3);
+            const float sf[4] = {r0 + after, r1 + after, r2 + after, r3 + after};
+            if (!wait_w(Lay::SC_EMPTY + (n & 1), ((n >> 1) & 1) ^ 1)) break;
+            const uint32_t o = sc(n) + 4 * j0;
+            SM_AT(float4, o + SC_LOC) = make_float4(before + l0, before + l1, before + l2, before + l3);
+            SM_AT(float4, o + SC_DELTA) = make_float4(d[0], d[1], d[2], d[3]);
+            SM_AT(float4, o + SC_ES) = make_float4(d[0] * ex2_approx(sf[0]), d[1] * ex2_approx(sf[1]), d[2] * ex2_approx(sf[2]), d[3] * ex2_approx(sf[3]));
+            SM_AT(float4, o + SC_W) = make_float4(d[0] * ex2_approx(sf[0] + rest), d[1] * ex2_approx(sf[1] + rest),
+                                                  d[2] * ex2_approx(sf[2] + rest), d[3] * ex2_approx(sf[3] + rest));
+            if (lane == 0) SM_AT(float4, sc(n) + SC_TOT) = make_float4(t0, t1, t2, t3);
+            arrive_w(Lay::SC_FULL + (n & 1));
+        }
+        if (!FULL && lane == 0)
+            t.ws[static_cast<size_t>(t.slots) * p.H * P * NS + static_cast<size_t>(slot) * p.H + h] = seg;
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- output stores
+        if constexpr (FULL) {
+            for (int n = 0; n < nch; ++n) {
+                if (!wait_w(Lay::OUT_FULL, n & 1)) break;
+                if (lane == 0) {
+                    if (live_of(n) == L) {
+#pragma unroll
+                        for (int k = 0; k < P / 64; ++k) tma_store_3d(&to, xt(n) + k * Lay::BOX, 64 * k, h, pc.bos + n * L);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                    mbar_arrive(bar(Lay::X_EMPTY + (n & 1)));
+                }
+                __syncwarp();
+            }
+            if (lane == 0) bulk_wait_all();
+        }
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- scores and outputs
+        if constexpr (FULL) {
+            const int q = warp & 3, row = 32 * q + lane;
+            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16);
+            const float Dh = p.D ? __ldg(p.D + h) : 0.f;
+            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P;
+            for (int n = 0; n < nch; ++n) {
+                const int Lv = live_of(n);
+                if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::G_DONE, n & 1)) break;
+                tc::fence_after();
+                const uint32_t s = sc(n);
+                const float4 tot = SM_AT(const float4, s + SC_TOT);
+                const float loc = SM_AT(const float, s + SC_LOC + 4 * row);
+                const float tb[4] = {tot.x, tot.y, tot.z, tot.w};
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t m[16];
+                    if (b > q) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) m[i] = 0u;
+                    } else {
+                        uint32_t g[32];
+                        tc::ld32(lb + T_G + 32 * b, g);
+                        if (b < q) {
+                            float e = loc;  // log2 decay from the end of block b to this row
+#pragma unroll
+                            for (int k = 1; k < 3; ++k)
+                                if (k > b && k < q) e += tb[k];
+                            e = ex2_approx(e);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 v = SM_AT(const float4, s + SC_ES + 128 * b + 4 * i);
+                                m[i / 2] = pack_bf16(__uint_as_float(g[i]) * (e * v.x), __uint_as_float(g[i + 1]) * (e * v.y));
+                                m[i / 2 + 1] = pack_bf16(__uint_as_float(g[i + 2]) * (e * v.z), __uint_as_float(g[i + 3]) * (e * v.w));
+                            }
+                        } else {
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 v = SM_AT(const float4, s + SC_LOC + 128 * b + 4 * i);
+                                const float4 d = SM_AT(const float4, s + SC_DELTA + 128 * b + 4 * i);
+                                const float lv[4] = {v.x, v.y, v.z, v.w}, dv[4] = {d.x, d.y, d.z, d.w};
+                                float o[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    o[k] = i + k <= lane ? __uint_as_float(g[i + k]) * (dv[k] * ex2_approx(loc - lv[k])) : 0.f;
+                                m[i / 2] = pack_bf16(o[0], o[1]);
+                                m[i / 2 + 1] = pack_bf16(o[2], o[3]);
+                            }
+                        }
+                    }
+                    tc::st16(lb + T_G + 16 * b, m);  // over columns of G that have been read
+                }
+                tc::wait_st();
+                tc::fence_before();
+                arrive_w(Lay::M_DONE);
+                float e = loc;  // log2 decay from the chunk's start
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (k < q) e += tb[k];
+                e = ex2_approx(e);
+                arrive_w(Lay::SC_EMPTY + (n & 1));
+                // the x tile is the output's buffer once the state product has read it
+                if (!wait_w(Lay::S_DONE, n & 1)) break;
+                tc::fence_after();
+                const uint32_t xr = xt(n) + row * 128;
+#pragma unroll 1
+                for (int g4 = 0; g4 < P / 32; ++g4) {
+                    uint32_t yi[32], yx[32];
+                    tc::ld32(lb + T_YI + 32 * g4, yi);
+                    tc::ld32(lb + T_YX + 32 * g4, yx);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // eight channels: 16 bytes, swizzled by the row
+                        const int c8 = 4 * g4 + i;
+                        const uint32_t at = xr + (c8 >> 3) * Lay::BOX + (((c8 & 7) ^ (row & 7)) << 4);
+                        float x[8], y[8];
+                        blk::unpack8(SM_AT(const uint4, at), x);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            y[k] = fmaf(e, __uint_as_float(yx[8 * i + k]), __uint_as_float(yi[8 * i + k]));
+                            if (p.D) y[k] = fmaf(Dh, x[k], y[k]);
+                        }
+                        const uint4 o = blk::pack8(y);
+                        if (Lv == L)
+                            SM_AT(uint4, at) = o;
+                        else if (row < Lv)  // a ragged end is stored from registers
+                            *reinterpret_cast<uint4 *>(op + static_cast<long long>(n) * L * p.os + 8 * c8) = o;
+                    }
+                }
+                tc::fence_before();
+                tc::fence_async_smem();
+                arrive_w(Lay::Y_FREE);
+                arrive_w(Lay::OUT_FULL);
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------- state
+        const int q = warp & 3, nn = 32 * q + lane;
+        const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_S;
+        const size_t unit = static_cast<size_t>(pc.seq) * p.H + h;
+        const size_t st_elems = static_cast<size_t>(p.nseq) * p.H * P * NS;
+        float *wsp = t.seg_chunks ? t.ws + (static_cast<size_t>(slot) * p.H + h) * P * NS + nn : nullptr;
+        // 32 columns (head channels 32 g4 ..) of the state this piece starts from
+        auto load_init = [&](int g4, uint32_t(&r)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const size_t at = static_cast<size_t>(32 * g4 + i) * NS;
+                r[i] = 0u;
+                if constexpr (!FULL) continue;
+                if (t.seg_chunks) {
+                    r[i] = __float_as_uint(wsp[at]);
+                } else if (p.init && gmem_ok(unit * P * NS + at + nn, 1, st_elems)) {
+                    r[i] = p.init_dtype == KDA_DTYPE_FP32
+                               ? __float_as_uint(static_cast<const float *>(p.init)[unit * P * NS + at + nn])
+                               : static_cast<uint32_t>(static_cast<const uint16_t *>(p.init)[unit * P * NS + at + nn]) << 16;
+                }
+            }
+        };
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1);
+            if (ok && n > 0) ok = wait_w(Lay::S_DONE, (n - 1) & 1);
+            if (!ok) break;
+            tc::fence_after();
+            const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
+            const float gam = ex2_approx((tot.x + tot.y) + (tot.z + tot.w));
+            arrive_w(Lay::SC_EMPTY + (n & 1));
+#pragma unroll 1
+            for (int g4 = 0; g4 < P / 32; ++g4) {
+                uint32_t r[32];
+                if (n == 0) {
+                    load_init(g4, r);
+                } else {
+                    tc::ld32(lb + 32 * g4, r);
+                    tc::wait_ld();
+                }
+                if constexpr (FULL) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c8 = 4 * g4 + i;
+                        const uint32_t at = sb + Lay::H + (c8 >> 3) * Lay::BOX + nn * 128 + (((c8 & 7) ^ (nn & 7)) << 4);
+                        SM_AT(uint4, at) = make_uint4(pack_bf16(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1])),
+                                                      pack_bf16(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3])),
+                                                      pack_bf16(__uint_as_float(r[8 * i + 4]), __uint_as_float(r[8 * i + 5])),
+                                                      pack_bf16(__uint_as_float(r[8 * i + 6]), __uint_as_float(r[8 * i + 7])));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(gam * __uint_as_float(r[i]));
+                tc::st32(lb + 32 * g4, r);
+            }
+            tc::wait_st();
+            tc::fence_before();
+            tc::fence_async_smem();
+            arrive_w(Lay::H_READY);
+        }
+        const bool write = FULL ? (pc.last && p.fin) : true;
+        if (ok && write) {
+            if (nch > 0) {
+                ok = wait_w(Lay::S_DONE, (nch - 1) & 1);
+                tc::fence_after();
+            }
+#pragma unroll 1
+            for (int g4 = 0; ok && g4 < P / 32; ++g4) {
+                uint32_t r[32];
+                if (nch > 0) {
+                    tc::ld32(lb + 32 * g4, r);
+                    tc::wait_ld();
+                } else {
+                    load_init(g4, r);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const size_t at = static_cast<size_t>(32 * g4 + i) * NS;
+                    if constexpr (!FULL)
+                        wsp[at] = __uint_as_float(r[i]);
+                    else if (!gmem_ok(unit * P * NS + at + nn, 1, st_elems))
+                        continue;
+                    else if (p.fin_dtype == KDA_DTYPE_FP32)
+                        static_cast<float *>(p.fin)[unit * P * NS + at + nn] = __uint_as_float(r[i]);
+                    else
+                        static_cast<uint16_t *>(p.fin)[unit * P * NS + at + nn] = f2bf_bits(__uint_as_float(r[i]));
+                }
+            }
+        }
+        tc::fence_before();
+    } else {
+        // ---------------------------------------------------------------- w B
+        const int u = threadIdx.x - 384;  // 0..127
+        int k = 0;
+        bool ok = true;
+        for (int n = 0; ok && n < nch; ++n) {
+            const int Lv = live_of(n), nsub = (Lv + SUB - 1) / SUB;
+            ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1);
+            if (ok && FULL) ok = wait_w(Lay::G_DONE, n & 1);  // the b tile has been read as it came
+            if (ok && Lv < L) {
+                // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
+                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1);
+                if (ok)
+                    for (int i = u; i < (L - Lv) * (P / 8); i += 128) {
+                        const int r = Lv + i / (P / 8), c8 = i % (P / 8);
+                        SM_AT(uint4, xt(n) + (c8 >> 3) * Lay::BOX + r * 128 + (c8 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+            }
+            for (int s = 0; ok && s < nsub; ++s, ++k) {
+                const int sl = k % Lay::NSLOT;
+                ok = wait_w(Lay::W_EMPTY + sl, ((k / Lay::NSLOT) & 1) ^ 1);
+                if (!ok) break;
+                const uint32_t ring = sb + Lay::RING + sl * Lay::SLOT;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int id = u + 128 * i, r = id >> 4, box = (id >> 3) & 1;
+                    const uint32_t off = r * 128 + (((id & 7) ^ (r & 7)) << 4);
+                    const uint32_t at = bt(n) + box * Lay::BOX + SUB * s * 128 + off;
+                    const float w = SM_AT(const float, sc(n) + SC_W + 4 * (SUB * s + r));
+                    const bool live = SUB * s + r < Lv;
+                    float v[8];
+                    blk::unpack8(SM_AT(const uint4, at), v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = live ? w * v[j] : 0.f;
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+                        const uint4 o = blk::pack8(v);
+                        float f[8];
+                        blk::unpack8(o, f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] -= f[j];
+                        SM_AT(uint4, part == 0 ? at : ring + (part - 1) * SUB * NS * 2 + box * SUB * 128 + off) = o;
+                    }
+                }
+                tc::fence_async_smem();
+                arrive_w(Lay::W_FULL + sl);
+            }
+            if (ok) arrive_w(Lay::SC_EMPTY + (n & 1));
+        }
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc::fence_after();
+        tc::dealloc(tmem, TMEM_COLS);
+    }
+#undef SM_AT
+}
+
+// Joins the pieces of every (sequence, head): in order, each piece's local state in the workspace is
+// replaced by the state that enters the piece, carry <- 2^decay carry + local. Reads and writes the
+// workspace once; one thread per four state elements.
+constexpr int JOIN_THREADS = 256;
+template <int P>
+__global__ void __launch_bounds__(JOIN_THREADS) kda_ssm_join_kernel(const TcParams t)
+{
+    const ssm::SsmParams &p = t.p;
+    constexpr int BLOCKS = P * NS / (4 * JOIN_THREADS);  // CTAs per (sequence, head)
+    const int unit = blockIdx.x / BLOCKS, h = unit % p.H, seq = unit / p.H;
+    const size_t e = 4 * (static_cast<size_t>(blockIdx.x % BLOCKS) * JOIN_THREADS + threadIdx.x);
+    const Span sp = ssm::ssm_span(p, seq);
+    if (!sp.ok) return;
+    long long base = static_cast<long long>(seq) * t.seg_per_seq;
+    if (p.cu) {
+        base = 0;
+        const int lane = threadIdx.x & 31;
+        for (int s0 = 0; s0 < seq; s0 += 32) {
+            int n = 0;
+            if (s0 + lane < seq) {
+                const Span o = ssm::ssm_span(p, s0 + lane);
+                n = o.ok ? pieces_of(o.len, t.seg_chunks) : 0;
+            }
+            base += __reduce_add_sync(0xffffffffu, n);
+        }
+    }
+    const int npieces = pieces_of(sp.len, t.seg_chunks);
+    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+    const size_t u = static_cast<size_t>(unit) * P * NS + e;
+    if (p.init) {
+        if (p.init_dtype == KDA_DTYPE_FP32) {
+            c = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.init) + u);
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.init) + u);
+            c = make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+        }
+    }
+    const float *dec = t.ws + static_cast<size_t>(t.slots) * p.H * P * NS;
+    for (int i = 0; i < npieces; ++i) {
+        const long long slot = base + i;
+        if (slot >= t.slots) return;  // overlapping bounds (flagged): more pieces than the call has room for
+        float4 *at = reinterpret_cast<float4 *>(t.ws + (static_cast<size_t>(slot) * p.H + h) * P * NS + e);
+        if (i + 1 == npieces) {
+            *at = c;
+            break;
+        }
+        const float4 l = *at;
+        const float g = ex2_approx(dec[static_cast<size_t>(slot) * p.H + h]);
+        *at = c;
+        c = make_float4(fmaf(g, c.x, l.x), fmaf(g, c.y, l.y), fmaf(g, c.z, l.z), fmaf(g, c.w, l.w));
+    }
+}
+
+}  // namespace ssmtc
+}  // namespace kda
