@@ -16,23 +16,29 @@
 // One CTA owns the state of one (sequence, head), or of one piece of its time axis, and walks its
 // chunks. The state lives in tensor memory, fp32, transposed (lane = state channel n, column = head
 // channel p), so that
-//   G   [128 x 128]  = C B^T                        A, B straight from the TMA tiles (K-major)
-//   Yx  [128 x P]    = C S0^T                       S0 rounded to bf16 in shared memory
-//   Yi  [128 x P]    = M X                          M bf16 in tensor memory, X straight from its tile
-//   S  += (w B)^T X                                 w B split into bf16 parts, X straight from its tile
-// Roundings: M and S0 to bf16 as operands (the output is bf16; the carried state itself is not
-// rounded); w B into PARTS bf16 parts, 3 where an fp32 state is returned (2^-25 of a term) and 2
-// where it is returned in bf16 or not at all (2^-17). Sums are fp32.
+//   G  [128 x 128] = C B^T               both straight from their TMA tiles (K-major)
+//   Y  [128 x P]   = C S0^T              S0 rounded to bf16 in shared memory; rows then scaled in place
+//   Y             += (M + diag(D)) X     scores bf16 in tensor memory, X straight from its tile
+//   S             += (w B)^T X           w B as bf16 parts in tensor memory, transposed on the way
+// Roundings: M + diag(D) and S0 to bf16 as operands (the output is bf16; the carried state itself is
+// not rounded); w B into PARTS bf16 parts of 8 bits each: 3, exact, where an fp32 state is returned,
+// 2 (2^-17 of a term) where it is returned in bf16 or not at all. Sums are fp32.
 //
-// Warp roles (512 threads):
-//   warp 0      TMA producer (lane 0): x and b tiles two deep, c one; tensor memory allocation
-//   warp 1      MMA issuer
-//   warp 2      step sizes, running sums and decays of a chunk, one chunk ahead
-//   warp 3      stores the output tile (written over the x tile) by TMA
-//   warps 4-7   scores G -> M, then the output rows (thread = token)
-//   warps 8-11  state: bf16 copy for Yx, decay in place (thread = state channel)
-//   warps 12-15 w B: 16 tokens at a time, first part over the b tile, the others into a ring
-// Tensor memory columns: G (M over it) [0, 128), Yi [128, 128 + P), Yx, S.
+// What bounds it: shared memory. Per chunk of P = 128 the MMAs read 256 KB of operands, TMA moves
+// 128 KB and the warps 96 KB, 480 KB at 128 bytes a cycle; that is why w B goes through tensor memory
+// (as a shared-memory operand it cost 160 KB more and the kernel ran at 148.7 us where it now takes
+// TIME_HERE, 8 x 4096 tokens of 16 heads).
+//
+// Warp roles (640 threads):
+//   warp 0       TMA producer (lane 0): x and b tiles two deep, c one; tensor memory allocation
+//   warp 1       MMA issuer
+//   warp 2       step sizes, running sums and decays of a chunk, one chunk ahead
+//   warp 3       stores the output tile (written over the x tile) by TMA
+//   warps 4-7    scores G -> M (thread = token)
+//   warps 8-11   row scaling of C S0^T, then the output rows (thread = token)
+//   warps 12-15  state: bf16 copy for the next product, decay in place (thread = state channel)
+//   warps 16-19  w B, 32 tokens at a time
+// Tensor memory columns: G (M over it) [0, 128), Y [128, 128 + P), S, then the w B buffers.
 #pragma once
 #include "kda_ssm_step.cuh"
 #include "tcgen05.cuh"
@@ -44,10 +50,10 @@ using ssm::MIN_LOG2_DECAY;
 using ssm::NS;
 
 constexpr int L = 128;          // tokens per chunk
-constexpr int SUB = 16;         // tokens per w B block (one MMA step)
-constexpr int NTHREADS = 512;
+constexpr int SUB = 32;         // tokens per w B block (two MMA steps)
+constexpr int NTHREADS = 640;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t T_G = 0, T_YI = 128;
+constexpr uint32_t T_G = 0, T_Y = 128;
 
 struct TcParams {
     ssm::SsmParams p;
@@ -65,18 +71,16 @@ template <int P, int PARTS, bool FULL>
 struct Layout {
     static constexpr int BOX = L * 128;            // 64 channels x 128 rows, 128-byte swizzle
     static constexpr int XT = P / 64 * BOX, BT = 2 * BOX;
-    static constexpr int SLOT = (PARTS - 1) * SUB * NS * 2;
-    static constexpr int NSLOT = FULL && P == 128 ? 3 : 4;
+    static constexpr int NSLOT = P == 128 ? 2 : 4;  // w B buffers of PARTS x 16 columns
     static constexpr int X = 0;                    // two stages
     static constexpr int B = X + 2 * XT;           // two stages
     static constexpr int C = B + 2 * BT;
     static constexpr int H = C + (FULL ? BT : 0);  // bf16 state, [n][p]
-    static constexpr int RING = H + (FULL ? XT : 0);
-    static constexpr int SC = RING + NSLOT * SLOT;
+    static constexpr int SC = H + (FULL ? XT : 0);
     static constexpr int BAR = SC + 2 * SC_BYTES;
     static constexpr int X_FULL = 0, X_EMPTY = 2, B_FULL = 4, B_EMPTY = 6, C_FULL = 8, C_EMPTY = 9, SC_FULL = 10, SC_EMPTY = 12,
-                         G_DONE = 14, M_DONE = 15, Y_DONE = 16, Y_FREE = 17, H_READY = 18, S_DONE = 19, OUT_FULL = 20,
-                         END = 21, W_FULL = 22, W_EMPTY = 26, NBARS = 30;
+                         G_DONE = 14, M_DONE = 15, YX_DONE = 16, SCALED = 17, Y_DONE = 18, Y_FREE = 19, H_READY = 20, S_DONE = 21,
+                         OUT_FULL = 22, END = 23, W_FULL = 24, W_EMPTY = 28, NBARS = 32;
     static constexpr int TMEMPTR = BAR + NBARS * 8;
     static constexpr int FLAGS = TMEMPTR + 16;
     static constexpr int ALLOC = FLAGS + 16 + 1024;
@@ -166,7 +170,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                       const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap to, const TcParams t)
 {
     using Lay = Layout<P, PARTS, FULL>;
-    constexpr uint32_t T_YX = T_YI + P, T_S = T_YI + 2 * P;
+    constexpr uint32_t T_S = T_Y + P, T_W = T_Y + 2 * P;
+    static_assert(T_W + Lay::NSLOT * PARTS * (SUB / 2) <= TMEM_COLS, "tensor memory budget");
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem);
@@ -203,20 +208,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(bar(Lay::X_FULL + i), 1);
             mbar_init(bar(Lay::X_EMPTY + i), 1);
             mbar_init(bar(Lay::B_FULL + i), 1);
-            mbar_init(bar(Lay::B_EMPTY + i), 1);
+            mbar_init(bar(Lay::B_EMPTY + i), FULL ? 5 : 4);  // the w B warps, and the score product
             mbar_init(bar(Lay::SC_FULL + i), 1);
-            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 12 : 8);
+            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 16 : 8);
         }
-        mbar_init(bar(Lay::C_FULL), 1);
-        mbar_init(bar(Lay::C_EMPTY), 1);
-        mbar_init(bar(Lay::G_DONE), 1);
-        mbar_init(bar(Lay::M_DONE), 4);
-        mbar_init(bar(Lay::Y_DONE), 1);
-        mbar_init(bar(Lay::Y_FREE), 4);
-        mbar_init(bar(Lay::H_READY), 4);
-        mbar_init(bar(Lay::S_DONE), 1);
-        mbar_init(bar(Lay::OUT_FULL), 4);
-        mbar_init(bar(Lay::END), 1);
+        for (int i : {Lay::C_FULL, Lay::C_EMPTY, Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::S_DONE, Lay::END}) mbar_init(bar(i), 1);
+        for (int i : {Lay::M_DONE, Lay::SCALED, Lay::Y_FREE, Lay::H_READY, Lay::OUT_FULL}) mbar_init(bar(i), 4);
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(Lay::W_FULL + i), 4);
             mbar_init(bar(Lay::W_EMPTY + i), 1);
@@ -277,10 +274,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (nch > 0) {
             constexpr uint32_t id_g = tc::idesc(tc::BF16, 128, 128, 0, 0);
             constexpr uint32_t id_y = tc::idesc(tc::BF16, 128, P, 0, 1);
-            constexpr uint32_t id_s = tc::idesc(tc::BF16, 128, P, 1, 1);
             const uint64_t dc = tc::sdesc(sb + Lay::C, 16, 1024, tc::SWZ_128B);
             const uint64_t dh = tc::sdesc(sb + Lay::H, Lay::BOX, 1024, tc::SWZ_128B);
             auto kstep = [](int i) { return static_cast<uint64_t>(((i >> 2) * Lay::BOX + (i & 3) * 32) >> 4); };
+            constexpr uint64_t rows16 = (16 * 128) >> 4;  // 16 rows of a 64-channel box
             auto issue_g = [&](int n) {
                 if (!wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::C_FULL, n & 1)) return false;
                 if (n > 0 && !wait_w(Lay::Y_DONE, (n - 1) & 1)) return false;  // M of the last chunk has been read
@@ -289,6 +286,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_G, dc + kstep(i), db + kstep(i), id_g, i > 0);
                 tc::commit_w(bar(Lay::G_DONE));
+                tc::commit_w(bar(Lay::B_EMPTY + (n & 1)));
                 return true;
             };
             int k = 0;  // w B blocks so far
@@ -297,44 +295,41 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int n = 0; ok && n < nch; ++n) {
                 const int nsub = (live_of(n) + SUB - 1) / SUB;
                 const uint64_t dx = tc::sdesc(xt(n), Lay::BOX, 1024, tc::SWZ_128B);
-                const uint64_t dhi = tc::sdesc(bt(n), Lay::BOX, 1024, tc::SWZ_128B);
                 ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::H_READY, n & 1);
+                if constexpr (FULL) {  // Y = C S0^T, over the accumulator whose last values have been read
+                    ok = ok && (n == 0 || wait_w(Lay::Y_FREE, (n - 1) & 1));
+                    if (!ok) break;
+                    tc::fence_after();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_Y, dc + kstep(i), dh + rows16 * i, id_y, i > 0);
+                    tc::commit_w(bar(Lay::YX_DONE));
+                    tc::commit_w(bar(Lay::C_EMPTY));
+                }
                 for (int s = 0; ok && s < nsub; ++s, ++k) {
                     const int sl = k % Lay::NSLOT;
                     ok = wait_w(Lay::W_FULL + sl, (k / Lay::NSLOT) & 1);
                     if (!ok) break;
                     tc::fence_after();
-                    const uint64_t step = static_cast<uint64_t>((SUB * 128 * s) >> 4);
-                    const uint64_t dr = tc::sdesc(sb + Lay::RING + sl * Lay::SLOT, SUB * 128, 1024, tc::SWZ_128B);
-                    tc::mma_ss_w(tmem + T_S, dhi + step, dx + step, id_s, 1);
+                    const uint32_t wb = tmem + T_W + sl * (PARTS * (SUB / 2));
 #pragma unroll
-                    for (int i = 0; i < PARTS - 1; ++i)
-                        tc::mma_ss_w(tmem + T_S, dr + ((i * SUB * NS * 2) >> 4), dx + step, id_s, 1);
+                    for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            tc::mma_ts_w(tmem + T_S, wb + i * (SUB / 2) + 8 * j, dx + rows16 * (2 * s + j), id_y, 1);
                     tc::commit_w(bar(Lay::W_EMPTY + sl));
                     if constexpr (FULL) {
-                        if (s == 0) {  // Yx = C S0^T, over the accumulator whose last values have been read
-                            ok = n == 0 || wait_w(Lay::Y_FREE, (n - 1) & 1);
+                        if (s == min(1, nsub - 1)) {  // Y += M X
+                            ok = wait_w(Lay::M_DONE, n & 1) && wait_w(Lay::SCALED, n & 1);
                             if (!ok) break;
                             tc::fence_after();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                tc::mma_ss_w(tmem + T_YX, dc + kstep(i), dh + ((i * 16 * 128) >> 4), id_y, i > 0);
-                            tc::commit_w(bar(Lay::C_EMPTY));
-                        }
-                        if (s == min(3, nsub - 1)) {  // Yi = M X
-                            ok = wait_w(Lay::M_DONE, n & 1);
-                            if (!ok) break;
-                            tc::fence_after();
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                tc::mma_ts_w(tmem + T_YI, tmem + T_G + 8 * i, dx + ((i * 16 * 128) >> 4), id_y, i > 0);
+                            for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_Y, tmem + T_G + 8 * i, dx + rows16 * i, id_y, 1);
                             tc::commit_w(bar(Lay::Y_DONE));
                         }
                     }
                 }
                 if (!ok) break;
                 tc::commit_w(bar(Lay::S_DONE));
-                tc::commit_w(bar(Lay::B_EMPTY + (n & 1)));
                 if constexpr (!FULL) tc::commit_w(bar(Lay::X_EMPTY + (n & 1)));
                 if constexpr (FULL)
                     if (n + 1 < nch) ok = issue_g(n + 1);
@@ -416,93 +411,119 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (lane == 0) bulk_wait_all();
         }
     } else if (warp < 8) {
-        // ---------------------------------------------------------------- scores and outputs
+        // ---------------------------------------------------------------- scores
         if constexpr (FULL) {
             const int q = warp & 3, row = 32 * q + lane;
-            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16);
+            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_G;
             const float Dh = p.D ? __ldg(p.D + h) : 0.f;
-            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P;
             for (int n = 0; n < nch; ++n) {
-                const int Lv = live_of(n);
                 if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::G_DONE, n & 1)) break;
                 tc::fence_after();
                 const uint32_t s = sc(n);
                 const float4 tot = SM_AT(const float4, s + SC_TOT);
                 const float loc = SM_AT(const float, s + SC_LOC + 4 * row);
-                const float tb[4] = {tot.x, tot.y, tot.z, tot.w};
+                // M is written over columns of G that have been read
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t m[16];
-                    if (b > q) {
+                for (int b = 0; b < q; ++b) {
+                    uint32_t g[32], m[16];
+                    tc::ld32(lb + 32 * b, g);
+                    // log2 decay from the end of block b to this row
+                    const float e = ex2_approx(loc + (b < 1 && q > 1 ? tot.y : 0.f) + (b < 2 && q > 2 ? tot.z : 0.f));
+                    tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) m[i] = 0u;
-                    } else {
-                        uint32_t g[32];
-                        tc::ld32(lb + T_G + 32 * b, g);
-                        if (b < q) {
-                            float e = loc;  // log2 decay from the end of block b to this row
-#pragma unroll
-                            for (int k = 1; k < 3; ++k)
-                                if (k > b && k < q) e += tb[k];
-                            e = ex2_approx(e);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 v = SM_AT(const float4, s + SC_ES + 128 * b + 4 * i);
-                                m[i / 2] = pack_bf16(__uint_as_float(g[i]) * (e * v.x), __uint_as_float(g[i + 1]) * (e * v.y));
-                                m[i / 2 + 1] = pack_bf16(__uint_as_float(g[i + 2]) * (e * v.z), __uint_as_float(g[i + 3]) * (e * v.w));
-                            }
-                        } else {
-                            tc::wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 v = SM_AT(const float4, s + SC_LOC + 128 * b + 4 * i);
-                                const float4 d = SM_AT(const float4, s + SC_DELTA + 128 * b + 4 * i);
-                                const float lv[4] = {v.x, v.y, v.z, v.w}, dv[4] = {d.x, d.y, d.z, d.w};
-                                float o[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    o[k] = i + k <= lane ? __uint_as_float(g[i + k]) * (dv[k] * ex2_approx(loc - lv[k])) : 0.f;
-                                m[i / 2] = pack_bf16(o[0], o[1]);
-                                m[i / 2 + 1] = pack_bf16(o[2], o[3]);
-                            }
-                        }
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 v = SM_AT(const float4, s + SC_ES + 128 * b + 4 * i);
+                        const float2 u0 = fmul2(make_float2(v.x, v.y), make_float2(e, e)), u1 = fmul2(make_float2(v.z, v.w), make_float2(e, e));
+                        const float2 o0 = fmul2(u0, make_float2(__uint_as_float(g[i]), __uint_as_float(g[i + 1])));
+                        const float2 o1 = fmul2(u1, make_float2(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3])));
+                        m[i / 2] = pack_bf16(o0.x, o0.y);
+                        m[i / 2 + 1] = pack_bf16(o1.x, o1.y);
                     }
-                    tc::st16(lb + T_G + 16 * b, m);  // over columns of G that have been read
+                    tc::st16(lb + 16 * b, m);
+                }
+                {
+                    uint32_t g[32], m[16];
+                    tc::ld32(lb + 32 * q, g);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 v = SM_AT(const float4, s + SC_LOC + 128 * q + 4 * i);
+                        const float4 d = SM_AT(const float4, s + SC_DELTA + 128 * q + 4 * i);
+                        const float lv[4] = {v.x, v.y, v.z, v.w}, dv[4] = {d.x, d.y, d.z, d.w};
+                        float o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float x = __uint_as_float(g[i + k]) * (dv[k] * ex2_approx(loc - lv[k]));
+                            o[k] = i + k < lane ? x : i + k == lane ? x + Dh : 0.f;
+                        }
+                        m[i / 2] = pack_bf16(o[0], o[1]);
+                        m[i / 2 + 1] = pack_bf16(o[2], o[3]);
+                    }
+                    tc::st16(lb + 16 * q, m);
+                }
+                if (q < 3) {
+                    uint32_t z[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] = 0u;
+#pragma unroll 1
+                    for (int b = q + 1; b < 4; ++b) tc::st16(lb + 16 * b, z);
                 }
                 tc::wait_st();
                 tc::fence_before();
                 arrive_w(Lay::M_DONE);
-                float e = loc;  // log2 decay from the chunk's start
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    if (k < q) e += tb[k];
-                e = ex2_approx(e);
                 arrive_w(Lay::SC_EMPTY + (n & 1));
-                // the x tile is the output's buffer once the state product has read it
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------- outputs
+        if constexpr (FULL) {
+            const int q = warp & 3, row = 32 * q + lane;
+            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y;
+            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P;
+            for (int n = 0; n < nch; ++n) {
+                const int Lv = live_of(n);
+                if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1)) break;
+                // decay from the chunk's start to this row
+                const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
+                const float e = ex2_approx(SM_AT(const float, sc(n) + SC_LOC + 4 * row) + (q > 0 ? tot.x : 0.f) + (q > 1 ? tot.y : 0.f) + (q > 2 ? tot.z : 0.f));
+                arrive_w(Lay::SC_EMPTY + (n & 1));
+                if (!wait_w(Lay::YX_DONE, n & 1)) break;
+                tc::fence_after();
+#pragma unroll 1
+                for (int g4 = 0; g4 < P / 32; ++g4) {
+                    uint32_t y[32];
+                    tc::ld32(lb + 32 * g4, y);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 v = fmul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), make_float2(e, e));
+                        y[i] = __float_as_uint(v.x);
+                        y[i + 1] = __float_as_uint(v.y);
+                    }
+                    tc::st32(lb + 32 * g4, y);
+                }
+                tc::wait_st();
+                tc::fence_before();
+                arrive_w(Lay::SCALED);
+                // the x tile is the output's buffer once the state product has read it (the last product
+                // of the chunk, so that Y is complete too)
                 if (!wait_w(Lay::S_DONE, n & 1)) break;
                 tc::fence_after();
                 const uint32_t xr = xt(n) + row * 128;
 #pragma unroll 1
                 for (int g4 = 0; g4 < P / 32; ++g4) {
-                    uint32_t yi[32], yx[32];
-                    tc::ld32(lb + T_YI + 32 * g4, yi);
-                    tc::ld32(lb + T_YX + 32 * g4, yx);
+                    uint32_t y[32];
+                    tc::ld32(lb + 32 * g4, y);
                     tc::wait_ld();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // eight channels: 16 bytes, swizzled by the row
                         const int c8 = 4 * g4 + i;
-                        const uint32_t at = xr + (c8 >> 3) * Lay::BOX + (((c8 & 7) ^ (row & 7)) << 4);
-                        float x[8], y[8];
-                        blk::unpack8(SM_AT(const uint4, at), x);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            y[k] = fmaf(e, __uint_as_float(yx[8 * i + k]), __uint_as_float(yi[8 * i + k]));
-                            if (p.D) y[k] = fmaf(Dh, x[k], y[k]);
-                        }
-                        const uint4 o = blk::pack8(y);
+                        const uint4 o = make_uint4(pack_bf16(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
+                                                   pack_bf16(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
+                                                   pack_bf16(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
+                                                   pack_bf16(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
                         if (Lv == L)
-                            SM_AT(uint4, at) = o;
+                            SM_AT(uint4, xr + (c8 >> 3) * Lay::BOX + (((c8 & 7) ^ (row & 7)) << 4)) = o;
                         else if (row < Lv)  // a ragged end is stored from registers
                             *reinterpret_cast<uint4 *>(op + static_cast<long long>(n) * L * p.os + 8 * c8) = o;
                     }
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 arrive_w(Lay::OUT_FULL);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ---------------------------------------------------------------- state
         const int q = warp & 3, nn = 32 * q + lane;
         const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_S;
@@ -606,13 +627,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc::fence_before();
     } else {
         // ---------------------------------------------------------------- w B
-        const int u = threadIdx.x - 384;  // 0..127
+        // Warp q owns state channels 32 q .. 32 q + 31. ldmatrix.trans hands a lane two tokens of one
+        // channel, the layout in which the 16-lane tensor-memory stores take them, so the transposition is free.
+        const int q = warp & 3, u = threadIdx.x - 512;
+        const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_W;
+        // matrix lane >> 3 of an ldmatrix: tokens 8 (lane >> 4) .., channels 8 ((lane >> 3) & 1) ..
+        const int jr = 8 * (lane >> 4) + (lane & 7);
         int k = 0;
         bool ok = true;
         for (int n = 0; ok && n < nch; ++n) {
             const int Lv = live_of(n), nsub = (Lv + SUB - 1) / SUB;
             ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1);
-            if (ok && FULL) ok = wait_w(Lay::G_DONE, n & 1);  // the b tile has been read as it came
             if (ok && Lv < L) {
                 // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
                 ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1);
@@ -621,37 +646,59 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         const int r = Lv + i / (P / 8), c8 = i % (P / 8);
                         SM_AT(uint4, xt(n) + (c8 >> 3) * Lay::BOX + r * 128 + (c8 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
+                tc::fence_async_smem();
             }
             for (int s = 0; ok && s < nsub; ++s, ++k) {
-                const int sl = k % Lay::NSLOT;
+                const int sl = k % Lay::NSLOT, j0 = SUB * s;
+                float2 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = SM_AT(const float2, sc(n) + SC_W + 4 * (j0 + 8 * i + 2 * (lane & 3)));
                 ok = wait_w(Lay::W_EMPTY + sl, ((k / Lay::NSLOT) & 1) ^ 1);
                 if (!ok) break;
-                const uint32_t ring = sb + Lay::RING + sl * Lay::SLOT;
+                tc::fence_after();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int id = u + 128 * i, r = id >> 4, box = (id >> 3) & 1;
-                    const uint32_t off = r * 128 + (((id & 7) ^ (r & 7)) << 4);
-                    const uint32_t at = bt(n) + box * Lay::BOX + SUB * s * 128 + off;
-                    const float w = SM_AT(const float, sc(n) + SC_W + 4 * (SUB * s + r));
-                    const bool live = SUB * s + r < Lv;
-                    float v[8];
-                    blk::unpack8(SM_AT(const uint4, at), v);
+                for (int hh = 0; hh < 2; ++hh) {  // sixteen channels
+                    const int c8 = 4 * q + 2 * hh + ((lane >> 3) & 1);  // eight-channel group of this lane's address
+                    uint32_t v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = live ? w * v[j] : 0.f;
+                    for (int i = 0; i < 2; ++i) {  // tokens j0 + 16 i ..
+                        const int j = j0 + 16 * i + jr;
+                        ldsm_x4_t(bt(n) + (c8 >> 3) * Lay::BOX + j * 128 + (((c8 & 7) ^ (j & 7)) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                    if (Lv < L) {  // past the end b may be anything
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = j0 + 8 * (i >> 1) + 2 * (lane & 3);
+                            v[i] &= j + 1 < Lv ? 0xffffffffu : j < Lv ? 0xffffu : 0u;
+                        }
+                    }
+                    float2 f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = fmul2(make_float2(bf16_lo(v[i]), bf16_hi(v[i])), w[i >> 1]);
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
-                        const uint4 o = blk::pack8(v);
-                        float f[8];
-                        blk::unpack8(o, f);
+                        uint32_t o[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] -= f[j];
-                        SM_AT(uint4, part == 0 ? at : ring + (part - 1) * SUB * NS * 2 + box * SUB * 128 + off) = o;
+                        for (int i = 0; i < 8; ++i) {
+                            if (part + 1 < PARTS) {  // the upper eight bits; what is left is exact
+                                const uint32_t a = __float_as_uint(f[i].x), b = __float_as_uint(f[i].y);
+                                o[i] = __byte_perm(a, b, 0x7632);
+                                f[i] = fsub2(f[i], make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)));
+                            } else {
+                                o[i] = pack_bf16(f[i].x, f[i].y);
+                            }
+                        }
+                        tc::st_16x128b_x4(lb + (static_cast<uint32_t>(16 * hh) << 16) + (sl * PARTS + part) * (SUB / 2), o);
                     }
                 }
-                tc::fence_async_smem();
+                tc::wait_st();
+                tc::fence_before();
                 arrive_w(Lay::W_FULL + sl);
             }
-            if (ok) arrive_w(Lay::SC_EMPTY + (n & 1));
+            if (ok) {
+                arrive_w(Lay::B_EMPTY + (n & 1));
+                arrive_w(Lay::SC_EMPTY + (n & 1));
+            }
         }
     }
 

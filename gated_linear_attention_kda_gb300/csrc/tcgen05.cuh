@@ -165,6 +165,15 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8])
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+// 16 lanes (the half of this warp's quarter that the address names) x 16 consecutive 32-bit columns, in
+// the fragment layout of ldmatrix: register 2 r + k of lane l holds row l / 4 + 8 k, column 4 r + l % 4
+__device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8])
+{
+    tmem_check(taddr, 16);
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
