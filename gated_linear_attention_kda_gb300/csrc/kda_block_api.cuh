@@ -149,15 +149,15 @@ static kda_status launch_ssm_steps(const ssm::SsmParams &p, cudaStream_t s)
 }
 
 // [tokens, groups, width] bf16 tensor with `stride` elements between tokens, boxes of 64 channels x 1
-// group x 128 tokens, 128-byte swizzle.
-static bool rows_map(CUtensorMap *m, const void *base, int64_t tokens, int64_t groups, int64_t width, int64_t stride)
+// group x `box_rows` tokens, 128-byte swizzle.
+static bool rows_map(CUtensorMap *m, const void *base, int64_t tokens, int64_t groups, int64_t width, int64_t stride, int box_rows = ssmtc::L)
 {
     std::memset(m, 0, sizeof *m);
     auto enc = get_encode();
     if (!enc) return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(groups), static_cast<cuuint64_t>(tokens)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(width * 2), static_cast<cuuint64_t>(stride * 2)};
-    cuuint32_t box[3] = {64, 1, ssmtc::L};
+    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -220,7 +220,7 @@ static kda_status launch_ssm(const ssm::SsmParams &p, const SsmPlan &plan, float
 {
     CUtensorMap mx, mb, mc, mo;
     if (!rows_map(&mx, p.x, p.total, p.H, P, p.xs) || !rows_map(&mb, p.b, p.total, p.G, ssm::NS, p.bs) ||
-        !rows_map(&mc, p.c, p.total, p.G, ssm::NS, p.cs) || !rows_map(&mo, p.out, p.total, p.H, P, p.os))
+        !rows_map(&mc, p.c, p.total, p.G, ssm::NS, p.cs) || !rows_map(&mo, p.out, p.total, p.H, P, p.os, 32))
         return fail(KDA_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad geometry)");
     ssmtc::TcParams t = {};
     t.p = p;

@@ -29,15 +29,17 @@
 // (as a shared-memory operand it cost 160 KB more and the kernel ran at 148.7 us where it now takes
 // TIME_HERE, 8 x 4096 tokens of 16 heads).
 //
-// Warp roles (640 threads):
+// Warp roles (1024 threads; the column work of a tensor-memory row is shared by two warps):
 //   warp 0       TMA producer (lane 0): x and b tiles two deep, c one; tensor memory allocation
-//   warp 1       MMA issuer
+//   warp 1       MMA issuer: scores and outputs
 //   warp 2       step sizes, running sums and decays of a chunk, one chunk ahead
-//   warp 3       stores the output tile (written over the x tile) by TMA
+//   warp 3       MMA issuer: state
 //   warps 4-7    scores G -> M (thread = token)
-//   warps 8-11   row scaling of C S0^T, then the output rows (thread = token)
-//   warps 12-15  state: bf16 copy for the next product, decay in place (thread = state channel)
-//   warps 16-19  w B, 32 tokens at a time
+//   warps 8-15   row scaling of C S0^T, then the output rows (thread = token and half of the columns)
+//   warps 16-23  state: bf16 copy for the next product, decay in place (state channel, half of the columns)
+//   warps 24-31  w B, 32 tokens at a time (16 state channels per warp)
+// MMA order per chunk: C S0^T, the state product, M X, and the next chunk's C B^T, so that the tensor
+// core works on the last two while the state warps prepare what the first two of the next chunk need.
 // Tensor memory columns: G (M over it) [0, 128), Y [128, 128 + P), S, then the w B buffers.
 #pragma once
 #include "kda_ssm_step.cuh"
@@ -51,7 +53,7 @@ using ssm::NS;
 
 constexpr int L = 128;          // tokens per chunk
 constexpr int SUB = 32;         // tokens per w B block (two MMA steps)
-constexpr int NTHREADS = 640;
+constexpr int NTHREADS = 1024;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t T_G = 0, T_Y = 128;
 
@@ -71,7 +73,7 @@ template <int P, int PARTS, bool FULL>
 struct Layout {
     static constexpr int BOX = L * 128;            // 64 channels x 128 rows, 128-byte swizzle
     static constexpr int XT = P / 64 * BOX, BT = 2 * BOX;
-    static constexpr int NSLOT = P == 128 ? 2 : 4;  // w B buffers of PARTS x 16 columns
+    static constexpr int NSLOT = P == 128 && PARTS == 3 ? 2 : 4;  // w B buffers of PARTS x 16 columns
     static constexpr int X = 0;                    // two stages
     static constexpr int B = X + 2 * XT;           // two stages
     static constexpr int C = B + 2 * BT;
@@ -80,7 +82,7 @@ struct Layout {
     static constexpr int BAR = SC + 2 * SC_BYTES;
     static constexpr int X_FULL = 0, X_EMPTY = 2, B_FULL = 4, B_EMPTY = 6, C_FULL = 8, C_EMPTY = 9, SC_FULL = 10, SC_EMPTY = 12,
                          G_DONE = 14, M_DONE = 15, YX_DONE = 16, SCALED = 17, Y_DONE = 18, Y_FREE = 19, H_READY = 20, S_DONE = 21,
-                         OUT_FULL = 22, END = 23, W_FULL = 24, W_EMPTY = 28, NBARS = 32;
+                         END = 23, W_FULL = 24, W_EMPTY = 28, X_ZERO = 32, END2 = 33, X_READ = 34, NBARS = 36;
     static constexpr int TMEMPTR = BAR + NBARS * 8;
     static constexpr int FLAGS = TMEMPTR + 16;
     static constexpr int ALLOC = FLAGS + 16 + 1024;
@@ -206,16 +208,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (threadIdx.x == 32) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(Lay::X_FULL + i), 1);
-            mbar_init(bar(Lay::X_EMPTY + i), 1);
+            mbar_init(bar(Lay::X_EMPTY + i), FULL ? 8 : 1);
+            mbar_init(bar(Lay::X_READ + i), 1);
             mbar_init(bar(Lay::B_FULL + i), 1);
-            mbar_init(bar(Lay::B_EMPTY + i), FULL ? 5 : 4);  // the w B warps, and the score product
+            mbar_init(bar(Lay::B_EMPTY + i), FULL ? 9 : 8);  // the w B warps, and the score product
             mbar_init(bar(Lay::SC_FULL + i), 1);
-            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 16 : 8);
+            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 28 : 16);
         }
-        for (int i : {Lay::C_FULL, Lay::C_EMPTY, Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::S_DONE, Lay::END}) mbar_init(bar(i), 1);
-        for (int i : {Lay::M_DONE, Lay::SCALED, Lay::Y_FREE, Lay::H_READY, Lay::OUT_FULL}) mbar_init(bar(i), 4);
+        for (int i : {Lay::C_FULL, Lay::C_EMPTY, Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::S_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
+        mbar_init(bar(Lay::M_DONE), 4);
+        for (int i : {Lay::SCALED, Lay::Y_FREE, Lay::H_READY, Lay::X_ZERO}) mbar_init(bar(i), 8);
         for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(Lay::W_FULL + i), 4);
+            mbar_init(bar(Lay::W_FULL + i), 8);
             mbar_init(bar(Lay::W_EMPTY + i), 1);
         }
         flags[0] = 0;
@@ -224,7 +228,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR);
+    // The allocation is the whole tensor memory, so it starts at address 0: as a constant, it leaves the
+    // MMA operands constants too.
+    constexpr uint32_t tmem = 0;
+    if (*reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR) != tmem && threadIdx.x == 0) {
+        atomicOr(&g_dev_error, DEVERR_TIMEOUT);
+        flags[0] = 1;
+    }
     // the whole warp goes on only when every lane saw the phase
     auto wait_w = [&](int b, uint32_t par) {
         const bool ok = __all_sync(0xffffffffu, wait_bar(bar(b), par, flags));
@@ -270,69 +280,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (ncc > 0) drain_bar(bar(Lay::C_FULL), (ncc - 1) & 1);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA issuer (whole warp)
-        if (nch > 0) {
+        // ---------------------------------------------------------------- MMA issuer: scores and outputs (whole warp)
+        if (FULL && nch > 0) {
             constexpr uint32_t id_g = tc::idesc(tc::BF16, 128, 128, 0, 0);
             constexpr uint32_t id_y = tc::idesc(tc::BF16, 128, P, 0, 1);
-            const uint64_t dc = tc::sdesc(sb + Lay::C, 16, 1024, tc::SWZ_128B);
-            const uint64_t dh = tc::sdesc(sb + Lay::H, Lay::BOX, 1024, tc::SWZ_128B);
-            auto kstep = [](int i) { return static_cast<uint64_t>(((i >> 2) * Lay::BOX + (i & 3) * 32) >> 4); };
-            constexpr uint64_t rows16 = (16 * 128) >> 4;  // 16 rows of a 64-channel box
+            constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B);
+            const uint32_t dc = tc::sdesc_lo(sb + Lay::C, 16), dh = tc::sdesc_lo(sb + Lay::H, Lay::BOX);
+            auto kmaj = [&](uint32_t lo, int i) {  // K step i of a K-major tile (two boxes of 64 channels)
+                return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(((i >> 2) * Lay::BOX + (i & 3) * 32) >> 4));
+            };
+            auto nmaj = [&](uint32_t lo, int i) {  // K step i (16 rows) of an MN-major tile
+                return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(i * ((16 * 128) >> 4)));
+            };
             auto issue_g = [&](int n) {
                 if (!wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::C_FULL, n & 1)) return false;
                 if (n > 0 && !wait_w(Lay::Y_DONE, (n - 1) & 1)) return false;  // M of the last chunk has been read
                 tc::fence_after();
-                const uint64_t db = tc::sdesc(bt(n), 16, 1024, tc::SWZ_128B);
+                const uint32_t db = tc::sdesc_lo(bt(n), 16);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_G, dc + kstep(i), db + kstep(i), id_g, i > 0);
+                for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_G, kmaj(dc, i), kmaj(db, i), id_g, i > 0);
                 tc::commit_w(bar(Lay::G_DONE));
                 tc::commit_w(bar(Lay::B_EMPTY + (n & 1)));
                 return true;
             };
-            int k = 0;  // w B blocks so far
-            bool ok = true;
-            if constexpr (FULL) ok = issue_g(0);
+            bool ok = issue_g(0);
             for (int n = 0; ok && n < nch; ++n) {
-                const int nsub = (live_of(n) + SUB - 1) / SUB;
-                const uint64_t dx = tc::sdesc(xt(n), Lay::BOX, 1024, tc::SWZ_128B);
-                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::H_READY, n & 1);
-                if constexpr (FULL) {  // Y = C S0^T, over the accumulator whose last values have been read
-                    ok = ok && (n == 0 || wait_w(Lay::Y_FREE, (n - 1) & 1));
-                    if (!ok) break;
-                    tc::fence_after();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_Y, dc + kstep(i), dh + rows16 * i, id_y, i > 0);
-                    tc::commit_w(bar(Lay::YX_DONE));
-                    tc::commit_w(bar(Lay::C_EMPTY));
-                }
-                for (int s = 0; ok && s < nsub; ++s, ++k) {
-                    const int sl = k % Lay::NSLOT;
-                    ok = wait_w(Lay::W_FULL + sl, (k / Lay::NSLOT) & 1);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const uint32_t wb = tmem + T_W + sl * (PARTS * (SUB / 2));
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            tc::mma_ts_w(tmem + T_S, wb + i * (SUB / 2) + 8 * j, dx + rows16 * (2 * s + j), id_y, 1);
-                    tc::commit_w(bar(Lay::W_EMPTY + sl));
-                    if constexpr (FULL) {
-                        if (s == min(1, nsub - 1)) {  // Y += M X
-                            ok = wait_w(Lay::M_DONE, n & 1) && wait_w(Lay::SCALED, n & 1);
-                            if (!ok) break;
-                            tc::fence_after();
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_Y, tmem + T_G + 8 * i, dx + rows16 * i, id_y, 1);
-                            tc::commit_w(bar(Lay::Y_DONE));
-                        }
-                    }
-                }
+                const uint32_t dx = tc::sdesc_lo(xt(n), Lay::BOX);
+                // Y = C S0^T, over the accumulator whose last values have been read
+                ok = wait_w(Lay::H_READY, n & 1) && (n == 0 || wait_w(Lay::Y_FREE, (n - 1) & 1));
                 if (!ok) break;
-                tc::commit_w(bar(Lay::S_DONE));
-                if constexpr (!FULL) tc::commit_w(bar(Lay::X_EMPTY + (n & 1)));
-                if constexpr (FULL)
-                    if (n + 1 < nch) ok = issue_g(n + 1);
+                tc::fence_after();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_Y, kmaj(dc, i), nmaj(dh, i), id_y, i > 0);
+                tc::commit_w(bar(Lay::YX_DONE));
+                tc::commit_w(bar(Lay::C_EMPTY));
+                // Y += M X
+                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1) && (live_of(n) == L || wait_w(Lay::X_ZERO, 0)) &&
+                     wait_w(Lay::M_DONE, n & 1) && wait_w(Lay::SCALED, n & 1);
+                if (!ok) break;
+                tc::fence_after();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_Y, tmem + T_G + 8 * i, nmaj(dx, i), id_y, 1);
+                tc::commit_w(bar(Lay::Y_DONE));
+                if (n + 1 < nch) ok = issue_g(n + 1);
             }
             tc::commit_w(bar(Lay::END));
             if (lane == 0) drain_bar(bar(Lay::END), 0);
@@ -393,22 +383,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!FULL && lane == 0)
             t.ws[static_cast<size_t>(t.slots) * p.H * P * NS + static_cast<size_t>(slot) * p.H + h] = seg;
     } else if (warp == 3) {
-        // ---------------------------------------------------------------- output stores
-        if constexpr (FULL) {
-            for (int n = 0; n < nch; ++n) {
-                if (!wait_w(Lay::OUT_FULL, n & 1)) break;
-                if (lane == 0) {
-                    if (live_of(n) == L) {
+        // ---------------------------------------------------------------- MMA issuer: state
+        if (nch > 0) {
+            constexpr uint32_t id_s = tc::idesc(tc::BF16, 128, P, 0, 1), HI = tc::sdesc_hi(1024, tc::SWZ_128B);
+            int k = 0;  // w B blocks so far
+            bool ok = true;
+            for (int n = 0; ok && n < nch; ++n) {
+                const int nsub = (live_of(n) + SUB - 1) / SUB;
+                uint32_t dx = tc::sdesc_lo(xt(n), Lay::BOX);
+                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::H_READY, n & 1);
+                for (int s = 0; ok && s < nsub; ++s, ++k, dx += (SUB * 128) >> 4) {
+                    const int sl = k % Lay::NSLOT;
+                    ok = wait_w(Lay::W_FULL + sl, (k / Lay::NSLOT) & 1);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t wb = tmem + T_W + sl * (PARTS * (SUB / 2));
 #pragma unroll
-                        for (int k = 0; k < P / 64; ++k) tma_store_3d(&to, xt(n) + k * Lay::BOX, 64 * k, h, pc.bos + n * L);
-                        bulk_commit();
-                        bulk_wait_read();
-                    }
-                    mbar_arrive(bar(Lay::X_EMPTY + (n & 1)));
+                    for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            tc::mma_ts_w(tmem + T_S, wb + i * (SUB / 2) + 8 * j, tc::sdesc_of<HI>(dx + ((j * 16 * 128) >> 4)), id_s, 1);
+                    tc::commit_w(bar(Lay::W_EMPTY + sl));
                 }
-                __syncwarp();
+                if (!ok) break;
+                tc::commit_w(bar(Lay::S_DONE));
+                tc::commit_w(bar((FULL ? Lay::X_READ : Lay::X_EMPTY) + (n & 1)));
             }
-            if (lane == 0) bulk_wait_all();
+            tc::commit_w(bar(Lay::END2));
+            if (lane == 0) drain_bar(bar(Lay::END2), 0);
+            __syncwarp();
         }
     } else if (warp < 8) {
         // ---------------------------------------------------------------- scores
@@ -422,44 +425,46 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const uint32_t s = sc(n);
                 const float4 tot = SM_AT(const float4, s + SC_TOT);
                 const float loc = SM_AT(const float, s + SC_LOC + 4 * row);
-                // M is written over columns of G that have been read
+                // M is written over columns of G that have been read, 16 columns at a time
 #pragma unroll 1
-                for (int b = 0; b < q; ++b) {
-                    uint32_t g[32], m[16];
-                    tc::ld32(lb + 32 * b, g);
-                    // log2 decay from the end of block b to this row
-                    const float e = ex2_approx(loc + (b < 1 && q > 1 ? tot.y : 0.f) + (b < 2 && q > 2 ? tot.z : 0.f));
+                for (int b = 0; b < 2 * q; ++b) {
+                    uint32_t g[16], m[8];
+                    tc::ld16(lb + 16 * b, g);
+                    // log2 decay from the end of the block to this row
+                    const float e = ex2_approx(loc + (b < 2 && q > 1 ? tot.y : 0.f) + (b < 4 && q > 2 ? tot.z : 0.f));
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 v = SM_AT(const float4, s + SC_ES + 128 * b + 4 * i);
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 v = SM_AT(const float4, s + SC_ES + 64 * b + 4 * i);
                         const float2 u0 = fmul2(make_float2(v.x, v.y), make_float2(e, e)), u1 = fmul2(make_float2(v.z, v.w), make_float2(e, e));
                         const float2 o0 = fmul2(u0, make_float2(__uint_as_float(g[i]), __uint_as_float(g[i + 1])));
                         const float2 o1 = fmul2(u1, make_float2(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3])));
                         m[i / 2] = pack_bf16(o0.x, o0.y);
                         m[i / 2 + 1] = pack_bf16(o1.x, o1.y);
                     }
-                    tc::st16(lb + 16 * b, m);
+                    tc::st8(lb + 8 * b, m);
                 }
-                {
-                    uint32_t g[32], m[16];
-                    tc::ld32(lb + 32 * q, g);
+#pragma unroll 1
+                for (int b = 2 * q; b < 2 * q + 2; ++b) {
+                    uint32_t g[16], m[8];
+                    tc::ld16(lb + 16 * b, g);
+                    const int col = lane - 16 * (b & 1);  // this row's own column in the piece
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 v = SM_AT(const float4, s + SC_LOC + 128 * q + 4 * i);
-                        const float4 d = SM_AT(const float4, s + SC_DELTA + 128 * q + 4 * i);
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 v = SM_AT(const float4, s + SC_LOC + 64 * b + 4 * i);
+                        const float4 d = SM_AT(const float4, s + SC_DELTA + 64 * b + 4 * i);
                         const float lv[4] = {v.x, v.y, v.z, v.w}, dv[4] = {d.x, d.y, d.z, d.w};
                         float o[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float x = __uint_as_float(g[i + k]) * (dv[k] * ex2_approx(loc - lv[k]));
-                            o[k] = i + k < lane ? x : i + k == lane ? x + Dh : 0.f;
+                            o[k] = (i + k <= col ? x : 0.f) + (i + k == col ? Dh : 0.f);
                         }
                         m[i / 2] = pack_bf16(o[0], o[1]);
                         m[i / 2 + 1] = pack_bf16(o[2], o[3]);
                     }
-                    tc::st16(lb + 16 * q, m);
+                    tc::st8(lb + 8 * b, m);
                 }
                 if (q < 3) {
                     uint32_t z[16];
@@ -474,14 +479,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 arrive_w(Lay::SC_EMPTY + (n & 1));
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ---------------------------------------------------------------- outputs
         if constexpr (FULL) {
-            const int q = warp & 3, row = 32 * q + lane;
-            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y;
-            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P;
+            const int q = warp & 3, row = 32 * q + lane, c0 = (warp < 12 ? 0 : P / 2);  // this thread's columns
+            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y + c0;
+            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P + c0;
             for (int n = 0; n < nch; ++n) {
-                const int Lv = live_of(n);
                 if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1)) break;
                 // decay from the chunk's start to this row
                 const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 if (!wait_w(Lay::YX_DONE, n & 1)) break;
                 tc::fence_after();
 #pragma unroll 1
-                for (int g4 = 0; g4 < P / 32; ++g4) {
+                for (int g4 = 0; g4 < P / 64; ++g4) {
                     uint32_t y[32];
                     tc::ld32(lb + 32 * g4, y);
                     tc::wait_ld();
@@ -505,47 +509,58 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::wait_st();
                 tc::fence_before();
                 arrive_w(Lay::SCALED);
-                // the x tile is the output's buffer once the state product has read it (the last product
-                // of the chunk, so that Y is complete too)
-                if (!wait_w(Lay::S_DONE, n & 1)) break;
+                if (!wait_w(Lay::Y_DONE, n & 1)) break;
                 tc::fence_after();
-                const uint32_t xr = xt(n) + row * 128;
-#pragma unroll 1
-                for (int g4 = 0; g4 < P / 32; ++g4) {
-                    uint32_t y[32];
-                    tc::ld32(lb + 32 * g4, y);
+                uint32_t o[P / 4];
+#pragma unroll
+                for (int g = 0; g < P / 32; ++g) {
+                    uint32_t y[16];
+                    tc::ld16(lb + 16 * g, y);
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // eight channels: 16 bytes, swizzled by the row
-                        const int c8 = 4 * g4 + i;
-                        const uint4 o = make_uint4(pack_bf16(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
-                                                   pack_bf16(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
-                                                   pack_bf16(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
-                                                   pack_bf16(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
-                        if (Lv == L)
-                            SM_AT(uint4, xr + (c8 >> 3) * Lay::BOX + (((c8 & 7) ^ (row & 7)) << 4)) = o;
-                        else if (row < Lv)  // a ragged end is stored from registers
-                            *reinterpret_cast<uint4 *>(op + static_cast<long long>(n) * L * p.os + 8 * c8) = o;
-                    }
+                    for (int i = 0; i < 8; ++i) o[8 * g + i] = pack_bf16(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
                 }
                 tc::fence_before();
-                tc::fence_async_smem();
                 arrive_w(Lay::Y_FREE);
-                arrive_w(Lay::OUT_FULL);
+                const int Lv = live_of(n);
+                if (Lv == L) {
+                    // the x tile is the output's buffer once the state product has read it too
+                    if (!wait_w(Lay::X_READ + (n & 1), (n >> 1) & 1)) break;
+                    const uint32_t xr = xt(n) + row * 128;
+#pragma unroll
+                    for (int i = 0; i < P / 16; ++i) {  // eight channels: 16 bytes, swizzled by the row
+                        const int c8 = (c0 >> 3) + i;
+                        SM_AT(uint4, xr + (c8 >> 3) * Lay::BOX + (((c8 & 7) ^ (row & 7)) << 4)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                    tc::fence_async_smem();
+                    // a warp stores its 32 tokens; of 64 channels, where a box holds both halves, for both
+                    if (P == 64) named_bar_sync(1 + q, 64);
+                    if (lane == 0 && (P == 128 || warp < 12)) {
+                        tma_store_3d(&to, xt(n) + (c0 >> 6) * Lay::BOX + 32 * q * 128, c0, h, pc.bos + n * L + 32 * q);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                } else if (row < Lv) {  // a ragged end is stored from registers
+                    uint4 *dst = reinterpret_cast<uint4 *>(op + static_cast<long long>(n) * L * p.os);
+#pragma unroll
+                    for (int i = 0; i < P / 16; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+                arrive_w(Lay::X_EMPTY + (n & 1));
             }
+            if (lane == 0) bulk_wait_all();
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
         // ---------------------------------------------------------------- state
-        const int q = warp & 3, nn = 32 * q + lane;
-        const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_S;
+        const int q = warp & 3, nn = 32 * q + lane, c0 = (warp < 20 ? 0 : P / 2);  // this thread's channel and columns
+        const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_S + c0;
         const size_t unit = static_cast<size_t>(pc.seq) * p.H + h;
         const size_t st_elems = static_cast<size_t>(p.nseq) * p.H * P * NS;
         float *wsp = t.seg_chunks ? t.ws + (static_cast<size_t>(slot) * p.H + h) * P * NS + nn : nullptr;
-        // 32 columns (head channels 32 g4 ..) of the state this piece starts from
+        // 32 columns (head channels c0 + 32 g4 ..) of the state this piece starts from
         auto load_init = [&](int g4, uint32_t(&r)[32]) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const size_t at = static_cast<size_t>(32 * g4 + i) * NS;
+                const size_t at = static_cast<size_t>(c0 + 32 * g4 + i) * NS;
                 r[i] = 0u;
                 if constexpr (!FULL) continue;
                 if (t.seg_chunks) {
@@ -560,14 +575,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
             ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1);
-            if (ok && n > 0) ok = wait_w(Lay::S_DONE, (n - 1) & 1);
+            if (ok && n > 0) ok = wait_w(Lay::S_DONE, (n - 1) & 1) && (!FULL || wait_w(Lay::YX_DONE, (n - 1) & 1));  // the bf16 copy has been read
             if (!ok) break;
             tc::fence_after();
             const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
             const float gam = ex2_approx((tot.x + tot.y) + (tot.z + tot.w));
             arrive_w(Lay::SC_EMPTY + (n & 1));
 #pragma unroll 1
-            for (int g4 = 0; g4 < P / 32; ++g4) {
+            for (int g4 = 0; g4 < P / 64; ++g4) {
                 uint32_t r[32];
                 if (n == 0) {
                     load_init(g4, r);
@@ -578,7 +593,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 if constexpr (FULL) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int c8 = 4 * g4 + i;
+                        const int c8 = (c0 >> 3) + 4 * g4 + i;
                         const uint32_t at = sb + Lay::H + (c8 >> 3) * Lay::BOX + nn * 128 + (((c8 & 7) ^ (nn & 7)) << 4);
                         SM_AT(uint4, at) = make_uint4(pack_bf16(__uint_as_float(r[8 * i]), __uint_as_float(r[8 * i + 1])),
                                                       pack_bf16(__uint_as_float(r[8 * i + 2]), __uint_as_float(r[8 * i + 3])),
@@ -602,7 +617,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::fence_after();
             }
 #pragma unroll 1
-            for (int g4 = 0; ok && g4 < P / 32; ++g4) {
+            for (int g4 = 0; ok && g4 < P / 64; ++g4) {
                 uint32_t r[32];
                 if (nch > 0) {
                     tc::ld32(lb + 32 * g4, r);
@@ -612,7 +627,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const size_t at = static_cast<size_t>(32 * g4 + i) * NS;
+                    const size_t at = static_cast<size_t>(c0 + 32 * g4 + i) * NS;
                     if constexpr (!FULL)
                         wsp[at] = __uint_as_float(r[i]);
                     else if (!gmem_ok(unit * P * NS + at + nn, 1, st_elems))
@@ -627,10 +642,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc::fence_before();
     } else {
         // ---------------------------------------------------------------- w B
-        // Warp q owns state channels 32 q .. 32 q + 31. ldmatrix.trans hands a lane two tokens of one
+        // A warp owns 16 state channels. ldmatrix.trans hands a lane two tokens of one
         // channel, the layout in which the 16-lane tensor-memory stores take them, so the transposition is free.
-        const int q = warp & 3, u = threadIdx.x - 512;
-        const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_W;
+        const int u = threadIdx.x - 768, ch16 = 2 * (warp & 3) + (warp < 28 ? 0 : 1);
+        const uint32_t lb = tmem + (static_cast<uint32_t>(16 * ch16) << 16) + T_W;
+        const int c8 = 2 * ch16 + ((lane >> 3) & 1);  // eight-channel group of this lane's address
         // matrix lane >> 3 of an ldmatrix: tokens 8 (lane >> 4) .., channels 8 ((lane >> 3) & 1) ..
         const int jr = 8 * (lane >> 4) + (lane & 7);
         int k = 0;
@@ -642,11 +658,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
                 ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1);
                 if (ok)
-                    for (int i = u; i < (L - Lv) * (P / 8); i += 128) {
+                    for (int i = u; i < (L - Lv) * (P / 8); i += 256) {
                         const int r = Lv + i / (P / 8), c8 = i % (P / 8);
                         SM_AT(uint4, xt(n) + (c8 >> 3) * Lay::BOX + r * 128 + (c8 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 tc::fence_async_smem();
+                if (ok) arrive_w(Lay::X_ZERO);
             }
             for (int s = 0; ok && s < nsub; ++s, ++k) {
                 const int sl = k % Lay::NSLOT, j0 = SUB * s;
@@ -656,40 +673,36 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 ok = wait_w(Lay::W_EMPTY + sl, ((k / Lay::NSLOT) & 1) ^ 1);
                 if (!ok) break;
                 tc::fence_after();
+                uint32_t v[8];
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {  // sixteen channels
-                    const int c8 = 4 * q + 2 * hh + ((lane >> 3) & 1);  // eight-channel group of this lane's address
-                    uint32_t v[8];
+                for (int i = 0; i < 2; ++i) {  // tokens j0 + 16 i ..
+                    const int j = j0 + 16 * i + jr;
+                    ldsm_x4_t(bt(n) + (c8 >> 3) * Lay::BOX + j * 128 + (((c8 & 7) ^ (j & 7)) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+                if (Lv < L) {  // past the end b may be anything
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {  // tokens j0 + 16 i ..
-                        const int j = j0 + 16 * i + jr;
-                        ldsm_x4_t(bt(n) + (c8 >> 3) * Lay::BOX + j * 128 + (((c8 & 7) ^ (j & 7)) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = j0 + 8 * (i >> 1) + 2 * (lane & 3);
+                        v[i] &= j + 1 < Lv ? 0xffffffffu : j < Lv ? 0xffffu : 0u;
                     }
-                    if (Lv < L) {  // past the end b may be anything
+                }
+                float2 f[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int j = j0 + 8 * (i >> 1) + 2 * (lane & 3);
-                            v[i] &= j + 1 < Lv ? 0xffffffffu : j < Lv ? 0xffffu : 0u;
+                for (int i = 0; i < 8; ++i) f[i] = fmul2(make_float2(bf16_lo(v[i]), bf16_hi(v[i])), w[i >> 1]);
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (part + 1 < PARTS) {  // the upper eight bits; what is left is exact
+                            const uint32_t a = __float_as_uint(f[i].x), b = __float_as_uint(f[i].y);
+                            o[i] = __byte_perm(a, b, 0x7632);
+                            f[i] = fsub2(f[i], make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)));
+                        } else {
+                            o[i] = pack_bf16(f[i].x, f[i].y);
                         }
                     }
-                    float2 f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = fmul2(make_float2(bf16_lo(v[i]), bf16_hi(v[i])), w[i >> 1]);
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (part + 1 < PARTS) {  // the upper eight bits; what is left is exact
-                                const uint32_t a = __float_as_uint(f[i].x), b = __float_as_uint(f[i].y);
-                                o[i] = __byte_perm(a, b, 0x7632);
-                                f[i] = fsub2(f[i], make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)));
-                            } else {
-                                o[i] = pack_bf16(f[i].x, f[i].y);
-                            }
-                        }
-                        tc::st_16x128b_x4(lb + (static_cast<uint32_t>(16 * hh) << 16) + (sl * PARTS + part) * (SUB / 2), o);
-                    }
+                    tc::st_16x128b_x4(lb + (sl * PARTS + part) * (SUB / 2), o);
                 }
                 tc::wait_st();
                 tc::fence_before();

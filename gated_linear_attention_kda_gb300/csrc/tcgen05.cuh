@@ -56,6 +56,22 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
 }
 constexpr uint32_t SWZ_NONE = 0, SWZ_128B = 2;
 
+// The two halves of sdesc: the upper one is a constant of the operand's layout, so a loop carries only
+// the lower one (start address >> 4 | LBO), to which byte offsets >> 4 are added.
+__host__ __device__ constexpr uint32_t sdesc_hi(uint32_t sbo, uint32_t swizzle)
+{
+    return ((sbo >> 4) & 0x3FFF) | (1u << 14) | ((swizzle & 7) << 29);
+}
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo)
+{
+    return ((saddr & 0x3FFFF) >> 4) | (((lbo >> 4) & 0x3FFF) << 16);
+}
+template <uint32_t HI>
+__device__ __forceinline__ uint64_t sdesc_of(uint32_t lo)
+{
+    return (static_cast<uint64_t>(HI) << 32) | lo;
+}
+
 // Instruction descriptor for kind::f16 / kind::tf32 with fp32 accumulation.
 // fmt: 0 = f16, 1 = bf16, 2 = tf32; a_mn / b_mn: operand stored MN-major.
 __host__ __device__ constexpr uint32_t idesc(uint32_t fmt, uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn)
@@ -117,6 +133,14 @@ __device__ __forceinline__ void mma_ts_tf32_w(uint32_t d, uint32_t a_tmem, uint6
                  "r"(a_tmem), "l"(b), "r"(id), "r"(accumulate)
                  : "memory");
 }
+// Shared memory -> tensor memory: 128 rows x 32 bytes of a K-major tile to eight columns (one K step of
+// a 16-bit A operand). In order with the MMAs that the same thread issues after it.
+__device__ __forceinline__ void cp_128x256b_w(uint32_t taddr, uint64_t sd)
+{
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
+                 "@e tcgen05.cp.cta_group::1.128x256b [%0], %1;\n\t}" ::"r"(taddr), "l"(sd)
+                 : "memory");
+}
 __device__ __forceinline__ void commit_w(uint32_t bar)
 {
     asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
@@ -165,6 +189,16 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8])
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+// 32 lanes x 16 consecutive 32-bit columns
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    tmem_check(taddr, 16);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
 // 16 lanes (the half of this warp's quarter that the address names) x 16 consecutive 32-bit columns, in
 // the fragment layout of ldmatrix: register 2 r + k of lane l holds row l / 4 + 8 k, column 4 r + l % 4
 __device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8])
@@ -172,6 +206,14 @@ __device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r
     tmem_check(taddr, 16);
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// the same over 8 columns
+__device__ __forceinline__ void st_16x128b_x2(uint32_t taddr, const uint32_t (&r)[4])
+{
+    tmem_check(taddr, 8);
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
                  : "memory");
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
