@@ -5,6 +5,9 @@ buffers it is given on the current CUDA stream, allocates nothing and returns th
 
 Token axes may be strided: a slice of a projection's row is passed as it stands. The elements of
 one token are contiguous, and batch rows follow one another at the token stride.
+
+The checks read each tensor's properties once and the calls pass plain integers: for a single
+token the host's time is the call's time (a call costs 5 to 9 us of it on the GB300's CPU).
 """
 from __future__ import annotations
 
@@ -12,9 +15,11 @@ import ctypes
 
 import torch
 
-from . import _check, _lib, _P, _F, _I, _I64, _ptr, _raise, _same_device, _state_code
+from . import DTYPE_BF16, DTYPE_FP32, DTYPE_NONE, _lib, _P, _F, _I, _I64, _raise
 
 _Z = ctypes.c_size_t
+_BF16, _F32 = torch.bfloat16, torch.float32
+_CODES = {_BF16: DTYPE_BF16, _F32: DTYPE_FP32}
 ACTS = {"none": 0, "sigmoid": 1, "silu": 2}  # KDA_ACT_*
 
 _lib.kda_conv.argtypes = [_P, _I64, _P, _P, _I, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P]
@@ -32,52 +37,91 @@ for _f in ("kda_conv", "kda_conv_step", "kda_ssm", "kda_ssm_workspace_bytes", "k
     getattr(_lib, _f).restype = _I
 
 
-def _rows(name, t, shape, lead, dtype=torch.bfloat16):
-    """Check an activation of the given shape and return the distance in elements between its
-    tokens; the first ``lead`` dimensions are the token axes ([B, T] or [S])."""
+def _tensor(name, t, dev, dtypes, shape):
+    """Check a tensor's kind, device, type and shape."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but x is on cuda:{dev}: all tensors must share one device")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    width = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
-        if t.shape[i] > 1 and t.stride(i) != width:
+
+
+def _x_device(x, dims, layout):
+    """The device of the leading argument, whose shape the others are checked against."""
+    if not isinstance(x, torch.Tensor) or x.dim() not in dims:
+        raise ValueError(f"x must be {layout}")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    return x.get_device()
+
+
+def _rows(name, t, shape, lead, dev, dtypes=(_BF16,)):
+    """Check an activation of the given shape; returns its address and the distance in elements
+    between its tokens. The first ``lead`` dimensions are the token axes ([B, T] or [S])."""
+    _tensor(name, t, dev, dtypes, shape)
+    stride, width = t.stride(), 1
+    for i in range(len(stride) - 1, lead - 1, -1):
+        if shape[i] > 1 and stride[i] != width:
             raise ValueError(f"{name}: the elements of one token must be contiguous")
-        width *= t.shape[i]
-    axes = [i for i in range(lead) if t.shape[i] > 1]
-    if not axes or t.numel() == 0:
-        return width
-    stride = t.stride(axes[-1])
-    if len(axes) == 2 and t.stride(axes[0]) != t.shape[axes[1]] * stride:
-        raise ValueError(f"{name}: batch rows must follow one another at the token stride")
-    return stride
+        width *= shape[i]
+    if lead == 1:
+        step = stride[0] if shape[0] > 1 else width
+    elif shape[1] > 1:
+        step = stride[1]
+        if shape[0] > 1 and stride[0] != shape[1] * step:
+            raise ValueError(f"{name}: batch rows must follow one another at the token stride")
+    else:
+        step = stride[0] if shape[0] > 1 else width
+    return t.data_ptr(), step
 
 
-def _param(name, t, shape):
-    _check(name, t, torch.float32, shape, True)
+def _dense(name, t, dev, dtypes, shape):
+    """Check an optional contiguous tensor (a parameter or a state); returns its address or None."""
+    if t is None:
+        return None
+    _tensor(name, t, dev, dtypes, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _act(act, allowed=("none", "sigmoid", "silu")):
-    if act not in allowed:
-        raise ValueError(f"act must be one of {allowed}, got {act!r}")
+def _act(act):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {tuple(ACTS)}, got {act!r}")
     return ACTS[act]
 
 
-def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+def _call(fn, dev, *args):
+    """One library call on the current stream of device ``dev``."""
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _raise(status)
 
 
-def _varlen(cu_seqlens, B):
+def _varlen(cu_seqlens, dev, B):
+    """Address of the bounds, their N, and the number of sequences."""
     if cu_seqlens is None:
-        return 0, B
-    _check("cu_seqlens", cu_seqlens, torch.int64, None, True)
+        return None, 0, B
+    p = _dense("cu_seqlens", cu_seqlens, dev, (torch.int64,), None)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [N+1] with N >= 1")
-    return cu_seqlens.numel() - 1, cu_seqlens.numel() - 1
+    return p, cu_seqlens.numel() - 1, cu_seqlens.numel() - 1
+
+
+def _taps(weight, bias, dev, C):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [C, W]")
+    W = weight.shape[1]
+    return _dense("weight", weight, dev, (_F32,), (C, W)), _dense("bias", bias, dev, (_F32,), (C,)), W
 
 
 def conv(x, weight, out, bias=None, silu=True, initial_state=None, final_state=None, cu_seqlens=None):
@@ -85,63 +129,47 @@ def conv(x, weight, out, bias=None, silu=True, initial_state=None, final_state=N
     allowed), ``weight`` fp32 [C, W] (W = 2, 3, 4; the last tap is the token's own), ``bias`` fp32
     [C], states bf16 [B|N, W - 1, C] (the same buffer allowed). ``silu`` applies u sigmoid(u).
     Returns ``(out, final_state)``."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3:
-        raise ValueError("x must be [B, T, C]")
-    B, T, C = x.shape
-    xs, os_ = _rows("x", x, x.shape, 2), _rows("out", out, x.shape, 2)
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError("weight must be [C, W]")
-    W = weight.shape[1]
-    _param("weight", weight, (C, W))
-    _param("bias", bias, (C,))
-    N, S = _varlen(cu_seqlens, B)
-    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
-        _check(name, t, torch.bfloat16, (S, W - 1, C), True)
-    _same_device(x.device, (("weight", weight), ("out", out), ("bias", bias), ("initial_state", initial_state),
-                            ("final_state", final_state), ("cu_seqlens", cu_seqlens)))
-    with torch.cuda.device(x.device):
-        _raise(_lib.kda_conv(_ptr(x), xs, _ptr(weight), _ptr(bias), ACTS["silu" if silu else "none"], _ptr(out), os_,
-                             _ptr(initial_state), _ptr(final_state), _ptr(cu_seqlens), N, B, T, C, W, _stream(x.device)))
+    dev = _x_device(x, (3,), "[B, T, C]")
+    shape = x.shape
+    B, T, C = shape
+    xp, xs = _rows("x", x, shape, 2, dev)
+    op, os_ = _rows("out", out, shape, 2, dev)
+    wp, bp, W = _taps(weight, bias, dev, C)
+    cu, N, S = _varlen(cu_seqlens, dev, B)
+    ip = _dense("initial_state", initial_state, dev, (_BF16,), (S, W - 1, C))
+    fp = _dense("final_state", final_state, dev, (_BF16,), (S, W - 1, C))
+    _call(_lib.kda_conv, dev, xp, xs, wp, bp, 2 if silu else 0, op, os_, ip, fp, cu, N, B, T, C, W)
     return out, final_state
 
 
 def conv_step(x, weight, out, state, bias=None, silu=True):
     """``conv`` for one token of S sequences: ``x``, ``out`` bf16 [S, C] (``out`` may be ``x``),
     ``state`` bf16 [S, W - 1, C] updated in place. Returns ``(out, state)``."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be [S, C]")
-    S, C = x.shape
-    xs, os_ = _rows("x", x, x.shape, 1), _rows("out", out, x.shape, 1)
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
-        raise ValueError("weight must be [C, W]")
-    W = weight.shape[1]
-    _param("weight", weight, (C, W))
-    _param("bias", bias, (C,))
+    dev = _x_device(x, (2,), "[S, C]")
+    shape = x.shape
+    S, C = shape
+    xp, xs = _rows("x", x, shape, 1, dev)
+    op, os_ = _rows("out", out, shape, 1, dev)
+    wp, bp, W = _taps(weight, bias, dev, C)
     if state is None:
         raise ValueError("state is required")
-    _check("state", state, torch.bfloat16, (S, W - 1, C), True)
-    _same_device(x.device, (("weight", weight), ("out", out), ("bias", bias), ("state", state)))
-    with torch.cuda.device(x.device):
-        _raise(_lib.kda_conv_step(_ptr(x), xs, _ptr(weight), _ptr(bias), ACTS["silu" if silu else "none"], _ptr(out), os_,
-                                  _ptr(state), S, C, W, _stream(x.device)))
+    sp = _dense("state", state, dev, (_BF16,), (S, W - 1, C))
+    _call(_lib.kda_conv_step, dev, xp, xs, wp, bp, 2 if silu else 0, op, os_, sp, S, C, W)
     return out, state
 
 
-def _ssm_args(x, dt, b, c, out, A_log, D, dt_bias, lead):
-    tok, (H, P) = tuple(x.shape[:lead]), x.shape[lead:]
+def _ssm_args(x, dt, b, c, out, A_log, D, dt_bias, lead, dev):
+    shape = x.shape
+    tok, (H, P) = shape[:lead], shape[lead:]
     if not isinstance(b, torch.Tensor) or b.dim() != lead + 2:
         raise ValueError("b and c must be [..., G, 128]")
-    G, K = b.shape[lead:]
-    strides = [_rows("x", x, x.shape, lead), _rows("dt", dt, tok + (H,), lead), _rows("b", b, tok + (G, K), lead),
-               _rows("c", c, tok + (G, K), lead), _rows("out", out, x.shape, lead)]
+    gk = tok + b.shape[lead:]
+    head = (*_rows("x", x, shape, lead, dev), *_rows("dt", dt, tok + (H,), lead, dev), *_rows("b", b, gk, lead, dev),
+            *_rows("c", c, gk, lead, dev))
     if A_log is None:
         raise ValueError("A_log is required")
-    for name, t in (("A_log", A_log), ("D", D), ("dt_bias", dt_bias)):
-        _param(name, t, (H,))
-    _same_device(x.device, (("dt", dt), ("b", b), ("c", c), ("out", out), ("A_log", A_log), ("D", D), ("dt_bias", dt_bias)))
-    head = (_ptr(x), strides[0], _ptr(dt), strides[1], _ptr(b), strides[2], _ptr(c), strides[3], _ptr(A_log), _ptr(D),
-            _ptr(dt_bias), _ptr(out), strides[4])
-    return head, H, P, G, K
+    params = tuple(_dense(name, t, dev, (_F32,), (H,)) for name, t in (("A_log", A_log), ("D", D), ("dt_bias", dt_bias)))
+    return (*head, *params, *_rows("out", out, shape, lead, dev)), H, P, gk[lead], gk[lead + 1]
 
 
 def ssm_workspace_bytes(states, tokens, H, P) -> int:
@@ -160,24 +188,16 @@ def ssm(x, dt, b, c, out, A_log, D=None, dt_bias=None, initial_state=None, final
     divides H), ``A_log``, ``D``, ``dt_bias`` fp32 [H], states bf16/fp32 [B|N, H, P, 128]. A CUDA
     uint8 ``workspace`` of ``ssm_workspace_bytes`` bytes lets calls with few (sequence, head) pairs
     split the time axis. Returns ``(out, final_state)``."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 4:
-        raise ValueError("x must be [B, T, H, P]")
+    dev = _x_device(x, (4,), "[B, T, H, P]")
     B, T = x.shape[:2]
-    head, H, P, G, K = _ssm_args(x, dt, b, c, out, A_log, D, dt_bias, 2)
-    N, S = _varlen(cu_seqlens, B)
-    for name, t in (("initial_state", initial_state), ("final_state", final_state)):
-        _check(name, t, None, (S, H, P, K), True)
-    nbytes = 0
-    if workspace is not None:
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor")
-        nbytes = workspace.numel()
-    _same_device(x.device, (("initial_state", initial_state), ("final_state", final_state), ("cu_seqlens", cu_seqlens),
-                            ("workspace", workspace)))
-    with torch.cuda.device(x.device):
-        _raise(_lib.kda_ssm(*head, _ptr(initial_state), _state_code(initial_state), _ptr(final_state),
-                            _state_code(final_state), _ptr(cu_seqlens), N, B, T, H, P, G, K,
-                            _ptr(workspace) if nbytes else None, nbytes, _stream(x.device)))
+    head, H, P, G, K = _ssm_args(x, dt, b, c, out, A_log, D, dt_bias, 2, dev)
+    cu, N, S = _varlen(cu_seqlens, dev, B)
+    ip = _dense("initial_state", initial_state, dev, (_BF16, _F32), (S, H, P, K))
+    fp = _dense("final_state", final_state, dev, (_BF16, _F32), (S, H, P, K))
+    wp = _dense("workspace", workspace, dev, (torch.uint8,), None)
+    nbytes = workspace.numel() if wp else 0
+    _call(_lib.kda_ssm, dev, *head, ip, DTYPE_NONE if ip is None else _CODES[initial_state.dtype],
+          fp, DTYPE_NONE if fp is None else _CODES[final_state.dtype], cu, N, B, T, H, P, G, K, wp if nbytes else None, nbytes)
     return out, final_state
 
 
@@ -185,16 +205,13 @@ def ssm_step(x, dt, b, c, out, state, A_log, D=None, dt_bias=None):
     """``ssm`` for one token of S sequences: ``x``, ``out`` bf16 [S, H, P], ``dt`` bf16 [S, H],
     ``b``, ``c`` bf16 [S, G, 128], ``state`` bf16/fp32 [S, H, P, 128] updated in place. Returns
     ``(out, state)``."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 3:
-        raise ValueError("x must be [S, H, P]")
-    head, H, P, G, K = _ssm_args(x, dt, b, c, out, A_log, D, dt_bias, 1)
+    dev = _x_device(x, (3,), "[S, H, P]")
+    head, H, P, G, K = _ssm_args(x, dt, b, c, out, A_log, D, dt_bias, 1, dev)
     S = x.shape[0]
     if state is None:
         raise ValueError("state is required")
-    _check("state", state, None, (S, H, P, K), True)
-    _same_device(x.device, (("state", state),))
-    with torch.cuda.device(x.device):
-        _raise(_lib.kda_ssm_step(*head, _ptr(state), _state_code(state), S, H, P, G, K, _stream(x.device)))
+    sp = _dense("state", state, dev, (_BF16, _F32), (S, H, P, K))
+    _call(_lib.kda_ssm_step, dev, *head, sp, _CODES[state.dtype], S, H, P, G, K)
     return out, state
 
 
@@ -203,20 +220,17 @@ def gated_norm(x, gate, weight, out, act="sigmoid", gate_first=False, eps=1e-5):
     ``out`` bf16 [B, T, R, D] or [S, R, D], rows of D channels; ``weight`` fp32 [D], [R, D] or None.
     ``gate_first`` multiplies by ``act(gate)`` before the norm, else after it. ``out`` may be ``x``
     or ``gate``. Returns ``out``."""
-    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
-        raise ValueError("x must be [B, T, R, D] or [S, R, D]")
-    lead = x.dim() - 2
-    R, D = x.shape[lead:]
-    xs, zs, os_ = (_rows(n, t, x.shape, lead) for n, t in (("x", x), ("gate", gate), ("out", out)))
-    w_rows = 1
-    if weight is not None:
-        w_rows = R if isinstance(weight, torch.Tensor) and weight.dim() == 2 else 1
-        _param("weight", weight, (R, D) if w_rows == R and weight.dim() == 2 else (D,))
-    _same_device(x.device, (("gate", gate), ("weight", weight), ("out", out)))
-    M = x.numel() // (R * D) if R * D else 0
-    with torch.cuda.device(x.device):
-        _raise(_lib.kda_gated_norm(_ptr(x), xs, _ptr(gate), zs, _ptr(weight), w_rows, _ptr(out), os_, float(eps), _act(act),
-                                   int(bool(gate_first)), M, R, D, _stream(x.device)))
+    dev = _x_device(x, (3, 4), "[B, T, R, D] or [S, R, D]")
+    shape = x.shape
+    lead = len(shape) - 2
+    R, D = shape[lead:]
+    xp, xs = _rows("x", x, shape, lead, dev)
+    zp, zs = _rows("gate", gate, shape, lead, dev)
+    op, os_ = _rows("out", out, shape, lead, dev)
+    per_row = isinstance(weight, torch.Tensor) and weight.dim() == 2
+    wp = _dense("weight", weight, dev, (_F32,), (R, D) if per_row else (D,))
+    M = shape[0] * shape[1] if lead == 2 else shape[0]
+    _call(_lib.kda_gated_norm, dev, xp, xs, zp, zs, wp, R if per_row else 1, op, os_, eps, _act(act), int(bool(gate_first)), M, R, D)
     return out
 
 
@@ -227,24 +241,18 @@ def residual_norm(x, residual, residual_out, weight=None, out=None, post_weight=
     ``residual``, ``residual_out`` bf16 or fp32 (the same buffer allowed; ``residual_out`` None: not
     written); ``weight``, ``post_weight``, ``channel_scale`` fp32 [D] or None. n(x) is x, or its RMS
     norm times ``post_weight`` where that is given. Returns ``(out, residual_out)``."""
-    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
-        raise ValueError("x must be [B, T, D] or [S, D]")
-    lead, D = x.dim() - 1, x.shape[-1]
-    if not isinstance(residual, torch.Tensor):
-        raise TypeError("residual must be a torch.Tensor")
-    if residual.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"residual must be bfloat16 or float32, got {residual.dtype}")
-    st = {"x": _rows("x", x, x.shape, lead), "residual": _rows("residual", residual, x.shape, lead, residual.dtype)}
-    for name, t, dt in (("residual_out", residual_out, residual.dtype), ("gate", gate, torch.bfloat16), ("out", out, torch.bfloat16)):
-        st[name] = D if t is None else _rows(name, t, x.shape, lead, dt)
-    for name, t in (("post_weight", post_weight), ("channel_scale", channel_scale), ("weight", weight)):
-        _param(name, t, (D,))
-    _same_device(x.device, (("residual", residual), ("residual_out", residual_out), ("gate", gate), ("out", out),
-                            ("post_weight", post_weight), ("channel_scale", channel_scale), ("weight", weight)))
-    M = x.numel() // D if D else 0
-    with torch.cuda.device(x.device):
-        _raise(_lib.kda_residual_norm(_ptr(x), st["x"], _ptr(residual), st["residual"], _ptr(residual_out), st["residual_out"],
-                                      _state_code(residual), _ptr(gate), st["gate"], _act(act), _ptr(post_weight),
-                                      _ptr(channel_scale), float(alpha), _ptr(weight), _ptr(out), st["out"], float(eps), M, D,
-                                      _stream(x.device)))
+    dev = _x_device(x, (2, 3), "[B, T, D] or [S, D]")
+    shape = x.shape
+    lead = len(shape) - 1
+    D = shape[lead]
+    xp, xs = _rows("x", x, shape, lead, dev)
+    rp, rs = _rows("residual", residual, shape, lead, dev, (_BF16, _F32))
+    rop, ros = (None, D) if residual_out is None else _rows("residual_out", residual_out, shape, lead, dev, (residual.dtype,))
+    zp, zs = (None, D) if gate is None else _rows("gate", gate, shape, lead, dev)
+    op, os_ = (None, D) if out is None else _rows("out", out, shape, lead, dev)
+    pw, ch, w = (_dense(name, t, dev, (_F32,), (D,)) for name, t in
+                 (("post_weight", post_weight), ("channel_scale", channel_scale), ("weight", weight)))
+    M = shape[0] * shape[1] if lead == 2 else shape[0]
+    _call(_lib.kda_residual_norm, dev, xp, xs, rp, rs, rop, ros, _CODES[residual.dtype], zp, zs, _act(act), pw, ch, alpha, w,
+          op, os_, eps, M, D)
     return out, residual_out

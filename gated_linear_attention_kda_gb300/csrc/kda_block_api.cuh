@@ -100,7 +100,8 @@ static kda_status launch_conv(const conv::ConvParams &q, cudaStream_t s)
 template <int W>
 static kda_status launch_conv_step(const conv::ConvParams &p, uint16_t *state, cudaStream_t s)
 {
-    const int64_t n = static_cast<int64_t>(p.nseq) * (p.C / 8), grid = (n + conv::THREADS - 1) / conv::THREADS;
+    const int64_t n = (static_cast<int64_t>(p.nseq) + conv::STEP_SEQS - 1) / conv::STEP_SEQS * (p.C / 8);
+    const int64_t grid = (n + conv::THREADS - 1) / conv::THREADS;
     if (grid > 0x7fffffff) return fail(KDA_ERR_SHAPE, "problem too large");
     conv::kda_conv_step_kernel<W><<<static_cast<unsigned>(grid), conv::THREADS, 0, s>>>(p, state);
     return launched("convolution step");
@@ -115,8 +116,8 @@ static kda_status check_conv(const void *x, int64_t xs, const float *weight, con
     if (!weight || (tokens && (!x || !out))) return fail(KDA_ERR_NULL, "x, weight and out are required");
     if (tokens && (!stride_ok(xs, C, 8) || !stride_ok(os, C, 8)))
         return fail(KDA_ERR_ALIGN, "token strides must be multiples of 8 elements and at least C (x %lld, out %lld)", (long long)xs, (long long)os);
-    if ((tokens && (!aligned(x, 16) || !aligned(out, 16))) || !aligned(weight, 4) || !aligned(bias, 4))
-        return fail(KDA_ERR_ALIGN, "x and out must be 16-byte, weight and bias 4-byte aligned");
+    if ((tokens && (!aligned(x, 16) || !aligned(out, 16))) || !aligned(weight, 16) || !aligned(bias, 16))
+        return fail(KDA_ERR_ALIGN, "x, out, weight and bias must be 16-byte aligned");
     return KDA_OK;
 }
 
@@ -241,32 +242,40 @@ static kda_status launch_ssm(const ssm::SsmParams &p, const SsmPlan &plan, float
                                                   : launch_ssm_tc<P, 2, true>(grid, mx, mb, mc, mo, t, s);
 }
 
-// Threads along a row of D channels: a power of two of lanes up to a warp (then one, two or four
-// vectors each), or a CTA of one or two vectors per thread.
+// Threads along a row of D channels and vectors of eight per thread. Few rows (less than four per SM)
+// are bound by latency and get many threads each; many rows by bandwidth, and get few threads with
+// four or eight vectors each, whose loads are all in flight at once (TIMES).
 struct RowShape {
     bool cta;
     int threads, vpt;
 };
-static RowShape row_shape(int64_t D)
+static RowShape row_shape(int64_t D, int64_t rows, int sms)
 {
     const int v = static_cast<int>((D + 7) / 8);
-    if (v <= 128) {
+    if (v <= 32) {
         int t = 1;
-        while (t < v && t < 32) t <<= 1;
-        const int n = (v + t - 1) / t;
-        return {false, t, n <= 1 ? 1 : n <= 2 ? 2 : 4};
+        while (t < v) t <<= 1;
+        return {false, t, 1};
     }
-    const int vpt = v <= 1024 ? 1 : 2;
+    auto vectors = [](int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; };
+    const bool many = rows >= 4 * static_cast<int64_t>(sms);
+    if (v <= (many ? 256 : 64)) return {false, 32, vectors((v + 31) / 32)};
+    const int vpt = many || v > 2 * norm::CTA_THREADS ? 4 : 2;
     return {true, (((v + vpt - 1) / vpt) + 31) / 32 * 32, vpt};
 }
 
 // Blocks that fill the machine at the kernel's occupancy, no more than there are row groups.
-template <typename Kern>
-static unsigned row_grid(Kern kern, const RowShape &sh, int64_t rows, const Device &d)
+template <auto KERN>
+static unsigned row_grid(const RowShape &sh, int64_t rows, const Device &d)
 {
+    // resident blocks for a block size, queried once per kernel instance, size and device
+    static thread_local int seen_dev = -1, seen_threads = 0, occ = 1;
     const int threads = sh.cta ? sh.threads : norm::WARP_THREADS;
-    int occ = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, 0) != cudaSuccess || occ < 1) occ = 1;
+    if (seen_dev != d.id || seen_threads != threads) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, KERN, threads, 0) != cudaSuccess || occ < 1) occ = 1;
+        seen_dev = d.id;
+        seen_threads = threads;
+    }
     const int64_t per = sh.cta ? 1 : norm::WARP_THREADS / sh.threads;
     return static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(d.sms) * occ, (rows + per - 1) / per));
 }
@@ -275,7 +284,7 @@ template <int VPT, bool CTA>
 static kda_status launch_gated(norm::GatedParams p, const RowShape &sh, const Device &d, cudaStream_t s)
 {
     p.tpr = sh.threads;
-    const unsigned grid = row_grid(norm::kda_gated_norm_kernel<VPT, CTA>, sh, p.rows, d);
+    const unsigned grid = row_grid<norm::kda_gated_norm_kernel<VPT, CTA>>(sh, p.rows, d);
     norm::kda_gated_norm_kernel<VPT, CTA><<<grid, CTA ? sh.threads : norm::WARP_THREADS, 0, s>>>(p);
     return launched("gated norm");
 }
@@ -286,9 +295,9 @@ static kda_status launch_residual(norm::ResidualParams p, bool f32, const RowSha
     p.tpr = sh.threads;
     const int threads = CTA ? sh.threads : norm::WARP_THREADS;
     if (f32)
-        norm::kda_residual_norm_kernel<VPT, CTA, true><<<row_grid(norm::kda_residual_norm_kernel<VPT, CTA, true>, sh, p.rows, d), threads, 0, s>>>(p);
+        norm::kda_residual_norm_kernel<VPT, CTA, true><<<row_grid<norm::kda_residual_norm_kernel<VPT, CTA, true>>(sh, p.rows, d), threads, 0, s>>>(p);
     else
-        norm::kda_residual_norm_kernel<VPT, CTA, false><<<row_grid(norm::kda_residual_norm_kernel<VPT, CTA, false>, sh, p.rows, d), threads, 0, s>>>(p);
+        norm::kda_residual_norm_kernel<VPT, CTA, false><<<row_grid<norm::kda_residual_norm_kernel<VPT, CTA, false>>(sh, p.rows, d), threads, 0, s>>>(p);
     return launched("residual norm");
 }
 
@@ -328,7 +337,7 @@ KDA_API kda_status kda_conv(const void *x, int64_t x_stride, const float *weight
     p.C = static_cast<int>(C);
     p.act = act;
     p.cg = 1;
-    while (p.cg < conv::THREADS && p.cg < C / 8) p.cg <<= 1;
+    while (p.cg < 32 && p.cg < C / 8) p.cg <<= 1;  // a warp along the channels, so that little of the last block idles
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return W == 2 ? blk::launch_conv<2>(p, s) : W == 3 ? blk::launch_conv<3>(p, s) : blk::launch_conv<4>(p, s);
 }
@@ -514,9 +523,12 @@ KDA_API kda_status kda_gated_norm(const void *x, int64_t x_stride, const void *g
     p.w_rows = weight_rows == 1 ? 1 : static_cast<int>(R);
     p.eps = eps;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const blk::RowShape sh = blk::row_shape(D);
-    if (sh.cta) return sh.vpt == 1 ? blk::launch_gated<1, true>(p, sh, d, s) : blk::launch_gated<2, true>(p, sh, d, s);
-    return sh.vpt == 1 ? blk::launch_gated<1, false>(p, sh, d, s) : sh.vpt == 2 ? blk::launch_gated<2, false>(p, sh, d, s) : blk::launch_gated<4, false>(p, sh, d, s);
+    const blk::RowShape sh = blk::row_shape(D, p.rows, d.sms);
+    if (sh.cta) return sh.vpt == 2 ? blk::launch_gated<2, true>(p, sh, d, s) : blk::launch_gated<4, true>(p, sh, d, s);
+    return sh.vpt == 1   ? blk::launch_gated<1, false>(p, sh, d, s)
+           : sh.vpt == 2 ? blk::launch_gated<2, false>(p, sh, d, s)
+           : sh.vpt == 4 ? blk::launch_gated<4, false>(p, sh, d, s)
+                         : blk::launch_gated<8, false>(p, sh, d, s);
 }
 
 KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
@@ -570,11 +582,12 @@ KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void
     p.eps = eps;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = residual_dtype == KDA_DTYPE_FP32;
-    const blk::RowShape sh = blk::row_shape(D);
-    if (sh.cta) return sh.vpt == 1 ? blk::launch_residual<1, true>(p, f32, sh, d, s) : blk::launch_residual<2, true>(p, f32, sh, d, s);
+    const blk::RowShape sh = blk::row_shape(D, p.rows, d.sms);
+    if (sh.cta) return sh.vpt == 2 ? blk::launch_residual<2, true>(p, f32, sh, d, s) : blk::launch_residual<4, true>(p, f32, sh, d, s);
     return sh.vpt == 1   ? blk::launch_residual<1, false>(p, f32, sh, d, s)
            : sh.vpt == 2 ? blk::launch_residual<2, false>(p, f32, sh, d, s)
-                         : blk::launch_residual<4, false>(p, f32, sh, d, s);
+           : sh.vpt == 4 ? blk::launch_residual<4, false>(p, f32, sh, d, s)
+                         : blk::launch_residual<8, false>(p, f32, sh, d, s);
 }
 
 }  // extern "C"

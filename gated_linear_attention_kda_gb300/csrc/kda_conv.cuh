@@ -5,8 +5,8 @@
 //
 // HBM-bound: 2 bytes in and 2 out per element against W FMAs and one sigmoid. A thread owns eight
 // channels (one 16-byte access per token) and walks RUN tokens of them with the last W - 1 rows in
-// registers, so a row is read once per run plus the W - 1 rows before it; BATCH rows are loaded
-// before any is used, which keeps the loads of a whole batch in flight.
+// registers, so a row is read once per run plus the W - 1 rows before it; the BATCH rows of the next
+// step are loaded before those of the present one are filtered. Arithmetic is in fp32 pairs.
 #pragma once
 #include "blk_common.cuh"
 
@@ -29,31 +29,50 @@ struct ConvParams {
     int cg;                 // threads along the channels (a power of two <= THREADS)
 };
 
-template <int W>
-__device__ __forceinline__ void load_weights(const float *weight, const float *bias, int c, float (&w)[W][8], float (&b)[8])
+// Eight channels as four pairs (paired fp32 arithmetic).
+struct Row {
+    float2 v[4];
+};
+__device__ __forceinline__ Row unpack(const uint4 &r)
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = __ldg(weight + static_cast<size_t>(c + i) * W + j);
-        b[i] = bias ? __ldg(bias + c + i) : 0.f;
-    }
+    return {{make_float2(bf16_lo(r.x), bf16_hi(r.x)), make_float2(bf16_lo(r.y), bf16_hi(r.y)),
+             make_float2(bf16_lo(r.z), bf16_hi(r.z)), make_float2(bf16_lo(r.w), bf16_hi(r.w))}};
 }
 
-// One output row from the W rows that end with it.
 template <int W>
-__device__ __forceinline__ uint4 filter_row(const float (*f)[8], const float (&w)[W][8], const float (&b)[8], int act)
-{
-    float u[8];
+struct Taps {
+    Row w[W], b;
+    __device__ __forceinline__ void load(const float *weight, const float *bias, int c)
+    {
+        float buf[8 * W];  // the eight channels' taps, contiguous
+        const float4 *src = reinterpret_cast<const float4 *>(weight + static_cast<size_t>(c) * W);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        u[i] = b[i];
+        for (int i = 0; i < 2 * W; ++i) {
+            const float4 q = __ldg(src + i);
+            buf[4 * i] = q.x; buf[4 * i + 1] = q.y; buf[4 * i + 2] = q.z; buf[4 * i + 3] = q.w;
+        }
 #pragma unroll
-        for (int j = 0; j < W; ++j) u[i] = fmaf(w[j][i], f[j][i], u[i]);
-        u[i] = blk::apply_act(u[i], act);
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j].v[i] = make_float2(buf[2 * i * W + j], buf[(2 * i + 1) * W + j]);
+            b.v[i] = bias ? __ldg(reinterpret_cast<const float2 *>(bias + c) + i) : make_float2(0.f, 0.f);
+        }
     }
-    return blk::pack8(u);
-}
+    // One output row from the W rows that end with it.
+    __device__ __forceinline__ uint4 row(const Row *f, bool silu) const
+    {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 u = b.v[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) u = ffma2(w[j].v[i], f[j].v[i], u);
+            if (silu) u = fmul2(u, make_float2(blk::sigmoid_fast(u.x), blk::sigmoid_fast(u.y)));
+            o[i] = pack_bf16(u.x, u.y);
+        }
+        return make_uint4(o[0], o[1], o[2], o[3]);
+    }
+};
 
 // The last W - 1 rows of [initial state ; x] of one sequence, eight channels. All rows are read
 // before any is written: the final state may be the initial state's buffer.
@@ -105,8 +124,9 @@ __global__ void __launch_bounds__(THREADS) kda_conv_kernel(const ConvParams p)
     const int c = 8 * c8, tg = THREADS / p.cg;
     long long t = (static_cast<long long>(blockIdx.x) * tg + threadIdx.x / p.cg) * RUN;
     const long long t_end = min(t + RUN, p.total);
-    float w[W][8], bias[8];
-    load_weights<W>(p.weight, p.bias, c, w, bias);
+    Taps<W> taps;
+    taps.load(p.weight, p.bias, c);
+    const bool silu = p.act == KDA_ACT_SILU;
     while (t < t_end) {
         blk::Enclosing sq;
         if (p.cu) {
@@ -121,7 +141,19 @@ __global__ void __launch_bounds__(THREADS) kda_conv_kernel(const ConvParams p)
             sq.e = sq.b + p.T;
         }
         const long long end = min(sq.e, t_end);
-        float f[W - 1 + BATCH][8];  // rows t - (W - 1) .. t + BATCH - 1
+        const uint16_t *src = p.x + t * p.xs + c;
+        uint16_t *dst = p.out + t * p.os + c;
+        int n = static_cast<int>(end - t);  // tokens of this sequence in the run
+        uint4 raw[BATCH];
+        auto fetch = [&] {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                raw[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (i < n) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + i * p.xs));
+            }
+        };
+        fetch();
+        Row f[W - 1 + BATCH];  // the W - 1 rows before the batch, and the batch
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const long long at = t - (W - 1) + j;
@@ -131,51 +163,61 @@ __global__ void __launch_bounds__(THREADS) kda_conv_kernel(const ConvParams p)
             else if (p.init)
                 r = *reinterpret_cast<const uint4 *>(
                     p.init + (static_cast<size_t>(sq.seq) * (W - 1) + static_cast<size_t>(at - sq.b + (W - 1))) * p.C + c);
-            blk::unpack8(r, f[j]);
+            f[j] = unpack(r);
         }
-        for (; t < end; t += BATCH) {
-            uint4 raw[BATCH];
+#pragma unroll 1
+        while (n > 0) {
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                raw[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (t + i < end) raw[i] = __ldg(reinterpret_cast<const uint4 *>(p.x + (t + i) * p.xs + c));
-            }
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) blk::unpack8(raw[i], f[W - 1 + i]);
+            for (int i = 0; i < BATCH; ++i) f[W - 1 + i] = unpack(raw[i]);
+            const int m = n;
+            n -= BATCH;
+            src += BATCH * p.xs;
+            fetch();  // the next batch's rows are in flight while this one is filtered
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
-                if (t + i < end) *reinterpret_cast<uint4 *>(p.out + (t + i) * p.os + c) = filter_row<W>(f + i, w, bias, p.act);
+                if (i < m) *reinterpret_cast<uint4 *>(dst + i * p.os) = taps.row(f + i, silu);
+            dst += BATCH * p.os;
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[j][i] = f[BATCH + j][i];
+            for (int j = 0; j < W - 1; ++j) f[j] = f[BATCH + j];
         }
         t = end;
     }
 }
 
-// One token of S sequences: a thread holds eight channels of one sequence, all rows read first
-// (out may be x), and shifts the state by one row. Launch latency bounds it.
+// One token of S sequences. A thread owns eight channels of STEP_SEQS sequences (it reads the taps once
+// for all of them; 128 sequences x 6144 channels: 14.8 us with one sequence per thread and scalar tap
+// loads). All rows of a sequence are read before its state or output is written: out may be x.
+constexpr int STEP_SEQS = 4;
 template <int W>
 __global__ void __launch_bounds__(THREADS) kda_conv_step_kernel(const ConvParams p, uint16_t *state)
 {
     const int nc8 = p.C >> 3;
     const long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
-    if (i >= static_cast<long long>(p.nseq) * nc8) return;
-    const long long s = i / nc8;
+    const long long s0 = i / nc8 * STEP_SEQS;
+    if (s0 >= p.nseq) return;
     const int c = static_cast<int>(i % nc8) * 8;
-    uint16_t *st = state + s * (W - 1) * p.C + c;
-    uint4 raw[W];
+    uint16_t *st = state + s0 * (W - 1) * p.C + c;
+    uint4 raw[STEP_SEQS][W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) raw[j] = *reinterpret_cast<const uint4 *>(st + static_cast<size_t>(j) * p.C);
-    raw[W - 1] = *reinterpret_cast<const uint4 *>(p.x + s * p.xs + c);
-    float w[W][8], bias[8], f[W][8];
-    load_weights<W>(p.weight, p.bias, c, w, bias);
+    for (int k = 0; k < STEP_SEQS; ++k)
+        if (s0 + k < p.nseq) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) blk::unpack8(raw[j], f[j]);
-    *reinterpret_cast<uint4 *>(p.out + s * p.os + c) = filter_row<W>(f, w, bias, p.act);
+            for (int j = 0; j < W - 1; ++j) raw[k][j] = *reinterpret_cast<const uint4 *>(st + static_cast<size_t>(k * (W - 1) + j) * p.C);
+            raw[k][W - 1] = *reinterpret_cast<const uint4 *>(p.x + (s0 + k) * p.xs + c);
+        }
+    Taps<W> taps;
+    taps.load(p.weight, p.bias, c);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<uint4 *>(st + static_cast<size_t>(j) * p.C) = raw[j + 1];
+    for (int k = 0; k < STEP_SEQS; ++k)
+        if (s0 + k < p.nseq) {
+            Row f[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) f[j] = unpack(raw[k][j]);
+            *reinterpret_cast<uint4 *>(p.out + (s0 + k) * p.os + c) = taps.row(f, p.act == KDA_ACT_SILU);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                *reinterpret_cast<uint4 *>(st + static_cast<size_t>(k * (W - 1) + j) * p.C) = raw[k][j + 1];
+        }
 }
 
 }  // namespace conv

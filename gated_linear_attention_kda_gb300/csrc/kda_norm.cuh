@@ -2,9 +2,10 @@
 //   gated norm     out = x rsqrt(mean x^2 + eps) w act(z), or the gate before the norm
 //   residual norm  r' = r + alpha ch act(z) n(x),  out = r' rsqrt(mean r'^2 + eps) w
 // HBM-bound: every row is read once into registers, reduced there, and written once. A group of
-// threads owns a row, eight channels per 16-byte access: up to 32 lanes for D <= 1024 (sums by
-// shuffles), a whole CTA above (sums through shared memory). Groups walk the rows of a grid that
-// fills the machine and load the next row before reducing the present one. Sums and the norm are fp32.
+// threads owns a row, eight channels per 16-byte access: up to 32 lanes (sums by shuffles) or a whole
+// CTA (sums through shared memory). Groups walk the rows of a grid that fills the machine; with one or
+// two vectors per thread the next row is loaded before the present one is reduced, with four or eight
+// a row's own loads are enough in flight. Sums and the norm are fp32.
 #pragma once
 #include "blk_common.cuh"
 
@@ -12,7 +13,8 @@ namespace kda {
 namespace norm {
 
 constexpr int WARP_THREADS = 128;  // CTA of the warp-group form
-constexpr int MAX_D = 16384;       // 1024 threads x 2 vectors of 8
+constexpr int CTA_THREADS = 512;   // most threads of the CTA form
+constexpr int MAX_D = 16384;       // CTA_THREADS x 4 vectors of 8
 
 // Threads that share a row, and where this thread stands among them. CTA: the whole block, with
 // two alternating rows of partial sums so that one barrier per sum is enough.
@@ -54,7 +56,7 @@ struct GatedParams {
 };
 
 template <int VPT, bool CTA>
-__global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_gated_norm_kernel(const GatedParams p)
+__global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_gated_norm_kernel(const GatedParams p)
 {
     __shared__ float part[2][32];
     Group<CTA> gr{CTA ? static_cast<int>(blockDim.x) : p.tpr, CTA ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (p.tpr - 1), part, 0};
@@ -72,10 +74,22 @@ __global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_gated_norm_kern
         for (int i = 0; i < 8; ++i) w[v][i] = 1.f;
         if (live[v] && p.w && p.w_rows == 1) blk::load8f(p.w + c[v], w[v]);
     }
+    constexpr bool AHEAD = VPT <= 2;  // the next row is loaded before the present one is reduced
     uint4 xn[VPT], zn[VPT];
-    auto fetch = [&](long long row) {
-        const long long m = row / p.R;
-        const int r = static_cast<int>(row - m * p.R);
+    // token and row of it, walked along without dividing
+    const long long step_m = step / p.R;
+    const int step_r = static_cast<int>(step - step_m * p.R);
+    long long m = first / p.R, fm = m;
+    int r = static_cast<int>(first - m * p.R), fr = r;
+    auto advance = [&](long long &mm, int &rr) {
+        mm += step_m;
+        rr += step_r;
+        if (rr >= p.R) {
+            rr -= p.R;
+            ++mm;
+        }
+    };
+    auto fetch = [&](long long row, long long m, int r) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             xn[v] = zn[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -85,17 +99,21 @@ __global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_gated_norm_kern
             }
         }
     };
-    fetch(first);
+    if (AHEAD) fetch(first, fm, fr);
     // every group of a warp makes the same number of steps (the shuffles need all lanes)
     for (long long base = static_cast<long long>(blockIdx.x) * per; base < p.rows; base += step) {
         const long long row = base + (first - static_cast<long long>(blockIdx.x) * per);
         float x[VPT][8], z[VPT][8], ss = 0.f;
+        if (!AHEAD) fetch(row, m, r);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             blk::unpack8(xn[v], x[v]);
             blk::unpack8(zn[v], z[v]);
         }
-        fetch(row + step);
+        if (AHEAD) {
+            advance(fm, fr);
+            fetch(row + step, fm, fr);
+        }
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -106,8 +124,6 @@ __global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_gated_norm_kern
             }
         const float inv = rsqrtf(fmaf(gr.sum(ss), inv_d, p.eps));
         if (row < p.rows) {
-            const long long m = row / p.R;
-            const int r = static_cast<int>(row - m * p.R);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 if (!live[v]) continue;
@@ -121,6 +137,7 @@ __global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_gated_norm_kern
                 *reinterpret_cast<uint4 *>(p.out + m * p.os + static_cast<long long>(r) * p.D + c[v]) = blk::pack8(o);
             }
         }
+        advance(m, r);
     }
 }
 
@@ -139,7 +156,7 @@ struct ResidualParams {
 
 // F32: the residual stream is fp32 (else bf16).
 template <int VPT, bool CTA, bool F32>
-__global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_residual_norm_kernel(const ResidualParams p)
+__global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_residual_norm_kernel(const ResidualParams p)
 {
     __shared__ float part[2][32];
     Group<CTA> gr{CTA ? static_cast<int>(blockDim.x) : p.tpr, CTA ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (p.tpr - 1), part, 0};
@@ -170,14 +187,17 @@ __global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_residual_norm_k
             }
         }
     };
-    fetch(static_cast<long long>(blockIdx.x) * per + sub);
+    constexpr bool AHEAD = VPT <= 2;
+    if (AHEAD) fetch(static_cast<long long>(blockIdx.x) * per + sub);
     for (long long base = static_cast<long long>(blockIdx.x) * per; base < p.rows; base += step) {
         const long long row = base + sub;
-        float x[VPT][8], z[VPT][8], r[VPT][8], ss = 0.f;
+        float x[VPT][8], r[VPT][8], ss = 0.f;
+        if (!AHEAD) fetch(row);
+        uint4 z[VPT];
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             blk::unpack8(xn[v], x[v]);
-            blk::unpack8(zn[v], z[v]);
+            z[v] = zn[v];
             if constexpr (F32) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -190,7 +210,7 @@ __global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_residual_norm_k
                 blk::unpack8(rn[v][0], r[v]);
             }
         }
-        fetch(row + step);
+        if (AHEAD) fetch(row + step);
         if (p.post) {
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
@@ -208,12 +228,13 @@ __global__ void __launch_bounds__(CTA ? 1024 : WARP_THREADS) kda_residual_norm_k
         ss = 0.f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            float ch[8];
+            float ch[8], zf[8];
             if (p.chan && live[v]) blk::load8f(p.chan + c[v], ch);
+            blk::unpack8(z[v], zf);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float u = x[v][i];
-                if (p.z) u *= blk::apply_act(z[v][i], p.act);
+                if (p.z) u *= blk::apply_act(zf[i], p.act);
                 if (p.chan) u *= ch[i];
                 r[v][i] = live[v] ? fmaf(p.alpha, u, r[v][i]) : 0.f;
                 ss = fmaf(r[v][i], r[v][i], ss);

@@ -376,7 +376,7 @@ typedef enum kda_act {
  * (oldest first), or zero.
  *   x, out   bf16 [B, T, C], token strides x_stride, out_stride; C a multiple
  *            of 8. out must not share an element with x (KDA_ERR_STATE_MISMATCH).
- *   weight   fp32 [C, W], W = 2, 3 or 4;  bias fp32 [C] or NULL.
+ *   weight   fp32 [C, W], W = 2, 3 or 4;  bias fp32 [C] or NULL (16-byte aligned).
  *   initial_state, final_state  bf16 [S, W - 1, C] or NULL (S = B, or N in
  *            varlen mode), contiguous; final_state receives the last W - 1
  *            rows of [initial_state ; x]. They may be the same buffer;
