@@ -37,8 +37,8 @@ for _f in ("kda_conv", "kda_conv_step", "kda_ssm", "kda_ssm_workspace_bytes", "k
     getattr(_lib, _f).restype = _I
 
 
-def _tensor(name, t, dev, dtypes, shape):
-    """Check a tensor's kind, device, type and shape."""
+def _refuse(name, t, dev, dtypes, shape):
+    """Say what is wrong with a tensor's kind, device, type or shape."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -47,8 +47,7 @@ def _tensor(name, t, dev, dtypes, shape):
         raise ValueError(f"{name} is on {t.device}, but x is on cuda:{dev}: all tensors must share one device")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _x_device(x, dims, layout):
@@ -63,12 +62,16 @@ def _x_device(x, dims, layout):
 def _rows(name, t, shape, lead, dev, dtypes=(_BF16,)):
     """Check an activation of the given shape; returns its address and the distance in elements
     between its tokens. The first ``lead`` dimensions are the token axes ([B, T] or [S])."""
-    _tensor(name, t, dev, dtypes, shape)
-    stride, width = t.stride(), 1
-    for i in range(len(stride) - 1, lead - 1, -1):
-        if shape[i] > 1 and stride[i] != width:
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.get_device() != dev:
+        _refuse(name, t, dev, dtypes, shape)
+    stride = t.stride()
+    width = shape[-1]
+    if stride[-1] != 1 and width > 1:
+        raise ValueError(f"{name}: the elements of one token must be contiguous")
+    if len(shape) == lead + 2:
+        if stride[-2] != width and shape[-2] > 1:
             raise ValueError(f"{name}: the elements of one token must be contiguous")
-        width *= shape[i]
+        width *= shape[-2]
     if lead == 1:
         step = stride[0] if shape[0] > 1 else width
     elif shape[1] > 1:
@@ -84,7 +87,8 @@ def _dense(name, t, dev, dtypes, shape):
     """Check an optional contiguous tensor (a parameter or a state); returns its address or None."""
     if t is None:
         return None
-    _tensor(name, t, dev, dtypes, shape)
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or (shape is not None and t.shape != shape) or t.get_device() != dev:
+        _refuse(name, t, dev, dtypes, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()

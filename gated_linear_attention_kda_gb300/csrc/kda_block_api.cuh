@@ -80,7 +80,7 @@ static kda_status launch_conv(const conv::ConvParams &q, cudaStream_t s)
     conv::ConvParams p = q;
     const int nc8 = p.C / 8;
     const int64_t states = p.fin ? (static_cast<int64_t>(p.nseq) * nc8 + conv::THREADS - 1) / conv::THREADS : 0;
-    const int64_t per = static_cast<int64_t>(conv::THREADS / p.cg) * conv::RUN;
+    const int64_t per = static_cast<int64_t>(conv::THREADS / p.cg) * p.run;
     p.tiles = (p.total + per - 1) / per;
     // in place, the final states are written once every block has read the initial ones
     const bool after = p.fin && p.fin == p.init && p.tiles > 0;
@@ -138,8 +138,10 @@ static kda_status check_ssm(const void *x, int64_t xs, const void *dt, int64_t d
     return KDA_OK;
 }
 
-// Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one.
-constexpr int64_t STEP_TOKENS = 16;
+// Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one: 8 heads of
+// 64, one sequence, 8 tokens 5.2 against 6.2 us, 16 tokens 7.8 against 6.3; 64 sequences of 16 heads of 128, 8
+// tokens 41 against 51 us, 16 tokens 74 against 53.
+constexpr int64_t STEP_TOKENS = 8;
 
 static kda_status launch_ssm_steps(const ssm::SsmParams &p, cudaStream_t s)
 {
@@ -243,8 +245,9 @@ static kda_status launch_ssm(const ssm::SsmParams &p, const SsmPlan &plan, float
 }
 
 // Threads along a row of D channels and vectors of eight per thread. Few rows (less than four per SM)
-// are bound by latency and get many threads each; many rows by bandwidth, and get few threads with
-// four or eight vectors each, whose loads are all in flight at once (TIMES).
+// are bound by latency and get many threads each (8 x 4096: 3.5 us); many rows by bandwidth, and get few
+// threads with up to four vectors each, whose loads are all in flight at once (residual norm of 32768 x
+// 2048: 91 us on 64 threads x 4, 108 us on 128 x 2 with the next row ahead, 111 us on a warp x 8).
 struct RowShape {
     bool cta;
     int threads, vpt;
@@ -257,9 +260,9 @@ static RowShape row_shape(int64_t D, int64_t rows, int sms)
         while (t < v) t <<= 1;
         return {false, t, 1};
     }
-    auto vectors = [](int n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8; };
+    auto vectors = [](int n) { return n <= 1 ? 1 : n <= 2 ? 2 : 4; };
     const bool many = rows >= 4 * static_cast<int64_t>(sms);
-    if (v <= (many ? 256 : 64)) return {false, 32, vectors((v + 31) / 32)};
+    if (v <= (many ? 128 : 64)) return {false, 32, vectors((v + 31) / 32)};
     const int vpt = many || v > 2 * norm::CTA_THREADS ? 4 : 2;
     return {true, (((v + vpt - 1) / vpt) + 31) / 32 * 32, vpt};
 }
@@ -338,6 +341,12 @@ KDA_API kda_status kda_conv(const void *x, int64_t x_stride, const float *weight
     p.act = act;
     p.cg = 1;
     while (p.cg < 32 && p.cg < C / 8) p.cg <<= 1;  // a warp along the channels, so that little of the last block idles
+    // tokens per thread: as many as leave 512 threads for every SM, between one batch and MAX_RUN (8 x 4096 x
+    // 2048 channels: 57.2 us at 32, 55.2 us at 64; a run's first W - 1 rows are read twice)
+    blk::Device d;
+    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+    const int64_t run = total * (C / 8) / (512 * static_cast<int64_t>(d.sms)) / conv::BATCH * conv::BATCH;
+    p.run = static_cast<int>(std::min<int64_t>(std::max<int64_t>(run, conv::BATCH), conv::MAX_RUN));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return W == 2 ? blk::launch_conv<2>(p, s) : W == 3 ? blk::launch_conv<3>(p, s) : blk::launch_conv<4>(p, s);
 }
@@ -527,8 +536,7 @@ KDA_API kda_status kda_gated_norm(const void *x, int64_t x_stride, const void *g
     if (sh.cta) return sh.vpt == 2 ? blk::launch_gated<2, true>(p, sh, d, s) : blk::launch_gated<4, true>(p, sh, d, s);
     return sh.vpt == 1   ? blk::launch_gated<1, false>(p, sh, d, s)
            : sh.vpt == 2 ? blk::launch_gated<2, false>(p, sh, d, s)
-           : sh.vpt == 4 ? blk::launch_gated<4, false>(p, sh, d, s)
-                         : blk::launch_gated<8, false>(p, sh, d, s);
+                         : blk::launch_gated<4, false>(p, sh, d, s);
 }
 
 KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
@@ -586,8 +594,7 @@ KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void
     if (sh.cta) return sh.vpt == 2 ? blk::launch_residual<2, true>(p, f32, sh, d, s) : blk::launch_residual<4, true>(p, f32, sh, d, s);
     return sh.vpt == 1   ? blk::launch_residual<1, false>(p, f32, sh, d, s)
            : sh.vpt == 2 ? blk::launch_residual<2, false>(p, f32, sh, d, s)
-           : sh.vpt == 4 ? blk::launch_residual<4, false>(p, f32, sh, d, s)
-                         : blk::launch_residual<8, false>(p, f32, sh, d, s);
+                         : blk::launch_residual<4, false>(p, f32, sh, d, s);
 }
 
 }  // extern "C"

@@ -4,7 +4,7 @@
 // with the rows of the initial state (or zeros) before a sequence's first token.
 //
 // HBM-bound: 2 bytes in and 2 out per element against W FMAs and one sigmoid. A thread owns eight
-// channels (one 16-byte access per token) and walks RUN tokens of them with the last W - 1 rows in
+// channels (one 16-byte access per token) and walks a run of tokens of them with the last W - 1 rows in
 // registers, so a row is read once per run plus the W - 1 rows before it; the BATCH rows of the next
 // step are loaded before those of the present one are filtered. Arithmetic is in fp32 pairs.
 #pragma once
@@ -14,8 +14,8 @@ namespace kda {
 namespace conv {
 
 constexpr int THREADS = 128;
-constexpr int RUN = 32;    // tokens per thread
-constexpr int BATCH = 4;   // rows in flight per thread
+constexpr int MAX_RUN = 64;  // tokens per thread at most
+constexpr int BATCH = 4;     // rows in flight per thread
 
 struct ConvParams {
     const uint16_t *x, *init;
@@ -27,6 +27,7 @@ struct ConvParams {
     long long tiles;        // blocks of the token axis (the blocks after them write final states)
     int nseq, C, act;
     int cg;                 // threads along the channels (a power of two <= THREADS)
+    int run;                // tokens per thread
 };
 
 // Eight channels as four pairs (paired fp32 arithmetic).
@@ -108,7 +109,7 @@ __device__ __forceinline__ void write_final(const ConvParams &p, int seq, int c)
 }
 
 template <int W>
-__global__ void __launch_bounds__(THREADS) kda_conv_kernel(const ConvParams p)
+__global__ void __launch_bounds__(THREADS, 4) kda_conv_kernel(const ConvParams p)
 {
     if (p.cu && blockIdx.x == 0 && blockIdx.y == 0) blk::check_bounds(p.cu, p.nseq, p.total);
     const int nc8 = p.C >> 3;
@@ -122,8 +123,8 @@ __global__ void __launch_bounds__(THREADS) kda_conv_kernel(const ConvParams p)
     const int c8 = blockIdx.y * p.cg + (threadIdx.x & (p.cg - 1));
     if (c8 >= nc8) return;
     const int c = 8 * c8, tg = THREADS / p.cg;
-    long long t = (static_cast<long long>(blockIdx.x) * tg + threadIdx.x / p.cg) * RUN;
-    const long long t_end = min(t + RUN, p.total);
+    long long t = (static_cast<long long>(blockIdx.x) * tg + threadIdx.x / p.cg) * p.run;
+    const long long t_end = min(t + p.run, p.total);
     Taps<W> taps;
     taps.load(p.weight, p.bias, c);
     const bool silu = p.act == KDA_ACT_SILU;

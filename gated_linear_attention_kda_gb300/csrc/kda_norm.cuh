@@ -4,8 +4,8 @@
 // HBM-bound: every row is read once into registers, reduced there, and written once. A group of
 // threads owns a row, eight channels per 16-byte access: up to 32 lanes (sums by shuffles) or a whole
 // CTA (sums through shared memory). Groups walk the rows of a grid that fills the machine; with one or
-// two vectors per thread the next row is loaded before the present one is reduced, with four or eight
-// a row's own loads are enough in flight. Sums and the norm are fp32.
+// two vectors per thread the next row is loaded before the present one is reduced, with four a row's own
+// loads are enough in flight. Sums and the norm are fp32.
 #pragma once
 #include "blk_common.cuh"
 
