@@ -29,13 +29,13 @@
 // (as a shared-memory operand it cost 160 KB more and the kernel ran at 148.7 us where it now takes
 // TIME_HERE, 8 x 4096 tokens of 16 heads).
 //
-// Warp roles (1024 threads; the column work of a tensor-memory row is shared by two warps):
-//   warp 0       TMA producer (lane 0): x and b tiles two deep, c one; tensor memory allocation
+// Warp roles (1024 threads):
+//   warp 0       TMA producer (lane 0): x tiles two or three deep, b two, c one or two; tensor memory allocation
 //   warp 1       MMA issuer: scores and outputs
 //   warp 2       step sizes, running sums and decays of a chunk, one chunk ahead
 //   warp 3       MMA issuer: state
-//   warps 4-7    scores G -> M (thread = token)
-//   warps 8-15   row scaling of C S0^T, then the output rows (thread = token and half of the columns)
+//   warps 4-11   scores G -> M (thread = token, two of the four 32-token blocks)
+//   warps 12-15  row scaling of C S0^T, then the output rows (thread = token)
 //   warps 16-23  state: bf16 copy for the next product, decay in place (state channel, half of the columns)
 //   warps 24-31  w B, 32 tokens at a time (16 state channels per warp)
 // MMA order per chunk: C S0^T, the state product, M X, and the next chunk's C B^T, so that the tensor
@@ -55,7 +55,6 @@ constexpr int L = 128;          // tokens per chunk
 constexpr int SUB = 32;         // tokens per w B block (two MMA steps)
 constexpr int NTHREADS = 1024;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t T_G = 0, T_Y = 128;
 
 struct TcParams {
     ssm::SsmParams p;
@@ -65,24 +64,28 @@ struct TcParams {
     float *ws;                  // [slots, H, P, NS] states, then [slots, H] log2 decays
 };
 
-// per-chunk scalars, two buffers: running log2 sums inside 32-token blocks, delta, delta 2^(rest of
-// the block), w, block totals
-constexpr int SC_LOC = 0, SC_DELTA = 512, SC_ES = 1024, SC_W = 1536, SC_TOT = 2048, SC_BYTES = 2112;
+// per-chunk scalars, two buffers: running log2 sums inside 32-token blocks, the same less log2 delta,
+// delta 2^(rest of the block), w, block totals
+constexpr int SC_LOC = 0, SC_LD = 512, SC_ES = 1024, SC_W = 1536, SC_TOT = 2048, SC_BYTES = 2112;
 
 template <int P, int PARTS, bool FULL>
 struct Layout {
     static constexpr int BOX = L * 128;            // 64 channels x 128 rows, 128-byte swizzle
     static constexpr int XT = P / 64 * BOX, BT = 2 * BOX;
-    static constexpr int NSLOT = P == 128 && PARTS == 3 ? 2 : 4;  // w B buffers of PARTS x 16 columns
-    static constexpr int X = 0;                    // two stages
-    static constexpr int B = X + 2 * XT;           // two stages
+    static constexpr int NSLOT = PARTS == 3 && P == 128 ? 2 : 4;  // w B buffers of PARTS x 16 columns
+    static constexpr int CS = P == 64 ? 2 : 1;     // c tiles in flight
+    static constexpr int XS = P == 64 ? 3 : 2;     // x tiles in flight (a tile is also its chunk's output buffer)
+    static constexpr int X = 0;
+    static constexpr int B = X + XS * XT;          // two stages
     static constexpr int C = B + 2 * BT;
-    static constexpr int H = C + (FULL ? BT : 0);  // bf16 state, [n][p]
+    static constexpr int H = C + (FULL ? CS * BT : 0);  // bf16 state, [n][p]
     static constexpr int SC = H + (FULL ? XT : 0);
     static constexpr int BAR = SC + 2 * SC_BYTES;
-    static constexpr int X_FULL = 0, X_EMPTY = 2, B_FULL = 4, B_EMPTY = 6, C_FULL = 8, C_EMPTY = 9, SC_FULL = 10, SC_EMPTY = 12,
-                         G_DONE = 14, M_DONE = 15, YX_DONE = 16, SCALED = 17, Y_DONE = 18, Y_FREE = 19, H_READY = 20, S_DONE = 21,
-                         END = 23, W_FULL = 24, W_EMPTY = 28, X_ZERO = 32, END2 = 33, X_READ = 34, NBARS = 36;
+    // YX_GO: the bf16 state is there and Y has been read; M_GO: M is there and Y is scaled; S_GO: the state is
+    // decayed; ST_GO: both products of the old state are done; OUT_GO: both products of an x tile are done
+    static constexpr int X_FULL = 0, X_EMPTY = 3, OUT_GO = 6, B_FULL = 9, B_EMPTY = 11, C_FULL = 13, C_EMPTY = 15, SC_FULL = 17,
+                         SC_EMPTY = 19, G_DONE = 21, M_GO = 22, YX_DONE = 23, Y_DONE = 24, YX_GO = 25, S_GO = 26, ST_GO = 27,
+                         X_ZERO = 28, END = 29, END2 = 30, W_FULL = 31, W_EMPTY = 35, NBARS = 40;
     static constexpr int TMEMPTR = BAR + NBARS * 8;
     static constexpr int FLAGS = TMEMPTR + 16;
     static constexpr int ALLOC = FLAGS + 16 + 1024;
@@ -172,7 +175,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                       const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap to, const TcParams t)
 {
     using Lay = Layout<P, PARTS, FULL>;
-    constexpr uint32_t T_S = T_Y + P, T_W = T_Y + 2 * P;
+    constexpr int CS = Lay::CS, XS = Lay::XS;
+    constexpr uint32_t T_G = 0, T_Y = FULL ? 128 : 0, T_S = T_Y + (FULL ? P : 0), T_W = T_S + P;
     static_assert(T_W + Lay::NSLOT * PARTS * (SUB / 2) <= TMEM_COLS, "tensor memory budget");
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
@@ -196,8 +200,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
     auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
-    auto xt = [&](int n) { return sb + Lay::X + (n & 1) * Lay::XT; };
+    auto xt = [&](int n) { return sb + Lay::X + (n % XS) * Lay::XT; };
     auto bt = [&](int n) { return sb + Lay::B + (n & 1) * Lay::BT; };
+    auto ct = [&](int n) { return sb + Lay::C + (n % CS) * Lay::BT; };
     auto sc = [&](int n) { return sb + Lay::SC + (n & 1) * SC_BYTES; };
     auto live_of = [&](int n) { return min(L, pc.len - n * L); };
 
@@ -206,18 +211,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc::relinquish();
     }
     if (threadIdx.x == 32) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < XS; ++i) {
             mbar_init(bar(Lay::X_FULL + i), 1);
-            mbar_init(bar(Lay::X_EMPTY + i), FULL ? 8 : 1);
-            mbar_init(bar(Lay::X_READ + i), 1);
+            mbar_init(bar(Lay::X_EMPTY + i), FULL ? 4 : 1);
+            mbar_init(bar(Lay::OUT_GO + i), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(Lay::B_FULL + i), 1);
             mbar_init(bar(Lay::B_EMPTY + i), FULL ? 9 : 8);  // the w B warps, and the score product
+            mbar_init(bar(Lay::C_FULL + i), 1);
+            mbar_init(bar(Lay::C_EMPTY + i), 1);
             mbar_init(bar(Lay::SC_FULL + i), 1);
             mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 28 : 16);
         }
-        for (int i : {Lay::C_FULL, Lay::C_EMPTY, Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::S_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
-        mbar_init(bar(Lay::M_DONE), 4);
-        for (int i : {Lay::SCALED, Lay::Y_FREE, Lay::H_READY, Lay::X_ZERO}) mbar_init(bar(i), 8);
+        for (int i : {Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
+        for (int i : {Lay::S_GO, Lay::X_ZERO}) mbar_init(bar(i), 8);
+        for (int i : {Lay::M_GO, Lay::YX_GO}) mbar_init(bar(i), 12);
+        mbar_init(bar(Lay::ST_GO), FULL ? 2 : 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(Lay::W_FULL + i), 8);
             mbar_init(bar(Lay::W_EMPTY + i), 1);
@@ -235,9 +245,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         atomicOr(&g_dev_error, DEVERR_TIMEOUT);
         flags[0] = 1;
     }
-    // the whole warp goes on only when every lane saw the phase
+    // the whole warp goes on only when every lane saw the phase (a wait on a phase that is over already costs
+    // about 100 cycles, so the roles' critical waits are few)
     auto wait_w = [&](int b, uint32_t par) {
-        const bool ok = __all_sync(0xffffffffu, wait_bar(bar(b), par, flags));
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), par))) return true;
+        const bool ok = __all_sync(0xffffffffu, wait_bar_slow(bar(b), par, flags));
         __syncwarp();
         return ok;
     };
@@ -261,23 +273,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) tma_load_3d(bt(n) + k * Lay::BOX, &tb, 64 * k, grp, tok, bar(Lay::B_FULL + s));
                 ++nb;
-                if (!wait_bar(bar(Lay::X_EMPTY + s), par, flags)) break;
-                mbar_arrive_expect_tx(bar(Lay::X_FULL + s), Lay::XT);
-#pragma unroll
-                for (int k = 0; k < P / 64; ++k) tma_load_3d(xt(n) + k * Lay::BOX, &tx, 64 * k, h, tok, bar(Lay::X_FULL + s));
-                ++nx;
                 if constexpr (FULL) {
-                    if (n > 0 && !wait_bar(bar(Lay::C_EMPTY), (n - 1) & 1, flags)) break;
-                    mbar_arrive_expect_tx(bar(Lay::C_FULL), Lay::BT);
+                    if (!wait_bar(bar(Lay::C_EMPTY + n % CS), ((n / CS) & 1) ^ 1, flags)) break;
+                    mbar_arrive_expect_tx(bar(Lay::C_FULL + n % CS), Lay::BT);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) tma_load_3d(sb + Lay::C + k * Lay::BOX, &tcm, 64 * k, grp, tok, bar(Lay::C_FULL));
+                    for (int k = 0; k < 2; ++k) tma_load_3d(ct(n) + k * Lay::BOX, &tcm, 64 * k, grp, tok, bar(Lay::C_FULL + n % CS));
                     ++ncc;
                 }
+                const int xs = n % XS;
+                if (!wait_bar(bar(Lay::X_EMPTY + xs), ((n / XS) & 1) ^ 1, flags)) break;
+                mbar_arrive_expect_tx(bar(Lay::X_FULL + xs), Lay::XT);
+#pragma unroll
+                for (int k = 0; k < P / 64; ++k) tma_load_3d(xt(n) + k * Lay::BOX, &tx, 64 * k, h, tok, bar(Lay::X_FULL + xs));
+                ++nx;
             }
             // no copy is in flight when the CTA ends, whichever way the loop was left
             for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) drain_bar(bar(Lay::B_FULL + (m & 1)), (m >> 1) & 1);
-            for (int m = nx > 2 ? nx - 2 : 0; m < nx; ++m) drain_bar(bar(Lay::X_FULL + (m & 1)), (m >> 1) & 1);
-            if (ncc > 0) drain_bar(bar(Lay::C_FULL), (ncc - 1) & 1);
+            for (int m = nx > XS ? nx - XS : 0; m < nx; ++m) drain_bar(bar(Lay::X_FULL + m % XS), (m / XS) & 1);
+            for (int m = ncc > CS ? ncc - CS : 0; m < ncc; ++m) drain_bar(bar(Lay::C_FULL + m % CS), (m / CS) & 1);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer: scores and outputs (whole warp)
@@ -285,18 +298,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             constexpr uint32_t id_g = tc::idesc(tc::BF16, 128, 128, 0, 0);
             constexpr uint32_t id_y = tc::idesc(tc::BF16, 128, P, 0, 1);
             constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B);
-            const uint32_t dc = tc::sdesc_lo(sb + Lay::C, 16), dh = tc::sdesc_lo(sb + Lay::H, Lay::BOX);
+            const uint32_t dh = tc::sdesc_lo(sb + Lay::H, Lay::BOX);
             auto kmaj = [&](uint32_t lo, int i) {  // K step i of a K-major tile (two boxes of 64 channels)
                 return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(((i >> 2) * Lay::BOX + (i & 3) * 32) >> 4));
             };
             auto nmaj = [&](uint32_t lo, int i) {  // K step i (16 rows) of an MN-major tile
                 return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(i * ((16 * 128) >> 4)));
             };
-            auto issue_g = [&](int n) {
-                if (!wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::C_FULL, n & 1)) return false;
-                if (n > 0 && !wait_w(Lay::Y_DONE, (n - 1) & 1)) return false;  // M of the last chunk has been read
+            auto issue_g = [&](int n) {  // its tensor memory holds the M of the last chunk until that has been read
+                if (!wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::C_FULL + n % CS, (n / CS) & 1)) return false;
+                if (n > 0 && !wait_w(Lay::Y_DONE, (n - 1) & 1)) return false;
                 tc::fence_after();
-                const uint32_t db = tc::sdesc_lo(bt(n), 16);
+                const uint32_t dc = tc::sdesc_lo(ct(n), 16), db = tc::sdesc_lo(bt(n), 16);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_G, kmaj(dc, i), kmaj(db, i), id_g, i > 0);
                 tc::commit_w(bar(Lay::G_DONE));
@@ -305,22 +318,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             };
             bool ok = issue_g(0);
             for (int n = 0; ok && n < nch; ++n) {
-                const uint32_t dx = tc::sdesc_lo(xt(n), Lay::BOX);
+                const uint32_t dx = tc::sdesc_lo(xt(n), Lay::BOX), dc = tc::sdesc_lo(ct(n), 16);
                 // Y = C S0^T, over the accumulator whose last values have been read
-                ok = wait_w(Lay::H_READY, n & 1) && (n == 0 || wait_w(Lay::Y_FREE, (n - 1) & 1));
+                ok = wait_w(Lay::X_FULL + n % XS, (n / XS) & 1) && wait_w(Lay::YX_GO, n & 1);
                 if (!ok) break;
                 tc::fence_after();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_Y, kmaj(dc, i), nmaj(dh, i), id_y, i > 0);
                 tc::commit_w(bar(Lay::YX_DONE));
-                tc::commit_w(bar(Lay::C_EMPTY));
+                tc::commit_w(bar(Lay::ST_GO));
+                tc::commit_w(bar(Lay::C_EMPTY + n % CS));
                 // Y += M X
-                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1) && (live_of(n) == L || wait_w(Lay::X_ZERO, 0)) &&
-                     wait_w(Lay::M_DONE, n & 1) && wait_w(Lay::SCALED, n & 1);
+                ok = (live_of(n) == L || wait_w(Lay::X_ZERO, 0)) && wait_w(Lay::M_GO, n & 1);
                 if (!ok) break;
                 tc::fence_after();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_Y, tmem + T_G + 8 * i, nmaj(dx, i), id_y, 1);
+                for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_Y, tmem + T_G + 64 * (i >> 2) + 8 * (i & 3), nmaj(dx, i), id_y, 1);
+                tc::commit_w(bar(Lay::OUT_GO + n % XS));
                 tc::commit_w(bar(Lay::Y_DONE));
                 if (n + 1 < nch) ok = issue_g(n + 1);
             }
@@ -373,7 +387,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (!wait_w(Lay::SC_EMPTY + (n & 1), ((n >> 1) & 1) ^ 1)) break;
             const uint32_t o = sc(n) + 4 * j0;
             SM_AT(float4, o + SC_LOC) = make_float4(before + l0, before + l1, before + l2, before + l3);
-            SM_AT(float4, o + SC_DELTA) = make_float4(d[0], d[1], d[2], d[3]);
+            // running sum less log2 delta (delta 0: no score at all)
+            SM_AT(float4, o + SC_LD) = make_float4(before + l0 - lg2_approx(d[0]), before + l1 - lg2_approx(d[1]), before + l2 - lg2_approx(d[2]), before + l3 - lg2_approx(d[3]));
             SM_AT(float4, o + SC_ES) = make_float4(d[0] * ex2_approx(sf[0]), d[1] * ex2_approx(sf[1]), d[2] * ex2_approx(sf[2]), d[3] * ex2_approx(sf[3]));
             SM_AT(float4, o + SC_W) = make_float4(d[0] * ex2_approx(sf[0] + rest), d[1] * ex2_approx(sf[1] + rest),
                                                   d[2] * ex2_approx(sf[2] + rest), d[3] * ex2_approx(sf[3] + rest));
@@ -391,10 +406,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int n = 0; ok && n < nch; ++n) {
                 const int nsub = (live_of(n) + SUB - 1) / SUB;
                 uint32_t dx = tc::sdesc_lo(xt(n), Lay::BOX);
-                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::H_READY, n & 1);
+                // (the first block's wait comes before the one that is on the chain)
+                ok = wait_w(Lay::X_FULL + n % XS, (n / XS) & 1) && wait_w(Lay::W_FULL + k % Lay::NSLOT, (k / Lay::NSLOT) & 1) && wait_w(Lay::S_GO, n & 1);
                 for (int s = 0; ok && s < nsub; ++s, ++k, dx += (SUB * 128) >> 4) {
                     const int sl = k % Lay::NSLOT;
-                    ok = wait_w(Lay::W_FULL + sl, (k / Lay::NSLOT) & 1);
+                    ok = s == 0 || wait_w(Lay::W_FULL + sl, (k / Lay::NSLOT) & 1);
                     if (!ok) break;
                     tc::fence_after();
                     const uint32_t wb = tmem + T_W + sl * (PARTS * (SUB / 2));
@@ -406,85 +422,95 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tc::commit_w(bar(Lay::W_EMPTY + sl));
                 }
                 if (!ok) break;
-                tc::commit_w(bar(Lay::S_DONE));
-                tc::commit_w(bar((FULL ? Lay::X_READ : Lay::X_EMPTY) + (n & 1)));
+                tc::commit_w(bar(Lay::ST_GO));
+                tc::commit_w(bar((FULL ? Lay::OUT_GO : Lay::X_EMPTY) + n % XS));
             }
             tc::commit_w(bar(Lay::END2));
             if (lane == 0) drain_bar(bar(Lay::END2), 0);
             __syncwarp();
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ---------------------------------------------------------------- scores
         if constexpr (FULL) {
-            const int q = warp & 3, row = 32 * q + lane;
-            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_G;
+            // This thread's columns are blocks 2 hf and 2 hf + 1 of its token's row; M is written over columns
+            // of G that it has read itself (the product takes M's halves from columns 0 and 64).
+            const int q = warp & 3, row = 32 * q + lane, hf = warp < 8 ? 0 : 1;
+            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_G + 64 * hf;
             const float Dh = p.D ? __ldg(p.D + h) : 0.f;
+            const int nfull = min(max(2 * (q - 2 * hf), 0), 4), nlive = min(max(2 * (q - 2 * hf) + 2, 0), 4);
             for (int n = 0; n < nch; ++n) {
-                if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::G_DONE, n & 1)) break;
+                if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1)) break;
+                const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
+                const float loc = SM_AT(const float, sc(n) + SC_LOC + 4 * row);
+                // log2 decay from the end of the second and of the first block to this row
+                const float l1 = loc + (q == 3 && hf == 0 ? tot.z : 0.f);
+                const float e1 = ex2_approx(l1), e0 = ex2_approx(l1 + (q >= 2 && hf == 0 ? tot.y : 0.f));
+                uint32_t s = sc(n) + 256 * hf;
+                if (!wait_w(Lay::G_DONE, n & 1)) break;
                 tc::fence_after();
-                const uint32_t s = sc(n);
-                const float4 tot = SM_AT(const float4, s + SC_TOT);
-                const float loc = SM_AT(const float, s + SC_LOC + 4 * row);
-                // M is written over columns of G that have been read, 16 columns at a time
 #pragma unroll 1
-                for (int b = 0; b < 2 * q; ++b) {
+                for (int b = 0; b < nfull; ++b) {
                     uint32_t g[16], m[8];
                     tc::ld16(lb + 16 * b, g);
-                    // log2 decay from the end of the block to this row
-                    const float e = ex2_approx(loc + (b < 2 && q > 1 ? tot.y : 0.f) + (b < 4 && q > 2 ? tot.z : 0.f));
+                    const float2 e = b < 2 ? make_float2(e0, e0) : make_float2(e1, e1);
+                    float2 u[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 v = SM_AT(const float4, s + SC_ES + 64 * b + 16 * i);
+                        u[2 * i] = fmul2(make_float2(v.x, v.y), e);
+                        u[2 * i + 1] = fmul2(make_float2(v.z, v.w), e);
+                    }
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 v = SM_AT(const float4, s + SC_ES + 64 * b + 4 * i);
-                        const float2 u0 = fmul2(make_float2(v.x, v.y), make_float2(e, e)), u1 = fmul2(make_float2(v.z, v.w), make_float2(e, e));
-                        const float2 o0 = fmul2(u0, make_float2(__uint_as_float(g[i]), __uint_as_float(g[i + 1])));
-                        const float2 o1 = fmul2(u1, make_float2(__uint_as_float(g[i + 2]), __uint_as_float(g[i + 3])));
-                        m[i / 2] = pack_bf16(o0.x, o0.y);
-                        m[i / 2 + 1] = pack_bf16(o1.x, o1.y);
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 o = fmul2(u[i], make_float2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1])));
+                        m[i] = pack_bf16(o.x, o.y);
                     }
                     tc::st8(lb + 8 * b, m);
                 }
 #pragma unroll 1
-                for (int b = 2 * q; b < 2 * q + 2; ++b) {
+                for (int b = nfull; b < nlive; ++b) {
                     uint32_t g[16], m[8];
                     tc::ld16(lb + 16 * b, g);
                     const int col = lane - 16 * (b & 1);  // this row's own column in the piece
-                    tc::wait_ld();
+                    float w[16];
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
-                        const float4 v = SM_AT(const float4, s + SC_LOC + 64 * b + 4 * i);
-                        const float4 d = SM_AT(const float4, s + SC_DELTA + 64 * b + 4 * i);
-                        const float lv[4] = {v.x, v.y, v.z, v.w}, dv[4] = {d.x, d.y, d.z, d.w};
-                        float o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x = __uint_as_float(g[i + k]) * (dv[k] * ex2_approx(loc - lv[k]));
-                            o[k] = (i + k <= col ? x : 0.f) + (i + k == col ? Dh : 0.f);
-                        }
-                        m[i / 2] = pack_bf16(o[0], o[1]);
-                        m[i / 2 + 1] = pack_bf16(o[2], o[3]);
+                        const float4 v = SM_AT(const float4, s + SC_LD + 64 * b + 4 * i);
+                        w[i] = ex2_approx(loc - v.x);
+                        w[i + 1] = ex2_approx(loc - v.y);
+                        w[i + 2] = ex2_approx(loc - v.z);
+                        w[i + 3] = ex2_approx(loc - v.w);
                     }
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x = w[i] * __uint_as_float(g[i]);
+                        if (i == col) x += Dh;
+                        w[i] = i <= col ? x : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
                     tc::st8(lb + 8 * b, m);
                 }
-                if (q < 3) {
-                    uint32_t z[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = 0u;
+                if (nlive < 4) {
+                    const uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll 1
-                    for (int b = q + 1; b < 4; ++b) tc::st16(lb + 16 * b, z);
+                    for (int b = nlive; b < 4; ++b) tc::st8(lb + 8 * b, z);
                 }
                 tc::wait_st();
                 tc::fence_before();
-                arrive_w(Lay::M_DONE);
+                arrive_w(Lay::M_GO);
                 arrive_w(Lay::SC_EMPTY + (n & 1));
             }
         }
     } else if (warp < 16) {
         // ---------------------------------------------------------------- outputs
         if constexpr (FULL) {
-            const int q = warp & 3, row = 32 * q + lane, c0 = (warp < 12 ? 0 : P / 2);  // this thread's columns
-            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y + c0;
-            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P + c0;
+            const int q = warp & 3, row = 32 * q + lane;
+            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y;
+            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P;
+            arrive_w(Lay::YX_GO);  // nothing of Y is waiting to be read
             for (int n = 0; n < nch; ++n) {
                 if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1)) break;
                 // decay from the chunk's start to this row
@@ -494,7 +520,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 if (!wait_w(Lay::YX_DONE, n & 1)) break;
                 tc::fence_after();
 #pragma unroll 1
-                for (int g4 = 0; g4 < P / 64; ++g4) {
+                for (int g4 = 0; g4 < P / 32; ++g4) {
                     uint32_t y[32];
                     tc::ld32(lb + 32 * g4, y);
                     tc::wait_ld();
@@ -508,44 +534,50 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 tc::wait_st();
                 tc::fence_before();
-                arrive_w(Lay::SCALED);
-                if (!wait_w(Lay::Y_DONE, n & 1)) break;
+                arrive_w(Lay::M_GO);
+                // the x tile is the output's buffer once both products have read it
+                if (!wait_w(Lay::OUT_GO + n % XS, (n / XS) & 1)) break;
                 tc::fence_after();
-                uint32_t o[P / 4];
-#pragma unroll
-                for (int g = 0; g < P / 32; ++g) {
-                    uint32_t y[16];
-                    tc::ld16(lb + 16 * g, y);
+                const bool whole = live_of(n) == L;
+                const uint32_t xr = xt(n) + row * 128;
+#pragma unroll 1
+                for (int g4 = 0; g4 < P / 32; ++g4) {
+                    uint32_t y[32];
+                    tc::ld32(lb + 32 * g4, y);
                     tc::wait_ld();
+                    const uint32_t box = xr + (g4 >> 1) * Lay::BOX;
+                    if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[8 * g + i] = pack_bf16(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+                        for (int i = 0; i < 4; ++i)  // eight channels: 16 bytes, swizzled by the row
+                            SM_AT(uint4, box + (((4 * (g4 & 1) + i) ^ (row & 7)) << 4)) =
+                                make_uint4(pack_bf16(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
+                                           pack_bf16(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
+                                           pack_bf16(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
+                                           pack_bf16(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
+                    } else if (row < live_of(n)) {  // a ragged end is stored from registers
+                        uint4 *dst = reinterpret_cast<uint4 *>(op + static_cast<long long>(n) * L * p.os + 32 * g4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(pack_bf16(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
+                                                pack_bf16(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
+                                                pack_bf16(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
+                                                pack_bf16(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
+                    }
                 }
                 tc::fence_before();
-                arrive_w(Lay::Y_FREE);
-                const int Lv = live_of(n);
-                if (Lv == L) {
-                    // the x tile is the output's buffer once the state product has read it too
-                    if (!wait_w(Lay::X_READ + (n & 1), (n >> 1) & 1)) break;
-                    const uint32_t xr = xt(n) + row * 128;
-#pragma unroll
-                    for (int i = 0; i < P / 16; ++i) {  // eight channels: 16 bytes, swizzled by the row
-                        const int c8 = (c0 >> 3) + i;
-                        SM_AT(uint4, xr + (c8 >> 3) * Lay::BOX + (((c8 & 7) ^ (row & 7)) << 4)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
+                arrive_w(Lay::YX_GO);
+                if (whole) {
                     tc::fence_async_smem();
-                    // a warp stores its 32 tokens; of 64 channels, where a box holds both halves, for both
-                    if (P == 64) named_bar_sync(1 + q, 64);
-                    if (lane == 0 && (P == 128 || warp < 12)) {
-                        tma_store_3d(&to, xt(n) + (c0 >> 6) * Lay::BOX + 32 * q * 128, c0, h, pc.bos + n * L + 32 * q);
+                    __syncwarp();
+                    if (lane == 0) {  // a warp stores its 32 tokens
+#pragma unroll
+                        for (int k = 0; k < P / 64; ++k)
+                            tma_store_3d(&to, xt(n) + k * Lay::BOX + 32 * q * 128, 64 * k, h, pc.bos + n * L + 32 * q);
                         bulk_commit();
                         bulk_wait_read();
                     }
-                } else if (row < Lv) {  // a ragged end is stored from registers
-                    uint4 *dst = reinterpret_cast<uint4 *>(op + static_cast<long long>(n) * L * p.os);
-#pragma unroll
-                    for (int i = 0; i < P / 16; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
-                arrive_w(Lay::X_EMPTY + (n & 1));
+                arrive_w(Lay::X_EMPTY + n % XS);
             }
             if (lane == 0) bulk_wait_all();
         }
@@ -575,12 +607,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
             ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1);
-            if (ok && n > 0) ok = wait_w(Lay::S_DONE, (n - 1) & 1) && (!FULL || wait_w(Lay::YX_DONE, (n - 1) & 1));  // the bf16 copy has been read
             if (!ok) break;
-            tc::fence_after();
             const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
             const float gam = ex2_approx((tot.x + tot.y) + (tot.z + tot.w));
             arrive_w(Lay::SC_EMPTY + (n & 1));
+            if (n > 0) ok = wait_w(Lay::ST_GO, (n - 1) & 1);
+            if (!ok) break;
+            tc::fence_after();
 #pragma unroll 1
             for (int g4 = 0; g4 < P / 64; ++g4) {
                 uint32_t r[32];
@@ -608,12 +641,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::wait_st();
             tc::fence_before();
             tc::fence_async_smem();
-            arrive_w(Lay::H_READY);
+            arrive_w(Lay::S_GO);
+            if constexpr (FULL) arrive_w(Lay::YX_GO);
         }
         const bool write = FULL ? (pc.last && p.fin) : true;
         if (ok && write) {
             if (nch > 0) {
-                ok = wait_w(Lay::S_DONE, (nch - 1) & 1);
+                ok = wait_w(Lay::ST_GO, (nch - 1) & 1);
                 tc::fence_after();
             }
 #pragma unroll 1
@@ -656,7 +690,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1);
             if (ok && Lv < L) {
                 // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
-                ok = wait_w(Lay::X_FULL + (n & 1), (n >> 1) & 1);
+                ok = wait_w(Lay::X_FULL + n % XS, (n / XS) & 1);
                 if (ok)
                     for (int i = u; i < (L - Lv) * (P / 8); i += 256) {
                         const int r = Lv + i / (P / 8), c8 = i % (P / 8);

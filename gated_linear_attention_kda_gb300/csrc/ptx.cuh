@@ -144,6 +144,13 @@ __device__ __forceinline__ float ex2_approx(float x)
     return y;
 }
 
+__device__ __forceinline__ float lg2_approx(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ---------------------------------------------------------------- paired fp32
 // (a.x * b.x, a.y * b.y) as one f32x2 instruction
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b)
