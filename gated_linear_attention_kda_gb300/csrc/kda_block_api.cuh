@@ -214,7 +214,7 @@ static kda_status launch_ssm_tc(int64_t grid, const CUtensorMap &mx, const CUten
         if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "scan set-up failed: %s", cudaGetErrorString(e));
         configured_dev = dev;
     }
-    ssmtc::kda_ssm_tc_kernel<P, PARTS, FULL><<<static_cast<unsigned>(grid), ssmtc::NTHREADS, Lay::ALLOC, s>>>(mx, mb, mc, mo, t);
+    ssmtc::kda_ssm_tc_kernel<P, PARTS, FULL><<<static_cast<unsigned>(grid), Lay::NTHREADS, Lay::ALLOC, s>>>(mx, mb, mc, mo, t);
     return launched("scan");
 }
 

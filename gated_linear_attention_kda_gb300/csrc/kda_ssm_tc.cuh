@@ -29,15 +29,17 @@
 // (as a shared-memory operand it cost 160 KB more and the kernel ran at 148.7 us where it now takes
 // TIME_HERE, 8 x 4096 tokens of 16 heads).
 //
-// Warp roles (1024 threads):
+// Warp roles (1024 threads; 896 for heads of 64):
 //   warp 0       TMA producer (lane 0): x tiles two or three deep, b two, c one or two; tensor memory allocation
 //   warp 1       MMA issuer: scores and outputs
 //   warp 2       step sizes, running sums and decays of a chunk, one chunk ahead
 //   warp 3       MMA issuer: state
 //   warps 4-11   scores G -> M (thread = token, two of the four 32-token blocks)
-//   warps 12-15  row scaling of C S0^T, then the output rows (thread = token)
-//   warps 16-23  state: bf16 copy for the next product, decay in place (state channel, half of the columns)
-//   warps 24-31  w B, 32 tokens at a time (16 state channels per warp)
+//   warps 12-15  row scaling of C S0^T, then the output rows (thread = token); for heads of 64 the score warps
+//                do this too, half of the columns each (16 packed prompts, 32 heads: 275 us against 308; heads
+//                of 128, 8 x 4096 tokens: 101 us against 92)
+//   then 8       state: bf16 copy for the next product, decay in place (state channel, half of the columns)
+//   last 8       w B, 32 tokens at a time (16 state channels per warp)
 // MMA order per chunk: C S0^T, the state product, M X, and the next chunk's C B^T, so that the tensor
 // core works on the last two while the state warps prepare what the first two of the next chunk need.
 // Tensor memory columns: G (M over it) [0, 128), Y [128, 128 + P), S, then the w B buffers.
@@ -53,7 +55,6 @@ using ssm::NS;
 
 constexpr int L = 128;          // tokens per chunk
 constexpr int SUB = 32;         // tokens per w B block (two MMA steps)
-constexpr int NTHREADS = 1024;
 constexpr uint32_t TMEM_COLS = 512;
 
 struct TcParams {
@@ -70,6 +71,10 @@ constexpr int SC_LOC = 0, SC_LD = 512, SC_ES = 1024, SC_W = 1536, SC_TOT = 2048,
 
 template <int P, int PARTS, bool FULL>
 struct Layout {
+    static constexpr bool MERGED = P == 64;        // the score warps write the output
+    static constexpr int EW = MERGED ? 0 : 4, NTHREADS = 32 * (4 + 8 + EW + 8 + 8);
+    static constexpr int EC = MERGED ? P / 2 : P;  // columns of an output thread
+    static constexpr int WST = 12 + EW, WWB = WST + 8;  // first state and first w B warp
     static constexpr int BOX = L * 128;            // 64 channels x 128 rows, 128-byte swizzle
     static constexpr int XT = P / 64 * BOX, BT = 2 * BOX;
     static constexpr int NSLOT = PARTS == 3 && P == 128 ? 2 : 4;  // w B buffers of PARTS x 16 columns
@@ -170,12 +175,12 @@ __device__ __forceinline__ int longest_first(const ssm::SsmParams &p, int rank)
 // FULL: outputs and states; else only the state that the piece leaves when it starts from zero (to
 // the workspace, with its decay), for the pieces that another one follows.
 template <int P, int PARTS, bool FULL>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
                       const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap to, const TcParams t)
 {
     using Lay = Layout<P, PARTS, FULL>;
-    constexpr int CS = Lay::CS, XS = Lay::XS;
+    constexpr int CS = Lay::CS, XS = Lay::XS, OUTW = Lay::MERGED ? 8 : 4;  // OUTW: warps that write the output
     constexpr uint32_t T_G = 0, T_Y = FULL ? 128 : 0, T_S = T_Y + (FULL ? P : 0), T_W = T_S + P;
     static_assert(T_W + Lay::NSLOT * PARTS * (SUB / 2) <= TMEM_COLS, "tensor memory budget");
     extern __shared__ uint8_t smem_dyn[];
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (threadIdx.x == 32) {
         for (int i = 0; i < XS; ++i) {
             mbar_init(bar(Lay::X_FULL + i), 1);
-            mbar_init(bar(Lay::X_EMPTY + i), FULL ? 4 : 1);
+            mbar_init(bar(Lay::X_EMPTY + i), FULL ? OUTW : 1);
             mbar_init(bar(Lay::OUT_GO + i), 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -222,11 +227,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(bar(Lay::C_FULL + i), 1);
             mbar_init(bar(Lay::C_EMPTY + i), 1);
             mbar_init(bar(Lay::SC_FULL + i), 1);
-            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 28 : 16);
+            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 24 + Lay::EW : 16);
         }
         for (int i : {Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
         for (int i : {Lay::S_GO, Lay::X_ZERO}) mbar_init(bar(i), 8);
-        for (int i : {Lay::M_GO, Lay::YX_GO}) mbar_init(bar(i), 12);
+        mbar_init(bar(Lay::M_GO), 8 + Lay::EW);
+        mbar_init(bar(Lay::YX_GO), 8 + OUTW);
         mbar_init(bar(Lay::ST_GO), FULL ? 2 : 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(Lay::W_FULL + i), 8);
@@ -256,6 +262,71 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto arrive_w = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
+    };
+
+    // The output's two steps, for a thread's token (quarter q, lane) and EC columns from c0.
+    // Y = C S0^T times the decay from the chunk's start to the token, in place:
+    auto scale_rows = [&](uint32_t ly, float e) {
+#pragma unroll 1
+        for (int g4 = 0; g4 < Lay::EC / 32; ++g4) {
+            uint32_t y[32];
+            tc::ld32(ly + 32 * g4, y);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 v = fmul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), make_float2(e, e));
+                y[i] = __float_as_uint(v.x);
+                y[i + 1] = __float_as_uint(v.y);
+            }
+            tc::st32(ly + 32 * g4, y);
+        }
+        tc::wait_st();
+        tc::fence_before();
+        arrive_w(Lay::M_GO);
+    };
+    // Y to bf16, over the x tile (both products have read it) and from there to memory by TMA, 32 tokens per
+    // warp; a ragged end is stored from registers.
+    auto write_rows = [&](uint32_t ly, int n, int q, int c0) {
+        const int row = 32 * q + lane, Lv = live_of(n);
+        const uint32_t xr = xt(n) + row * 128;
+        uint16_t *op = p.out + static_cast<long long>(pc.bos + n * L + row) * p.os + static_cast<long long>(h) * P + c0;
+#pragma unroll 1
+        for (int g4 = 0; g4 < Lay::EC / 32; ++g4) {
+            uint32_t y[32], o[16];
+            tc::ld32(ly + 32 * g4, y);
+            tc::wait_ld();
+            if (g4 + 1 == Lay::EC / 32) {
+                tc::fence_before();
+                arrive_w(Lay::YX_GO);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+            const int c8 = (c0 >> 3) + 4 * g4;  // first of four groups of eight channels
+            if (Lv == L) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // 16 bytes each, swizzled by the row
+                    SM_AT(uint4, xr + (c8 >> 3) * Lay::BOX + ((((c8 & 7) + i) ^ (row & 7)) << 4)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else if (row < Lv) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(op + 32 * g4)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+        }
+        if (Lv == L) {
+            tc::fence_async_smem();
+            if constexpr (Lay::MERGED) named_bar_sync(1 + q, 64);  // two warps fill the rows; the first stores them
+            __syncwarp();
+            if (lane == 0 && c0 == 0) {
+#pragma unroll
+                for (int k = 0; k < P / 64; ++k)
+                    tma_store_3d(&to, xt(n) + k * Lay::BOX + 32 * q * 128, 64 * k, h, pc.bos + n * L + 32 * q);
+                bulk_commit();
+            }
+        }
+    };
+    // ... and once the store has read the tile it is free for another chunk's x
+    auto release_rows = [&](int n) {
+        if (lane == 0) bulk_wait_read();
+        arrive_w(Lay::X_EMPTY + n % XS);
     };
 
     if (warp == 0) {
@@ -436,6 +507,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // of G that it has read itself (the product takes M's halves from columns 0 and 64).
             const int q = warp & 3, row = 32 * q + lane, hf = warp < 8 ? 0 : 1;
             const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_G + 64 * hf;
+            const int c0 = hf * Lay::EC;  // output columns, where these warps write it
+            const uint32_t ly = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y + c0;
+            if (Lay::MERGED) arrive_w(Lay::YX_GO);  // nothing of Y is waiting to be read
             const float Dh = p.D ? __ldg(p.D + h) : 0.f;
             const int nfull = min(max(2 * (q - 2 * hf), 0), 4), nlive = min(max(2 * (q - 2 * hf) + 2, 0), 4);
             for (int n = 0; n < nch; ++n) {
@@ -499,91 +573,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     for (int b = nlive; b < 4; ++b) tc::st8(lb + 8 * b, z);
                 }
                 tc::wait_st();
-                tc::fence_before();
-                arrive_w(Lay::M_GO);
-                arrive_w(Lay::SC_EMPTY + (n & 1));
+                if constexpr (Lay::MERGED) {
+                    const float e = ex2_approx(loc + (q > 0 ? tot.x : 0.f) + (q > 1 ? tot.y : 0.f) + (q > 2 ? tot.z : 0.f));
+                    arrive_w(Lay::SC_EMPTY + (n & 1));
+                    if (n > 0) release_rows(n - 1);
+                    if (!wait_w(Lay::YX_DONE, n & 1)) break;
+                    tc::fence_after();
+                    scale_rows(ly, e);
+                    if (!wait_w(Lay::OUT_GO + n % XS, (n / XS) & 1)) break;
+                    tc::fence_after();
+                    write_rows(ly, n, q, c0);
+                } else {
+                    tc::fence_before();
+                    arrive_w(Lay::M_GO);
+                    arrive_w(Lay::SC_EMPTY + (n & 1));
+                }
             }
+            if (Lay::MERGED && lane == 0) bulk_wait_all();
         }
-    } else if (warp < 16) {
+    } else if (warp < Lay::WST) {
         // ---------------------------------------------------------------- outputs
-        if constexpr (FULL) {
-            const int q = warp & 3, row = 32 * q + lane;
-            const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y;
-            uint16_t *op = p.out + static_cast<long long>(pc.bos + row) * p.os + static_cast<long long>(h) * P;
+        if constexpr (FULL && !Lay::MERGED) {
+            const int q = warp & 3;
+            const uint32_t ly = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y;
             arrive_w(Lay::YX_GO);  // nothing of Y is waiting to be read
             for (int n = 0; n < nch; ++n) {
                 if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1)) break;
-                // decay from the chunk's start to this row
                 const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
-                const float e = ex2_approx(SM_AT(const float, sc(n) + SC_LOC + 4 * row) + (q > 0 ? tot.x : 0.f) + (q > 1 ? tot.y : 0.f) + (q > 2 ? tot.z : 0.f));
+                const float loc = SM_AT(const float, sc(n) + SC_LOC + 4 * (32 * q + lane));
+                const float e = ex2_approx(loc + (q > 0 ? tot.x : 0.f) + (q > 1 ? tot.y : 0.f) + (q > 2 ? tot.z : 0.f));
                 arrive_w(Lay::SC_EMPTY + (n & 1));
                 if (!wait_w(Lay::YX_DONE, n & 1)) break;
                 tc::fence_after();
-#pragma unroll 1
-                for (int g4 = 0; g4 < P / 32; ++g4) {
-                    uint32_t y[32];
-                    tc::ld32(lb + 32 * g4, y);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float2 v = fmul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), make_float2(e, e));
-                        y[i] = __float_as_uint(v.x);
-                        y[i + 1] = __float_as_uint(v.y);
-                    }
-                    tc::st32(lb + 32 * g4, y);
-                }
-                tc::wait_st();
-                tc::fence_before();
-                arrive_w(Lay::M_GO);
-                // the x tile is the output's buffer once both products have read it
+                scale_rows(ly, e);
                 if (!wait_w(Lay::OUT_GO + n % XS, (n / XS) & 1)) break;
                 tc::fence_after();
-                const bool whole = live_of(n) == L;
-                const uint32_t xr = xt(n) + row * 128;
-#pragma unroll 1
-                for (int g4 = 0; g4 < P / 32; ++g4) {
-                    uint32_t y[32];
-                    tc::ld32(lb + 32 * g4, y);
-                    tc::wait_ld();
-                    const uint32_t box = xr + (g4 >> 1) * Lay::BOX;
-                    if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)  // eight channels: 16 bytes, swizzled by the row
-                            SM_AT(uint4, box + (((4 * (g4 & 1) + i) ^ (row & 7)) << 4)) =
-                                make_uint4(pack_bf16(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
-                                           pack_bf16(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
-                                           pack_bf16(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
-                                           pack_bf16(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
-                    } else if (row < live_of(n)) {  // a ragged end is stored from registers
-                        uint4 *dst = reinterpret_cast<uint4 *>(op + static_cast<long long>(n) * L * p.os + 32 * g4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack_bf16(__uint_as_float(y[8 * i]), __uint_as_float(y[8 * i + 1])),
-                                                pack_bf16(__uint_as_float(y[8 * i + 2]), __uint_as_float(y[8 * i + 3])),
-                                                pack_bf16(__uint_as_float(y[8 * i + 4]), __uint_as_float(y[8 * i + 5])),
-                                                pack_bf16(__uint_as_float(y[8 * i + 6]), __uint_as_float(y[8 * i + 7])));
-                    }
-                }
-                tc::fence_before();
-                arrive_w(Lay::YX_GO);
-                if (whole) {
-                    tc::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {  // a warp stores its 32 tokens
-#pragma unroll
-                        for (int k = 0; k < P / 64; ++k)
-                            tma_store_3d(&to, xt(n) + k * Lay::BOX + 32 * q * 128, 64 * k, h, pc.bos + n * L + 32 * q);
-                        bulk_commit();
-                        bulk_wait_read();
-                    }
-                }
-                arrive_w(Lay::X_EMPTY + n % XS);
+                write_rows(ly, n, q, 0);
+                release_rows(n);
             }
             if (lane == 0) bulk_wait_all();
         }
-    } else if (warp < 24) {
+    } else if (warp < Lay::WWB) {
         // ---------------------------------------------------------------- state
-        const int q = warp & 3, nn = 32 * q + lane, c0 = (warp < 20 ? 0 : P / 2);  // this thread's channel and columns
+        const int q = warp & 3, nn = 32 * q + lane, c0 = warp < Lay::WST + 4 ? 0 : P / 2;  // this thread's channel and columns
         const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_S + c0;
         const size_t unit = static_cast<size_t>(pc.seq) * p.H + h;
         const size_t st_elems = static_cast<size_t>(p.nseq) * p.H * P * NS;
@@ -678,7 +710,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // ---------------------------------------------------------------- w B
         // A warp owns 16 state channels. ldmatrix.trans hands a lane two tokens of one
         // channel, the layout in which the 16-lane tensor-memory stores take them, so the transposition is free.
-        const int u = threadIdx.x - 768, ch16 = 2 * (warp & 3) + (warp < 28 ? 0 : 1);
+        const int u = threadIdx.x - 32 * Lay::WWB, ch16 = 2 * (warp & 3) + (warp < Lay::WWB + 4 ? 0 : 1);
         const uint32_t lb = tmem + (static_cast<uint32_t>(16 * ch16) << 16) + T_W;
         const int c8 = 2 * ch16 + ((lane >> 3) & 1);  // eight-channel group of this lane's address
         // matrix lane >> 3 of an ldmatrix: tokens 8 (lane >> 4) .., channels 8 ((lane >> 3) & 1) ..
@@ -704,9 +736,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 float2 w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = SM_AT(const float2, sc(n) + SC_W + 4 * (j0 + 8 * i + 2 * (lane & 3)));
-                ok = wait_w(Lay::W_EMPTY + sl, ((k / Lay::NSLOT) & 1) ^ 1);
-                if (!ok) break;
-                tc::fence_after();
                 uint32_t v[8];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {  // tokens j0 + 16 i ..
@@ -723,21 +752,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 float2 f[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = fmul2(make_float2(bf16_lo(v[i]), bf16_hi(v[i])), w[i >> 1]);
+                // everything is at hand in registers before the buffer is waited for
+                uint32_t o[PARTS][8];
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    uint32_t o[8];
+                for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         if (part + 1 < PARTS) {  // the upper eight bits; what is left is exact
                             const uint32_t a = __float_as_uint(f[i].x), b = __float_as_uint(f[i].y);
-                            o[i] = __byte_perm(a, b, 0x7632);
+                            o[part][i] = __byte_perm(a, b, 0x7632);
                             f[i] = fsub2(f[i], make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)));
                         } else {
-                            o[i] = pack_bf16(f[i].x, f[i].y);
+                            o[part][i] = pack_bf16(f[i].x, f[i].y);
                         }
                     }
-                    tc::st_16x128b_x4(lb + (sl * PARTS + part) * (SUB / 2), o);
-                }
+                ok = wait_w(Lay::W_EMPTY + sl, ((k / Lay::NSLOT) & 1) ^ 1);
+                if (!ok) break;
+                tc::fence_after();
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) tc::st_16x128b_x4(lb + (sl * PARTS + part) * (SUB / 2), o[part]);
                 tc::wait_st();
                 tc::fence_before();
                 arrive_w(Lay::W_FULL + sl);
