@@ -173,7 +173,10 @@ __device__ __forceinline__ int longest_first(const ssm::SsmParams &p, int rank)
 }
 
 // FULL: outputs and states; else only the state that the piece leaves when it starts from zero (to
-// the workspace, with its decay), for the pieces that another one follows.
+// the workspace, with its decay), for the pieces that another one follows. That state is one sum over the
+// piece's tokens, each weighted by the decay from it to the piece's end, so the chunks are taken from the
+// last to the first: the weights follow from a running sum, and the accumulator is never decayed, so no
+// chunk waits for the one before it.
 template <int P, int PARTS, bool FULL>
 __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
@@ -209,7 +212,9 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     auto bt = [&](int n) { return sb + Lay::B + (n & 1) * Lay::BT; };
     auto ct = [&](int n) { return sb + Lay::C + (n % CS) * Lay::BT; };
     auto sc = [&](int n) { return sb + Lay::SC + (n & 1) * SC_BYTES; };
-    auto live_of = [&](int n) { return min(L, pc.len - n * L); };
+    // step n is chunk n, or the n-th from the end
+    auto chunk_of = [&](int n) { return FULL ? n : nch - 1 - n; };
+    auto live_of = [&](int n) { return min(L, pc.len - chunk_of(n) * L); };
 
     if (warp == 0) {
         tc::alloc(sb + Lay::TMEMPTR, TMEM_COLS);
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             mbar_init(bar(Lay::C_FULL + i), 1);
             mbar_init(bar(Lay::C_EMPTY + i), 1);
             mbar_init(bar(Lay::SC_FULL + i), 1);
-            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 24 + Lay::EW : 16);
+            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 24 + Lay::EW : 8);
         }
         for (int i : {Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
         for (int i : {Lay::S_GO, Lay::X_ZERO}) mbar_init(bar(i), 8);
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             if (FULL) tma_prefetch_desc(&tcm);
             int nb = 0, nx = 0, ncc = 0;  // tiles issued
             for (int n = 0; n < nch; ++n) {
-                const int s = n & 1, tok = pc.bos + n * L;
+                const int s = n & 1, tok = pc.bos + chunk_of(n) * L;
                 const uint32_t par = ((n >> 1) & 1) ^ 1;
                 if (!wait_bar(bar(Lay::B_EMPTY + s), par, flags)) break;
                 mbar_arrive_expect_tx(bar(Lay::B_FULL + s), Lay::BT);
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
         auto fetch = [&](int n) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (n * L + j0 + i < pc.len) raw[i] = dp[static_cast<long long>(n * L + j0 + i) * p.dts];
+                if (n < nch && chunk_of(n) * L + j0 + i < pc.len) raw[i] = dp[static_cast<long long>(chunk_of(n) * L + j0 + i) * p.dts];
         };
         fetch(0);
         float seg = 0.f;
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             const float t0 = __shfl_sync(0xffffffffu, pre, 7), t1 = __shfl_sync(0xffffffffu, pre, 15);
             const float t2 = __shfl_sync(0xffffffffu, pre, 23), t3 = __shfl_sync(0xffffffffu, pre, 31);
             const int blkq = lane >> 3;
-            const float rest = blkq == 0 ? t1 + (t2 + t3) : blkq == 1 ? t2 + t3 : blkq == 2 ? t3 : 0.f;
+            const float rest = (blkq == 0 ? t1 + (t2 + t3) : blkq == 1 ? t2 + t3 : blkq == 2 ? t3 : 0.f) + (FULL ? 0.f : seg);
             seg += (t0 + t1) + (t2 + t3);
             const float sf[4] = {r0 + after, r1 + after, r2 + after, r3 + after};
             if (!wait_w(Lay::SC_EMPTY + (n & 1), ((n >> 1) & 1) ^ 1)) break;
@@ -478,7 +483,8 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 const int nsub = (live_of(n) + SUB - 1) / SUB;
                 uint32_t dx = tc::sdesc_lo(xt(n), Lay::BOX);
                 // (the first block's wait comes before the one that is on the chain)
-                ok = wait_w(Lay::X_FULL + n % XS, (n / XS) & 1) && wait_w(Lay::W_FULL + k % Lay::NSLOT, (k / Lay::NSLOT) & 1) && wait_w(Lay::S_GO, n & 1);
+                ok = wait_w(Lay::X_FULL + n % XS, (n / XS) & 1) && wait_w(Lay::W_FULL + k % Lay::NSLOT, (k / Lay::NSLOT) & 1) &&
+                     (!FULL && n > 0 ? true : wait_w(Lay::S_GO, n & 1));
                 for (int s = 0; ok && s < nsub; ++s, ++k, dx += (SUB * 128) >> 4) {
                     const int sl = k % Lay::NSLOT;
                     ok = s == 0 || wait_w(Lay::W_FULL + sl, (k / Lay::NSLOT) & 1);
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                     tc::commit_w(bar(Lay::W_EMPTY + sl));
                 }
                 if (!ok) break;
-                tc::commit_w(bar(Lay::ST_GO));
+                if (FULL || n + 1 == nch) tc::commit_w(bar(Lay::ST_GO));
                 tc::commit_w(bar((FULL ? Lay::OUT_GO : Lay::X_EMPTY) + n % XS));
             }
             tc::commit_w(bar(Lay::END2));
@@ -637,7 +643,15 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             }
         };
         bool ok = true;
-        for (int n = 0; n < nch; ++n) {
+        if (!FULL && nch > 0) {
+            const uint32_t z[32] = {};
+#pragma unroll 1
+            for (int g4 = 0; g4 < P / 64; ++g4) tc::st32(lb + 32 * g4, z);
+            tc::wait_st();
+            tc::fence_before();
+            arrive_w(Lay::S_GO);
+        }
+        for (int n = 0; FULL && n < nch; ++n) {
             ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1);
             if (!ok) break;
             const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
@@ -679,7 +693,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
         const bool write = FULL ? (pc.last && p.fin) : true;
         if (ok && write) {
             if (nch > 0) {
-                ok = wait_w(Lay::ST_GO, (nch - 1) & 1);
+                ok = wait_w(Lay::ST_GO, FULL ? (nch - 1) & 1 : 0);
                 tc::fence_after();
             }
 #pragma unroll 1
