@@ -77,20 +77,21 @@ struct Layout {
     static constexpr int WST = 12 + EW, WWB = WST + 8;  // first state and first w B warp
     static constexpr int BOX = L * 128;            // 64 channels x 128 rows, 128-byte swizzle
     static constexpr int XT = P / 64 * BOX, BT = 2 * BOX;
-    static constexpr int NSLOT = PARTS == 3 && P == 128 ? 2 : 4;  // w B buffers of PARTS x 16 columns
+    static constexpr int NSLOT = FULL && PARTS == 3 && P == 128 ? 2 : 4;  // w B buffers of PARTS x 16 columns
     static constexpr int CS = P == 64 ? 2 : 1;     // c tiles in flight
-    static constexpr int XS = P == 64 ? 3 : 2;     // x tiles in flight (a tile is also its chunk's output buffer)
+    static constexpr int XS = P == 64 || !FULL ? 3 : 2;  // x tiles in flight (a tile is also its chunk's output buffer)
+    static constexpr int BS = FULL ? 2 : 3;        // b tiles in flight
     static constexpr int X = 0;
-    static constexpr int B = X + XS * XT;          // two stages
-    static constexpr int C = B + 2 * BT;
+    static constexpr int B = X + XS * XT;
+    static constexpr int C = B + BS * BT;
     static constexpr int H = C + (FULL ? CS * BT : 0);  // bf16 state, [n][p]
     static constexpr int SC = H + (FULL ? XT : 0);
     static constexpr int BAR = SC + 2 * SC_BYTES;
     // YX_GO: the bf16 state is there and Y has been read; M_GO: M is there and Y is scaled; S_GO: the state is
     // decayed; ST_GO: both products of the old state are done; OUT_GO: both products of an x tile are done
-    static constexpr int X_FULL = 0, X_EMPTY = 3, OUT_GO = 6, B_FULL = 9, B_EMPTY = 11, C_FULL = 13, C_EMPTY = 15, SC_FULL = 17,
-                         SC_EMPTY = 19, G_DONE = 21, M_GO = 22, YX_DONE = 23, Y_DONE = 24, YX_GO = 25, S_GO = 26, ST_GO = 27,
-                         X_ZERO = 28, END = 29, END2 = 30, W_FULL = 31, W_EMPTY = 35, NBARS = 40;
+    static constexpr int X_FULL = 0, X_EMPTY = 3, OUT_GO = 6, B_FULL = 9, B_EMPTY = 12, C_FULL = 15, C_EMPTY = 17, SC_FULL = 19,
+                         SC_EMPTY = 21, G_DONE = 23, M_GO = 24, YX_DONE = 25, Y_DONE = 26, YX_GO = 27, S_GO = 28, ST_GO = 29,
+                         X_ZERO = 30, END = 31, END2 = 32, W_FULL = 33, W_EMPTY = 37, NBARS = 42;
     static constexpr int TMEMPTR = BAR + NBARS * 8;
     static constexpr int FLAGS = TMEMPTR + 16;
     static constexpr int ALLOC = FLAGS + 16 + 1024;
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                       const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap to, const TcParams t)
 {
     using Lay = Layout<P, PARTS, FULL>;
-    constexpr int CS = Lay::CS, XS = Lay::XS, OUTW = Lay::MERGED ? 8 : 4;  // OUTW: warps that write the output
+    constexpr int CS = Lay::CS, XS = Lay::XS, BS = Lay::BS, OUTW = Lay::MERGED ? 8 : 4;  // OUTW: warps that write the output
     constexpr uint32_t T_G = 0, T_Y = FULL ? 128 : 0, T_S = T_Y + (FULL ? P : 0), T_W = T_S + P;
     static_assert(T_W + Lay::NSLOT * PARTS * (SUB / 2) <= TMEM_COLS, "tensor memory budget");
     extern __shared__ uint8_t smem_dyn[];
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
     auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
     auto xt = [&](int n) { return sb + Lay::X + (n % XS) * Lay::XT; };
-    auto bt = [&](int n) { return sb + Lay::B + (n & 1) * Lay::BT; };
+    auto bt = [&](int n) { return sb + Lay::B + (n % BS) * Lay::BT; };
     auto ct = [&](int n) { return sb + Lay::C + (n % CS) * Lay::BT; };
     auto sc = [&](int n) { return sb + Lay::SC + (n & 1) * SC_BYTES; };
     // step n is chunk n, or the n-th from the end
@@ -226,13 +227,15 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             mbar_init(bar(Lay::X_EMPTY + i), FULL ? OUTW : 1);
             mbar_init(bar(Lay::OUT_GO + i), 2);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < BS; ++i) {
             mbar_init(bar(Lay::B_FULL + i), 1);
-            mbar_init(bar(Lay::B_EMPTY + i), FULL ? 9 : 8);  // the w B warps, and the score product
+            mbar_init(bar(Lay::B_EMPTY + i), FULL ? 9 : 16);  // the w B warps, and the score product
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(Lay::C_FULL + i), 1);
             mbar_init(bar(Lay::C_EMPTY + i), 1);
             mbar_init(bar(Lay::SC_FULL + i), 1);
-            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 24 + Lay::EW : 8);
+            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 24 + Lay::EW : 16);
         }
         for (int i : {Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
         for (int i : {Lay::S_GO, Lay::X_ZERO}) mbar_init(bar(i), 8);
@@ -334,6 +337,85 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
         arrive_w(Lay::X_EMPTY + n % XS);
     };
 
+    // w B: warp wi of eight, every GROUPS-th block from `group` on (a piece that only leaves its state has whole
+    // chunks alone, so only one group ever meets a ragged one)
+    constexpr int GROUPS = FULL ? 1 : 2;
+    auto make_wb = [&](int wi, int group) {
+        // A warp owns 16 state channels. ldmatrix.trans hands a lane two tokens of one
+        // channel, the layout in which the 16-lane tensor-memory stores take them, so the transposition is free.
+        const int u = 32 * wi + lane, ch16 = 2 * (warp & 3) + (wi < 4 ? 0 : 1);
+        const uint32_t lb = tmem + (static_cast<uint32_t>(16 * ch16) << 16) + T_W;
+        const int c8 = 2 * ch16 + ((lane >> 3) & 1);  // eight-channel group of this lane's address
+        // matrix lane >> 3 of an ldmatrix: tokens 8 (lane >> 4) .., channels 8 ((lane >> 3) & 1) ..
+        const int jr = 8 * (lane >> 4) + (lane & 7);
+        int k = 0;
+        bool ok = true;
+        for (int n = 0; ok && n < nch; ++n) {
+            const int Lv = live_of(n), nsub = (Lv + SUB - 1) / SUB;
+            ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::B_FULL + n % BS, (n / BS) & 1);
+            if (ok && Lv < L) {
+                // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
+                ok = wait_w(Lay::X_FULL + n % XS, (n / XS) & 1);
+                if (ok)
+                    for (int i = u; i < (L - Lv) * (P / 8); i += 256) {
+                        const int r = Lv + i / (P / 8), c8 = i % (P / 8);
+                        SM_AT(uint4, xt(n) + (c8 >> 3) * Lay::BOX + r * 128 + (c8 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                tc::fence_async_smem();
+                if (ok) arrive_w(Lay::X_ZERO);
+            }
+            for (int s = group; ok && s < nsub; s += GROUPS) {
+                const int sl = (k + s) % Lay::NSLOT, j0 = SUB * s;
+                float2 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = SM_AT(const float2, sc(n) + SC_W + 4 * (j0 + 8 * i + 2 * (lane & 3)));
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {  // tokens j0 + 16 i ..
+                    const int j = j0 + 16 * i + jr;
+                    ldsm_x4_t(bt(n) + (c8 >> 3) * Lay::BOX + j * 128 + (((c8 & 7) ^ (j & 7)) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+                if (Lv < L) {  // past the end b may be anything
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = j0 + 8 * (i >> 1) + 2 * (lane & 3);
+                        v[i] &= j + 1 < Lv ? 0xffffffffu : j < Lv ? 0xffffu : 0u;
+                    }
+                }
+                float2 f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = fmul2(make_float2(bf16_lo(v[i]), bf16_hi(v[i])), w[i >> 1]);
+                // everything is at hand in registers before the buffer is waited for
+                uint32_t o[PARTS][8];
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (part + 1 < PARTS) {  // the upper eight bits; what is left is exact
+                            const uint32_t a = __float_as_uint(f[i].x), b = __float_as_uint(f[i].y);
+                            o[part][i] = __byte_perm(a, b, 0x7632);
+                            f[i] = fsub2(f[i], make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)));
+                        } else {
+                            o[part][i] = pack_bf16(f[i].x, f[i].y);
+                        }
+                    }
+                ok = wait_w(Lay::W_EMPTY + sl, (((k + s) / Lay::NSLOT) & 1) ^ 1);
+                if (!ok) break;
+                tc::fence_after();
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) tc::st_16x128b_x4(lb + (sl * PARTS + part) * (SUB / 2), o[part]);
+                tc::wait_st();
+                tc::fence_before();
+                arrive_w(Lay::W_FULL + sl);
+            }
+            k += nsub;
+            if (ok) {
+                arrive_w(Lay::B_EMPTY + n % BS);
+                arrive_w(Lay::SC_EMPTY + (n & 1));
+            }
+        }
+    };
+
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
         if (lane == 0) {
@@ -342,9 +424,8 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             if (FULL) tma_prefetch_desc(&tcm);
             int nb = 0, nx = 0, ncc = 0;  // tiles issued
             for (int n = 0; n < nch; ++n) {
-                const int s = n & 1, tok = pc.bos + chunk_of(n) * L;
-                const uint32_t par = ((n >> 1) & 1) ^ 1;
-                if (!wait_bar(bar(Lay::B_EMPTY + s), par, flags)) break;
+                const int s = n % BS, tok = pc.bos + chunk_of(n) * L;
+                if (!wait_bar(bar(Lay::B_EMPTY + s), ((n / BS) & 1) ^ 1, flags)) break;
                 mbar_arrive_expect_tx(bar(Lay::B_FULL + s), Lay::BT);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) tma_load_3d(bt(n) + k * Lay::BOX, &tb, 64 * k, grp, tok, bar(Lay::B_FULL + s));
@@ -364,7 +445,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 ++nx;
             }
             // no copy is in flight when the CTA ends, whichever way the loop was left
-            for (int m = nb > 2 ? nb - 2 : 0; m < nb; ++m) drain_bar(bar(Lay::B_FULL + (m & 1)), (m >> 1) & 1);
+            for (int m = nb > BS ? nb - BS : 0; m < nb; ++m) drain_bar(bar(Lay::B_FULL + m % BS), (m / BS) & 1);
             for (int m = nx > XS ? nx - XS : 0; m < nx; ++m) drain_bar(bar(Lay::X_FULL + m % XS), (m / XS) & 1);
             for (int m = ncc > CS ? ncc - CS : 0; m < ncc; ++m) drain_bar(bar(Lay::C_FULL + m % CS), (m / CS) & 1);
         }
@@ -382,14 +463,14 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(i * ((16 * 128) >> 4)));
             };
             auto issue_g = [&](int n) {  // its tensor memory holds the M of the last chunk until that has been read
-                if (!wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1) || !wait_w(Lay::C_FULL + n % CS, (n / CS) & 1)) return false;
+                if (!wait_w(Lay::B_FULL + n % BS, (n / BS) & 1) || !wait_w(Lay::C_FULL + n % CS, (n / CS) & 1)) return false;
                 if (n > 0 && !wait_w(Lay::Y_DONE, (n - 1) & 1)) return false;
                 tc::fence_after();
                 const uint32_t dc = tc::sdesc_lo(ct(n), 16), db = tc::sdesc_lo(bt(n), 16);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_G, kmaj(dc, i), kmaj(db, i), id_g, i > 0);
                 tc::commit_w(bar(Lay::G_DONE));
-                tc::commit_w(bar(Lay::B_EMPTY + (n & 1)));
+                tc::commit_w(bar(Lay::B_EMPTY + n % BS));
                 return true;
             };
             bool ok = issue_g(0);
@@ -596,6 +677,8 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 }
             }
             if (Lay::MERGED && lane == 0) bulk_wait_all();
+        } else {
+            make_wb(warp - 4, 0);  // no scores here: these warps share the work on w B
         }
     } else if (warp < Lay::WST) {
         // ---------------------------------------------------------------- outputs
@@ -721,79 +804,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
         }
         tc::fence_before();
     } else {
-        // ---------------------------------------------------------------- w B
-        // A warp owns 16 state channels. ldmatrix.trans hands a lane two tokens of one
-        // channel, the layout in which the 16-lane tensor-memory stores take them, so the transposition is free.
-        const int u = threadIdx.x - 32 * Lay::WWB, ch16 = 2 * (warp & 3) + (warp < Lay::WWB + 4 ? 0 : 1);
-        const uint32_t lb = tmem + (static_cast<uint32_t>(16 * ch16) << 16) + T_W;
-        const int c8 = 2 * ch16 + ((lane >> 3) & 1);  // eight-channel group of this lane's address
-        // matrix lane >> 3 of an ldmatrix: tokens 8 (lane >> 4) .., channels 8 ((lane >> 3) & 1) ..
-        const int jr = 8 * (lane >> 4) + (lane & 7);
-        int k = 0;
-        bool ok = true;
-        for (int n = 0; ok && n < nch; ++n) {
-            const int Lv = live_of(n), nsub = (Lv + SUB - 1) / SUB;
-            ok = wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1) && wait_w(Lay::B_FULL + (n & 1), (n >> 1) & 1);
-            if (ok && Lv < L) {
-                // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
-                ok = wait_w(Lay::X_FULL + n % XS, (n / XS) & 1);
-                if (ok)
-                    for (int i = u; i < (L - Lv) * (P / 8); i += 256) {
-                        const int r = Lv + i / (P / 8), c8 = i % (P / 8);
-                        SM_AT(uint4, xt(n) + (c8 >> 3) * Lay::BOX + r * 128 + (c8 & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                tc::fence_async_smem();
-                if (ok) arrive_w(Lay::X_ZERO);
-            }
-            for (int s = 0; ok && s < nsub; ++s, ++k) {
-                const int sl = k % Lay::NSLOT, j0 = SUB * s;
-                float2 w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = SM_AT(const float2, sc(n) + SC_W + 4 * (j0 + 8 * i + 2 * (lane & 3)));
-                uint32_t v[8];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {  // tokens j0 + 16 i ..
-                    const int j = j0 + 16 * i + jr;
-                    ldsm_x4_t(bt(n) + (c8 >> 3) * Lay::BOX + j * 128 + (((c8 & 7) ^ (j & 7)) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                }
-                if (Lv < L) {  // past the end b may be anything
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int j = j0 + 8 * (i >> 1) + 2 * (lane & 3);
-                        v[i] &= j + 1 < Lv ? 0xffffffffu : j < Lv ? 0xffffu : 0u;
-                    }
-                }
-                float2 f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = fmul2(make_float2(bf16_lo(v[i]), bf16_hi(v[i])), w[i >> 1]);
-                // everything is at hand in registers before the buffer is waited for
-                uint32_t o[PARTS][8];
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (part + 1 < PARTS) {  // the upper eight bits; what is left is exact
-                            const uint32_t a = __float_as_uint(f[i].x), b = __float_as_uint(f[i].y);
-                            o[part][i] = __byte_perm(a, b, 0x7632);
-                            f[i] = fsub2(f[i], make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)));
-                        } else {
-                            o[part][i] = pack_bf16(f[i].x, f[i].y);
-                        }
-                    }
-                ok = wait_w(Lay::W_EMPTY + sl, ((k / Lay::NSLOT) & 1) ^ 1);
-                if (!ok) break;
-                tc::fence_after();
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) tc::st_16x128b_x4(lb + (sl * PARTS + part) * (SUB / 2), o[part]);
-                tc::wait_st();
-                tc::fence_before();
-                arrive_w(Lay::W_FULL + sl);
-            }
-            if (ok) {
-                arrive_w(Lay::B_EMPTY + (n & 1));
-                arrive_w(Lay::SC_EMPTY + (n & 1));
-            }
-        }
+        make_wb(warp - Lay::WWB, GROUPS - 1);
     }
 
     tc::fence_before();
@@ -807,7 +818,9 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
 
 // Joins the pieces of every (sequence, head): in order, each piece's local state in the workspace is
 // replaced by the state that enters the piece, carry <- 2^decay carry + local. Reads and writes the
-// workspace once; one thread per four state elements.
+// workspace once; one thread per four state elements. The chain itself is short; JOIN_BATCH pieces'
+// loads are in flight together, as one load's latency per piece is what it would otherwise cost.
+constexpr int JOIN_BATCH = 8;
 constexpr int JOIN_THREADS = 256;
 template <int P>
 __global__ void __launch_bounds__(JOIN_THREADS) kda_ssm_join_kernel(const TcParams t)
@@ -843,18 +856,30 @@ __global__ void __launch_bounds__(JOIN_THREADS) kda_ssm_join_kernel(const TcPara
         }
     }
     const float *dec = t.ws + static_cast<size_t>(t.slots) * p.H * P * NS;
-    for (int i = 0; i < npieces; ++i) {
-        const long long slot = base + i;
-        if (slot >= t.slots) return;  // overlapping bounds (flagged): more pieces than the call has room for
-        float4 *at = reinterpret_cast<float4 *>(t.ws + (static_cast<size_t>(slot) * p.H + h) * P * NS + e);
-        if (i + 1 == npieces) {
-            *at = c;
-            break;
+    const size_t unit_elems = static_cast<size_t>(P) * NS;
+    for (int i0 = 0; i0 < npieces; i0 += JOIN_BATCH) {
+        float4 l[JOIN_BATCH];
+        float g[JOIN_BATCH];
+#pragma unroll
+        for (int j = 0; j < JOIN_BATCH; ++j) {
+            const long long slot = base + i0 + j;
+            // the last piece leaves no local state; overlapping bounds (flagged) have more pieces than there is room for
+            if (i0 + j + 1 < npieces && slot < t.slots) {
+                const size_t at = static_cast<size_t>(slot) * p.H + h;
+                l[j] = __ldcg(reinterpret_cast<const float4 *>(t.ws + at * unit_elems + e));
+                g[j] = __ldcg(dec + at);
+            }
         }
-        const float4 l = *at;
-        const float g = ex2_approx(dec[static_cast<size_t>(slot) * p.H + h]);
-        *at = c;
-        c = make_float4(fmaf(g, c.x, l.x), fmaf(g, c.y, l.y), fmaf(g, c.z, l.z), fmaf(g, c.w, l.w));
+#pragma unroll
+        for (int j = 0; j < JOIN_BATCH; ++j) {
+            const long long slot = base + i0 + j;
+            if (i0 + j >= npieces || slot >= t.slots) return;
+            *reinterpret_cast<float4 *>(t.ws + (static_cast<size_t>(slot) * p.H + h) * unit_elems + e) = c;
+            if (i0 + j + 1 < npieces) {
+                const float k = ex2_approx(g[j]);
+                c = make_float4(fmaf(k, c.x, l[j].x), fmaf(k, c.y, l[j].y), fmaf(k, c.z, l[j].z), fmaf(k, c.w, l[j].w));
+            }
+        }
     }
 }
 
