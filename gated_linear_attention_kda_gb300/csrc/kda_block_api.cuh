@@ -444,9 +444,12 @@ KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int6
     p.total = static_cast<int>(total);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (total <= (cu_seqlens ? 1 : nseq) * blk::STEP_TOKENS) return blk::launch_ssm_steps(p, s);
-    blk::Device d;
-    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
-    const blk::SsmPlan plan = blk::ssm_plan(nseq, total, H, P, d.sms);
+    blk::SsmPlan plan = {0, 1, nseq, 0};
+    if (workspace) {
+        blk::Device d;
+        if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+        plan = blk::ssm_plan(nseq, total, H, P, d.sms);
+    }
     if (workspace && workspace_bytes < plan.bytes)
         return fail(KDA_ERR_RANGE, "workspace of %zu bytes is smaller than the %zu this call needs", workspace_bytes, plan.bytes);
     float *ws = static_cast<float *>(workspace);

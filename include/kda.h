@@ -422,9 +422,15 @@ KDA_API kda_status kda_conv_step(const void *x, int64_t x_stride, const float *w
  *            by side. Without it such a call runs one piece per pair. Scratch
  *            after the call; calls that overlap in time must not share it.
  *            Too small: KDA_ERR_RANGE. Misaligned: KDA_ERR_ALIGN.
+ * Calls of up to 8 tokens per sequence (8 in all in varlen mode) run token by
+ * token in fp32. Longer ones run in chunks of 128 tokens, whose score matrix
+ * and carried state are rounded to bf16 as operands of the output; the state
+ * itself is held in fp32, and increments keep 24 bits where final_state is
+ * fp32, 16 otherwise. A token's log2 decay is held at -160 or above.
  * A NaN or infinity in x at one token can reach the outputs of up to 127
  * earlier tokens of the same sequence, head and channel (the tokens of a
- * chunk are one matrix product); it never reaches another sequence.
+ * chunk are one matrix product); it never reaches another sequence. What an
+ * infinity reaches may come out as NaN.
  */
 KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const void *b,
                            int64_t b_stride, const void *c, int64_t c_stride, const float *A_log, const float *D,

@@ -66,7 +66,7 @@ def check_conv(kda, B, T, C, W, silu=True, bias=True, init=True, lengths=None, s
     st = randn(g, S, W - 1, C) if init else None
     ref, fin, mag = R.conv(x, w, bs, silu, st, cu)
     out = torch.full((B, T, C + (16 if strided else 0)), NAN, dtype=torch.bfloat16, device="cuda")[..., :C]
-    final = st if in_place else torch.full((S, W - 1, C), NAN, dtype=torch.bfloat16, device="cuda")
+    final = st if in_place and init else torch.full((S, W - 1, C), NAN, dtype=torch.bfloat16, device="cuda")
     kda.conv(x, w, out, bs, silu=silu, initial_state=st, final_state=final, cu_seqlens=cu)
     kda.check_device_status()
     close(out, ref, HALF * ref.abs() + 2.0 ** -18 * mag + 1e-37, "out")
@@ -191,7 +191,7 @@ def check_ssm(kda, B, T, H, P, G, state="fp32", init=True, lengths=None, strided
     st = randn(g, S, H, P, 128, dtype=_SDT[state], scale=0.3) if init else None
     ref, fin, mag, fmag = R.ssm(x, dt, b, c, A_log, D, dt_bias, st, cu)
     out = torch.full((B, T, H * P + (8 if strided else 0)), NAN, dtype=torch.bfloat16, device="cuda")[..., :H * P].unflatten(-1, (H, P))
-    final = st if in_place else torch.full((S, H, P, 128), NAN, dtype=_SDT[state], device="cuda")
+    final = st if in_place and init else torch.full((S, H, P, 128), NAN, dtype=_SDT[state], device="cuda")
     ws = torch.full((kda.ssm_workspace_bytes(S, B * T, H, P),), 0xff, dtype=torch.uint8, device="cuda") if workspace else None
     kda.ssm(x, dt, b, c, out, A_log, D, dt_bias, initial_state=st, final_state=final, cu_seqlens=cu, workspace=ws)
     kda.check_device_status()
@@ -461,3 +461,116 @@ def test_repeated_calls_are_bitwise_equal(kda):
     kda.check_device_status()
     for o, f in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(f, got[0][1])
+
+
+# ------------------------------------------------------------------- refusals on tensors, far offsets
+
+def test_calls_refuse_mismatched_tensors(kda):
+    g = gen(30)
+    x = randn(g, 2, 6, 64)
+    w = randn(g, 64, 4, dtype=torch.float32)
+    out = torch.full_like(x, NAN)
+    for bad, match in ((dict(weight=w.bfloat16()), "weight must be torch.float32"), (dict(weight=w[:, :1].contiguous()), "W must be 2, 3 or 4"),
+                       (dict(out=out.float()), "out must be torch.bfloat16"), (dict(out=out[:, :3]), "out has shape"),
+                       (dict(initial_state=torch.zeros(1, 3, 64, dtype=torch.bfloat16, device="cuda")), "initial_state has shape"),
+                       (dict(x=x.expand(2, 6, 64)[:, :, :60], out=out[:, :, :60], weight=w[:60].contiguous()), "multiple of 8"),
+                       (dict(out=x), "must not share memory"), (dict(bias=torch.zeros(64)), "bias must be a CUDA tensor"),
+                       (dict(cu_seqlens=torch.tensor([0, 12], device="cuda")), "varlen mode needs B == 1")):
+        args = {**dict(x=x, weight=w, out=out), **bad}
+        with pytest.raises(ValueError, match=match):
+            kda.conv(**args)
+    assert torch.isnan(out).all()
+    xs, dt, b, c, A_log, D, dt_bias = ssm_inputs(g, 1, 300, 4, 64, 2)
+    o = torch.empty(1, 300, 4, 64, dtype=torch.bfloat16, device="cuda")
+    need = kda.ssm_workspace_bytes(1, 300, 4, 64)
+    for bad, match in ((dict(A_log=None), "A_log is required"), (dict(c=c[..., :1, :]), "c has shape"), (dict(D=D[:3].contiguous()), "D has shape"),
+                       (dict(x=xs[:, ::2], dt=dt[:, ::2], b=b[:, ::2], c=c[:, ::2], out=xs[:, 1::2]), "token strides|share memory|out must"),
+                       (dict(final_state=torch.empty(1, 4, 64, 128, dtype=torch.float16, device="cuda")), "final_state must be")):
+        args = {**dict(x=xs, dt=dt, b=b, c=c, out=o, A_log=A_log), **bad}
+        if "x" in bad:  # every other token, written to the tokens between: rows that interleave are allowed
+            kda.ssm(**args)
+            continue
+        with pytest.raises(ValueError, match=match):
+            kda.ssm(**args)
+    if need:
+        with pytest.raises(ValueError, match="workspace of"):
+            kda.ssm(xs, dt, b, c, o, A_log, workspace=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
+    kda.check_device_status()
+
+
+def test_conv_offsets_past_32_bits(kda):
+    """Token strides that put the last rows more than 2^32 elements from the first."""
+    T, C, stride = 70000, 16, 65536
+    big = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((1, T, C), (T * stride, stride, 1))
+    g = gen(31)
+    x.copy_(randn(g, 1, T, C))
+    w = randn(g, C, 4, dtype=torch.float32)
+    ref, fin, mag = R.conv(x, w, None, True, None)
+    out = x.as_strided((1, T, C), (T * stride, stride, 1), 64)  # 64 channels further on in the same rows
+    final = torch.empty(1, 3, C, dtype=torch.bfloat16, device="cuda")
+    kda.conv(x, w, out, final_state=final)
+    close(out, ref, HALF * ref.abs() + 2.0 ** -18 * mag + 1e-37, "out")
+    assert torch.equal(final.double(), fin)
+
+
+def test_ssm_offsets_past_32_bits(kda):
+    T, stride = 70000, 65536
+    big = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda")
+    view = lambda off, *s: big.as_strided((1, T, *s), (T * stride, stride) + ((s[1], 1) if len(s) == 2 else (1,)), off)  # noqa: E731
+    g = gen(32)
+    x, b, c, dt, out = view(0, 1, 64), view(64, 1, 128), view(192, 1, 128), view(321, 1), view(512, 1, 64)
+    for v in (x, b, c):
+        v.copy_(randn(g, *v.shape))
+    dt.copy_(randn(g, 1, T, 1))
+    A_log = torch.zeros(1, device="cuda")
+    tail = slice(T - 300, T)
+    # the decay over a few thousand tokens leaves nothing of what came before: the tail's own recurrence is the reference
+    near = [v[:, T - 6000:].contiguous() for v in (x, dt, b, c)]
+    ref, fin, mag, fmag = R.ssm(*near, A_log, None, None, None)
+    ws = torch.empty(max(16, kda.ssm_workspace_bytes(1, T, 1, 64)), dtype=torch.uint8, device="cuda")
+    final = torch.empty(1, 1, 64, 128, device="cuda")
+    kda.ssm(x, dt, b, c, out, A_log, final_state=final, workspace=ws)
+    kda.check_device_status()
+    r, m = ref[:, -300:], mag[:, -300:]
+    close(out[:, tail], r, HALF * r.abs() + 2 * HALF * (1 + HALF) * m, "out")
+    check_states(final, fin, fmag, "state")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_ssm_random_shapes(kda, seed):
+    import random
+    r = random.Random(seed)
+    G = r.choice([1, 2, 3])
+    lengths = [r.choice([0, 1, 7, 9, 128, 129, r.randint(1, 500)]) for _ in range(r.randint(1, 7))] if r.random() < 0.5 else None
+    if lengths is not None and not sum(lengths):
+        lengths[0] = 5
+    T = sum(lengths) if lengths is not None else r.choice([r.randint(1, 40), r.randint(100, 900)])
+    check_ssm(kda, 1 if lengths is not None else r.randint(1, 4), T, G * r.randint(1, 4), r.choice([64, 128]), G, state=r.choice(["fp32", "bf16"]),
+              init=r.random() < 0.6, lengths=lengths, strided=r.random() < 0.5, in_place=r.random() < 0.5, use_D=r.random() < 0.7,
+              workspace=r.random() < 0.7, seed=seed, dt_scale=r.choice([1.0, 4.0]))
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_conv_random_shapes(kda, seed):
+    import random
+    r = random.Random(seed)
+    lengths = [r.choice([0, 1, 2, 3, 63, 64, 65, r.randint(1, 300)]) for _ in range(r.randint(1, 9))] if r.random() < 0.5 else None
+    if lengths is not None and not sum(lengths):
+        lengths[0] = 2
+    T = sum(lengths) if lengths is not None else r.randint(1, 400)
+    check_conv(kda, 1 if lengths is not None else r.randint(1, 5), T, 8 * r.choice([1, 5, 31, 32, 33, 70, r.randint(1, 300)]), r.choice([2, 3, 4]),
+               silu=r.random() < 0.5, bias=r.random() < 0.5, init=r.random() < 0.6, lengths=lengths, strided=r.random() < 0.5,
+               in_place=r.random() < 0.4, seed=seed)
+
+
+def test_layers_hand_their_states_from_a_prompt_to_steps(kda):
+    """examples/hybrid_layers.py: prompts, then single tokens, against one longer prompt. Both are bf16
+    models of two layers whose roundings differ along the way: ten roundings of 2^-8 that add as squares."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_layers.py")
+    spec = importlib.util.spec_from_file_location("hybrid_layers", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.main() <= 10 ** 0.5 * HALF
