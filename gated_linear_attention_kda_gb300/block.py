@@ -7,7 +7,7 @@ Token axes may be strided: a slice of a projection's row is passed as it stands.
 one token are contiguous, and batch rows follow one another at the token stride.
 
 The checks read each tensor's properties once and the calls pass plain integers: for a single
-token the host's time is the call's time (a call costs 5 to 9 us of it on the GB300's CPU).
+token the host's time is the call's time (a call costs 8 to 16 us of it on the GB300's CPU).
 """
 from __future__ import annotations
 

@@ -24,10 +24,20 @@
 // not rounded); w B into PARTS bf16 parts of 8 bits each: 3, exact, where an fp32 state is returned,
 // 2 (2^-17 of a term) where it is returned in bf16 or not at all. Sums are fp32.
 //
-// What bounds it: shared memory. Per chunk of P = 128 the MMAs read 256 KB of operands, TMA moves
-// 128 KB and the warps 96 KB, 480 KB at 128 bytes a cycle; that is why w B goes through tensor memory
-// (as a shared-memory operand it cost 160 KB more and the kernel ran at 148.7 us where it now takes
-// TIME_HERE, 8 x 4096 tokens of 16 heads).
+// NaN: a product multiplies what the mask leaves out by zero, so a NaN or infinity in x (which is an MMA
+// operand as it stands) reaches its channel's outputs of the whole chunk. Finding such channels and making
+// them again token by token, or masking x on the way, was built and cost 8 to 14 % (8 x 4096 tokens of 16 heads:
+// 104 to 109 us against 95). In dt, b and c, which the warps handle, NaN reaches later tokens alone.
+//
+// What bounds it: 8 x 4096 tokens of 16 heads of 128 take 95 us (3.1 TB/s of HBM; 128 of the 152 SMs have a
+// state), about 5,600 cycles a chunk. Of these the MMAs take 3,072 (1,536 of them for the three parts of w B)
+// and shared memory 3,840: the MMAs read 256 KB of operands, TMA moves 128 KB and the warps 96 KB at 128 bytes a
+// cycle. w B goes through tensor memory for that reason: as a shared-memory operand it cost 160 KB more (149 us
+// then, 112 us with it). The rest is latency: a chunk's state chain (ST_GO, decay, S_GO, MMA) and output chain
+// (G, M, M X) each cross four barriers of some 110 cycles, and the roles share the issue slots. Measured and not
+// kept: one MMA issuer for all products (112 us); four state warps (102); C as a tensor-memory operand (116);
+// polling instead of suspended waits (149).
+// Pieces (1 x 131,072 tokens, 32 heads): state pass 350 us, join 16 us, this pass 606 us.
 //
 // Warp roles (1024 threads; 896 for heads of 64):
 //   warp 0       TMA producer (lane 0): x tiles two or three deep, b two, c one or two; tensor memory allocation
@@ -40,8 +50,9 @@
 //                of 128, 8 x 4096 tokens: 101 us against 92)
 //   then 8       state: bf16 copy for the next product, decay in place (state channel, half of the columns)
 //   last 8       w B, 32 tokens at a time (16 state channels per warp)
-// MMA order per chunk: C S0^T, the state product, M X, and the next chunk's C B^T, so that the tensor
-// core works on the last two while the state warps prepare what the first two of the next chunk need.
+// Warp 1 issues C S0^T, M X and the next chunk's C B^T; warp 3 the state product block by block as w B
+// comes. Neither waits for the other's order, only for the data (a product of the old state and its decay
+// meet in ST_GO and S_GO).
 // Tensor memory columns: G (M over it) [0, 128), Y [128, 128 + P), S, then the w B buffers.
 #pragma once
 #include "kda_ssm_step.cuh"

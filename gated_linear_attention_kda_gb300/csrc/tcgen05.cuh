@@ -133,14 +133,6 @@ __device__ __forceinline__ void mma_ts_tf32_w(uint32_t d, uint32_t a_tmem, uint6
                  "r"(a_tmem), "l"(b), "r"(id), "r"(accumulate)
                  : "memory");
 }
-// Shared memory -> tensor memory: 128 rows x 32 bytes of a K-major tile to eight columns (one K step of
-// a 16-bit A operand). In order with the MMAs that the same thread issues after it.
-__device__ __forceinline__ void cp_128x256b_w(uint32_t taddr, uint64_t sd)
-{
-    asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-                 "@e tcgen05.cp.cta_group::1.128x256b [%0], %1;\n\t}" ::"r"(taddr), "l"(sd)
-                 : "memory");
-}
 __device__ __forceinline__ void commit_w(uint32_t bar)
 {
     asm volatile("{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
@@ -206,14 +198,6 @@ __device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r
     tmem_check(taddr, 16);
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-// the same over 8 columns
-__device__ __forceinline__ void st_16x128b_x2(uint32_t taddr, const uint32_t (&r)[4])
-{
-    tmem_check(taddr, 8);
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3])
                  : "memory");
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }

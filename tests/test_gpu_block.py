@@ -269,6 +269,52 @@ def test_ssm_does_not_mix_sequences_that_hold_nan_or_infinity(kda):
     assert torch.isnan(out[:, 70:130]).all()
 
 
+@pytest.mark.parametrize("bad", [NAN, float("inf"), -float("inf")])
+@pytest.mark.parametrize("P,T,at", [(64, 300, 200), (128, 400, 130), (64, 5, 3), (128, 128, 127), (64, 1400, 700)])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_ssm_a_non_finite_x_stays_in_its_channel_and_chunk(kda, P, T, at, bad, workspace):
+    """NaN or infinity in one channel of x at one token: other channels and earlier chunks of 128 tokens (earlier tokens,
+    where the call has no chunks) are as without it, and that channel's later outputs and its state hold no number."""
+    g = gen(40 + T)
+    x, dt, b, c, A_log, D, dt_bias = (v.clone() for v in ssm_inputs(g, 1, T, 2, P, 1))
+    A_log -= 6  # weak decay: what was spoilt stays
+    ws = torch.empty(max(16, kda.ssm_workspace_bytes(1, T, 2, P)), dtype=torch.uint8, device="cuda") if workspace else None
+
+    def run():
+        out, fin = torch.full_like(x, 7.0), torch.full((1, 2, P, 128), 7.0, device="cuda")
+        kda.ssm(x, dt, b, c, out, A_log, D, dt_bias, final_state=fin, workspace=ws)
+        kda.check_device_status()
+        return out, fin
+
+    ref_out, ref_fin = run()
+    x[0, at, 1, 9] = bad
+    out, fin = run()
+    same = torch.ones(1, T, 2, P, dtype=torch.bool, device="cuda")
+    same[:, at // 128 * 128 if T > 8 else at:, 1, 9] = False
+    assert torch.equal(out[same], ref_out[same])
+    assert not torch.isfinite(out[0, at:, 1, 9]).any()
+    rest = torch.ones(1, 2, P, dtype=torch.bool, device="cuda")
+    rest[0, 1, 9] = False
+    assert torch.equal(fin[rest], ref_fin[rest]) and not torch.isfinite(fin[0, 1, 9]).any()
+
+
+@pytest.mark.parametrize("which", ["dt", "b", "c"])
+@pytest.mark.parametrize("T,at", [(300, 200), (140, 131), (400, 40)])
+def test_ssm_a_nan_never_reaches_earlier_tokens(kda, which, T, at):
+    g = gen(60 + T)
+    args = dict(zip(("x", "dt", "b", "c", "A_log", "D", "dt_bias"), (v.clone() for v in ssm_inputs(g, 1, T, 2, 64, 1))))
+    out, ref = torch.empty_like(args["x"]), torch.empty_like(args["x"])
+    kda.ssm(out=ref, **args)
+    args[which][:, at] = NAN
+    kda.ssm(out=out, **args)
+    kda.check_device_status()
+    assert torch.equal(out[:, :at], ref[:, :at]) and torch.isnan(out[:, at]).all()
+    if which == "c":
+        assert torch.equal(out[:, at + 1:], ref[:, at + 1:])
+    else:
+        assert torch.isnan(out[:, at:]).all()
+
+
 def test_ssm_empty_call(kda):
     z = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
     st = randn(gen(1), 2, 3, 64, 128, dtype=torch.float32)
