@@ -1,6 +1,8 @@
 // kda_block_api.cuh -- host side of the operators around the mixer (include/kda.h): argument
 // checks, launch shapes and launches. Included by kda_fwd.cu, whose error reporting it uses.
 #pragma once
+#include <type_traits>
+
 #include "kda_conv.cuh"
 #include "kda_norm.cuh"
 #include "kda_ssm_step.cuh"
@@ -284,11 +286,24 @@ static unsigned row_grid(const RowShape &sh, int64_t rows, const Device &d)
 }
 
 template <int VPT, bool CTA>
-static kda_status launch_gated(norm::GatedParams p, const RowShape &sh, const Device &d, cudaStream_t s)
+static kda_status launch_gated(norm::GatedParams p, kda_act act, bool gate_first, const RowShape &sh, const Device &d, cudaStream_t s)
 {
     p.tpr = sh.threads;
-    const unsigned grid = row_grid<norm::kda_gated_norm_kernel<VPT, CTA>>(sh, p.rows, d);
-    norm::kda_gated_norm_kernel<VPT, CTA><<<grid, CTA ? sh.threads : norm::WARP_THREADS, 0, s>>>(p);
+    auto go = [&](auto act) {
+        constexpr auto FIRST = norm::kda_gated_norm_kernel<VPT, CTA, decltype(act)::value, true>;
+        constexpr auto AFTER = norm::kda_gated_norm_kernel<VPT, CTA, decltype(act)::value, false>;
+        const int threads = CTA ? sh.threads : norm::WARP_THREADS;
+        if (gate_first)
+            FIRST<<<row_grid<FIRST>(sh, p.rows, d), threads, 0, s>>>(p);
+        else
+            AFTER<<<row_grid<AFTER>(sh, p.rows, d), threads, 0, s>>>(p);
+    };
+    if (act == KDA_ACT_SILU)
+        go(std::integral_constant<int, KDA_ACT_SILU>());
+    else if (act == KDA_ACT_SIGMOID)
+        go(std::integral_constant<int, KDA_ACT_SIGMOID>());
+    else
+        go(std::integral_constant<int, KDA_ACT_NONE>());
     return launched("gated norm");
 }
 
@@ -341,12 +356,20 @@ KDA_API kda_status kda_conv(const void *x, int64_t x_stride, const float *weight
     p.act = act;
     p.cg = 1;
     while (p.cg < 32 && p.cg < C / 8) p.cg <<= 1;  // a warp along the channels, so that little of the last block idles
-    // tokens per thread: as many as leave 512 threads for every SM, between one batch and MAX_RUN (8 x 4096 x
-    // 2048 channels: 57.2 us at 32, 55.2 us at 64; a run's first W - 1 rows are read twice)
+    // tokens per thread: the length whose waves of blocks take the fewest steps, a run's start (the first W - 1 rows
+    // read again, the taps, the first load's latency) counted as RUN_COST tokens. 8 x 4096 x 2048 channels: 49.9 us;
+    // at 64 tokens whatever the waves, 55.7 us (1.7 waves). 16 packed prompts, 4352 channels: 188 us and 203 us.
     blk::Device d;
     if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
-    const int64_t run = total * (C / 8) / (512 * static_cast<int64_t>(d.sms)) / conv::BATCH * conv::BATCH;
-    p.run = static_cast<int>(std::min<int64_t>(std::max<int64_t>(run, conv::BATCH), conv::MAX_RUN));
+    const int64_t tg = conv::THREADS / p.cg, gy = (C / 8 + p.cg - 1) / p.cg, slots = conv::BLOCKS * static_cast<int64_t>(d.sms);
+    int64_t best = INT64_MAX;
+    for (int run = conv::BATCH; run <= conv::MAX_RUN; run += conv::BATCH) {
+        const int64_t ctas = (total + tg * run - 1) / (tg * run) * gy, cost = (ctas + slots - 1) / slots * (run + conv::RUN_COST);
+        if (cost <= best) {
+            best = cost;
+            p.run = run;
+        }
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return W == 2 ? blk::launch_conv<2>(p, s) : W == 3 ? blk::launch_conv<3>(p, s) : blk::launch_conv<4>(p, s);
 }
@@ -530,16 +553,14 @@ KDA_API kda_status kda_gated_norm(const void *x, int64_t x_stride, const void *g
     p.rows = M * R;
     p.R = static_cast<int>(R);
     p.D = static_cast<int>(D);
-    p.act = act;
-    p.gate_first = gate_first != 0;
     p.w_rows = weight_rows == 1 ? 1 : static_cast<int>(R);
     p.eps = eps;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const blk::RowShape sh = blk::row_shape(D, p.rows, d.sms);
-    if (sh.cta) return sh.vpt == 2 ? blk::launch_gated<2, true>(p, sh, d, s) : blk::launch_gated<4, true>(p, sh, d, s);
-    return sh.vpt == 1   ? blk::launch_gated<1, false>(p, sh, d, s)
-           : sh.vpt == 2 ? blk::launch_gated<2, false>(p, sh, d, s)
-                         : blk::launch_gated<4, false>(p, sh, d, s);
+    if (sh.cta) return sh.vpt == 2 ? blk::launch_gated<2, true>(p, act, gate_first != 0, sh, d, s) : blk::launch_gated<4, true>(p, act, gate_first != 0, sh, d, s);
+    return sh.vpt == 1   ? blk::launch_gated<1, false>(p, act, gate_first != 0, sh, d, s)
+           : sh.vpt == 2 ? blk::launch_gated<2, false>(p, act, gate_first != 0, sh, d, s)
+                         : blk::launch_gated<4, false>(p, act, gate_first != 0, sh, d, s);
 }
 
 KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,

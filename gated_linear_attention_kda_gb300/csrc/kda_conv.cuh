@@ -7,9 +7,9 @@
 // channels (one 16-byte access per token) and walks a run of tokens of them with the last W - 1 rows in
 // registers, so a row is read once per run plus the W - 1 rows before it; the BATCH rows of the next
 // step are loaded before those of the present one are filtered. Arithmetic is in fp32 pairs.
-// Four taps with SiLU: 8 x 4096 tokens of 2048 channels 55 us (4.9 TB/s), 16 packed prompts of 65,536 tokens and
-// 4352 channels 203 us (5.6 TB/s). What is missing to a plain copy (6.7 TB/s): the two approximations of the
-// sigmoid per element, which share one pipe (16 a cycle and SM: 28 of the 55 us), and the first rows of a run.
+// Four taps with SiLU: 8 x 4096 tokens of 2048 channels 49.9 us (5.4 TB/s), 16 packed prompts of 65,536 tokens and
+// 4352 channels 188 us (6.1 TB/s; a plain copy makes 6.7). Warps wait for loads (long scoreboard) more than for
+// anything else; the sigmoid's two approximations per element take 30 % of their pipe.
 #pragma once
 #include "blk_common.cuh"
 
@@ -17,8 +17,10 @@ namespace kda {
 namespace conv {
 
 constexpr int THREADS = 128;
-constexpr int MAX_RUN = 64;  // tokens per thread at most
-constexpr int BATCH = 4;     // rows in flight per thread
+constexpr int BLOCKS = 4;    // resident CTAs per SM (five spill: 95 us where four take 55)
+constexpr int RUN_COST = 8;  // what starting a run costs, in tokens
+constexpr int MAX_RUN = 256; // tokens per thread at most
+constexpr int BATCH = 4;     // rows in flight per thread (eight, at three CTAs per SM: 68 us)
 
 struct ConvParams {
     const uint16_t *x, *init;
@@ -71,7 +73,7 @@ struct Taps {
             float2 u = b.v[i];
 #pragma unroll
             for (int j = 0; j < W; ++j) u = ffma2(w[j].v[i], f[j].v[i], u);
-            if (silu) u = fmul2(u, make_float2(blk::sigmoid_fast(u.x), blk::sigmoid_fast(u.y)));
+            if (silu) u = fmul2(u, blk::sigmoid_fast2(u));
             o[i] = pack_bf16(u.x, u.y);
         }
         return make_uint4(o[0], o[1], o[2], o[3]);
@@ -112,7 +114,7 @@ __device__ __forceinline__ void write_final(const ConvParams &p, int seq, int c)
 }
 
 template <int W>
-__global__ void __launch_bounds__(THREADS, 4) kda_conv_kernel(const ConvParams p)
+__global__ void __launch_bounds__(THREADS, BLOCKS) kda_conv_kernel(const ConvParams p)
 {
     if (p.cu && blockIdx.x == 0 && blockIdx.y == 0) blk::check_bounds(p.cu, p.nseq, p.total);
     const int nc8 = p.C >> 3;

@@ -6,8 +6,7 @@
 // CTA (sums through shared memory). Groups walk the rows of a grid that fills the machine; with one or
 // two vectors per thread the next row is loaded before the present one is reduced, with four a row's own
 // loads are enough in flight. Sums and the norm are fp32.
-// Gated norm of 32,768 tokens x 16 heads of 128: 76 us (5.3 TB/s; a plain copy makes 6.7), where the gate's two
-// approximations per element share one pipe; residual norm of 32,768 x 2048, bf16 stream: 90 us (5.9 TB/s).
+// Residual norm of 32,768 x 2048, bf16 stream: 90 us (5.9 TB/s; a plain copy makes 6.7; arithmetic in pairs 92 us).
 // Rows of one token's worth (128 x 2048 gated, 8 x 4096 residual) take 2.3 and 3.5 us, the chain of loads and sums.
 #pragma once
 #include "blk_common.cuh"
@@ -53,13 +52,17 @@ struct GatedParams {
     const float *w;
     long long xs, zs, os;   // elements between tokens
     long long rows;         // M * R
-    int R, D, act, gate_first, w_rows;
+    int R, D, w_rows;
     float eps;
     int tpr;                // threads per row (warp-group form; a power of two)
 };
 
-template <int VPT, bool CTA>
-__global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_gated_norm_kernel(const GatedParams p)
+// Instances by activation and gate order and arithmetic in pairs keep the issue slots free for the loads (32,768 x
+// 16 rows of 128: 76.5 us with both as run-time choices and scalar arithmetic, 67.5 us so, 89 % of a plain copy); the
+// one-vector form is held to 48 registers for ten CTAs per SM (seven: 69.6 us, twelve, which spill: 98.5 us).
+template <int VPT, bool CTA, int ACT, bool FIRST>
+__global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS, !CTA && VPT == 1 ? 10 : 1)
+    kda_gated_norm_kernel(const GatedParams p)
 {
     __shared__ float part[2][32];
     Group<CTA> gr{CTA ? static_cast<int>(blockDim.x) : p.tpr, CTA ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (p.tpr - 1), part, 0};
@@ -68,13 +71,13 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_gated_no
     const float inv_d = 1.f / static_cast<float>(p.D);
     int c[VPT];
     bool live[VPT];
-    float w[VPT][8];
+    float2 w[VPT][4];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         c[v] = 8 * (gr.rank + v * gr.tpr);
         live[v] = c[v] < p.D;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[v][i] = 1.f;
+        for (int i = 0; i < 4; ++i) w[v][i] = make_float2(1.f, 1.f);
         if (live[v] && p.w && p.w_rows == 1) blk::load8f(p.w + c[v], w[v]);
     }
     constexpr bool AHEAD = VPT <= 2;  // the next row is loaded before the present one is reduced
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_gated_no
             ++mm;
         }
     };
-    auto fetch = [&](long long row, long long m, int r) {
+    auto fetch = [&](long long row, long long m, int r) {  // channels and rows that are not there count as zeros
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             xn[v] = zn[v] = make_uint4(0u, 0u, 0u, 0u);
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_gated_no
     // every group of a warp makes the same number of steps (the shuffles need all lanes)
     for (long long base = static_cast<long long>(blockIdx.x) * per; base < p.rows; base += step) {
         const long long row = base + (first - static_cast<long long>(blockIdx.x) * per);
-        float x[VPT][8], z[VPT][8], ss = 0.f;
+        float2 x[VPT][4], z[VPT][4], ss = make_float2(0.f, 0.f);
         if (!AHEAD) fetch(row, m, r);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
@@ -120,22 +123,22 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_gated_no
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                z[v][i] = blk::apply_act(z[v][i], p.act);
-                if (p.gate_first) x[v][i] = live[v] ? x[v][i] * z[v][i] : 0.f;
-                ss = fmaf(x[v][i], x[v][i], ss);
+            for (int i = 0; i < 4; ++i) {
+                z[v][i] = blk::apply_act2<ACT>(z[v][i]);
+                if (FIRST) x[v][i] = fmul2(x[v][i], z[v][i]);
+                ss = ffma2(x[v][i], x[v][i], ss);
             }
-        const float inv = rsqrtf(fmaf(gr.sum(ss), inv_d, p.eps));
+        const float inv = rsqrtf(fmaf(gr.sum(ss.x + ss.y), inv_d, p.eps));
         if (row < p.rows) {
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 if (!live[v]) continue;
                 if (p.w && p.w_rows != 1) blk::load8f(p.w + static_cast<size_t>(r) * p.D + c[v], w[v]);
-                float o[8];
+                float2 o[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    o[i] = x[v][i] * inv * w[v][i];
-                    if (!p.gate_first) o[i] *= z[v][i];
+                for (int i = 0; i < 4; ++i) {
+                    o[i] = fmul2(fmul2(x[v][i], make_float2(inv, inv)), w[v][i]);
+                    if (!FIRST) o[i] = fmul2(o[i], z[v][i]);
                 }
                 *reinterpret_cast<uint4 *>(p.out + m * p.os + static_cast<long long>(r) * p.D + c[v]) = blk::pack8(o);
             }
