@@ -7,7 +7,7 @@
 // channels (one 16-byte access per token) and walks a run of tokens of them with the last W - 1 rows in
 // registers, so a row is read once per run plus the W - 1 rows before it; the BATCH rows of the next
 // step are loaded before those of the present one are filtered. Arithmetic is in fp32 pairs.
-// Four taps with SiLU: 8 x 4096 tokens of 2048 channels 49.9 us (5.4 TB/s), 16 packed prompts of 65,536 tokens and
+// Four taps with SiLU: 8 x 4096 tokens of 2048 channels 49.9 us (5.4 TB/s), 16 packed prompts, 65,519 tokens in all,
 // 4352 channels 188 us (6.1 TB/s; a plain copy makes 6.7). Warps wait for loads (long scoreboard) more than for
 // anything else; the sigmoid's two approximations per element take 30 % of their pipe.
 #pragma once

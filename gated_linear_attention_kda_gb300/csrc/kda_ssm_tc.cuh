@@ -26,18 +26,19 @@
 //
 // NaN: a product multiplies what the mask leaves out by zero, so a NaN or infinity in x (which is an MMA
 // operand as it stands) reaches its channel's outputs of the whole chunk. Finding such channels and making
-// them again token by token, or masking x on the way, was built and cost 8 to 14 % (8 x 4096 tokens of 16 heads:
-// 104 to 109 us against 95). In dt, b and c, which the warps handle, NaN reaches later tokens alone.
+// them again token by token, or masking x on the way, was built and cost 12 to 19 % (8 x 4096 tokens of 16 heads:
+// 108 to 114 us against 95). In dt, b and c, which the warps handle, NaN reaches later tokens alone.
 //
 // What bounds it: 8 x 4096 tokens of 16 heads of 128 take 95 us (3.1 TB/s of HBM; 128 of the 152 SMs have a
-// state), about 5,600 cycles a chunk. Of these the MMAs take 3,072 (1,536 of them for the three parts of w B)
+// state), about 5,800 cycles a chunk. Of these the MMAs take 3,072 (1,536 of them for the three parts of w B)
 // and shared memory 3,840: the MMAs read 256 KB of operands, TMA moves 128 KB and the warps 96 KB at 128 bytes a
 // cycle. w B goes through tensor memory for that reason: as a shared-memory operand it cost 160 KB more (149 us
-// then, 112 us with it). The rest is latency: a chunk's state chain (ST_GO, decay, S_GO, MMA) and output chain
-// (G, M, M X) each cross four barriers of some 110 cycles, and the roles share the issue slots. Measured and not
+// then, 112 us with it). The rest is latency: a chunk's state chain (ST_GO, decay, S_GO, MMA) and its output
+// chain (G_DONE, M, M_GO, M X, Y_DONE, the next G) hand over at barriers, some 110 cycles each, and the warps' work
+// between them waits for tensor-memory loads while the roles share the issue slots (0.56 used). Measured and not
 // kept: one MMA issuer for all products (112 us); four state warps (102); C as a tensor-memory operand (116);
 // polling instead of suspended waits (149).
-// Pieces (1 x 131,072 tokens, 32 heads): state pass 350 us, join 16 us, this pass 606 us.
+// Pieces (1 x 131,072 tokens, 32 heads): state pass 352 us, join 15 us, this pass 617 us.
 //
 // Warp roles (1024 threads; 896 for heads of 64):
 //   warp 0       TMA producer (lane 0): x tiles two or three deep, b two, c one or two; tensor memory allocation
