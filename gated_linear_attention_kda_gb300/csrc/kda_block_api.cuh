@@ -235,15 +235,19 @@ static kda_status launch_ssm(const ssm::SsmParams &p, const SsmPlan &plan, float
     t.slots = static_cast<int>(split ? (p.cu ? plan.slots : static_cast<int64_t>(p.nseq) * plan.seg_per_seq) : p.nseq);
     t.ws = ws;
     const int64_t grid = static_cast<int64_t>(t.slots) * p.H;
+    // an fp32 final state keeps three parts of w b in both passes, otherwise two are enough (1 x 131,072 tokens, 32
+    // heads of 128, cut: fp32 985 us; bf16 936 us, 974 us with three in the first pass)
+    const bool exact = p.fin && p.fin_dtype == KDA_DTYPE_FP32;
     if (split) {
-        if (const kda_status st = launch_ssm_tc<P, 3, false>(grid, mx, mb, mc, mo, t, s); st != KDA_OK) return st;
+        if (const kda_status st = exact ? launch_ssm_tc<P, 3, false>(grid, mx, mb, mc, mo, t, s)
+                                        : launch_ssm_tc<P, 2, false>(grid, mx, mb, mc, mo, t, s); st != KDA_OK)
+            return st;
         ssmtc::kda_ssm_join_kernel<P><<<static_cast<unsigned>(static_cast<int64_t>(p.nseq) * p.H * (P * ssm::NS / (4 * ssmtc::JOIN_THREADS))),
                                        ssmtc::JOIN_THREADS, 0, s>>>(t);
         if (const kda_status st = launched("join"); st != KDA_OK) return st;
     }
-    // an fp32 final state keeps three parts of w b, otherwise two are enough
-    return p.fin && p.fin_dtype == KDA_DTYPE_FP32 ? launch_ssm_tc<P, 3, true>(grid, mx, mb, mc, mo, t, s)
-                                                  : launch_ssm_tc<P, 2, true>(grid, mx, mb, mc, mo, t, s);
+    return exact ? launch_ssm_tc<P, 3, true>(grid, mx, mb, mc, mo, t, s)
+                 : launch_ssm_tc<P, 2, true>(grid, mx, mb, mc, mo, t, s);
 }
 
 // Threads along a row of D channels and vectors of eight per thread. Few rows (less than four per SM)
