@@ -170,10 +170,14 @@ static bool rows_map(CUtensorMap *m, const void *base, int64_t tokens, int64_t g
 }
 
 // Pieces of the time axis. One CTA walks a piece, so a call of fewer (sequence, head) pairs than SMs
-// leaves SMs idle unless sequences are cut. A cut call walks every chunk twice (states first, without
-// the score and output products: about 0.45 of a full walk) and pays two more launches (about three
-// chunks' time together). Chosen: the piece length with the least modelled time, 0 for no cut. Packed
-// sequences are modelled by their mean length; a longer one is cut into more pieces.
+// leaves SMs idle unless sequences are cut. A cut call walks every chunk but the last pieces' twice: the first pass,
+// without the score and output products, takes 1.6 us a chunk, the second 2.75 us (heads of 64: 2.25). A CTA's start
+// and end cost 6.2 us, CTAs follow one another in waves of one per SM, and the two more launches and the join some
+// 5 us. Chosen: the piece length with the least modelled time, 0 for no cut. Packed sequences are modelled by their
+// mean length; a longer one is cut into more pieces. fp32 states, uncut against the chosen cut:
+// 4 x 8192 tokens of 16 heads of 128 175.7 and 153.3 us, 1 x 4096 of 32 93.5 and 52.5, 1 x 131,072 of 32 2,700 and
+// 979, 1 x 2048 of 8 heads of 64 39.5 and 19.3. Where the model says no cut, a cut was slower: 6 x 16,384 of 16 heads
+// 346 uncut, 391 in three pieces; 1 x 2048 of 64 heads 50 uncut, 81 in eight; 2 x 4096 of 32 heads of 64 76 and 92.
 struct SsmPlan {
     int seg_chunks, seg_per_seq;
     int64_t slots;
@@ -185,10 +189,11 @@ static SsmPlan ssm_plan(int64_t states, int64_t tokens, int64_t H, int64_t P, in
     if (states < 1 || tokens < 1) return best;
     const int64_t units = states * H, mean = (tokens + states - 1) / states, nc = (mean + ssmtc::L - 1) / ssmtc::L;
     auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
-    double cost = static_cast<double>(waves(units)) * nc;
+    const double full = P == 64 ? 2.25 : 2.75, states_only = 1.6, cta = 6.2, cut = 5.0;  // us: a chunk, a chunk, a CTA, a call
+    double cost = waves(units) * (full * nc + cta);
     for (int64_t s = 2; s <= nc && units * s <= 4 * static_cast<int64_t>(sms); ++s) {
         const int64_t seg = (nc + s - 1) / s, pieces = (nc + seg - 1) / seg;
-        const double c = static_cast<double>(waves(units * pieces)) * seg + 0.45 * waves(units * (pieces - 1)) * seg + 3.0;
+        const double c = waves(units * pieces) * (full * seg + cta) + waves(units * (pieces - 1)) * (states_only * seg + cta) + cut;
         if (c < cost) {
             cost = c;
             best.seg_chunks = static_cast<int>(seg);
