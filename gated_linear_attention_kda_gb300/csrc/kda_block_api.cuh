@@ -142,7 +142,7 @@ static kda_status check_ssm(const void *x, int64_t xs, const void *dt, int64_t d
 
 // Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one: 8 heads of
 // 64, one sequence, 8 tokens 5.2 against 6.2 us, 16 tokens 7.8 against 6.3; 64 sequences of 16 heads of 128, 8
-// tokens 41 against 51 us, 16 tokens 74 against 53.
+// tokens 38 against 51 us, 16 tokens 50 in chunks, 74 token by token.
 constexpr int64_t STEP_TOKENS = 8;
 
 static kda_status launch_ssm_steps(const ssm::SsmParams &p, cudaStream_t s)

@@ -8,6 +8,9 @@
 // writes the state once, so the step is bound by HBM (128 sequences x 16 heads of 128, fp32 states: 43.4 us,
 // 6.2 TB/s, 93 % of a plain copy); a prompt walks its tokens one after another and is bound by the latency
 // of one token's chain.
+// A few tokens against many states are bound by issue and the chain: 1024 sequences of 8 tokens, 16 heads of 128, take
+// 552 us (658 with scalar arithmetic and every lane working out each token's step size and decay, which a lane now
+// does for one token of 32).
 #pragma once
 #include "blk_common.cuh"
 
@@ -60,17 +63,19 @@ __global__ void __launch_bounds__(STEP_THREADS) kda_ssm_step_kernel(const SsmPar
     if (!sp.ok) return;  // flagged by check_bounds
     const size_t st = (static_cast<size_t>(unit) * p.P + r0) * NS + 4 * lane;
     const size_t st_elems = static_cast<size_t>(p.nseq) * p.H * p.P * NS;
-    float s[ROWS][4];
+    float2 s[ROWS][2];  // paired arithmetic
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
+        s[r][0] = s[r][1] = make_float2(0.f, 0.f);
         if (p.init && gmem_ok(st + r * NS, 4, st_elems)) {
             if (p.init_dtype == KDA_DTYPE_FP32) {
                 const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.init) + st + r * NS);
-                s[r][0] = v.x; s[r][1] = v.y; s[r][2] = v.z; s[r][3] = v.w;
+                s[r][0] = make_float2(v.x, v.y);
+                s[r][1] = make_float2(v.z, v.w);
             } else {
                 const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.init) + st + r * NS);
-                s[r][0] = bf16_lo(v.x); s[r][1] = bf16_hi(v.x); s[r][2] = bf16_lo(v.y); s[r][3] = bf16_hi(v.y);
+                s[r][0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+                s[r][1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
             }
         }
     }
@@ -83,34 +88,41 @@ __global__ void __launch_bounds__(STEP_THREADS) kda_ssm_step_kernel(const SsmPar
     uint16_t *op = p.out + static_cast<long long>(sp.bos) * p.os + static_cast<long long>(h) * p.P + r0 + (lane >> 2);
     uint4 xn = make_uint4(0u, 0u, 0u, 0u);
     uint2 bn = make_uint2(0u, 0u), cn = bn;
-    uint32_t dn = 0u;
+    float deltas = 0.f, keeps = 0.f;  // of token 32 k + lane
     auto fetch = [&](int t) {  // token t's inputs, one token ahead of their use
         xn = *reinterpret_cast<const uint4 *>(xp + t * p.xs);
         bn = *reinterpret_cast<const uint2 *>(bp + t * p.bs);
         cn = *reinterpret_cast<const uint2 *>(cp + t * p.cs);
-        dn = dp[t * p.dts];
     };
+    // dt of 32 tokens, a lane each
+    auto fetch_dt = [&](int t) { return t + lane < sp.len ? static_cast<uint32_t>(dp[(t + lane) * p.dts]) : 0u; };
+    uint32_t dn = fetch_dt(0);
     if (sp.len > 0) fetch(0);
     for (int t = 0; t < sp.len; ++t) {
         float x[8];
         blk::unpack8(xn, x);
-        const float bf[4] = {bf16_lo(bn.x), bf16_hi(bn.x), bf16_lo(bn.y), bf16_hi(bn.y)};
-        const float cf[4] = {bf16_lo(cn.x), bf16_hi(cn.x), bf16_lo(cn.y), bf16_hi(cn.y)};
-        const float delta = softplus(__uint_as_float(dn << 16) + bias);
+        const float2 bf[2] = {make_float2(bf16_lo(bn.x), bf16_hi(bn.x)), make_float2(bf16_lo(bn.y), bf16_hi(bn.y))};
+        const float2 cf[2] = {make_float2(bf16_lo(cn.x), bf16_hi(cn.x)), make_float2(bf16_lo(cn.y), bf16_hi(cn.y))};
+        // x of row lane >> 2, whose output this lane may write
+        const uint32_t xw = lane & 16 ? (lane & 8 ? xn.w : xn.z) : (lane & 8 ? xn.y : xn.x);
+        const float xo = lane & 4 ? bf16_hi(xw) : bf16_lo(xw);
         if (t + 1 < sp.len) fetch(t + 1);
-        const float keep = exp2f(A2 * delta);
+        if ((t & 31) == 0) {
+            deltas = softplus(__uint_as_float(dn << 16) + bias);
+            keeps = exp2f(A2 * deltas);
+            dn = fetch_dt(t + 32);
+        }
+        const float delta = __shfl_sync(0xffffffffu, deltas, t & 31), keep = __shfl_sync(0xffffffffu, keeps, t & 31);
         float y[8];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const float dx = delta * x[r];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[r][j] = fmaf(keep, s[r][j], dx * bf[j]);
-            y[r] = fmaf(s[r][0], cf[0], fmaf(s[r][1], cf[1], fmaf(s[r][2], cf[2], s[r][3] * cf[3])));
+            for (int j = 0; j < 2; ++j) s[r][j] = ffma2(make_float2(keep, keep), s[r][j], fmul2(make_float2(dx, dx), bf[j]));
+            const float2 u = ffma2(s[r][0], cf[0], fmul2(s[r][1], cf[1]));
+            y[r] = u.x + u.y;
         }
         // reduce-scatter: lane l ends with the sum of row l >> 2
-        float xr[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) xr[r] = x[r];
 #pragma unroll
         for (int m = 16, n = 4; m >= 4; m >>= 1, n >>= 1) {
             const bool up = lane & m;
@@ -118,22 +130,21 @@ __global__ void __launch_bounds__(STEP_THREADS) kda_ssm_step_kernel(const SsmPar
             for (int i = 0; i < n; ++i) {
                 const float keepv = up ? y[i + n] : y[i], send = up ? y[i] : y[i + n];
                 y[i] = keepv + __shfl_xor_sync(0xffffffffu, send, m);
-                xr[i] = up ? xr[i + n] : xr[i];
             }
         }
         y[0] += __shfl_xor_sync(0xffffffffu, y[0], 2);
         y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
-        if ((lane & 3) == 0) op[t * p.os] = f2bf_bits(p.D ? fmaf(Dh, xr[0], y[0]) : y[0]);
+        if ((lane & 3) == 0) op[t * p.os] = f2bf_bits(p.D ? fmaf(Dh, xo, y[0]) : y[0]);
     }
     if (!p.fin) return;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
         if (gmem_ok(st + r * NS, 4, st_elems)) {
             if (p.fin_dtype == KDA_DTYPE_FP32)
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.fin) + st + r * NS) = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.fin) + st + r * NS) = make_float4(s[r][0].x, s[r][0].y, s[r][1].x, s[r][1].y);
             else
                 *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.fin) + st + r * NS) =
-                    make_uint2(pack_bf16(s[r][0], s[r][1]), pack_bf16(s[r][2], s[r][3]));
+                    make_uint2(pack_bf16(s[r][0].x, s[r][0].y), pack_bf16(s[r][1].x, s[r][1].y));
         }
 }
 
