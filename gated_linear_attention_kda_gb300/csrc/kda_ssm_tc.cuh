@@ -531,7 +531,8 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             for (int i = 0; i < 4; ++i) {
                 const bool live = j0 + i < Lv;
                 d[i] = live ? ssm::softplus(__uint_as_float(raw[i] << 16) + bias) : 0.f;
-                a[i] = live ? fmaxf(A2 * d[i], MIN_LOG2_DECAY) : 0.f;
+                const float u = A2 * d[i];  // held at the least decay by a comparison that lets NaN through (fmaxf would not)
+                a[i] = !live ? 0.f : u < MIN_LOG2_DECAY ? MIN_LOG2_DECAY : u;
             }
             fetch(n + 1);
             // running sums inside the lane, then over the eight lanes of a block, from both ends
