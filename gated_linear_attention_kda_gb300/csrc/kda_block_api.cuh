@@ -171,13 +171,13 @@ static bool rows_map(CUtensorMap *m, const void *base, int64_t tokens, int64_t g
 
 // Pieces of the time axis. One CTA walks a piece, so a call of fewer (sequence, head) pairs than SMs
 // leaves SMs idle unless sequences are cut. A cut call walks every chunk but the last pieces' twice: the first pass,
-// without the score and output products, takes 1.6 us a chunk, the second 2.75 us (heads of 64: 2.25). A CTA's start
+// without the score and output products, takes 1.6 us a chunk, the second 2.95 us (heads of 64: 2.35). A CTA's start
 // and end cost 6.2 us, CTAs follow one another in waves of one per SM, and the two more launches and the join some
 // 5 us. Chosen: the piece length with the least modelled time, 0 for no cut. Packed sequences are modelled by their
 // mean length; a longer one is cut into more pieces. fp32 states, uncut against the chosen cut:
-// 4 x 8192 tokens of 16 heads of 128 175.7 and 153.3 us, 1 x 4096 of 32 93.5 and 52.5, 1 x 131,072 of 32 2,700 and
-// 979, 1 x 2048 of 8 heads of 64 39.5 and 19.3. Where the model says no cut, a cut was slower: 6 x 16,384 of 16 heads
-// 346 uncut, 391 in three pieces; 1 x 2048 of 64 heads 50 uncut, 81 in eight; 2 x 4096 of 32 heads of 64 76 and 92.
+// 4 x 8192 tokens of 16 heads of 128 191 and 161 us, 1 x 4096 of 32 96 and 53, 1 x 131,072 of 32 2,923 and 1,039,
+// 1 x 2048 of 8 heads of 64 41.5 and 19.4, 2 x 4096 of 32 heads of 64 80 and 75. Where the model says no cut, a cut was
+// slower: 1 x 2048 of 64 heads of 128 takes 52 us uncut and 54 in two pieces.
 struct SsmPlan {
     int seg_chunks, seg_per_seq;
     int64_t slots;
@@ -189,7 +189,7 @@ static SsmPlan ssm_plan(int64_t states, int64_t tokens, int64_t H, int64_t P, in
     if (states < 1 || tokens < 1) return best;
     const int64_t units = states * H, mean = (tokens + states - 1) / states, nc = (mean + ssmtc::L - 1) / ssmtc::L;
     auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
-    const double full = P == 64 ? 2.25 : 2.75, states_only = 1.6, cta = 6.2, cut = 5.0;  // us: a chunk, a chunk, a CTA, a call
+    const double full = P == 64 ? 2.35 : 2.95, states_only = 1.6, cta = 6.2, cut = 5.0;  // us: a chunk, a chunk, a CTA, a call
     double cost = waves(units) * (full * nc + cta);
     for (int64_t s = 2; s <= nc && units * s <= 4 * static_cast<int64_t>(sms); ++s) {
         const int64_t seg = (nc + s - 1) / s, pieces = (nc + seg - 1) / seg;

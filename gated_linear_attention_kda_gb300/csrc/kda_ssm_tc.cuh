@@ -18,26 +18,33 @@
 // channel p), so that
 //   G  [128 x 128] = C B^T               both straight from their TMA tiles (K-major)
 //   Y  [128 x P]   = C S0^T              S0 rounded to bf16 in shared memory; rows then scaled in place
-//   Y             += (M + diag(D)) X     scores bf16 in tensor memory, X straight from its tile
+//   Y             += M X                 scores bf16 in tensor memory, X straight from its tile
 //   S             += (w B)^T X           w B as bf16 parts in tensor memory, transposed on the way
-// Roundings: M + diag(D) and S0 to bf16 as operands (the output is bf16; the carried state itself is
-// not rounded); w B into PARTS bf16 parts of 8 bits each: 3, exact, where an fp32 state is returned,
-// 2 (2^-17 of a term) where it is returned in bf16 or not at all. Sums are fp32.
+// and D X is added to Y in fp32 as the rows are written.
+// Roundings: M and S0 to bf16 as operands (the output is bf16; the carried state itself is not rounded);
+// w B into PARTS bf16 parts of 8 bits each: 3, exact, where an fp32 state is returned, 2 (2^-17 of a term)
+// where it is returned in bf16 or not at all. D is not rounded: on the diagonal of M it would lose sixteen
+// bits, by the same error for every token of a head, and a score that is small against D most of its own
+// (8 x 4096 tokens of 16 heads of 128 would take 96 us instead of 104, 16 packed prompts of 32 heads of 64
+// 269 instead of 286; the outputs' relative error would be 2.36e-3 instead of 2.10e-3, of which 1.66e-3 are
+// their own rounding). Sums are fp32.
 //
 // NaN: a product multiplies what the mask leaves out by zero, so a NaN or infinity in x (which is an MMA
 // operand as it stands) reaches its channel's outputs of the whole chunk. Finding such channels and making
-// them again token by token, or masking x on the way, was built and cost 12 to 19 % (8 x 4096 tokens of 16 heads:
-// 108 to 114 us against 95). In dt, b and c, which the warps handle, NaN reaches later tokens alone.
+// them again token by token, or masking x on the way, was built and cost 12 to 19 %. In dt, b and c, which the
+// warps handle, NaN reaches later tokens alone.
 //
-// What bounds it: 8 x 4096 tokens of 16 heads of 128 take 95 us (3.1 TB/s of HBM; 128 of the 152 SMs have a
-// state), about 5,800 cycles a chunk. Of these the MMAs take 3,072 (1,536 of them for the three parts of w B)
-// and shared memory 3,840: the MMAs read 256 KB of operands, TMA moves 128 KB and the warps 96 KB at 128 bytes a
+// What bounds it: 8 x 4096 tokens of 16 heads of 128 take 104 us (2.8 TB/s of HBM; 128 of the 152 SMs have a
+// state), about 6,300 cycles a chunk. Of these the MMAs take 3,072 (1,536 of them for the three parts of w B)
+// and shared memory 4,096: the MMAs read 256 KB of operands, TMA moves 128 KB and the warps 128 KB at 128 bytes a
 // cycle. w B goes through tensor memory for that reason: as a shared-memory operand it cost 160 KB more (149 us
 // then, 112 us with it). The rest is latency: a chunk's state chain (ST_GO, decay, S_GO, MMA) and its output
 // chain (G_DONE, M, M_GO, M X, Y_DONE, the next G) hand over at barriers, some 110 cycles each, and the warps' work
-// between them waits for tensor-memory loads while the roles share the issue slots (0.56 used). Measured and not
-// kept: one MMA issuer for all products (112 us); four state warps (102); C as a tensor-memory operand (116);
-// polling instead of suspended waits (149).
+// between them waits for tensor-memory and shared-memory loads while the roles share the issue slots. D X is added
+// by the warps that write the rows, from x loaded ahead of Y (113 us with x loaded beside Y, 117 with D X added as the
+// rows are scaled, 123 with one set of warps for both). Measured and not kept, each against 92 to 95 us when D still
+// lay on the diagonal: one MMA issuer for all products (112 us); four state warps (102); C as a tensor-memory operand
+// (116); polling instead of suspended waits (149); for heads of 128, rows written by the score warps (101).
 // Pieces (1 x 131,072 tokens, 32 heads): state pass 352 us, join 15 us, this pass 617 us.
 //
 // Warp roles (1024 threads; 896 for heads of 64):
@@ -46,9 +53,9 @@
 //   warp 2       step sizes, running sums and decays of a chunk, one chunk ahead
 //   warp 3       MMA issuer: state
 //   warps 4-11   scores G -> M (thread = token, two of the four 32-token blocks)
-//   warps 12-15  row scaling of C S0^T, then the output rows (thread = token); for heads of 64 the score warps
-//                do this too, half of the columns each (16 packed prompts, 32 heads: 275 us against 308; heads
-//                of 128, 8 x 4096 tokens: 101 us against 92)
+//                then row scaling of C S0^T, half of the columns each
+//   warps 12-15  the output rows (thread = token); for heads of 64 the score warps do this too, half of the
+//                columns each (16 packed prompts, 32 heads: 286 us against 300)
 //   then 8       state: bf16 copy for the next product, decay in place (state channel, half of the columns)
 //   last 8       w B, 32 tokens at a time (16 state channels per warp)
 // Warp 1 issues C S0^T, M X and the next chunk's C B^T; warp 3 the state product block by block as w B
@@ -247,11 +254,11 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             mbar_init(bar(Lay::C_FULL + i), 1);
             mbar_init(bar(Lay::C_EMPTY + i), 1);
             mbar_init(bar(Lay::SC_FULL + i), 1);
-            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 24 + Lay::EW : 16);
+            mbar_init(bar(Lay::SC_EMPTY + i), FULL ? 24 : 16);
         }
         for (int i : {Lay::G_DONE, Lay::YX_DONE, Lay::Y_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
         for (int i : {Lay::S_GO, Lay::X_ZERO}) mbar_init(bar(i), 8);
-        mbar_init(bar(Lay::M_GO), 8 + Lay::EW);
+        mbar_init(bar(Lay::M_GO), 8);
         mbar_init(bar(Lay::YX_GO), 8 + OUTW);
         mbar_init(bar(Lay::ST_GO), FULL ? 2 : 1);
         for (int i = 0; i < 4; ++i) {
@@ -284,11 +291,11 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
         if (lane == 0) mbar_arrive(bar(b));
     };
 
-    // The output's two steps, for a thread's token (quarter q, lane) and EC columns from c0.
-    // Y = C S0^T times the decay from the chunk's start to the token, in place:
+    // The output's two steps, for a thread's token (quarter q, lane).
+    // Y = C S0^T times the decay from the chunk's start to the token, in place, half of the columns:
     auto scale_rows = [&](uint32_t ly, float e) {
 #pragma unroll 1
-        for (int g4 = 0; g4 < Lay::EC / 32; ++g4) {
+        for (int g4 = 0; g4 < P / 64; ++g4) {
             uint32_t y[32];
             tc::ld32(ly + 32 * g4, y);
             tc::wait_ld();
@@ -304,14 +311,25 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
         tc::fence_before();
         arrive_w(Lay::M_GO);
     };
-    // Y to bf16, over the x tile (both products have read it) and from there to memory by TMA, 32 tokens per
-    // warp; a ragged end is stored from registers.
-    auto write_rows = [&](uint32_t ly, int n, int q, int c0) {
+    // Y + D x, summed in fp32, to bf16, over the x tile (both products have read it, and a thread reads its own elements
+    // of it first) and from there to memory by TMA, 32 tokens per warp; a ragged end is stored from registers.
+    const float Dh = p.D ? __ldg(p.D + h) : 0.f;
+    auto row_at = [&](int n, int row, int c) { return xt(n) + (c >> 6) * Lay::BOX + row * 128; };
+    auto group_at = [&](int row, int c, int i) { return ((((c >> 3) & 7) + i) ^ (row & 7)) << 4; };  // eight channels, swizzled by the row
+    auto load_x = [&](int n, int q, int c, uint4(&x)[4]) {  // channels c .. c + 31
+        const int row = 32 * q + lane;
+        const uint32_t xr = row_at(n, row, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = SM_AT(const uint4, xr + group_at(row, c, i));
+    };
+    // x holds the first 32 columns' elements already; the next ones' are loaded while these are stored.
+    auto write_rows = [&](uint32_t ly, int n, int q, int c0, uint4(&x)[4]) {
         const int row = 32 * q + lane, Lv = live_of(n);
-        const uint32_t xr = xt(n) + row * 128;
-        uint16_t *op = p.out + static_cast<long long>(pc.bos + n * L + row) * p.os + static_cast<long long>(h) * P + c0;
+        uint16_t *op = p.out + static_cast<long long>(pc.bos + n * L + row) * p.os + static_cast<long long>(h) * P;
 #pragma unroll 1
         for (int g4 = 0; g4 < Lay::EC / 32; ++g4) {
+            const int c = c0 + 32 * g4;
+            const uint32_t xr = row_at(n, row, c);
             uint32_t y[32], o[16];
             tc::ld32(ly + 32 * g4, y);
             tc::wait_ld();
@@ -320,15 +338,22 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 arrive_w(Lay::YX_GO);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
-            const int c8 = (c0 >> 3) + 4 * g4;  // first of four groups of eight channels
+            for (int i = 0; i < 4; ++i) {
+                float2 f[4];
+                blk::unpack8(x[i], f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = ffma2(make_float2(Dh, Dh), f[j], make_float2(__uint_as_float(y[8 * i + 2 * j]), __uint_as_float(y[8 * i + 2 * j + 1])));
+                    o[4 * i + j] = pack_bf16(v.x, v.y);
+                }
+            }
+            if (g4 + 1 < Lay::EC / 32) load_x(n, q, c + 32, x);
             if (Lv == L) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)  // 16 bytes each, swizzled by the row
-                    SM_AT(uint4, xr + (c8 >> 3) * Lay::BOX + ((((c8 & 7) + i) ^ (row & 7)) << 4)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 4; ++i) SM_AT(uint4, xr + group_at(row, c, i)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             } else if (row < Lv) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(op + 32 * g4)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(op + c)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
         }
         if (Lv == L) {
@@ -607,10 +632,9 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             // of G that it has read itself (the product takes M's halves from columns 0 and 64).
             const int q = warp & 3, row = 32 * q + lane, hf = warp < 8 ? 0 : 1;
             const uint32_t lb = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_G + 64 * hf;
-            const int c0 = hf * Lay::EC;  // output columns, where these warps write it
+            const int c0 = hf * (P / 2);  // Y columns that this warp scales and, for heads of 64, writes
             const uint32_t ly = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y + c0;
             if (Lay::MERGED) arrive_w(Lay::YX_GO);  // nothing of Y is waiting to be read
-            const float Dh = p.D ? __ldg(p.D + h) : 0.f;
             const int nfull = min(max(2 * (q - 2 * hf), 0), 4), nlive = min(max(2 * (q - 2 * hf) + 2, 0), 4);
             for (int n = 0; n < nch; ++n) {
                 if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1)) break;
@@ -620,6 +644,10 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 const float l1 = loc + (q == 3 && hf == 0 ? tot.z : 0.f);
                 const float e1 = ex2_approx(l1), e0 = ex2_approx(l1 + (q >= 2 && hf == 0 ? tot.y : 0.f));
                 uint32_t s = sc(n) + 256 * hf;
+                if constexpr (Lay::MERGED) {  // x is read as the rows are written: waited for here, ahead of the chain
+                    if (!wait_w(Lay::X_FULL + n % XS, (n / XS) & 1)) break;
+                    if (n > 0) release_rows(n - 1);
+                }
                 if (!wait_w(Lay::G_DONE, n & 1)) break;
                 tc::fence_after();
 #pragma unroll 1
@@ -658,11 +686,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                     }
                     tc::wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x = w[i] * __uint_as_float(g[i]);
-                        if (i == col) x += Dh;
-                        w[i] = i <= col ? x : 0.f;
-                    }
+                    for (int i = 0; i < 16; ++i) w[i] = i <= col ? w[i] * __uint_as_float(g[i]) : 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) m[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
                     tc::st8(lb + 8 * b, m);
@@ -673,20 +697,17 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                     for (int b = nlive; b < 4; ++b) tc::st8(lb + 8 * b, z);
                 }
                 tc::wait_st();
+                const float e = ex2_approx(loc + (q > 0 ? tot.x : 0.f) + (q > 1 ? tot.y : 0.f) + (q > 2 ? tot.z : 0.f));
+                arrive_w(Lay::SC_EMPTY + (n & 1));
+                if (!wait_w(Lay::YX_DONE, n & 1)) break;
+                tc::fence_after();
+                scale_rows(ly, e);
                 if constexpr (Lay::MERGED) {
-                    const float e = ex2_approx(loc + (q > 0 ? tot.x : 0.f) + (q > 1 ? tot.y : 0.f) + (q > 2 ? tot.z : 0.f));
-                    arrive_w(Lay::SC_EMPTY + (n & 1));
-                    if (n > 0) release_rows(n - 1);
-                    if (!wait_w(Lay::YX_DONE, n & 1)) break;
-                    tc::fence_after();
-                    scale_rows(ly, e);
+                    uint4 x[4];
+                    load_x(n, q, c0, x);
                     if (!wait_w(Lay::OUT_GO + n % XS, (n / XS) & 1)) break;
                     tc::fence_after();
-                    write_rows(ly, n, q, c0);
-                } else {
-                    tc::fence_before();
-                    arrive_w(Lay::M_GO);
-                    arrive_w(Lay::SC_EMPTY + (n & 1));
+                    write_rows(ly, n, q, c0, x);
                 }
             }
             if (Lay::MERGED && lane == 0) bulk_wait_all();
@@ -700,17 +721,12 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             const uint32_t ly = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_Y;
             arrive_w(Lay::YX_GO);  // nothing of Y is waiting to be read
             for (int n = 0; n < nch; ++n) {
-                if (!wait_w(Lay::SC_FULL + (n & 1), (n >> 1) & 1)) break;
-                const float4 tot = SM_AT(const float4, sc(n) + SC_TOT);
-                const float loc = SM_AT(const float, sc(n) + SC_LOC + 4 * (32 * q + lane));
-                const float e = ex2_approx(loc + (q > 0 ? tot.x : 0.f) + (q > 1 ? tot.y : 0.f) + (q > 2 ? tot.z : 0.f));
-                arrive_w(Lay::SC_EMPTY + (n & 1));
-                if (!wait_w(Lay::YX_DONE, n & 1)) break;
-                tc::fence_after();
-                scale_rows(ly, e);
+                if (!wait_w(Lay::X_FULL + n % XS, (n / XS) & 1)) break;
+                uint4 x[4];
+                load_x(n, q, 0, x);
                 if (!wait_w(Lay::OUT_GO + n % XS, (n / XS) & 1)) break;
                 tc::fence_after();
-                write_rows(ly, n, q, 0);
+                write_rows(ly, n, q, 0, x);
                 release_rows(n);
             }
             if (lane == 0) bulk_wait_all();

@@ -426,7 +426,8 @@ KDA_API kda_status kda_conv_step(const void *x, int64_t x_stride, const float *w
  * token in fp32. Longer ones run in chunks of 128 tokens, whose score matrix
  * and carried state are rounded to bf16 as operands of the output; the state
  * itself is held in fp32, and increments keep 24 bits where final_state is
- * fp32, 16 otherwise. A token's log2 decay is held at -160 or above.
+ * fp32, 16 otherwise. D x is formed and added in fp32 in either form. A
+ * token's log2 decay is held at -160 or above.
  * A NaN or infinity in x at one token can reach the outputs of up to 127
  * earlier tokens of the same sequence, head and channel (the tokens of a
  * chunk are one matrix product); it never reaches another sequence. What an
