@@ -29,10 +29,13 @@
 // 269 instead of 286; the outputs' relative error would be 2.36e-3 instead of 2.10e-3, of which 1.66e-3 are
 // their own rounding). Sums are fp32.
 //
-// NaN: a product multiplies what the mask leaves out by zero, so a NaN or infinity in x (which is an MMA
-// operand as it stands) reaches its channel's outputs of the whole chunk. Finding such channels and making
-// them again token by token, or masking x on the way, was built and cost 12 to 19 %. In dt, b and c, which the
-// warps handle, NaN reaches later tokens alone.
+// NaN: a product multiplies what the mask leaves out by zero, and 0 NaN is NaN, so a NaN or infinity in x (which is
+// an MMA operand as it stands) reaches its channel's outputs of the whole chunk. It also leaves no number in that
+// channel's state up to the end of the piece, where such channels show without a look at x. Their outputs ahead of the
+// first such x in its chunk are then made again in fp32 (finish_spoilt): only calls that hold such an x pay for it
+// (8 x 4096 tokens of 16 heads of 128, one NaN near the end of every sequence and head: 0.76 ms; in every channel
+// 2.1 ms). A scan of each x tile would cost every call 14 to 19 %. In dt, b and c, which the warps handle, NaN reaches
+// later tokens alone.
 //
 // What bounds it: 8 x 4096 tokens of 16 heads of 128 take 104 us (2.8 TB/s of HBM; 128 of the 152 SMs have a
 // state), about 6,300 cycles a chunk. Of these the MMAs take 3,072 (1,536 of them for the three parts of w B)
@@ -192,6 +195,198 @@ __device__ __forceinline__ int longest_first(const ssm::SsmParams &p, int rank)
     return found;
 }
 
+// The piece of the CTAs of one slot.
+__device__ __forceinline__ Piece piece_of(const TcParams &t, int slot)
+{
+    if (t.seg_chunks) return locate(t, slot);
+    const ssm::SsmParams &p = t.p;
+    const int seq = p.cu && p.nseq <= LPT_MAX_SEQS ? longest_first(p, slot) : slot;
+    const Span sp = ssm::ssm_span(p, seq);
+    return {seq, sp.bos, sp.len, sp.ok, true};
+}
+
+__device__ __forceinline__ bool no_number(uint32_t fp32_bits) { return (fp32_bits & 0x7f800000u) == 0x7f800000u; }
+
+// What is left of a piece when all its roles are done and some state of it is no number (every thread of the CTA), in
+// three steps. Each is out of line: this is rare, and the roles' registers are to stay as they are.
+// 1. The first token of every channel that `spoilt` names whose x is NaN or infinity, found row by row.
+template <int P, int WARPS>
+__device__ __noinline__ void find_spoilt(const ssm::SsmParams &p, const volatile uint32_t *spoilt, int *first, int bos, int len)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint16_t *xp = p.x + static_cast<long long>(bos) * p.xs + static_cast<long long>(blockIdx.x % p.H) * P;
+    constexpr int AHEAD = 8;  // loads in flight
+    for (int c = threadIdx.x; c < P; c += 32 * WARPS) first[c] = len;
+    __syncthreads();
+    constexpr int WORDS = P / 64;  // channel pairs per lane
+    for (int t0 = warp; t0 < len; t0 += WARPS * AHEAD) {
+        uint32_t x[AHEAD][WORDS];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) {
+                const int tok = t0 + WARPS * j;
+                x[j][k] = tok < len ? __ldg(reinterpret_cast<const uint32_t *>(xp + tok * p.xs) + 32 * k + lane) : 0u;
+            }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) {
+                const int c = 64 * k + 2 * lane;
+                const uint32_t m = (spoilt[c >> 5] >> (c & 31)) & ((no_number(x[j][k] << 16) ? 1u : 0u) | (no_number(x[j][k]) ? 2u : 0u));
+                if (m & 1u) atomicMin(first + c, t0 + WARPS * j);
+                if (m & 2u) atomicMin(first + c + 1, t0 + WARPS * j);
+            }
+    }
+}
+
+// 2. The outputs of such a channel from the start of that token's chunk up to the token, made again in fp32: a warp
+//    takes channels, four state channels per lane, through the tokens before the chunk and then through the chunk's.
+//    Channels whose x holds numbers only are left alone. Inputs are read as constants, so that loads run ahead of stores.
+template <int P, int WARPS>
+__device__ __noinline__ void repair_spoilt(const TcParams &t, const int *first, int seq, int bos, int len)
+{
+    const ssm::SsmParams &p = t.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H;
+    const size_t unit = static_cast<size_t>(seq) * p.H + h;
+    const uint16_t *xp = p.x + static_cast<long long>(bos) * p.xs + static_cast<long long>(h) * P;
+    constexpr int AHEAD = 8;  // loads in flight
+    constexpr int NC = (P + WARPS - 1) / WARPS;  // channels of a warp
+    int start[NC], stop[NC], last = 0;
+    float2 s[NC][2];
+    auto four = [](const uint16_t *src) { return __ldg(reinterpret_cast<const uint2 *>(src)); };  // of state channels
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+        const int c = warp + WARPS * k;
+        stop[k] = c < P && first[c] < len ? first[c] : 0;
+        start[k] = stop[k] / L * L;
+        last = max(last, stop[k] > start[k] ? start[k] : 0);
+        s[k][0] = s[k][1] = make_float2(0.f, 0.f);
+        if (stop[k] == start[k]) continue;
+        const size_t row = (unit * P + c) * NS + 4 * lane;
+        if (t.seg_chunks || (p.init && p.init_dtype == KDA_DTYPE_FP32)) {
+            const float4 v = *reinterpret_cast<const float4 *>(
+                t.seg_chunks ? t.ws + ((static_cast<size_t>(slot) * p.H + h) * P + c) * NS + 4 * lane : static_cast<const float *>(p.init) + row);
+            s[k][0] = make_float2(v.x, v.y);
+            s[k][1] = make_float2(v.z, v.w);
+        } else if (p.init) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.init) + row);
+            s[k][0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+            s[k][1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+        }
+    }
+    const float A2 = -expf(__ldg(p.A_log + h)) * LOG2E, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f, Dh = p.D ? __ldg(p.D + h) : 0.f;
+    const long long grp = static_cast<long long>(h / (p.H / p.G)) * NS + 4 * lane;
+    const uint16_t *dp = p.dt + static_cast<long long>(bos) * p.dts + h;
+    const uint16_t *bp = p.b + static_cast<long long>(bos) * p.bs + grp, *cp = p.c + static_cast<long long>(bos) * p.cs + grp;
+    uint16_t *op = p.out + static_cast<long long>(bos) * p.os + static_cast<long long>(h) * P;
+    uint32_t xn[NC], dn = 0u;  // of the lane's token of 32, fetched ahead
+    auto fetch = [&](int tok) {
+        dn = __ldg(dp + tok * p.dts);
+#pragma unroll
+        for (int k = 0; k < NC; ++k) xn[k] = warp + WARPS * k < P ? __ldg(xp + tok * p.xs + warp + WARPS * k) : 0u;
+    };
+    auto step = [](float2(&v)[2], float keep, float dx, const uint2 &b) {
+        v[0] = ffma2(make_float2(keep, keep), v[0], fmul2(make_float2(dx, dx), make_float2(bf16_lo(b.x), bf16_hi(b.x))));
+        v[1] = ffma2(make_float2(keep, keep), v[1], fmul2(make_float2(dx, dx), make_float2(bf16_lo(b.y), bf16_hi(b.y))));
+    };
+    if (last > 0) fetch(lane);
+    for (int t0 = 0; t0 < last; t0 += 32) {
+        const float delta = ssm::softplus(__uint_as_float(dn << 16) + bias), keep = exp2f(A2 * delta);
+        float dx[NC];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) dx[k] = delta * __uint_as_float(xn[k] << 16);
+        fetch(min(t0 + 32, last - 32) + lane);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += AHEAD) {
+            uint2 b[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) b[i] = four(bp + (t0 + i0 + i) * p.bs);
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                if (t0 >= start[k]) continue;
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) step(s[k], __shfl_sync(0xffffffffu, keep, i0 + i), __shfl_sync(0xffffffffu, dx[k], i0 + i), b[i]);
+            }
+        }
+    }
+#pragma unroll 1
+    for (int k = 0; k < NC; ++k) {
+        const int c = warp + WARPS * k;
+        float2 v[2] = {s[0][0], s[0][1]};
+        int from = start[0], to = stop[0];
+#pragma unroll
+        for (int j = 1; j < NC; ++j)
+            if (j == k) {
+                v[0] = s[j][0];
+                v[1] = s[j][1];
+                from = start[j];
+                to = stop[j];
+            }
+        for (int t0 = from; t0 < to; t0 += 32) {
+            const int n = min(32, to - t0), own = t0 + min(lane, n - 1);
+            const float x = __uint_as_float(static_cast<uint32_t>(__ldg(xp + own * p.xs + c)) << 16);
+            const float delta = ssm::softplus(__uint_as_float(static_cast<uint32_t>(__ldg(dp + own * p.dts)) << 16) + bias);
+            const float keep = exp2f(A2 * delta), dx = delta * x;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const uint2 b = four(bp + (t0 + i) * p.bs), q = four(cp + (t0 + i) * p.cs);
+                step(v, __shfl_sync(0xffffffffu, keep, i), __shfl_sync(0xffffffffu, dx, i), b);
+                const float2 u = ffma2(v[0], make_float2(bf16_lo(q.x), bf16_hi(q.x)), fmul2(v[1], make_float2(bf16_lo(q.y), bf16_hi(q.y))));
+                float y = u.x + u.y;
+#pragma unroll
+                for (int m = 16; m >= 1; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+                if (lane == i) op[(t0 + i) * p.os + c] = f2bf_bits(p.D ? fmaf(Dh, x, y) : y);
+            }
+        }
+    }
+}
+
+// 3. The final states that are no numbers, from tensor memory: until here they have left the initial state, maybe the
+//    same buffer, to step 2.
+template <int P, int WST>
+__device__ __noinline__ void store_spoilt(const ssm::SsmParams &p, int seq)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < WST || warp >= WST + 8) return;
+    const int q = warp & 3, c0 = warp < WST + 4 ? 0 : P / 2;
+    const size_t at0 = ((static_cast<size_t>(seq) * p.H + blockIdx.x % p.H) * P + c0) * NS + 32 * q + lane, st_elems = static_cast<size_t>(p.nseq) * p.H * P * NS;
+    __syncwarp();
+    tc::fence_after();
+#pragma unroll 1
+    for (int g4 = 0; g4 < P / 64; ++g4) {
+        uint32_t r[32];
+        tc::ld32((static_cast<uint32_t>(32 * q) << 16) + 128 + P + c0 + 32 * g4, r);
+        tc::wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const size_t at = at0 + static_cast<size_t>(32 * g4 + i) * NS;
+            if (!no_number(r[i]) || !gmem_ok(at, 1, st_elems)) continue;
+            if (p.fin_dtype == KDA_DTYPE_FP32)
+                static_cast<float *>(p.fin)[at] = __uint_as_float(r[i]);
+            else
+                static_cast<uint16_t *>(p.fin)[at] = f2bf_bits(__uint_as_float(r[i]));
+        }
+    }
+    tc::fence_before();
+}
+
+template <int P, int PARTS>
+__device__ __noinline__ void finish_spoilt(const TcParams &t, const volatile uint32_t *spoilt)
+{
+    using Lay = Layout<P, PARTS, true>;
+    constexpr int WARPS = Lay::NTHREADS / 32;
+    __shared__ int first[P];
+    const Piece pc = piece_of(t, blockIdx.x / t.p.H);
+    find_spoilt<P, WARPS>(t.p, spoilt, first, pc.bos, pc.len);
+    __syncthreads();
+    repair_spoilt<P, WARPS>(t, first, pc.seq, pc.bos, pc.len);
+    __syncthreads();
+    if (pc.last && t.p.fin) store_spoilt<P, Lay::WST>(t.p, pc.seq);
+    __syncthreads();
+}
+
 // FULL: outputs and states; else only the state that the piece leaves when it starts from zero (to
 // the workspace, with its decay), for the pieces that another one follows. That state is one sum over the
 // piece's tokens, each weighted by the decay from it to the piece's end, so the chunks are taken from the
@@ -200,7 +395,7 @@ __device__ __forceinline__ int longest_first(const ssm::SsmParams &p, int rank)
 template <int P, int PARTS, bool FULL>
 __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     kda_ssm_tc_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tb,
-                      const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap to, const TcParams t)
+                      const __grid_constant__ CUtensorMap tcm, const __grid_constant__ CUtensorMap to, const __grid_constant__ TcParams t)
 {
     using Lay = Layout<P, PARTS, FULL>;
     constexpr int CS = Lay::CS, XS = Lay::XS, BS = Lay::BS, OUTW = Lay::MERGED ? 8 : 4;  // OUTW: warps that write the output
@@ -213,20 +408,14 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     const ssm::SsmParams &p = t.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H;
-    Piece pc;
-    if (t.seg_chunks) {
-        pc = locate(t, slot);
-    } else {
-        const int seq = p.cu && p.nseq <= LPT_MAX_SEQS ? longest_first(p, slot) : slot;
-        const Span sp = ssm::ssm_span(p, seq);
-        pc = {seq, sp.bos, sp.len, sp.ok, true};
-    }
+    const Piece pc = piece_of(t, slot);
     if (FULL && p.cu && blockIdx.x == 0) blk::check_bounds(p.cu, p.nseq, p.total);
     if (!pc.ok || (!FULL && pc.last)) return;  // CTA-uniform, before any tensor memory is taken
     const int nch = (pc.len + L - 1) / L;
     const int grp = h / (p.H / p.G);
 
     volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
+    __shared__ volatile uint32_t spoilt[5];  // a bit per channel: its state holds no number; last word: some state is none
     auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
     auto xt = [&](int n) { return sb + Lay::X + (n % XS) * Lay::XT; };
     auto bt = [&](int n) { return sb + Lay::B + (n % BS) * Lay::BT; };
@@ -266,6 +455,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             mbar_init(bar(Lay::W_EMPTY + i), 1);
         }
         flags[0] = 0;
+        for (int i = 0; i < 5; ++i) spoilt[i] = 0u;
         fence_mbar_init();
     }
     tc::fence_before();
@@ -624,6 +814,25 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             tc::commit_w(bar(Lay::END2));
             if (lane == 0) drain_bar(bar(Lay::END2), 0);
             __syncwarp();
+            // NaN or infinity in x leaves no number in its whole column of the state, and for good (0 NaN and 0 inf are
+            // NaN): this warp's lanes show it.
+            if (FULL && ok) {
+                tc::fence_after();
+#pragma unroll 1
+                for (int g4 = 0; g4 < P / 32; ++g4) {
+                    uint32_t r[32], m = 0u;
+                    tc::ld32(tmem + (static_cast<uint32_t>(32 * 3) << 16) + T_S + 32 * g4, r);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) m |= no_number(r[i]) ? 1u << i : 0u;
+                    m = __reduce_and_sync(0xffffffffu, m);
+                    if (lane == 0) {
+                        spoilt[g4] = m;
+                        if (m) spoilt[4] = 1u;
+                    }
+                }
+                tc::fence_before();
+            }
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------- scores
@@ -822,6 +1031,8 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                     const size_t at = static_cast<size_t>(c0 + 32 * g4 + i) * NS;
                     if constexpr (!FULL)
                         wsp[at] = __uint_as_float(r[i]);
+                    else if (nch > 0 && no_number(r[i]))  // stored at the very end, see finish_spoilt
+                        spoilt[4] = 1u;
                     else if (!gmem_ok(unit * P * NS + at + nn, 1, st_elems))
                         continue;
                     else if (p.fin_dtype == KDA_DTYPE_FP32)
@@ -838,6 +1049,10 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
 
     tc::fence_before();
     __syncthreads();
+    if constexpr (FULL)
+        if (spoilt[4])
+            finish_spoilt<P, PARTS>(t, spoilt);
+
     if (warp == 0) {
         tc::fence_after();
         tc::dealloc(tmem, TMEM_COLS);

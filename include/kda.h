@@ -428,10 +428,11 @@ KDA_API kda_status kda_conv_step(const void *x, int64_t x_stride, const float *w
  * itself is held in fp32, and increments keep 24 bits where final_state is
  * fp32, 16 otherwise. D x is formed and added in fp32 in either form. A
  * token's log2 decay is held at -160 or above.
- * A NaN or infinity in x at one token can reach the outputs of up to 127
- * earlier tokens of the same sequence, head and channel (the tokens of a
- * chunk are one matrix product); it never reaches another sequence. What an
- * infinity reaches may come out as NaN.
+ * A NaN or infinity in x reaches its own channel's outputs and state from its
+ * token on, in dt, b, c or a parameter what the formulas say; it never reaches
+ * an earlier token or another sequence. What an infinity reaches may come out
+ * as NaN. Calls of chunks whose x holds such a value take longer: outputs ahead
+ * of it in its chunk are made again from the start of the sequence.
  */
 KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const void *b,
                            int64_t b_stride, const void *c, int64_t c_stride, const float *A_log, const float *D,
