@@ -1,6 +1,7 @@
 // kda_block_api.cuh -- host side of the operators around the mixer (include/kda.h): argument
 // checks, launch shapes and launches. Included by kda_fwd.cu, whose error reporting it uses.
 #pragma once
+#include <initializer_list>
 #include <type_traits>
 
 #include "kda_conv.cuh"
@@ -17,21 +18,42 @@ struct Rows {
     int64_t stride, width, tokens;
 };
 
+// A contiguous buffer.
+static Rows block(const void *base, int64_t bytes) { return {base, bytes, bytes, 1}; }
+
 // Whether two strided tensors share an element. Rows of one stride may interleave (slices of one
-// wider row); of different strides, overlapping ranges count as shared.
+// wider row), and a block may lie between rows; of different strides, overlapping ranges count as shared.
 static bool share(const Rows &a, const Rows &b)
 {
     if (!a.base || !b.base || a.tokens < 1 || b.tokens < 1) return false;
+    if (a.tokens > 1 && b.tokens == 1) return share(b, a);
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.base), b0 = reinterpret_cast<uintptr_t>(b.base);
     const uintptr_t a1 = a0 + static_cast<uintptr_t>((a.tokens - 1) * a.stride + a.width);
     const uintptr_t b1 = b0 + static_cast<uintptr_t>((b.tokens - 1) * b.stride + b.width);
     if (a1 <= b0 || b1 <= a0) return false;
+    if (a.tokens == 1) {  // the first row that ends behind the block's start
+        const uintptr_t row = a0 < b0 + b.width ? 0 : (a0 - b0 - b.width) / b.stride + 1;
+        return row < static_cast<uintptr_t>(b.tokens) && b0 + row * b.stride < a1;
+    }
     if (a.stride != b.stride) return true;
     const int64_t d = static_cast<int64_t>(b0 - a0) % a.stride, off = d < 0 ? d + a.stride : d;
     return !(off >= a.width && off + b.width <= a.stride);
 }
 // The same elements in the same places (an element-wise kernel may write over its input).
 static bool same(const Rows &a, const Rows &b) { return a.base == b.base && (a.stride == b.stride || a.tokens <= 1); }
+
+// A buffer that a call writes against others of the call.
+struct Named {
+    const char *name;
+    Rows rows;
+};
+static kda_status check_apart(const Named &written, std::initializer_list<Named> others)
+{
+    for (const Named &o : others)
+        if (share(written.rows, o.rows)) return fail(KDA_ERR_STATE_MISMATCH, "%s must not share memory with %s", written.name, o.name);
+    return KDA_OK;
+}
+static Named bounds_of(const int64_t *cu, int64_t N) { return {"cu_seqlens", block(cu, 8 * (N + 1))}; }
 
 static bool stride_ok(int64_t stride, int64_t elems, int64_t multiple)
 {
@@ -139,6 +161,20 @@ static kda_status check_ssm(const void *x, int64_t xs, const void *dt, int64_t d
         return fail(KDA_ERR_ALIGN, "x, b, c and out must be 16-byte, dt 2-byte aligned");
     return KDA_OK;
 }
+
+// The buffers of a scan but for its states and workspace.
+struct SsmBuffers {
+    Named x, dt, b, c, A_log, D, dt_bias, out, cu;
+    SsmBuffers(const void *x, int64_t xs, const void *dt, int64_t dts, const void *b, int64_t bs, const void *c, int64_t cs, const float *A_log,
+               const float *D, const float *dt_bias, const void *out, int64_t os, const int64_t *cu, int64_t N, int64_t tokens, int64_t H, int64_t P, int64_t GK)
+        : x{"x", {x, 2 * xs, 2 * H * P, tokens}}, dt{"dt", {dt, 2 * dts, 2 * H, tokens}}, b{"b", {b, 2 * bs, 2 * GK, tokens}},
+          c{"c", {c, 2 * cs, 2 * GK, tokens}}, A_log{"A_log", block(A_log, 4 * H)}, D{"D", block(D, 4 * H)}, dt_bias{"dt_bias", block(dt_bias, 4 * H)},
+          out{"out", {out, 2 * os, 2 * H * P, tokens}}, cu(bounds_of(cu, N))
+    {
+    }
+    kda_status check_out(const Named &state) const { return check_apart(out, {x, dt, b, c, A_log, D, dt_bias, cu, state}); }
+    kda_status check_other(const Named &written) const { return check_apart(written, {x, dt, b, c, A_log, D, dt_bias, cu, out}); }
+};
 
 // Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one: 8 heads of
 // 64, one sequence, 8 tokens 5.2 against 6.2 us, 16 tokens 7.8 against 6.3; 64 sequences of 16 heads of 128, 8
@@ -346,8 +382,15 @@ KDA_API kda_status kda_conv(const void *x, int64_t x_stride, const float *weight
     if (!aligned(initial_state, 16) || !aligned(final_state, 16)) return fail(KDA_ERR_ALIGN, "state buffers must be 16-byte aligned");
     if (blk::share({x, 2 * x_stride, 2 * C, total}, {out, 2 * out_stride, 2 * C, total}))
         return fail(KDA_ERR_STATE_MISMATCH, "out must not share memory with x");
-    if (blk::partial_overlap(initial_state, final_state, nseq * (W - 1) * C * 2))
+    const int64_t state_bytes = nseq * (W - 1) * C * 2;
+    if (blk::partial_overlap(initial_state, final_state, state_bytes))
         return fail(KDA_ERR_STATE_MISMATCH, "initial_state and final_state overlap partially");
+    {
+        const blk::Named orow{"out", {out, 2 * out_stride, 2 * C, total}}, xrow{"x", {x, 2 * x_stride, 2 * C, total}};
+        const blk::Named w{"weight", blk::block(weight, 4 * C * W)}, bs{"bias", blk::block(bias, 4 * C)}, cu = blk::bounds_of(cu_seqlens, N);
+        if (const kda_status st = blk::check_apart(orow, {{"initial_state", blk::block(initial_state, state_bytes)}, w, bs, cu}); st != KDA_OK) return st;
+        if (const kda_status st = blk::check_apart({"final_state", blk::block(final_state, state_bytes)}, {xrow, orow, w, bs, cu}); st != KDA_OK) return st;
+    }
     conv::ConvParams p = {};
     p.x = static_cast<const uint16_t *>(x);
     p.init = static_cast<const uint16_t *>(initial_state);
@@ -393,6 +436,11 @@ KDA_API kda_status kda_conv_step(const void *x, int64_t x_stride, const float *w
     if (!aligned(state, 16)) return fail(KDA_ERR_ALIGN, "state must be 16-byte aligned");
     const blk::Rows xr{x, 2 * x_stride, 2 * C, S}, orow{out, 2 * out_stride, 2 * C, S};
     if (!blk::same(xr, orow) && blk::share(xr, orow)) return fail(KDA_ERR_STATE_MISMATCH, "out must be x or share no memory with it");
+    {
+        const blk::Named w{"weight", blk::block(weight, 4 * C * W)}, bs{"bias", blk::block(bias, 4 * C)};
+        if (const kda_status st = blk::check_apart({"out", orow}, {w, bs}); st != KDA_OK) return st;
+        if (const kda_status st = blk::check_apart({"state", blk::block(state, S * (W - 1) * C * 2)}, {{"x", xr}, {"out", orow}, w, bs}); st != KDA_OK) return st;
+    }
     conv::ConvParams p = {};
     p.x = static_cast<const uint16_t *>(x);
     p.out = static_cast<uint16_t *>(out);
@@ -440,15 +488,16 @@ KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int6
         return fail(KDA_ERR_DTYPE, "state dtype codes must be BF16/FP32 for a given buffer and NONE for an absent one");
     if (!aligned(initial_state, 16) || !aligned(final_state, 16)) return fail(KDA_ERR_ALIGN, "state buffers must be 16-byte aligned");
     if (workspace && !aligned(workspace, 16)) return fail(KDA_ERR_ALIGN, "workspace must be 16-byte aligned");
+    auto state_block = [&](const void *ptr, kda_dtype d) { return blk::block(ptr, nseq * H * P * K * (d == KDA_DTYPE_FP32 ? 4 : 2)); };
     if (initial_state && final_state) {
         if (initial_dtype != final_dtype) return fail(KDA_ERR_STATE_MISMATCH, "final_state must match initial_state's dtype");
-        if (blk::partial_overlap(initial_state, final_state, nseq * H * P * K * (initial_dtype == KDA_DTYPE_FP32 ? 4 : 2)))
+        if (blk::partial_overlap(initial_state, final_state, state_block(initial_state, initial_dtype).width))
             return fail(KDA_ERR_STATE_MISMATCH, "initial_state and final_state overlap partially");
     }
-    const blk::Rows orow{out, 2 * out_stride, 2 * H * P, total};
-    if (blk::share(orow, {x, 2 * x_stride, 2 * H * P, total}) || blk::share(orow, {b, 2 * b_stride, 2 * G * K, total}) ||
-        blk::share(orow, {c, 2 * c_stride, 2 * G * K, total}) || blk::share(orow, {dt, 2 * dt_stride, 2 * H, total}))
-        return fail(KDA_ERR_STATE_MISMATCH, "out must not share memory with x, b, c or dt");
+    const blk::SsmBuffers bufs(x, x_stride, dt, dt_stride, b, b_stride, c, c_stride, A_log, D, dt_bias, out, out_stride, cu_seqlens, N, total, H, P, G * K);
+    const blk::Named init{"initial_state", state_block(initial_state, initial_dtype)}, fin{"final_state", state_block(final_state, final_dtype)};
+    if (const kda_status st = bufs.check_out(init); st != KDA_OK) return st;
+    if (const kda_status st = bufs.check_other(fin); st != KDA_OK) return st;
     ssm::SsmParams p = {};
     p.x = static_cast<const uint16_t *>(x);
     p.dt = static_cast<const uint16_t *>(dt);
@@ -484,6 +533,11 @@ KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int6
     }
     if (workspace && workspace_bytes < plan.bytes)
         return fail(KDA_ERR_RANGE, "workspace of %zu bytes is smaller than the %zu this call needs", workspace_bytes, plan.bytes);
+    if (workspace && plan.bytes) {
+        const blk::Named ws{"workspace", blk::block(workspace, static_cast<int64_t>(plan.bytes))};
+        if (const kda_status st = bufs.check_other(ws); st != KDA_OK) return st;
+        if (const kda_status st = blk::check_apart(ws, {init, fin}); st != KDA_OK) return st;
+    }
     float *ws = static_cast<float *>(workspace);
     return P == 64 ? blk::launch_ssm<64>(p, plan, ws, s) : blk::launch_ssm<128>(p, plan, ws, s);
 }
@@ -501,10 +555,10 @@ KDA_API kda_status kda_ssm_step(const void *x, int64_t x_stride, const void *dt,
     if (!state) return fail(KDA_ERR_NULL, "state is required");
     if (state_dtype != KDA_DTYPE_BF16 && state_dtype != KDA_DTYPE_FP32) return fail(KDA_ERR_DTYPE, "state dtype must be BF16 or FP32");
     if (!aligned(state, 16)) return fail(KDA_ERR_ALIGN, "state must be 16-byte aligned");
-    const blk::Rows orow{out, 2 * out_stride, 2 * H * P, S};
-    if (blk::share(orow, {x, 2 * x_stride, 2 * H * P, S}) || blk::share(orow, {b, 2 * b_stride, 2 * G * K, S}) ||
-        blk::share(orow, {c, 2 * c_stride, 2 * G * K, S}) || blk::share(orow, {dt, 2 * dt_stride, 2 * H, S}))
-        return fail(KDA_ERR_STATE_MISMATCH, "out must not share memory with x, b, c or dt");
+    const blk::SsmBuffers bufs(x, x_stride, dt, dt_stride, b, b_stride, c, c_stride, A_log, D, dt_bias, out, out_stride, nullptr, 0, S, H, P, G * K);
+    const blk::Named st_buf{"state", blk::block(state, S * H * P * K * (state_dtype == KDA_DTYPE_FP32 ? 4 : 2))};
+    if (const kda_status st = bufs.check_out(st_buf); st != KDA_OK) return st;
+    if (const kda_status st = bufs.check_other(st_buf); st != KDA_OK) return st;
     ssm::SsmParams p = {};
     p.x = static_cast<const uint16_t *>(x);
     p.dt = static_cast<const uint16_t *>(dt);
@@ -549,6 +603,7 @@ KDA_API kda_status kda_gated_norm(const void *x, int64_t x_stride, const void *g
     const blk::Rows orow{out, 2 * out_stride, 2 * R * D, M}, xr{x, 2 * x_stride, 2 * R * D, M}, zr{gate, 2 * gate_stride, 2 * R * D, M};
     if ((!blk::same(orow, xr) && blk::share(orow, xr)) || (!blk::same(orow, zr) && blk::share(orow, zr)))
         return fail(KDA_ERR_STATE_MISMATCH, "out must be x, gate, or share no memory with them");
+    if (const kda_status st = blk::check_apart({"out", orow}, {{"weight", blk::block(weight, 4 * weight_rows * D)}}); st != KDA_OK) return st;
     blk::Device d;
     if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
     norm::GatedParams p = {};
@@ -600,6 +655,11 @@ KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void
     if (clash(orow, xr) || clash(orow, zr) || blk::share(orow, rr) || blk::share(orow, ror) || clash(ror, rr) ||
         blk::share(ror, xr) || blk::share(ror, zr))
         return fail(KDA_ERR_STATE_MISMATCH, "out may be x or gate and residual_out may be residual; no other buffers share memory");
+    {
+        const blk::Named pw{"post_weight", blk::block(post_weight, 4 * D)}, ch{"channel_scale", blk::block(channel_scale, 4 * D)}, w{"weight", blk::block(weight, 4 * D)};
+        if (const kda_status st = blk::check_apart({"out", orow}, {pw, ch, w}); st != KDA_OK) return st;
+        if (const kda_status st = blk::check_apart({"residual_out", ror}, {pw, ch, w}); st != KDA_OK) return st;
+    }
     blk::Device d;
     if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
     norm::ResidualParams p = {};

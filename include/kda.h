@@ -360,6 +360,10 @@ KDA_API kda_status kda_decode_ex(const void *q, const void *k, const void *v, co
  * and the tokens of batch row b follow those of row b - 1 at the same
  * distance. Strides are >= the elements of one token and, like base pointers,
  * multiples of 16 bytes (dt: any stride).
+ * A buffer that a call writes (out, residual_out, a final or in-place state,
+ * the bytes of the workspace that it needs) shares no memory with any other
+ * buffer of the call, but for the pairs that an entry point names
+ * (KDA_ERR_STATE_MISMATCH). Tensors may lie between the rows of a strided one.
  */
 typedef enum kda_act {
     KDA_ACT_NONE = 0,            /* z */
