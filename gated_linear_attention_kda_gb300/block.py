@@ -179,7 +179,8 @@ def _ssm_args(x, dt, b, c, out, A_log, D, dt_bias, lead, dev):
 def ssm_workspace_bytes(states, tokens, H, P) -> int:
     """Bytes of workspace with which ``ssm`` may split the time axis of a call with ``states``
     sequences, ``tokens`` tokens in all and ``H`` heads of ``P`` channels on the current device
-    (0: it would not split)."""
+    (0: it would not split). Never more than 24 x SMs x (128 P + 1), so that one buffer of that
+    size serves calls of any sizes."""
     n = _Z(0)
     _raise(_lib.kda_ssm_workspace_bytes(int(states), int(tokens), int(H), int(P), ctypes.byref(n)))
     return int(n.value)

@@ -237,6 +237,7 @@ static SsmPlan ssm_plan(int64_t states, int64_t tokens, int64_t H, int64_t P, in
         }
     }
     if (best.seg_chunks) {
+        // slots x H is at most units x (pieces + 1): units x pieces within 4 SMs' worth, two pieces at least, so 6 x SMs in all
         best.slots = tokens / (static_cast<int64_t>(ssmtc::L) * best.seg_chunks) + states;
         best.bytes = static_cast<size_t>(best.slots) * H * (P * ssm::NS + 1) * sizeof(float);
     }

@@ -449,7 +449,10 @@ KDA_API kda_status kda_ssm(const void *x, int64_t x_stride, const void *dt, int6
  * kda_ssm_workspace_bytes -- the workspace with which kda_ssm may split the
  * time axis of a call with `states` sequences (N in varlen mode, else B),
  * `tokens` tokens in all (B * T) and H heads of P channels on the current
- * device; 0 when it would not split. Needs a CUDA device.
+ * device; 0 when it would not split. It neither rises nor falls with the sizes
+ * in order, but never passes 24 x (SMs of the device) x (P K + 1): one buffer
+ * of that many bytes (60 MB on a GB300 for P = 128) serves every call. Needs a
+ * CUDA device.
  */
 KDA_API kda_status kda_ssm_workspace_bytes(int64_t states, int64_t tokens, int64_t H, int64_t P, size_t *bytes);
 
