@@ -35,6 +35,12 @@ struct ConvParams {
     int run;                // tokens per thread
 };
 
+// Eight channels of a token row, `stride` elements apart, lie in a tensor of `rows` rows (the checked build looks).
+__device__ __forceinline__ bool row_ok(long long row, int c, long long rows, long long stride, int C)
+{
+    return gmem_ok(static_cast<size_t>(row * stride + c), 8, static_cast<size_t>((rows - 1) * stride + C));
+}
+
 // Eight channels as four pairs (paired fp32 arithmetic).
 struct Row {
     float2 v[4];
@@ -102,9 +108,9 @@ __device__ __forceinline__ void write_final(const ConvParams &p, int seq, int c)
     for (int j = 0; j < W - 1; ++j) {
         const long long at = len + j;  // row of [init ; x]
         row[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= W - 1)
-            row[j] = *reinterpret_cast<const uint4 *>(p.x + (b + at - (W - 1)) * p.xs + c);
-        else if (p.init && gmem_ok(st + at * p.C, 8, st_elems))
+        if (at >= W - 1) {
+            if (row_ok(b + at - (W - 1), c, p.total, p.xs, p.C)) row[j] = *reinterpret_cast<const uint4 *>(p.x + (b + at - (W - 1)) * p.xs + c);
+        } else if (p.init && gmem_ok(st + at * p.C, 8, st_elems))
             row[j] = *reinterpret_cast<const uint4 *>(p.init + st + at * p.C);
     }
 #pragma unroll
@@ -150,12 +156,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) kda_conv_kernel(const ConvPar
         const uint16_t *src = p.x + t * p.xs + c;
         uint16_t *dst = p.out + t * p.os + c;
         int n = static_cast<int>(end - t);  // tokens of this sequence in the run
+        long long tok = t;                  // of src and dst
         uint4 raw[BATCH];
         auto fetch = [&] {
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 raw[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (i < n) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + i * p.xs));
+                if (i < n && row_ok(tok + i, c, p.total, p.xs, p.C)) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + i * p.xs));
             }
         };
         fetch();
@@ -164,11 +171,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) kda_conv_kernel(const ConvPar
         for (int j = 0; j < W - 1; ++j) {
             const long long at = t - (W - 1) + j;
             uint4 r = make_uint4(0u, 0u, 0u, 0u);
-            if (at >= sq.b)
-                r = __ldg(reinterpret_cast<const uint4 *>(p.x + at * p.xs + c));
-            else if (p.init)
-                r = *reinterpret_cast<const uint4 *>(
-                    p.init + (static_cast<size_t>(sq.seq) * (W - 1) + static_cast<size_t>(at - sq.b + (W - 1))) * p.C + c);
+            if (at >= sq.b) {
+                if (row_ok(at, c, p.total, p.xs, p.C)) r = __ldg(reinterpret_cast<const uint4 *>(p.x + at * p.xs + c));
+            } else if (p.init) {
+                const size_t st = (static_cast<size_t>(sq.seq) * (W - 1) + static_cast<size_t>(at - sq.b + (W - 1))) * p.C + c;
+                if (gmem_ok(st, 8, static_cast<size_t>(p.nseq) * (W - 1) * p.C)) r = *reinterpret_cast<const uint4 *>(p.init + st);
+            }
             f[j] = unpack(r);
         }
 #pragma unroll 1
@@ -178,10 +186,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) kda_conv_kernel(const ConvPar
             const int m = n;
             n -= BATCH;
             src += BATCH * p.xs;
+            tok += BATCH;
             fetch();  // the next batch's rows are in flight while this one is filtered
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
-                if (i < m) *reinterpret_cast<uint4 *>(dst + i * p.os) = taps.row(f + i, silu);
+                if (i < m && row_ok(tok - BATCH + i, c, p.total, p.os, p.C)) *reinterpret_cast<uint4 *>(dst + i * p.os) = taps.row(f + i, silu);
             dst += BATCH * p.os;
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) f[j] = f[BATCH + j];
@@ -203,13 +212,15 @@ __global__ void __launch_bounds__(THREADS) kda_conv_step_kernel(const ConvParams
     if (s0 >= p.nseq) return;
     const int c = static_cast<int>(i % nc8) * 8;
     uint16_t *st = state + s0 * (W - 1) * p.C + c;
-    uint4 raw[STEP_SEQS][W];
+    auto st_ok = [&](int k, int j) { return gmem_ok(static_cast<size_t>((s0 + k) * (W - 1) + j) * p.C + c, 8, static_cast<size_t>(p.nseq) * (W - 1) * p.C); };
+    uint4 raw[STEP_SEQS][W] = {};
 #pragma unroll
     for (int k = 0; k < STEP_SEQS; ++k)
         if (s0 + k < p.nseq) {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) raw[k][j] = *reinterpret_cast<const uint4 *>(st + static_cast<size_t>(k * (W - 1) + j) * p.C);
-            raw[k][W - 1] = *reinterpret_cast<const uint4 *>(p.x + (s0 + k) * p.xs + c);
+            for (int j = 0; j < W - 1; ++j)
+                if (st_ok(k, j)) raw[k][j] = *reinterpret_cast<const uint4 *>(st + static_cast<size_t>(k * (W - 1) + j) * p.C);
+            if (row_ok(s0 + k, c, p.nseq, p.xs, p.C)) raw[k][W - 1] = *reinterpret_cast<const uint4 *>(p.x + (s0 + k) * p.xs + c);
         }
     Taps<W> taps;
     taps.load(p.weight, p.bias, c);
@@ -219,10 +230,10 @@ __global__ void __launch_bounds__(THREADS) kda_conv_step_kernel(const ConvParams
             Row f[W];
 #pragma unroll
             for (int j = 0; j < W; ++j) f[j] = unpack(raw[k][j]);
-            *reinterpret_cast<uint4 *>(p.out + (s0 + k) * p.os + c) = taps.row(f, p.act == KDA_ACT_SILU);
+            if (row_ok(s0 + k, c, p.nseq, p.os, p.C)) *reinterpret_cast<uint4 *>(p.out + (s0 + k) * p.os + c) = taps.row(f, p.act == KDA_ACT_SILU);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
-                *reinterpret_cast<uint4 *>(st + static_cast<size_t>(k * (W - 1) + j) * p.C) = raw[k][j + 1];
+                if (st_ok(k, j)) *reinterpret_cast<uint4 *>(st + static_cast<size_t>(k * (W - 1) + j) * p.C) = raw[k][j + 1];
         }
 }
 

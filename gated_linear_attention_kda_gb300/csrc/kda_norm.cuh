@@ -18,6 +18,12 @@ constexpr int WARP_THREADS = 128;  // CTA of the warp-group form
 constexpr int CTA_THREADS = 512;   // most threads of the CTA form
 constexpr int MAX_D = 16384;       // CTA_THREADS x 4 vectors of 8
 
+// Eight channels at `at` of a tensor whose `rows` rows of `width` elements lie `stride` apart (the checked build looks)
+__device__ __forceinline__ bool vec_ok(long long at, long long rows, long long stride, long long width)
+{
+    return gmem_ok(static_cast<size_t>(at), 8, static_cast<size_t>((rows - 1) * stride + width));
+}
+
 // Threads that share a row, and where this thread stands among them. CTA: the whole block, with
 // two alternating rows of partial sums so that one barrier per sum is enough.
 template <bool CTA>
@@ -95,13 +101,15 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS, !CTA && VPT 
             ++mm;
         }
     };
+    const long long tokens = p.rows / p.R, width = static_cast<long long>(p.R) * p.D;
     auto fetch = [&](long long row, long long m, int r) {  // channels and rows that are not there count as zeros
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             xn[v] = zn[v] = make_uint4(0u, 0u, 0u, 0u);
             if (row < p.rows && live[v]) {
-                xn[v] = *reinterpret_cast<const uint4 *>(p.x + m * p.xs + static_cast<long long>(r) * p.D + c[v]);
-                zn[v] = *reinterpret_cast<const uint4 *>(p.z + m * p.zs + static_cast<long long>(r) * p.D + c[v]);
+                const long long at = static_cast<long long>(r) * p.D + c[v];
+                if (vec_ok(m * p.xs + at, tokens, p.xs, width)) xn[v] = *reinterpret_cast<const uint4 *>(p.x + m * p.xs + at);
+                if (vec_ok(m * p.zs + at, tokens, p.zs, width)) zn[v] = *reinterpret_cast<const uint4 *>(p.z + m * p.zs + at);
             }
         }
     };
@@ -140,7 +148,8 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS, !CTA && VPT 
                     o[i] = fmul2(fmul2(x[v][i], make_float2(inv, inv)), w[v][i]);
                     if (!FIRST) o[i] = fmul2(o[i], z[v][i]);
                 }
-                *reinterpret_cast<uint4 *>(p.out + m * p.os + static_cast<long long>(r) * p.D + c[v]) = blk::pack8(o);
+                const long long at = m * p.os + static_cast<long long>(r) * p.D + c[v];
+                if (vec_ok(at, tokens, p.os, width)) *reinterpret_cast<uint4 *>(p.out + at) = blk::pack8(o);
             }
         }
         advance(m, r);
@@ -185,11 +194,13 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_residual
 #pragma unroll
             for (int k = 0; k < RV; ++k) rn[v][k] = make_uint4(0u, 0u, 0u, 0u);
             if (row < p.rows && live[v]) {
-                xn[v] = *reinterpret_cast<const uint4 *>(p.x + row * p.xs + c[v]);
-                if (p.z) zn[v] = *reinterpret_cast<const uint4 *>(p.z + row * p.zs + c[v]);
+                if (vec_ok(row * p.xs + c[v], p.rows, p.xs, p.D)) xn[v] = *reinterpret_cast<const uint4 *>(p.x + row * p.xs + c[v]);
+                if (p.z && vec_ok(row * p.zs + c[v], p.rows, p.zs, p.D)) zn[v] = *reinterpret_cast<const uint4 *>(p.z + row * p.zs + c[v]);
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.r) + (row * p.rs + c[v]) * (F32 ? 4 : 2));
+                if (vec_ok(row * p.rs + c[v], p.rows, p.rs, p.D)) {
 #pragma unroll
-                for (int k = 0; k < RV; ++k) rn[v][k] = src[k];
+                    for (int k = 0; k < RV; ++k) rn[v][k] = src[k];
+                }
             }
         }
     };
@@ -245,7 +256,7 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_residual
                 r[v][i] = live[v] ? fmaf(p.alpha, u, r[v][i]) : 0.f;
                 ss = fmaf(r[v][i], r[v][i], ss);
             }
-            if (p.ro && live[v] && row < p.rows) {
+            if (p.ro && live[v] && row < p.rows && vec_ok(row * p.ros + c[v], p.rows, p.ros, p.D)) {
                 if constexpr (F32) {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.ro) + row * p.ros + c[v]);
                     dst[0] = make_float4(r[v][0], r[v][1], r[v][2], r[v][3]);
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(CTA ? CTA_THREADS : WARP_THREADS) kda_residual
         const float inv = rsqrtf(fmaf(gr.sum(ss), inv_d, p.eps));
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            if (!live[v] || row >= p.rows) continue;
+            if (!live[v] || row >= p.rows || !vec_ok(row * p.os + c[v], p.rows, p.os, p.D)) continue;
             float o[8], w[8];
             if (p.w) blk::load8f(p.w + c[v], w);
 #pragma unroll
