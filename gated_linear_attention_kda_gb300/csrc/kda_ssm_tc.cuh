@@ -209,9 +209,9 @@ __device__ __forceinline__ bool no_number(uint32_t fp32_bits) { return (fp32_bit
 
 // What is left of a piece when all its roles are done and some state of it is no number (every thread of the CTA), in
 // three steps. Each is out of line: this is rare, and the roles' registers are to stay as they are.
-// 1. The first token of every channel that `spoilt` names whose x is NaN or infinity, found row by row.
+// 1. The first token of every channel whose x is NaN or infinity (`len` where there is none), found row by row.
 template <int P, int WARPS>
-__device__ __noinline__ void find_spoilt(const ssm::SsmParams &p, const volatile uint32_t *spoilt, int *first, int bos, int len)
+__device__ __noinline__ void find_spoilt(const ssm::SsmParams &p, int *first, int bos, int len)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint16_t *xp = p.x + static_cast<long long>(bos) * p.xs + static_cast<long long>(blockIdx.x % p.H) * P;
@@ -233,9 +233,8 @@ __device__ __noinline__ void find_spoilt(const ssm::SsmParams &p, const volatile
 #pragma unroll
             for (int k = 0; k < WORDS; ++k) {
                 const int c = 64 * k + 2 * lane;
-                const uint32_t m = (spoilt[c >> 5] >> (c & 31)) & ((no_number(x[j][k] << 16) ? 1u : 0u) | (no_number(x[j][k]) ? 2u : 0u));
-                if (m & 1u) atomicMin(first + c, t0 + WARPS * j);
-                if (m & 2u) atomicMin(first + c + 1, t0 + WARPS * j);
+                if (no_number(x[j][k] << 16)) atomicMin(first + c, t0 + WARPS * j);
+                if (no_number(x[j][k])) atomicMin(first + c + 1, t0 + WARPS * j);
             }
     }
 }
@@ -343,47 +342,57 @@ __device__ __noinline__ void repair_spoilt(const TcParams &t, const int *first, 
     }
 }
 
-// 3. The final states that are no numbers, from tensor memory: until here they have left the initial state, maybe the
-//    same buffer, to step 2.
-template <int P, int WST>
-__device__ __noinline__ void store_spoilt(const ssm::SsmParams &p, int seq)
+// Whether some lane of the warp holds a value that is no number (0 NaN and 0 inf are NaN).
+__device__ __forceinline__ bool any_spoilt(const uint32_t (&r)[32])
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp < WST || warp >= WST + 8) return;
-    const int q = warp & 3, c0 = warp < WST + 4 ? 0 : P / 2;
-    const size_t at0 = ((static_cast<size_t>(seq) * p.H + blockIdx.x % p.H) * P + c0) * NS + 32 * q + lane, st_elems = static_cast<size_t>(p.nseq) * p.H * P * NS;
-    __syncwarp();
-    tc::fence_after();
-#pragma unroll 1
-    for (int g4 = 0; g4 < P / 64; ++g4) {
-        uint32_t r[32];
-        tc::ld32((static_cast<uint32_t>(32 * q) << 16) + 128 + P + c0 + 32 * g4, r);
-        tc::wait_ld();
+    float2 z = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const size_t at = at0 + static_cast<size_t>(32 * g4 + i) * NS;
-            if (!no_number(r[i]) || !gmem_ok(at, 1, st_elems)) continue;
-            if (p.fin_dtype == KDA_DTYPE_FP32)
-                static_cast<float *>(p.fin)[at] = __uint_as_float(r[i]);
-            else
-                static_cast<uint16_t *>(p.fin)[at] = f2bf_bits(__uint_as_float(r[i]));
-        }
+    for (int i = 0; i < 32; i += 2) z = ffma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(0.f, 0.f), z);
+    return __any_sync(0xffffffffu, !(z.x + z.y == 0.f));
+}
+
+// 3. Final states of which a warp holds some that are no numbers: until here they have left the initial state, maybe the
+//    same buffer, to step 2. 32 columns of the state in tensor memory at `taddr`, to the final state's elements from
+//    `first` on.
+__device__ __noinline__ void store_spoilt(const ssm::SsmParams &p, uint32_t taddr, size_t first)
+{
+    const size_t st_elems = static_cast<size_t>(p.nseq) * p.H * p.P * NS;
+    uint32_t r[32];
+    tc::ld32(taddr, r);
+    tc::wait_ld();
+    if (!any_spoilt(r)) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const size_t at = first + static_cast<size_t>(i) * NS;
+        if (!gmem_ok(at, 1, st_elems)) continue;
+        if (p.fin_dtype == KDA_DTYPE_FP32)
+            static_cast<float *>(p.fin)[at] = __uint_as_float(r[i]);
+        else
+            static_cast<uint16_t *>(p.fin)[at] = f2bf_bits(__uint_as_float(r[i]));
     }
-    tc::fence_before();
 }
 
 template <int P, int PARTS>
-__device__ __noinline__ void finish_spoilt(const TcParams &t, const volatile uint32_t *spoilt)
+__device__ __noinline__ void finish_spoilt(const TcParams &t)
 {
     using Lay = Layout<P, PARTS, true>;
     constexpr int WARPS = Lay::NTHREADS / 32;
     __shared__ int first[P];
     const Piece pc = piece_of(t, blockIdx.x / t.p.H);
-    find_spoilt<P, WARPS>(t.p, spoilt, first, pc.bos, pc.len);
+    find_spoilt<P, WARPS>(t.p, first, pc.bos, pc.len);
     __syncthreads();
     repair_spoilt<P, WARPS>(t, first, pc.seq, pc.bos, pc.len);
     __syncthreads();
-    if (pc.last && t.p.fin) store_spoilt<P, Lay::WST>(t.p, pc.seq);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (pc.last && t.p.fin && warp >= Lay::WST && warp < Lay::WST + 8) {  // the state warps
+        const int q = warp & 3, c0 = warp < Lay::WST + 4 ? 0 : P / 2;
+        __syncwarp();
+        tc::fence_after();
+        for (int c = c0; c < c0 + P / 2; c += 32)
+            store_spoilt(t.p, (static_cast<uint32_t>(32 * q) << 16) + 128 + P + c,
+                       ((static_cast<size_t>(pc.seq) * t.p.H + blockIdx.x % t.p.H) * P + c) * NS + 32 * q + lane);
+        tc::fence_before();
+    }
     __syncthreads();
 }
 
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     const int grp = h / (p.H / p.G);
 
     volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
-    __shared__ volatile uint32_t spoilt[5];  // a bit per channel: its state holds no number; last word: some state is none
+    __shared__ volatile uint32_t spoilt;  // some state at the end of the piece is no number
     auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
     auto xt = [&](int n) { return sb + Lay::X + (n % XS) * Lay::XT; };
     auto bt = [&](int n) { return sb + Lay::B + (n % BS) * Lay::BT; };
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
             mbar_init(bar(Lay::W_EMPTY + i), 1);
         }
         flags[0] = 0;
-        for (int i = 0; i < 5; ++i) spoilt[i] = 0u;
+        spoilt = 0u;
         fence_mbar_init();
     }
     tc::fence_before();
@@ -820,16 +829,10 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 tc::fence_after();
 #pragma unroll 1
                 for (int g4 = 0; g4 < P / 32; ++g4) {
-                    uint32_t r[32], m = 0u;
+                    uint32_t r[32];
                     tc::ld32(tmem + (static_cast<uint32_t>(32 * 3) << 16) + T_S + 32 * g4, r);
                     tc::wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) m |= no_number(r[i]) ? 1u << i : 0u;
-                    m = __reduce_and_sync(0xffffffffu, m);
-                    if (lane == 0) {
-                        spoilt[g4] = m;
-                        if (m) spoilt[4] = 1u;
-                    }
+                    if (any_spoilt(r)) spoilt = 1u;
                 }
                 tc::fence_before();
             }
@@ -1023,6 +1026,10 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                 if (nch > 0) {
                     tc::ld32(lb + 32 * g4, r);
                     tc::wait_ld();
+                    if (FULL && any_spoilt(r)) {  // stored at the very end, see finish_spoilt
+                        spoilt = 1u;
+                        continue;
+                    }
                 } else {
                     load_init(g4, r);
                 }
@@ -1031,8 +1038,6 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
                     const size_t at = static_cast<size_t>(c0 + 32 * g4 + i) * NS;
                     if constexpr (!FULL)
                         wsp[at] = __uint_as_float(r[i]);
-                    else if (nch > 0 && no_number(r[i]))  // stored at the very end, see finish_spoilt
-                        spoilt[4] = 1u;
                     else if (!gmem_ok(unit * P * NS + at + nn, 1, st_elems))
                         continue;
                     else if (p.fin_dtype == KDA_DTYPE_FP32)
@@ -1050,9 +1055,7 @@ __global__ void __launch_bounds__(Layout<P, PARTS, FULL>::NTHREADS, 1)
     tc::fence_before();
     __syncthreads();
     if constexpr (FULL)
-        if (spoilt[4])
-            finish_spoilt<P, PARTS>(t, spoilt);
-
+        if (spoilt) finish_spoilt<P, PARTS>(t);
     if (warp == 0) {
         tc::fence_after();
         tc::dealloc(tmem, TMEM_COLS);
