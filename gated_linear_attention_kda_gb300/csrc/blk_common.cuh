@@ -13,9 +13,11 @@ __device__ __forceinline__ float rcp_approx(float x)
     return y;
 }
 
-// 1 / (1 + 2^(-z log2 e)). The exponential and the reciprocal are the hardware approximations
-// (relative error below 2^-20 together for |z| < 88, far under the bf16 rounding that follows);
-// z -> -inf gives 0, z -> +inf gives 1. The tanh form would lose the lower tail's relative precision.
+// 1 / (1 + 2^(-z log2 e)). The exponential and the reciprocal are the hardware approximations. What counts is the
+// rounding of the exponent, which has an ulp of 2^-17 for |z| above 44: the relative error is below 2^-20 for z > -22 and
+// grows to about 2^-18 at z = -87, far under the bf16 rounding that follows. Below -87.3 the reciprocal is subnormal and
+// comes out as 0, an error of less than 2^-126. z -> -inf gives 0, z -> +inf gives 1. The tanh form would lose the lower
+// tail's relative precision.
 __device__ __forceinline__ float sigmoid_fast(float z) { return rcp_approx(1.f + ex2_approx(-LOG2E * z)); }
 
 __device__ __forceinline__ float apply_act(float z, int act)

@@ -177,8 +177,8 @@ struct SsmBuffers {
 };
 
 // Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one: 8 heads of
-// 64, one sequence, 8 tokens 5.2 against 6.2 us, 16 tokens 7.8 against 6.3; 64 sequences of 16 heads of 128, 8
-// tokens 38 against 51 us, 16 tokens 50 in chunks, 74 token by token.
+// 64, one sequence, 8 tokens 5.1 against 6.7 us, 16 tokens 7.5 against 6.7; 64 sequences of 16 heads of 128, 8
+// tokens 35 against 52 us, 16 tokens 59 against 53.
 constexpr int64_t STEP_TOKENS = 8;
 
 static kda_status launch_ssm_steps(const ssm::SsmParams &p, cudaStream_t s)
@@ -277,8 +277,9 @@ static kda_status launch_ssm(const ssm::SsmParams &p, const SsmPlan &plan, float
     t.slots = static_cast<int>(split ? (p.cu ? plan.slots : static_cast<int64_t>(p.nseq) * plan.seg_per_seq) : p.nseq);
     t.ws = ws;
     const int64_t grid = static_cast<int64_t>(t.slots) * p.H;
-    // an fp32 final state keeps three parts of w b in both passes, otherwise two are enough (1 x 131,072 tokens, 32
-    // heads of 128, cut: fp32 985 us; bf16 936 us, 974 us with three in the first pass)
+    // an fp32 final state keeps three parts of w b in both passes, otherwise two are enough: what they leave out, 2^-17 of
+    // a term, is 2^-8 of the state's own rounding to bf16, be it as a result or as the output's operand (1 x 131,072
+    // tokens, 32 heads of 128, cut: fp32 1036 us, bf16 969 us)
     const bool exact = p.fin && p.fin_dtype == KDA_DTYPE_FP32;
     if (split) {
         if (const kda_status st = exact ? launch_ssm_tc<P, 3, false>(grid, mx, mb, mc, mo, t, s)

@@ -20,8 +20,9 @@ namespace ssm {
 constexpr int NS = 128;        // state channels
 constexpr int ROWS = 8;        // state rows per warp
 constexpr int STEP_THREADS = 128;
-// The log2 decay of one token is held at or above this: 2^-160 is zero in fp32 either way, and the
-// running sums of a chunk stay small enough for their differences to be exact to 2^-11.
+// The log2 decay of one token is held at or above this: 2^-160 is zero in fp32 either way, and a running sum over 32
+// tokens stays above -5120, so that each of its at most seven roundings is below 2^-12. The difference of two such sums is
+// off by 2^-8 at worst, and only behind tokens whose decay is at the limit; where the sums stay above -64, by 2^-15.
 constexpr float MIN_LOG2_DECAY = -160.f;
 
 struct SsmParams {

@@ -26,7 +26,7 @@
 // where it is returned in bf16 or not at all. D is not rounded: on the diagonal of M it would lose sixteen
 // bits, by the same error for every token of a head, and a score that is small against D most of its own
 // (8 x 4096 tokens of 16 heads of 128 would take 96 us instead of 104, 16 packed prompts of 32 heads of 64
-// 269 instead of 286; the outputs' relative error would be 2.36e-3 instead of 2.10e-3, of which 1.66e-3 are
+// 269 instead of 288; the outputs' relative error would be 2.36e-3 instead of 2.10e-3, of which 1.66e-3 are
 // their own rounding). Sums are fp32.
 //
 // NaN: a product multiplies what the mask leaves out by zero, and 0 NaN is NaN, so a NaN or infinity in x (which is
@@ -48,7 +48,7 @@
 // rows are scaled, 123 with one set of warps for both). Measured and not kept, each against 92 to 95 us when D still
 // lay on the diagonal: one MMA issuer for all products (112 us); four state warps (102); C as a tensor-memory operand
 // (116); polling instead of suspended waits (149); for heads of 128, rows written by the score warps (101).
-// Pieces (1 x 131,072 tokens, 32 heads): state pass 352 us, join 15 us, this pass 617 us.
+// Pieces (1 x 131,072 tokens, 32 heads): state pass 351 us, join 16 us, this pass 688 us.
 //
 // Warp roles (1024 threads; 896 for heads of 64):
 //   warp 0       TMA producer (lane 0): x tiles two or three deep, b two, c one or two; tensor memory allocation
