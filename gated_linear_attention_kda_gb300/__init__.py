@@ -461,3 +461,4 @@ def library():
 
 from .block import (conv, conv_step, gated_norm, residual_norm, ssm, ssm_step,  # noqa: E402
                     ssm_workspace_bytes)
+from .mixers import (attn_step, attn_step_workspace_bytes, gdn, gdn_step, kv_append, qk_rope)  # noqa: E402

@@ -13,7 +13,7 @@
 
 namespace kda {
 
-enum : unsigned { DEVERR_SEQLENS = 1u, DEVERR_TIMEOUT = 2u, DEVERR_BOUNDS = 4u };
+enum : unsigned { DEVERR_SEQLENS = 1u, DEVERR_TIMEOUT = 2u, DEVERR_BOUNDS = 4u, DEVERR_PAGES = 8u };
 __device__ unsigned int g_dev_error;
 
 #ifdef KDA_DEBUG

@@ -768,9 +768,10 @@ KDA_API kda_status kda_check_device_status(void *stream)
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "reading the device status failed: %s", cudaGetErrorString(e));
     if (word)
-        return fail(KDA_ERR_DEVICE, "device error word 0x%x:%s%s%s", word, (word & DEVERR_SEQLENS) ? " bad cu_seqlens" : "",
+        return fail(KDA_ERR_DEVICE, "device error word 0x%x:%s%s%s%s", word, (word & DEVERR_SEQLENS) ? " bad cu_seqlens" : "",
                     (word & DEVERR_TIMEOUT) ? " pipeline wait timed out" : "",
-                    (word & DEVERR_BOUNDS) ? " out-of-bounds access caught (debug build)" : "");
+                    (word & DEVERR_BOUNDS) ? " out-of-bounds access caught (debug build)" : "",
+                    (word & DEVERR_PAGES) ? " bad page table entry or position" : "");
     return KDA_OK;
 }
 
@@ -897,3 +898,4 @@ KDA_API kda_status kda_fwd_host(const void *q, const void *k, const void *v, con
 }  // extern "C"
 
 #include "kda_block_api.cuh"
+#include "kda_mixer_api.cuh"

@@ -506,6 +506,123 @@ KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void
                                      int64_t out_stride, float eps, int64_t M, int64_t D, void *stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Mixers beside KDA. Hybrid stacks put layers of the gated delta rule with one
+ * decay per head, and of softmax attention over a paged cache, next to KDA's:
+ *   kda_conv -> kda_gdn (or kda_gdn_step) -> kda_gated_norm
+ *   kda_qk_rope (queries), kda_kv_append (keys, values) -> kda_attn_step
+ * The pages have no counterpart for these. Ownership, execution, strided token
+ * axes and the rule on shared memory are those of the operators around the
+ * mixer above.
+ */
+
+/*
+ * kda_gdn -- the gated delta rule over prompts: for every sequence and value
+ * head h, with state S (V x K, stored [v][k], as kda_fwd's) and per token
+ *   a = -exp(A_log[h]) softplus(a_t + dt_bias[h]),   b = sigmoid(beta_t)
+ *   S <- exp(a) S (I - b k k^T) + b v k^T,   out = scale S q
+ * where head h reads queries and keys of head h / (H / HK).
+ *   q, k     bf16 [B, T, HK, K], v, out bf16 [B, T, H, V], K = V = 128, token
+ *            strides q_stride, k_stride, v_stride, out_stride; HK divides H.
+ *   a, beta  bf16 [B, T, H], token strides a_stride, beta_stride (any).
+ *   A_log    fp32 [H];  dt_bias  fp32 [H] or NULL (0).
+ *   initial_state, final_state  [S, H, V, K], bf16 or fp32, or NULL, as kda_fwd's
+ *            (same buffer allowed; the running state is held in fp32).
+ *   cu_seqlens, N  as kda_fwd's varlen mode (B == 1).
+ *   flags    0 or KDA_FLAG_QK_L2NORM: q and k are used as
+ *            x / sqrt(sum x^2 + 1e-6), formed in fp32.
+ */
+KDA_API kda_status kda_gdn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                           const void *a, int64_t a_stride, const void *beta, int64_t beta_stride, float scale, void *out,
+                           int64_t out_stride, const float *A_log, const float *dt_bias, const void *initial_state,
+                           kda_dtype initial_dtype, void *final_state, kda_dtype final_dtype, const int64_t *cu_seqlens,
+                           int64_t N, int64_t B, int64_t T, int64_t H, int64_t HK, int64_t K, int64_t V, uint32_t flags,
+                           void *stream);
+
+/*
+ * kda_gdn_step -- kda_gdn for one token of S sequences against a state updated
+ * in place: q, k bf16 [S, HK, K], v, out bf16 [S, H, V], a, beta bf16 [S, H] (row
+ * strides as above), state [S, H, V, K] in state_dtype (BF16 or FP32). All
+ * arithmetic is fp32; a bf16 state is rounded to nearest even when stored.
+ */
+KDA_API kda_status kda_gdn_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                const void *a, int64_t a_stride, const void *beta, int64_t beta_stride, float scale, void *out,
+                                int64_t out_stride, const float *A_log, const float *dt_bias, void *state, kda_dtype state_dtype,
+                                int64_t S, int64_t H, int64_t HK, int64_t K, int64_t V, uint32_t flags, void *stream);
+
+/*
+ * kda_qk_rope -- heads of queries and keys, normed and turned by their token's
+ * position in one pass:
+ *   n = x rsqrt(mean(x^2) + eps) weight         (norm == 0: n = x; weight NULL: 1)
+ *   (n_i, n_j) <- (n_i cos t - n_j sin t, n_j cos t + n_i sin t),  t = position inv_freq[p]
+ * for the pairs p < R / 2 of channels (i, j) = (p, p + R / 2), or (2 p, 2 p + 1)
+ * where interleaved != 0. Channels from R on are normed and not turned.
+ *   q, q_out  bf16 [M, H, D];  k, k_out  bf16 [M, HK, D] (HK == 0: no keys), token
+ *             strides *_stride; D = 64, 128 or 256. q_out may be q, k_out may be k.
+ *   positions int64 [M], any value;  inv_freq fp32 [R / 2] (R == 0: NULL allowed);
+ *             R a multiple of 16, 0 .. D. Angles are exact to 2^-31 turns for
+ *             positions below 2^32.
+ *   q_weight, k_weight  fp32 [D] or NULL, 16-byte aligned; read only with norm != 0.
+ */
+KDA_API kda_status kda_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, void *q_out, int64_t q_out_stride,
+                               void *k_out, int64_t k_out_stride, const float *q_weight, const float *k_weight, int norm, float eps,
+                               const int64_t *positions, const float *inv_freq, int64_t R, int interleaved, int64_t M, int64_t H,
+                               int64_t HK, int64_t D, void *stream);
+
+/*
+ * kda_kv_append -- keys and values of new tokens into a paged cache, the keys
+ * normed and turned on the way as in kda_qk_rope (with R == 0 and norm == 0 they
+ * are copied as they are).
+ *   k, v      bf16 [B, T, HK, D], token strides k_stride, v_stride.
+ *   k_cache, v_cache  bf16 [pages, HK, page_size, D], pages page_stride elements
+ *             apart (both; keys and values of a page may stand side by side),
+ *             16-byte aligned; page_size a power of two in 8 .. 4096.
+ *   page_table  int32 [S, table_width] (S = B, or N in varlen mode): page of
+ *             position x of sequence s is page_table[s][x / page_size].
+ *   positions int64 [B * T], each token's position in its sequence, for its place
+ *             in the cache and for the turn. A position below 0 marks padding: the
+ *             token is not written. Two tokens of a call have different places.
+ *   cu_seqlens, N  as kda_fwd's varlen mode (B == 1).
+ * A position past the table's width and a page outside 0 .. pages - 1 flag
+ * KDA_ERR_DEVICE; the token is not written. Nothing else of the cache changes.
+ */
+KDA_API kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *k_cache, void *v_cache,
+                                 int64_t page_stride, int64_t pages, int64_t page_size, const int32_t *page_table, int64_t table_width,
+                                 const int64_t *positions, const float *inv_freq, int64_t R, int interleaved, const float *k_weight,
+                                 int norm, float eps, const int64_t *cu_seqlens, int64_t N, int64_t B, int64_t T, int64_t HK, int64_t D,
+                                 void *stream);
+
+/*
+ * kda_attn_step -- softmax attention of one new token of each of S sequences over
+ * a paged cache (kda_kv_append's):
+ *   out[s, h] = sum_t softmax_t(scale q[s, h] . k_t) v_t,   t = 0 .. positions[s]
+ * with the keys and values of head h / (H / HK).
+ *   q, out    bf16 [S, H, D], row strides q_stride, out_stride; D = 64 or 128.
+ *   positions int64 [S], of the new tokens, which are in the cache already. Below
+ *             0: the row sees nothing, its out is 0 and its lse -infinity.
+ *   lse       fp32 [S, H] or NULL: log of the sum of exp(scale q . k_t).
+ *   workspace 16-byte aligned device buffer or NULL. With at least the
+ *             kda_attn_step_workspace_bytes bytes the caches of few sequences are
+ *             read by many CTAs and their parts joined; without it one CTA reads
+ *             a sequence's keys and values of a head. Scratch after the call; calls
+ *             that overlap in time must not share it. Too small: KDA_ERR_RANGE.
+ * A position past the table's width flags KDA_ERR_DEVICE and counts as below 0;
+ * a page outside 0 .. pages - 1 flags it and its tokens are left out. Cached rows
+ * behind a position are never used, whatever they hold. Scores, the softmax and
+ * its sums are fp32; weights are rounded to bf16 as operands of the output.
+ */
+KDA_API kda_status kda_attn_step(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache, int64_t page_stride,
+                                 int64_t pages, int64_t page_size, const int32_t *page_table, int64_t table_width,
+                                 const int64_t *positions, float scale, void *out, int64_t out_stride, float *lse, int64_t S, int64_t H,
+                                 int64_t HK, int64_t D, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_attn_step_workspace_bytes -- the workspace with which kda_attn_step may cut
+ * the caches of S sequences on the current device, whatever their lengths.
+ */
+KDA_API kda_status kda_attn_step_workspace_bytes(int64_t S, int64_t H, int64_t HK, int64_t D, size_t *bytes);
+
+/*
  * kda_probe_chunk -- test hook: one 16-token chunk of one head through the
  * forward pass's per-chunk steps, built from the same device code as the
  * kernels, so that each step can be checked on its own.
