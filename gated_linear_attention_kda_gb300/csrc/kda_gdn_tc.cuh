@@ -1,0 +1,710 @@
+// kda_gdn_tc.cuh -- the gated delta rule with one decay per head over prompts, on the 5th-generation tensor core, 64 tokens
+// at a time.
+//
+// Chunk algebra. Over a chunk of tokens j = 0..63 that starts from S0 (V x K), with G_i the running sum of the log2 decays
+// up to and with token i, the corrected values n_i = b_i (v_i - 2^(a_i) S_{i-1} k_i) satisfy
+//   (I + A) N = diag(b) (V - diag(2^G) K S0^T),   A[i, j] = b_i 2^(G_i - G_j) k_i . k_j   for j < i, else 0
+// so that with T = (I + A)^-1 diag(b)
+//   N     = T V - T diag(2^G) K S0^T
+//   out_i = scale (2^(G_i) S0 q_i + sum_{j <= i} 2^(G_i - G_j) (q_i . k_j) n_j)
+//   S1    = 2^(G_63) S0 + sum_j 2^(G_63 - G_j) n_j k_j^T
+// No exponent is positive, so nothing overflows, and with one decay per head every scaling is by a token: K, Q and V enter
+// the products as they lie in memory, and norms of queries and keys are factors of the same kind.
+//
+// One CTA owns the state of one (sequence, head). It lives in tensor memory, fp32, lane = value channel, column = key
+// channel, and everything on the chain from chunk to chunk keeps the value channel in its lane:
+//   D1  [128 x 64]  = S K^T           S as bf16 in tensor memory (its own copy)
+//   D2  [128 x 64]  = V^T T^T         V^T straight from V's tile (its transpose is a layout of the operand)
+//   D2             += D1' T^T         D1' = -2^(G_j) D1 as bf16, written over D1
+//   S              += N' K            N' = 2^(G_63 - G_j) N^T as bf16, written over D2; S decayed before
+//   O   [128 x 64]  = S Q^T,  N^T P^T and the output is their sum, the first scaled per token
+// Beside the chain, one or two chunks ahead: [K; Q] K^T, its scaled halves A and P, and T.
+// Roundings: the state, D1', N, N', P and T enter products as bf16 (the output is bf16; the state that is carried and
+// returned is fp32). The inverse is fp32 within 16 x 16 blocks and tf32 (rounded to nearest) between them, an eighth of
+// the step of T's own rounding.
+//
+// NaN: a product multiplies what a mask leaves out by zero, and 0 NaN is NaN, so a token that holds a NaN or infinity
+// would reach earlier ones of its chunk. What holds one leaves no number in the state's rows it reaches, up to the end of
+// the sequence, where such rows show; their eight neighbours' outputs and states are then made again token by token from
+// the start of the sequence (walk_rows). A NaN in q stays in its token without that.
+//
+// Warp roles (768 threads):
+//   warp 0       TMA producer (lane 0): [K; Q] tiles three deep, V tiles two
+//   warp 1       MMA issuer: everything on the chain, and the output
+//   warp 2       MMA issuer: [K; Q] K^T
+//   warp 3       running sums of the decays, steps
+//   warps 4-11   chain: bf16 state, D1', N and N', decay (value channel, half of the columns each)
+//   warps 12-15  output (value channel), transposed through the chunk's Q tile
+//   warps 16-23  norms of queries and keys, A, P and T of a chunk
+#pragma once
+#include "kda_gdn_step.cuh"
+#include "kda_ssm_tc.cuh"
+#include "tcgen05.cuh"
+
+namespace kda {
+namespace gdntc {
+
+using gdn::GdnParams;
+
+constexpr int C = 64;           // tokens per chunk
+constexpr int NTHREADS = 768;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t T_S = 0, T_SB = 128, T_D1 = 192, T_SQ = 256, T_D2 = 320, T_PV = 384, T_KQ = 448;
+
+// scalars of a chunk: running log2 sums, steps, 2^G (then the factors of D1'), 2^(G_63 - G) (then those of N'), the
+// output's factors, 1 / |k| and scale / |q|, the chunk's whole decay
+constexpr int SC_G = 0, SC_B = 256, SC_D = 512, SC_N = 768, SC_O = 1024, SC_RK = 1280, SC_RQ = 1536, SC_GAM = 1792, SC_BYTES = 1808;
+
+struct Layout {
+    static constexpr int BOX = C * 128;             // 64 channels x 64 rows, 128-byte swizzle
+    static constexpr int KQS = 3, KQT = 4 * BOX;    // a tile: per 64 channels the rows of K, then those of Q
+    static constexpr int VS = 2, VT = 2 * BOX;
+    static constexpr int LD = 68;                   // floats per row of the inverse's scratch
+    static constexpr int KQ = 0;
+    static constexpr int V = KQ + KQS * KQT;
+    static constexpr int P = V + VS * VT;           // scores [i][j] and T [i][j], bf16, 128-byte rows
+    static constexpr int T = P + KQS * BOX;
+    static constexpr int SCR = T + KQS * BOX;
+    static constexpr int SC = SCR + C * LD * 4;
+    static constexpr int BAR = SC + KQS * SC_BYTES;
+    static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 8, SC_FULL = 10, T_FULL = 13, G_DONE = 16, KQ_FREE = 17,
+                         KQ_ZERO = 18, SB_GO = 19, D1_DONE = 20, D1_GO = 21, N_DONE = 22, N_GO = 23, S_DONE = 24, O_DONE = 25,
+                         OUT_RD = 26, END = 27, END2 = 28, NBARS = 29;
+    static constexpr int TMEMPTR = (BAR + NBARS * 8 + 15) / 16 * 16;
+    static constexpr int FLAGS = TMEMPTR + 16;
+    static constexpr int ALLOC = FLAGS + 16 + 1024;
+    static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+    static_assert(SC % 16 == 0 && SC_BYTES % 16 == 0 && BAR % 8 == 0, "alignment");
+};
+
+// An operand of a tf32 product, rounded to nearest.
+__device__ __forceinline__ uint32_t tf32(float x)
+{
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+
+// The rows of a sequence that hold no numbers at its end, made again: rows 8 g .. 8 g + 7 for every set bit of `groups`.
+__device__ __noinline__ void redo_rows(const GdnParams &p, int seq, int h, const Span &sp, uint32_t groups)
+{
+    for (int g = threadIdx.x >> 5; g < DH / gdn::ROWS; g += NTHREADS / 32)
+        if (groups >> g & 1) gdn::walk_rows(p, seq, h, sp, gdn::ROWS * g);
+}
+
+__global__ void __launch_bounds__(NTHREADS, 1)
+    kda_gdn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                      const __grid_constant__ CUtensorMap to, const __grid_constant__ GdnParams p)
+{
+    using Lay = Layout;
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+#define SM_AT(T, a) (*reinterpret_cast<T *>(smem + (smem_checked((a), sizeof(T), sb) - sb)))
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H, hk = h / (p.H / p.HK);
+    const int seq = p.cu && p.nseq <= LPT_MAX_SEQS ? ssmtc::longest_first(p, slot) : slot;
+    if (p.cu && blockIdx.x == 0) blk::check_bounds(p.cu, p.nseq, p.total);
+    const Span sp = gdn::gdn_span(p, seq);
+    if (!sp.ok) return;  // CTA-uniform, before any tensor memory is taken
+    const int nch = (sp.len + C - 1) / C;
+
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
+    __shared__ uint32_t spoilt;  // groups of eight rows that hold no numbers at the end
+    auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
+    auto kq = [&](int n) { return sb + Lay::KQ + (n % Lay::KQS) * Lay::KQT; };
+    auto vt = [&](int n) { return sb + Lay::V + (n % Lay::VS) * Lay::VT; };
+    auto pt = [&](int n) { return sb + Lay::P + (n % Lay::KQS) * Lay::BOX; };
+    auto tt = [&](int n) { return sb + Lay::T + (n % Lay::KQS) * Lay::BOX; };
+    auto sc = [&](int n) { return sb + Lay::SC + (n % Lay::KQS) * SC_BYTES; };
+    auto live_of = [&](int n) { return min(C, sp.len - n * C); };
+
+    if (warp == 0) {
+        tc::alloc(sb + Lay::TMEMPTR, TMEM_COLS);
+        tc::relinquish();
+    }
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < Lay::KQS; ++i) {
+            mbar_init(bar(Lay::KQ_FULL + i), 1);
+            mbar_init(bar(Lay::KQ_EMPTY + i), 4);
+            mbar_init(bar(Lay::SC_FULL + i), 1);
+            mbar_init(bar(Lay::T_FULL + i), 8);
+        }
+        for (int i = 0; i < Lay::VS; ++i) {
+            mbar_init(bar(Lay::V_FULL + i), 1);
+            mbar_init(bar(Lay::V_EMPTY + i), 1);
+        }
+        for (int i : {Lay::G_DONE, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
+        mbar_init(bar(Lay::OUT_RD), 4);
+        for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO, Lay::KQ_FREE, Lay::KQ_ZERO}) mbar_init(bar(i), 8);
+        flags[0] = 0;
+        spoilt = 0u;
+        fence_mbar_init();
+    }
+    // the parts of P and T above their diagonal blocks are zero for good
+    for (int i = threadIdx.x; i < 2 * Lay::KQS * Lay::BOX / 16; i += NTHREADS) SM_AT(uint4, sb + Lay::P + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    tc::fence_async_smem();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    // the allocation is the whole tensor memory, so it starts at address 0
+    constexpr uint32_t tmem = 0;
+    if (*reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR) != tmem && threadIdx.x == 0) {
+        atomicOr(&g_dev_error, DEVERR_TIMEOUT);
+        flags[0] = 1;
+    }
+    // the whole warp goes on only when every lane saw the phase
+    auto wait_w = [&](int b, uint32_t par) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), par))) return true;
+        const bool ok = __all_sync(0xffffffffu, wait_bar_slow(bar(b), par, flags));
+        __syncwarp();
+        return ok;
+    };
+    auto arrive_w = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+    };
+    auto kq_par = [](int n) { return static_cast<uint32_t>((n / Lay::KQS) & 1); };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tq);
+            tma_prefetch_desc(&tk);
+            tma_prefetch_desc(&tv);
+            int nk = 0, nv = 0;  // tiles issued
+            for (int n = 0; n < nch; ++n) {
+                const int tok = sp.bos + n * C, full = Lay::KQ_FULL + n % Lay::KQS, vfull = Lay::V_FULL + n % Lay::VS;
+                if (!wait_bar(bar(Lay::KQ_EMPTY + n % Lay::KQS), kq_par(n) ^ 1, flags)) break;
+                mbar_arrive_expect_tx(bar(full), Lay::KQT);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    tma_load_3d(kq(n) + 2 * c * Lay::BOX, &tk, 64 * c, hk, tok, bar(full));
+                    tma_load_3d(kq(n) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
+                }
+                ++nk;
+                if (!wait_bar(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flags)) break;
+                mbar_arrive_expect_tx(bar(vfull), Lay::VT);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) tma_load_3d(vt(n) + c * Lay::BOX, &tv, 64 * c, h, tok, bar(vfull));
+                ++nv;
+            }
+            // no copy is in flight when the CTA ends, whichever way the loop was left
+            for (int m = max(nk - Lay::KQS, 0); m < nk; ++m) drain_bar(bar(Lay::KQ_FULL + m % Lay::KQS), kq_par(m));
+            for (int m = max(nv - Lay::VS, 0); m < nv; ++m) drain_bar(bar(Lay::V_FULL + m % Lay::VS), (m / Lay::VS) & 1);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer: chain and output (whole warp)
+        constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B);
+        constexpr uint32_t id_n = tc::idesc(tc::BF16, 128, C, 0, 0), id_u = tc::idesc(tc::BF16, 128, C, 1, 0),
+                           id_s = tc::idesc(tc::BF16, 128, DH, 0, 1);
+        auto halves = [](int i) { return static_cast<uint32_t>(32 * (i >> 1) + 8 * (i & 1)); };  // K step i of an operand in two halves
+        auto issue_u = [&](int n) {
+            if (!wait_w(Lay::T_FULL + n % Lay::KQS, kq_par(n)) || !wait_w(Lay::V_FULL + n % Lay::VS, (n / Lay::VS) & 1)) return false;
+            if (const int Lv = live_of(n); Lv < C) {  // as the rows of K and Q past the end, which other warps clear
+                for (int i = lane; i < (C - Lv) * 16; i += 32) {
+                    const int r = Lv + (i >> 4), c = i & 15;
+                    SM_AT(uint4, vt(n) + (c >> 3) * Lay::BOX + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+            }
+            tc::fence_after();
+            const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(n), 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tc::mma_ss_w(tmem + T_D2, tc::sdesc_of<HI>(dv + i * ((16 * 128) >> 4)), tc::sdesc_of<HI>(dt + i * (32 >> 4)), id_u, i > 0);
+            tc::commit_w(bar(Lay::V_EMPTY + n % Lay::VS));
+            return true;
+        };
+        bool ok = true;
+        for (int n = 0; ok && n < nch; ++n) {
+            const uint32_t dk = tc::sdesc_lo(kq(n), 16), dq = dk + (Lay::BOX >> 4), dt = tc::sdesc_lo(tt(n), 16), dp = tc::sdesc_lo(pt(n), 16);
+            const uint32_t dkn = tc::sdesc_lo(kq(n), 2 * Lay::BOX);  // K with its channels as rows
+            auto kmaj = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(((i >> 2) * 2 * Lay::BOX + (i & 3) * 32) >> 4)); };
+            if (!(ok = wait_w(Lay::SB_GO, n & 1))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_D1, tmem + T_SB + 8 * i, kmaj(dk, i), id_n, i > 0);
+            tc::commit_w(bar(Lay::D1_DONE));
+            // N's columns have been read up by the products of the last chunk
+            if (!(ok = (n == 0 || wait_w(Lay::O_DONE, (n - 1) & 1)) && issue_u(n) && wait_w(Lay::D1_GO, n & 1))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_D2, tmem + T_D1 + halves(i), tc::sdesc_of<HI>(dt + i * (32 >> 4)), id_n, 1);
+            tc::commit_w(bar(Lay::N_DONE));
+            if (n > 0 && !(ok = wait_w(Lay::OUT_RD, (n - 1) & 1))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
+            if (!(ok = wait_w(Lay::N_GO, n & 1))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 + halves(i), tc::sdesc_of<HI>(dkn + i * ((16 * 128) >> 4)), id_s, 1);
+            tc::commit_w(bar(Lay::S_DONE));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + halves(i), tc::sdesc_of<HI>(dp + i * (32 >> 4)), id_n, i > 0);
+            tc::commit_w(bar(Lay::O_DONE));
+        }
+        if (nch > 0) {
+            tc::commit_w(bar(Lay::END));
+            if (lane == 0) drain_bar(bar(Lay::END), 0);
+            __syncwarp();
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- MMA issuer: [K; Q] K^T
+        constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B), id_g = tc::idesc(tc::BF16, 128, C, 0, 0);
+        for (int n = 0; n < nch; ++n) {
+            if (!wait_w(Lay::KQ_FULL + n % Lay::KQS, kq_par(n))) break;
+            if (live_of(n) < C && !wait_w(Lay::KQ_ZERO, 0)) break;
+            if (n > 0 && !wait_w(Lay::KQ_FREE, (n - 1) & 1)) break;
+            tc::fence_after();
+            const uint32_t d = tc::sdesc_lo(kq(n), 16);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t at = tc::sdesc_of<HI>(d + static_cast<uint32_t>(((i >> 2) * 2 * Lay::BOX + (i & 3) * 32) >> 4));
+                tc::mma_ss_w(tmem + T_KQ, at, at, id_g, i > 0);
+            }
+            tc::commit_w(bar(Lay::G_DONE));
+        }
+        if (nch > 0) {
+            tc::commit_w(bar(Lay::END2));
+            if (lane == 0) drain_bar(bar(Lay::END2), 0);
+            __syncwarp();
+        }
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- decays and steps, two tokens per lane
+        const float A2 = -expf(__ldg(p.A_log + h)) * LOG2E, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
+        const uint16_t *ap = p.a + static_cast<long long>(sp.bos) * p.as + h, *bp = p.beta + static_cast<long long>(sp.bos) * p.bs + h;
+        uint32_t ra[2] = {0u, 0u}, rb[2] = {0u, 0u};
+        auto fetch = [&](int n) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = n * C + 2 * lane + i;
+                if (t < sp.len) {
+                    ra[i] = ap[t * p.as];
+                    rb[i] = bp[t * p.bs];
+                }
+            }
+        };
+        fetch(0);
+        for (int n = 0; n < nch; ++n) {
+            const int Lv = live_of(n);
+            float a[2], b[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool live = 2 * lane + i < Lv;
+                // held at the least decay by a comparison that lets NaN through (fmaxf would not)
+                const float u = A2 * gdn::softplus(__uint_as_float(ra[i] << 16) + bias);
+                a[i] = !live ? 0.f : u < ssm::MIN_LOG2_DECAY ? ssm::MIN_LOG2_DECAY : u;
+                b[i] = live ? gdn::sigmoid(__uint_as_float(rb[i] << 16)) : 0.f;
+            }
+            fetch(n + 1);
+            float pre = a[0] + a[1];
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, pre, m);
+                if (lane >= m) pre += u;
+            }
+            const float all = __shfl_sync(0xffffffffu, pre, 31);
+            const float g1 = pre, before = __shfl_up_sync(0xffffffffu, pre, 1), g0 = (lane ? before : 0.f) + a[0];
+            if (!wait_w(Lay::KQ_FULL + n % Lay::KQS, kq_par(n))) break;  // the buffer is free as the tile's is
+            const uint32_t o = sc(n) + 8 * lane;
+            SM_AT(float2, o + SC_G) = make_float2(g0, g1);
+            SM_AT(float2, o + SC_B) = make_float2(b[0], b[1]);
+            SM_AT(float2, o + SC_D) = make_float2(ex2_approx(g0), ex2_approx(g1));
+            SM_AT(float2, o + SC_N) = make_float2(ex2_approx(all - g0), ex2_approx(all - g1));
+            if (lane == 0) SM_AT(float, sc(n) + SC_GAM) = ex2_approx(all);
+            arrive_w(Lay::SC_FULL + n % Lay::KQS);
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------- chain
+        const int q = warp & 3, hf = warp < 8 ? 0 : 1, v = 32 * q + lane;
+        const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        const uint32_t ls = lq + T_S + 64 * hf, lsb = lq + T_SB + 32 * hf, l1 = lq + T_D1 + 32 * hf, l2 = lq + T_D2 + 32 * hf;
+        const size_t row = ((static_cast<size_t>(seq) * p.H + h) * DH + v) * DH + 64 * hf;  // of this thread's part of the state
+        auto load_init = [&](int c, uint32_t(&r)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+            if (!p.init || !gmem_ok(row + c, 32, gdn::state_elems(p))) return;
+            if (p.init_dtype == KDA_DTYPE_FP32) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const float *>(p.init) + row + c + i);
+                    r[i] = w.x; r[i + 1] = w.y; r[i + 2] = w.z; r[i + 3] = w.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.init) + row + c + i);
+                    r[i] = w.x << 16; r[i + 1] = w.x & 0xffff0000u; r[i + 2] = w.y << 16; r[i + 3] = w.y & 0xffff0000u;
+                    r[i + 4] = w.z << 16; r[i + 5] = w.z & 0xffff0000u; r[i + 6] = w.w << 16; r[i + 7] = w.w & 0xffff0000u;
+                }
+            }
+        };
+        auto store_fin = [&](int c, const uint32_t(&r)[32]) {
+            if (!gmem_ok(row + c, 32, gdn::state_elems(p))) return;
+            if (p.fin_dtype == KDA_DTYPE_FP32) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4 *>(static_cast<float *>(p.fin) + row + c + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    auto two = [&](int j) { return pack_bf16(__uint_as_float(r[i + j]), __uint_as_float(r[i + j + 1])); };
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.fin) + row + c + i) = make_uint4(two(0), two(2), two(4), two(6));
+                }
+            }
+        };
+        auto pack = [](const uint32_t(&r)[32], uint32_t(&o)[16]) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        };
+        // 32 columns times the factors at `at`
+        auto scale = [&](uint32_t(&r)[32], uint32_t at) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 f = SM_AT(const float4, at + 4 * i);
+                const float2 x = fmul2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(f.x, f.y));
+                const float2 y = fmul2(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), make_float2(f.z, f.w));
+                r[i] = __float_as_uint(x.x); r[i + 1] = __float_as_uint(x.y); r[i + 2] = __float_as_uint(y.x); r[i + 3] = __float_as_uint(y.y);
+            }
+        };
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            uint32_t r[32], o[16];
+            // the state as an operand
+            if (n > 0 && !(ok = wait_w(Lay::S_DONE, (n - 1) & 1))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (n == 0) {
+                    load_init(32 * g, r);
+                } else {
+                    tc::ld32(ls + 32 * g, r);
+                    tc::wait_ld();
+                }
+                pack(r, o);
+                tc::st16(lsb + 16 * g, o);
+            }
+            tc::wait_st();
+            tc::fence_before();
+            arrive_w(Lay::SB_GO);
+            // decayed in place
+            if (!(ok = wait_w(Lay::SC_FULL + n % Lay::KQS, kq_par(n)))) break;
+            const float gam = SM_AT(const float, sc(n) + SC_GAM);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (n == 0) {
+                    load_init(32 * g, r);
+                } else {
+                    tc::ld32(ls + 32 * g, r);
+                    tc::wait_ld();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(gam * __uint_as_float(r[i]));
+                tc::st32(ls + 32 * g, r);
+            }
+            // D1' over D1
+            if (!(ok = wait_w(Lay::T_FULL + n % Lay::KQS, kq_par(n)) && wait_w(Lay::D1_DONE, n & 1))) break;
+            tc::fence_after();
+            tc::ld32(l1, r);
+            tc::wait_ld();
+            scale(r, sc(n) + SC_D + 128 * hf);
+            pack(r, o);
+            tc::st16(l1, o);
+            tc::wait_st();
+            tc::fence_before();
+            arrive_w(Lay::D1_GO);
+            // N and N' over D2
+            if (!(ok = wait_w(Lay::N_DONE, n & 1))) break;
+            tc::fence_after();
+            tc::ld32(l2, r);
+            tc::wait_ld();
+            pack(r, o);
+            tc::st16(l2, o);
+            scale(r, sc(n) + SC_N + 128 * hf);
+            pack(r, o);
+            tc::st16(l2 + 16, o);
+            tc::wait_st();
+            tc::fence_before();
+            arrive_w(Lay::N_GO);
+        }
+        if (ok && nch > 0) ok = wait_w(Lay::S_DONE, (nch - 1) & 1);
+        tc::fence_after();
+        if (ok && nch > 0) {
+            float2 z = make_float2(0.f, 0.f);  // 0 NaN and 0 inf are NaN
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t r[32];
+                tc::ld32(ls + 32 * g, r);
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) z = ffma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(0.f, 0.f), z);
+            }
+            if (!(z.x + z.y == 0.f)) atomicOr(&spoilt, 1u << (v / gdn::ROWS));
+        }
+        named_bar_sync(4 + q, 64);  // both halves of these rows have been looked at
+        if (ok && p.fin) {
+            const bool number = !(*const_cast<volatile uint32_t *>(&spoilt) >> (v / gdn::ROWS) & 1u);  // else made again at the end
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                uint32_t r[32];
+                if (nch > 0) {  // every lane of the warp takes part in the load
+                    tc::ld32(ls + 32 * g, r);
+                    tc::wait_ld();
+                } else {
+                    load_init(32 * g, r);
+                }
+                if (number) store_fin(32 * g, r);
+                __syncwarp();
+            }
+        }
+        tc::fence_before();
+    } else if (warp < 16) {
+        // ---------------------------------------------------------------- output
+        const int q = warp & 3;
+        const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16);
+        for (int n = 0; n < nch; ++n) {
+            const int Lv = live_of(n);
+            const bool ok = wait_w(Lay::T_FULL + n % Lay::KQS, kq_par(n)) && wait_w(Lay::O_DONE, n & 1);
+            tc::fence_after();
+            // The Q tile has been read: token i is its row i. The accumulators are loaded as warp MMA fragments (8 channels
+            // x 8 tokens), so that stmatrix.trans hands a token's row its 16 bytes of eight channels.
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {  // 16 channels x 32 tokens
+                const int lh = g >> 1, c0 = 32 * (g & 1);
+                const uint32_t la = lq + (static_cast<uint32_t>(16 * lh) << 16) + c0;
+                uint32_t s[16], u[16], o[8];
+                tc::ld_16x256b_x4(la + T_SQ, s);
+                tc::ld_16x256b_x4(la + T_PV, u);
+                float2 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = SM_AT(const float2, sc(n) + SC_O + 4 * (c0 + 8 * i + 2 * (lane & 3)));
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 y = ffma2(f[i >> 1], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                           make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
+                    o[i] = pack_bf16(y.x, y.y);
+                }
+                const int v8 = 4 * q + 2 * lh + ((lane >> 3) & 1), r = lane & 7;  // eight channels and token row of this lane's address
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = c0 + 16 * i + 8 * (lane >> 4) + r;
+                    stsm_x4_t(kq(n) + (2 * (v8 >> 3) + 1) * Lay::BOX + t * 128 + (((v8 & 7) ^ r) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            tc::fence_before();
+            arrive_w(Lay::OUT_RD);
+            tc::fence_async_smem();
+            if (named_bar_or(1, 128, !ok)) break;  // all four warps leave together
+            if (Lv == C) {
+                if (warp == 12 && lane == 0) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tma_store_3d(&to, kq(n) + (2 * c + 1) * Lay::BOX, 64 * c, h, sp.bos + n * C);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+            } else {
+                for (int i = threadIdx.x - 384; i < Lv * 16; i += 128) {
+                    const int t = i >> 4, g = i & 15;
+                    const long long e = static_cast<long long>(sp.bos + n * C + t) * p.os + static_cast<long long>(h) * DH + 8 * g;
+                    if (!gmem_ok(e, 8, (p.total - 1) * p.os + static_cast<long long>(p.H) * DH)) continue;
+                    *reinterpret_cast<uint4 *>(p.out + e) =
+                        SM_AT(const uint4, kq(n) + (2 * (g >> 3) + 1) * Lay::BOX + t * 128 + (((g & 7) ^ (t & 7)) << 4));
+                }
+            }
+            arrive_w(Lay::KQ_EMPTY + n % Lay::KQS);
+        }
+        if (warp == 12 && lane == 0) bulk_wait_all();
+    } else {
+        // ---------------------------------------------------------------- A, P and T
+        // Quarters 0 and 1 of tensor memory hold K K^T, 2 and 3 Q K^T; two warps share a quarter's columns.
+        const int q = warp & 3, hf = warp < 20 ? 0 : 1, w8 = warp - 16, tid = threadIdx.x - 512;
+        const int lo = q & 1, i0 = 32 * lo + lane;  // this thread's row
+        const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_KQ;
+        const uint32_t scr = sb + Lay::SCR;
+        auto A = [&](int i, int j) -> float & { return SM_AT(float, scr + 4 * (i * Lay::LD + j)); };
+        auto sync = [&] { named_bar_sync(2, 256); };
+        const int g8 = lane >> 2, t4 = lane & 3;
+        // d += X[xr.., xc..] Y[yr.., yc..], 16 x 16 by 16 x 8, both in the scratch
+        auto product = [&](float(&d)[4], int xr, int xc, int yr, int yc) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 8) {
+                const uint32_t a[4] = {tf32(A(xr + g8, xc + k + t4)), tf32(A(xr + g8 + 8, xc + k + t4)), tf32(A(xr + g8, xc + k + t4 + 4)),
+                                       tf32(A(xr + g8 + 8, xc + k + t4 + 4))};
+                mma_tf32(d, a, tf32(A(yr + k + t4, yc + g8)), tf32(A(yr + k + t4 + 4, yc + g8)));
+            }
+        };
+        auto put = [&](const float(&d)[4], int r, int c, float f) {
+            SM_AT(float2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_float2(f * d[0], f * d[1]);
+            SM_AT(float2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_float2(f * d[2], f * d[3]);
+        };
+        for (int n = 0; n < nch; ++n) {
+            const int Lv = live_of(n);
+            const uint32_t s = sc(n), t0 = tt(n);
+            // where T[i][j] stands as an operand, times its column's step
+            auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
+            auto put_t = [&](const float(&d)[4], int r, int c) {
+                const float2 b = SM_AT(const float2, s + SC_B + 4 * (c + 2 * t4));
+                SM_AT(uint32_t, t_at(r + g8, c + 2 * t4)) = pack_bf16(-d[0] * b.x, -d[1] * b.y);
+                SM_AT(uint32_t, t_at(r + g8 + 8, c + 2 * t4)) = pack_bf16(-d[2] * b.x, -d[3] * b.y);
+            };
+            bool ok = wait_w(Lay::KQ_FULL + n % Lay::KQS, kq_par(n));
+            if (Lv < C) {
+                // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
+                for (int i = tid; i < (C - Lv) * 32; i += 256) {
+                    const int r = Lv + (i >> 5), c = i & 31;
+                    SM_AT(uint4, kq(n) + (c >> 3) * Lay::BOX + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                tc::fence_async_smem();
+                arrive_w(Lay::KQ_ZERO);
+                sync();
+            }
+            if (p.l2) {  // four threads a row
+                const int r = tid >> 2, c0 = 4 * (tid & 3);
+                float2 ss[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float2 f[4];
+                        blk::unpack8(SM_AT(const uint4, kq(n) + (2 * (c0 >> 3) + m) * Lay::BOX + r * 128 + ((((c0 + c) & 7) ^ (r & 7)) << 4)), f);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) ss[m] = ffma2(f[j], f[j], ss[m]);
+                    }
+                float kk = ss[0].x + ss[0].y, qq = ss[1].x + ss[1].y;
+#pragma unroll
+                for (int m = 1; m < 4; m <<= 1) {
+                    kk += __shfl_xor_sync(0xffffffffu, kk, m);
+                    qq += __shfl_xor_sync(0xffffffffu, qq, m);
+                }
+                if ((lane & 3) == 0) {
+                    SM_AT(float, s + SC_RK + 4 * r) = rsqrtf(kk + gdn::L2_EPS);
+                    SM_AT(float, s + SC_RQ + 4 * r) = p.scale * rsqrtf(qq + gdn::L2_EPS);
+                }
+            } else if (tid < C) {
+                SM_AT(float, s + SC_RK + 4 * tid) = 1.f;
+                SM_AT(float, s + SC_RQ + 4 * tid) = p.scale;
+            }
+            ok = ok && wait_w(Lay::SC_FULL + n % Lay::KQS, kq_par(n));
+            if (named_bar_or(2, 256, !ok)) break;  // all eight warps leave together
+            const float Gi = SM_AT(const float, s + SC_G + 4 * i0), rk = SM_AT(const float, s + SC_RK + 4 * i0);
+            const float fi = q < 2 ? SM_AT(const float, s + SC_B + 4 * i0) * rk : SM_AT(const float, s + SC_RQ + 4 * i0);
+            if (q >= 2) {
+                if (hf == 0) SM_AT(float, s + SC_O + 4 * i0) = fi * ex2_approx(Gi);
+            } else if (hf == 0) {
+                SM_AT(float, s + SC_D + 4 * i0) *= -rk;
+            } else {
+                SM_AT(float, s + SC_N + 4 * i0) *= rk;
+            }
+            ok = wait_w(Lay::G_DONE, n & 1);
+            tc::fence_after();
+            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
+            const int last = q < 2 ? i0 - 1 : i0;
+#pragma unroll 1
+            for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
+                uint32_t r[16];
+                float w[16];
+                tc::ld16(lq + b, r);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 g = SM_AT(const float4, s + SC_G + 4 * (b + j)), k = SM_AT(const float4, s + SC_RK + 4 * (b + j));
+                    w[j] = ex2_approx(Gi - g.x) * k.x;
+                    w[j + 1] = ex2_approx(Gi - g.y) * k.y;
+                    w[j + 2] = ex2_approx(Gi - g.z) * k.z;
+                    w[j + 3] = ex2_approx(Gi - g.w) * k.w;
+                }
+                tc::wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = b + j <= last ? fi * w[j] * __uint_as_float(r[j]) : 0.f;
+                if (q < 2) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + j)) = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8)
+                        SM_AT(uint4, pt(n) + i0 * 128 + ((((b + j) >> 3) ^ (i0 & 7)) << 4)) =
+                            make_uint4(pack_bf16(w[j], w[j + 1]), pack_bf16(w[j + 2], w[j + 3]), pack_bf16(w[j + 4], w[j + 5]), pack_bf16(w[j + 6], w[j + 7]));
+                }
+            }
+            tc::fence_before();
+            arrive_w(Lay::KQ_FREE);
+            if (named_bar_or(2, 256, !ok)) break;
+            // (I + A)^-1: the four diagonal blocks, a column per lane, row by row
+            if (hf == 0) {
+                const int d0 = 16 * q, c = lane & 15;
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float u = i == c ? 1.f : 0.f, w = 0.f;
+#pragma unroll
+                    for (int j = 0; j < i; j += 4) {
+                        const float4 a = SM_AT(const float4, scr + 4 * ((d0 + i) * Lay::LD + d0 + j));
+                        u = fmaf(-a.x, x[j], u);
+                        if (j + 1 < i) w = fmaf(-a.y, x[j + 1], w);
+                        if (j + 2 < i) u = fmaf(-a.z, x[j + 2], u);
+                        if (j + 3 < i) w = fmaf(-a.w, x[j + 3], w);
+                    }
+                    x[i] = u + w;
+                }
+                __syncwarp();
+                if (lane < 16) {
+                    const float b = SM_AT(const float, s + SC_B + 4 * (d0 + c));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        A(d0 + i, d0 + c) = x[i];
+                        SM_AT(uint16_t, t_at(d0 + i, d0 + c)) = f2bf_bits(b * x[i]);
+                    }
+                }
+            }
+            sync();
+            // the blocks below: -T_hi A_hl T_lo, first of 16 (eight columns per warp), then of 32
+            if (hf == 0) {
+                const int c0 = 32 * (q & 1), r0 = c0 + 16, n8 = 8 * (q >> 1);
+                float d[4] = {}, e[4] = {};
+                product(d, r0, c0, c0, c0 + n8);
+                put(d, c0, r0 + n8, 1.f);  // above the diagonal, where nothing stands
+                __syncwarp();
+                product(e, r0, r0, c0, r0 + n8);
+                __syncwarp();
+                put(e, c0, r0 + n8, -1.f);  // there too: the other warp may still read A
+                put_t(e, r0, c0 + n8);
+            }
+            sync();
+            {
+                const int mi = 16 * (w8 >> 2), ni = 8 * (w8 & 3);
+                float d[4] = {}, e[4] = {};
+                for (int k = ni & 16; k < 32; k += 16) {
+                    const bool below = k > (ni & 16);  // the block below the diagonal ones stands above them
+                    product(d, 32 + mi, k, below ? 0 : k, below ? 16 + ni : ni);
+                }
+                put(d, mi, 32 + ni, 1.f);
+                sync();
+                for (int k = 0; k <= mi; k += 16) {
+                    const bool below = k < mi;
+                    product(e, below ? 32 : 32 + mi, below ? 48 : 32 + k, k, 32 + ni);
+                }
+                put_t(e, 32 + mi, ni);
+            }
+            tc::fence_async_smem();
+            arrive_w(Lay::T_FULL + n % Lay::KQS);
+        }
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    const uint32_t groups = spoilt;
+    if (groups) redo_rows(p, seq, h, sp, groups);
+    if (warp == 0) {
+        __syncwarp();
+        tc::fence_after();
+        tc::dealloc(tmem, TMEM_COLS);
+    }
+#undef SM_AT
+}
+
+}  // namespace gdntc
+}  // namespace kda

@@ -4,6 +4,7 @@
 #pragma once
 #include "kda_attn.cuh"
 #include "kda_gdn_step.cuh"
+#include "kda_gdn_tc.cuh"
 #include "kda_rope.cuh"
 
 namespace kda {
@@ -78,6 +79,27 @@ static kda_status launch_gdn_steps(const gdn::GdnParams &p, cudaStream_t s)
     const int64_t grid = (warps + gdn::STEP_THREADS / 32 - 1) / (gdn::STEP_THREADS / 32);
     gdn::kda_gdn_step_kernel<<<static_cast<unsigned>(grid), gdn::STEP_THREADS, 0, s>>>(p, warps);
     return blk::launched("gated delta rule step");
+}
+
+// Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one.
+constexpr int64_t STEP_TOKENS = 8;
+
+static kda_status launch_gdn_tc(const gdn::GdnParams &p, cudaStream_t s)
+{
+    CUtensorMap mq, mk, mv, mo;
+    if (!blk::rows_map(&mq, p.q, p.total, p.HK, DH, p.qs, gdntc::C) || !blk::rows_map(&mk, p.k, p.total, p.HK, DH, p.ks, gdntc::C) ||
+        !blk::rows_map(&mv, p.v, p.total, p.H, DH, p.vs, gdntc::C) || !blk::rows_map(&mo, p.out, p.total, p.H, DH, p.os, gdntc::C))
+        return fail(KDA_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad geometry)");
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        const cudaError_t e = cudaFuncSetAttribute(gdntc::kda_gdn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, gdntc::Layout::ALLOC);
+        if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "gated delta rule set-up failed: %s", cudaGetErrorString(e));
+        configured_dev = dev;
+    }
+    gdntc::kda_gdn_tc_kernel<<<static_cast<unsigned>(p.nseq * static_cast<int64_t>(p.H)), gdntc::NTHREADS, gdntc::Layout::ALLOC, s>>>(mq, mk, mv, mo, p);
+    return blk::launched("gated delta rule");
 }
 
 // What qk_rope and kv_append share: the turn and the norm of heads of D channels.
@@ -167,7 +189,8 @@ KDA_API kda_status kda_gdn(const void *q, int64_t q_stride, const void *k, int64
     const mix::GdnBuffers bufs(p, N);
     if (const kda_status st = bufs.check_out({"initial_state", state_block(initial_state, initial_dtype)}); st != KDA_OK) return st;
     if (const kda_status st = bufs.check_state({"final_state", state_block(final_state, final_dtype)}); st != KDA_OK) return st;
-    return mix::launch_gdn_steps(p, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return total <= (cu_seqlens ? 1 : nseq) * mix::STEP_TOKENS ? mix::launch_gdn_steps(p, s) : mix::launch_gdn_tc(p, s);
 }
 
 KDA_API kda_status kda_gdn_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,

@@ -177,7 +177,8 @@ __device__ __forceinline__ Piece locate(const TcParams &t, int slot)
 
 // Varlen order, longest sequences first (up to LPT_MAX_SEQS sequences), so that the long chains start
 // in the first wave.
-__device__ __forceinline__ int longest_first(const ssm::SsmParams &p, int rank)
+template <class Params>
+__device__ __forceinline__ int longest_first(const Params &p, int rank)
 {
     const int lane = threadIdx.x & 31;
     int found = rank;

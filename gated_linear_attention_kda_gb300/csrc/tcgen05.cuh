@@ -191,6 +191,18 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16])
                  : "r"(taddr)
                  : "memory");
 }
+// 16 lanes (the half of this warp's quarter that the address names) x 32 consecutive 32-bit columns, in the
+// accumulator layout of a warp MMA: registers 4 c + {0, 1} of lane l hold row l / 4, columns 8 c + 2 (l % 4) + {0, 1},
+// registers 4 c + {2, 3} row l / 4 + 8
+__device__ __forceinline__ void ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    tmem_check(taddr, 32);
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
 // 16 lanes (the half of this warp's quarter that the address names) x 16 consecutive 32-bit columns, in
 // the fragment layout of ldmatrix: register 2 r + k of lane l holds row l / 4 + 8 k, column 4 r + l % 4
 __device__ __forceinline__ void st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8])

@@ -6,7 +6,12 @@ Longer prompts run in chunks whose operands are bf16: the carried state, its pro
 corrected values (twice), the scores and the output itself, seven roundings of 2^-8 / sqrt(12) to 2^-9 / sqrt(3) of a term
 at random signs. A rounding of random mantissas is 1.66e-3 of a term in the mean square, so seven of them are 4.4e-3 where
 every term is as large as the result: 5e-3 of a head's norm for outputs, and for states, which see five of them and bf16's
-own. No element may be off by more than 8 times that of the head's root mean square (64 x 128 normal errors stay under 5)."""
+own. An element's error is a sum of roundings of its own token's terms (of a state: its own value channel's), e.g.
+sum_c S[v, c] q[c] d_c with |d_c| <= 2^-8, whose mean square goes with that row's and not with the head's: a row behind a
+large initial state is larger than rows after it has decayed. So no element may be off by more than 8 times 5e-3 of the root
+mean square of its row or of the head, whichever is larger (64 x 128 normal errors stay under 5 times).
+Two of the seven, T[i, i] and P[i, i], are one number for all channels of a token, so that they average over tokens alone: a
+sequence of fewer than 16 is given their largest values, 2^-8 each, on top."""
 import pytest
 import torch
 
@@ -57,12 +62,14 @@ def want(d, cu=None):
     return ref.gdn(d["q"], d["k"], d["v"], d["a"], d["beta"], SCALE, d["A_log"], d["dt_bias"], d["init"], cu, d["l2"])
 
 
-def close(got, exp, rel, what):
-    """got, exp [..., rows, 128] of one head."""
-    err, rms = (got.double() - exp), exp.pow(2).mean().sqrt()
+def close(got, exp, rel, what, tokens=16):
+    """got, exp [..., rows, 128] of one head, behind so many tokens."""
+    if rel == REL and tokens < 16:
+        rel += 2.0 ** -7
+    err, rms = (got.double() - exp), exp.pow(2).mean(-1, keepdim=True).clamp(min=exp.pow(2).mean()).sqrt()
     assert torch.isfinite(got).all(), what
     assert err.norm() <= rel * exp.norm() + 1e-12, (what, float(err.norm() / exp.norm()))
-    assert (err.abs() <= 8 * rel * rms + 2.0 ** -8 * exp.abs()).all(), (what, float(err.abs().max() / rms))
+    assert (err.abs() <= 8 * rel * rms + 2.0 ** -8 * exp.abs()).all(), (what, float((err.abs() / rms).max()))
 
 
 def check(got, fin, exp, efin, spans, short=False):
@@ -74,10 +81,10 @@ def check(got, fin, exp, efin, spans, short=False):
                 rms = o[b:e, h].pow(2).mean().sqrt()
                 assert ((out[b:e, h].double() - o[b:e, h]).abs() <= 2.0 ** -8 * o[b:e, h].abs() + 8 * FEW * rms).all(), (i, h)
             elif e > b:
-                close(out[b:e, h], o[b:e, h], REL, ("out", i, h))
+                close(out[b:e, h], o[b:e, h], REL, ("out", i, h), e - b)
             if fin is not None:
                 state_rel = REL if not few else FEW + (2.0 ** -8 if fin.dtype == BF16 else 0.0)
-                close(fin[i, h], efin[i, h], state_rel, ("state", i, h))
+                close(fin[i, h], efin[i, h], state_rel, ("state", i, h), e - b)
 
 
 @pytest.mark.parametrize("T", [1, 2, 8, 9, 31, 53, 63, 64, 65, 127, 128, 129, 200, 517])
@@ -183,15 +190,15 @@ def test_gdn_no_number_reaches_no_earlier_token(kda, T, bad, name):
     else:
         d[name][0, t0, 1, 5] = bad
     out, fin = run(kda, d, cu, nseq=2)
-    check(out[:, :t0], None, clean[:, :t0], None, [(0, T), (T, t0)], short=True)
-    check(out[:, :, :1], None, clean[:, :, :1], None, [(0, T), (T, 2 * T)], short=True)
-    close(fin[0, 0], cfin[0, 0], REL, "first sequence")
-    close(fin[1, 0], cfin[1, 0], REL, "other head")
+    check(out[:, :t0], None, clean[:, :t0], None, [(0, T), (T, t0)])
+    check(out[:, :, :1], None, clean[:, :, :1], None, [(0, T), (T, 2 * T)])
+    close(fin[0, 0], cfin[0, 0], REL, "first sequence", T)
+    close(fin[1, 0], cfin[1, 0], REL, "other head", T)
     hit = nan_where(out[0, t0:, 1])
     if name == "v":
         assert hit[:, 5].all() and not hit[:, :5].any() and not hit[:, 6:].any()
         other = [c for c in range(128) if c != 5]
-        close(out[0, t0:, 1][:, other], clean[0, t0:, 1][:, other], REL, "other channels")
+        close(out[0, t0:, 1][:, other], clean[0, t0:, 1][:, other], REL, "other channels", T)
         assert nan_where(fin[1, 1, 5]).all() and torch.isfinite(fin[1, 1, other]).all()
     elif name == "q":
         assert hit[0].all() and not hit[1:].any() and torch.isfinite(fin).all()
