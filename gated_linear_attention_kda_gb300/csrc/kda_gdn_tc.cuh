@@ -52,8 +52,10 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t T_S = 0, T_SB = 128, T_D1 = 192, T_SQ = 256, T_D2 = 320, T_PV = 384, T_KQ = 448;
 
 // scalars of a chunk: running log2 sums, steps, 2^G (then the factors of D1'), 2^(G_63 - G) (then those of N'), the
-// output's factors, 1 / |k| and scale / |q|, the chunk's whole decay
-constexpr int SC_G = 0, SC_B = 256, SC_D = 512, SC_N = 768, SC_O = 1024, SC_RK = 1280, SC_RQ = 1536, SC_GAM = 1792, SC_BYTES = 1808;
+// output's factors; by key column G less log2 1 / |k|, and 2^(G at the end of its 16 - G) / |k|; by row b / |k| and
+// scale / |q|; the chunk's whole decay
+constexpr int SC_G = 0, SC_B = 256, SC_D = 512, SC_N = 768, SC_O = 1024, SC_GK = 1280, SC_CF = 1536, SC_FK = 1792, SC_FQ = 2048, SC_GAM = 2304,
+              SC_BYTES = 2320;
 
 struct Layout {
     static constexpr int BOX = C * 128;             // 64 channels x 64 rows, 128-byte swizzle
@@ -69,12 +71,25 @@ struct Layout {
     static constexpr int BAR = SC + KQS * SC_BYTES;
     static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 8, SC_FULL = 10, T_FULL = 13, G_DONE = 16, KQ_FREE = 17,
                          KQ_ZERO = 18, SB_GO = 19, D1_DONE = 20, D1_GO = 21, N_DONE = 22, N_GO = 23, S_DONE = 24, O_DONE = 25,
-                         OUT_RD = 26, END = 27, END2 = 28, NBARS = 29;
+                         SQ_DONE = 26, U_DONE = 27, END = 28, END2 = 29, END3 = 30, NBARS = 31;
     static constexpr int TMEMPTR = (BAR + NBARS * 8 + 15) / 16 * 16;
     static constexpr int FLAGS = TMEMPTR + 16;
     static constexpr int ALLOC = FLAGS + 16 + 1024;
     static_assert(ALLOC <= 227 * 1024, "shared memory budget");
     static_assert(SC % 16 == 0 && SC_BYTES % 16 == 0 && BAR % 8 == 0, "alignment");
+};
+
+// Place in the ring of KQS buffers and the parity of the round, of one chunk after another.
+struct Ring {
+    int s = 0;
+    uint32_t par = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == Layout::KQS) {
+            s = 0;
+            par ^= 1;
+        }
+    }
 };
 
 // An operand of a tf32 product, rounded to nearest.
@@ -112,11 +127,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
     __shared__ uint32_t spoilt;  // groups of eight rows that hold no numbers at the end
     auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
-    auto kq = [&](int n) { return sb + Lay::KQ + (n % Lay::KQS) * Lay::KQT; };
+    auto kq = [&](const Ring &g) { return sb + Lay::KQ + g.s * Lay::KQT; };
     auto vt = [&](int n) { return sb + Lay::V + (n % Lay::VS) * Lay::VT; };
-    auto pt = [&](int n) { return sb + Lay::P + (n % Lay::KQS) * Lay::BOX; };
-    auto tt = [&](int n) { return sb + Lay::T + (n % Lay::KQS) * Lay::BOX; };
-    auto sc = [&](int n) { return sb + Lay::SC + (n % Lay::KQS) * SC_BYTES; };
+    auto pt = [&](const Ring &g) { return sb + Lay::P + g.s * Lay::BOX; };
+    auto tt = [&](const Ring &g) { return sb + Lay::T + g.s * Lay::BOX; };
+    auto sc = [&](const Ring &g) { return sb + Lay::SC + g.s * SC_BYTES; };
     auto live_of = [&](int n) { return min(C, sp.len - n * C); };
 
     if (warp == 0) {
@@ -134,8 +149,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(bar(Lay::V_FULL + i), 1);
             mbar_init(bar(Lay::V_EMPTY + i), 1);
         }
-        for (int i : {Lay::G_DONE, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::END, Lay::END2}) mbar_init(bar(i), 1);
-        mbar_init(bar(Lay::OUT_RD), 4);
+        for (int i : {Lay::G_DONE, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::SQ_DONE, Lay::U_DONE, Lay::END, Lay::END2, Lay::END3})
+            mbar_init(bar(i), 1);
         for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO, Lay::KQ_FREE, Lay::KQ_ZERO}) mbar_init(bar(i), 8);
         flags[0] = 0;
         spoilt = 0u;
@@ -160,11 +175,36 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         return ok;
     };
+    // the same, polled for a while first: a suspended warp takes some 300 cycles to come back
+    auto wait_p = [&](int b, uint32_t par) {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+            if (__all_sync(0xffffffffu, mbar_test_wait(bar(b), par))) return true;
+        return wait_w(b, par);
+    };
     auto arrive_w = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
     };
-    auto kq_par = [](int n) { return static_cast<uint32_t>((n / Lay::KQS) & 1); };
+    // operands: K step i of a K-major [K; Q] tile, of an MN-major tile (16 rows), of a tile of 128-byte rows, and of an
+    // operand in tensor memory that two warps have written halves of
+    constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B);
+    constexpr uint32_t id_n = tc::idesc(tc::BF16, 128, C, 0, 0), id_u = tc::idesc(tc::BF16, 128, C, 1, 0), id_s = tc::idesc(tc::BF16, 128, DH, 0, 1);
+    auto kmaj = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(((i >> 2) * 2 * Lay::BOX + (i & 3) * 32) >> 4)); };
+    auto nmaj = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>((i * 16 * 128) >> 4)); };
+    auto rows = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>((i * 32) >> 4)); };
+    auto halves = [](int i) { return static_cast<uint32_t>(32 * (i >> 1) + 8 * (i & 1)); };
+    // a [K; Q] tile is there, with the rows past the sequence's end cleared
+    auto wait_kq = [&](int n, const Ring &g) {
+        return wait_w(Lay::KQ_FULL + g.s, g.par) && (live_of(n) == C || wait_w(Lay::KQ_ZERO, 0));
+    };
+    // the products of an issuer that are still on their way when its loop is left
+    auto finish = [&](int b) {
+        if (nch == 0) return;
+        tc::commit_w(bar(b));
+        if (lane == 0) drain_bar(bar(b), 0);
+        __syncwarp();
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -172,15 +212,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tma_prefetch_desc(&tq);
             tma_prefetch_desc(&tk);
             tma_prefetch_desc(&tv);
+            Ring rg;
             int nk = 0, nv = 0;  // tiles issued
-            for (int n = 0; n < nch; ++n) {
-                const int tok = sp.bos + n * C, full = Lay::KQ_FULL + n % Lay::KQS, vfull = Lay::V_FULL + n % Lay::VS;
-                if (!wait_bar(bar(Lay::KQ_EMPTY + n % Lay::KQS), kq_par(n) ^ 1, flags)) break;
+#pragma unroll 1
+            for (int n = 0; n < nch; ++n, rg.next()) {
+                const int tok = sp.bos + n * C, full = Lay::KQ_FULL + rg.s, vfull = Lay::V_FULL + n % Lay::VS;
+                if (!wait_bar(bar(Lay::KQ_EMPTY + rg.s), rg.par ^ 1, flags)) break;
                 mbar_arrive_expect_tx(bar(full), Lay::KQT);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    tma_load_3d(kq(n) + 2 * c * Lay::BOX, &tk, 64 * c, hk, tok, bar(full));
-                    tma_load_3d(kq(n) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
+                    tma_load_3d(kq(rg) + 2 * c * Lay::BOX, &tk, 64 * c, hk, tok, bar(full));
+                    tma_load_3d(kq(rg) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
                 }
                 ++nk;
                 if (!wait_bar(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flags)) break;
@@ -190,17 +232,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 ++nv;
             }
             // no copy is in flight when the CTA ends, whichever way the loop was left
-            for (int m = max(nk - Lay::KQS, 0); m < nk; ++m) drain_bar(bar(Lay::KQ_FULL + m % Lay::KQS), kq_par(m));
+            for (int m = max(nk - Lay::KQS, 0); m < nk; ++m) drain_bar(bar(Lay::KQ_FULL + m % Lay::KQS), (m / Lay::KQS) & 1);
             for (int m = max(nv - Lay::VS, 0); m < nv; ++m) drain_bar(bar(Lay::V_FULL + m % Lay::VS), (m / Lay::VS) & 1);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA issuer: chain and output (whole warp)
-        constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B);
-        constexpr uint32_t id_n = tc::idesc(tc::BF16, 128, C, 0, 0), id_u = tc::idesc(tc::BF16, 128, C, 1, 0),
-                           id_s = tc::idesc(tc::BF16, 128, DH, 0, 1);
-        auto halves = [](int i) { return static_cast<uint32_t>(32 * (i >> 1) + 8 * (i & 1)); };  // K step i of an operand in two halves
-        auto issue_u = [&](int n) {
-            if (!wait_w(Lay::T_FULL + n % Lay::KQS, kq_par(n)) || !wait_w(Lay::V_FULL + n % Lay::VS, (n / Lay::VS) & 1)) return false;
+        // ---------------------------------------------------------------- MMA issuer: chain (whole warp)
+        Ring rg;
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n, rg.next()) {
+            const uint32_t dk = tc::sdesc_lo(kq(rg), 16), dt = tc::sdesc_lo(tt(rg), 16), dkn = tc::sdesc_lo(kq(rg), 2 * Lay::BOX);
+            if (!wait_kq(n, rg) || !wait_p(Lay::SB_GO, n & 1)) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_D1, tmem + T_SB + 8 * i, kmaj(dk, i), id_n, i > 0);
+            tc::commit_w(bar(Lay::D1_DONE));
+            if (!wait_w(Lay::U_DONE, n & 1) || !wait_p(Lay::D1_GO, n & 1)) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_D2, tmem + T_D1 + halves(i), rows(dt, i), id_n, 1);
+            tc::commit_w(bar(Lay::N_DONE));
+            // (with the product of this state and Q done, S_DONE frees its copy too)
+            if (!wait_w(Lay::SQ_DONE, n & 1) || !wait_p(Lay::N_GO, n & 1)) break;
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 + halves(i), nmaj(dkn, i), id_s, 1);
+            tc::commit_w(bar(Lay::S_DONE));
+        }
+        finish(Lay::END);
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- MMA issuer: [K; Q] K^T, V^T T^T
+        auto issue_g = [&](int n, const Ring &rg) {
+            if (!wait_kq(n, rg)) return false;
+            if (n > 0 && !wait_w(Lay::KQ_FREE, (n - 1) & 1)) return false;
+            tc::fence_after();
+            const uint32_t d = tc::sdesc_lo(kq(rg), 16);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_KQ, kmaj(d, i), kmaj(d, i), id_n, i > 0);
+            tc::commit_w(bar(Lay::G_DONE));
+            return true;
+        };
+        auto issue_u = [&](int n, const Ring &rg) {
+            if (!wait_w(Lay::V_FULL + n % Lay::VS, (n / Lay::VS) & 1)) return false;
             if (const int Lv = live_of(n); Lv < C) {  // as the rows of K and Q past the end, which other warps clear
                 for (int i = lane; i < (C - Lv) * 16; i += 32) {
                     const int r = Lv + (i >> 4), c = i & 15;
@@ -209,72 +281,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::fence_async_smem();
                 __syncwarp();
             }
+            if (!wait_w(Lay::T_FULL + rg.s, rg.par)) return false;
+            // both products of the last chunk's N, whose columns these are, have been made
+            if (n > 0 && (!wait_w(Lay::O_DONE, (n - 1) & 1) || !wait_w(Lay::S_DONE, (n - 1) & 1))) return false;
             tc::fence_after();
-            const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(n), 16);
+            const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(rg), 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tc::mma_ss_w(tmem + T_D2, tc::sdesc_of<HI>(dv + i * ((16 * 128) >> 4)), tc::sdesc_of<HI>(dt + i * (32 >> 4)), id_u, i > 0);
+            for (int i = 0; i < 4; ++i) tc::mma_ss_w(tmem + T_D2, nmaj(dv, i), rows(dt, i), id_u, i > 0);
+            tc::commit_w(bar(Lay::U_DONE));
             tc::commit_w(bar(Lay::V_EMPTY + n % Lay::VS));
             return true;
         };
-        bool ok = true;
-        for (int n = 0; ok && n < nch; ++n) {
-            const uint32_t dk = tc::sdesc_lo(kq(n), 16), dq = dk + (Lay::BOX >> 4), dt = tc::sdesc_lo(tt(n), 16), dp = tc::sdesc_lo(pt(n), 16);
-            const uint32_t dkn = tc::sdesc_lo(kq(n), 2 * Lay::BOX);  // K with its channels as rows
-            auto kmaj = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(((i >> 2) * 2 * Lay::BOX + (i & 3) * 32) >> 4)); };
-            if (!(ok = wait_w(Lay::SB_GO, n & 1))) break;
-            tc::fence_after();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_D1, tmem + T_SB + 8 * i, kmaj(dk, i), id_n, i > 0);
-            tc::commit_w(bar(Lay::D1_DONE));
-            // N's columns have been read up by the products of the last chunk
-            if (!(ok = (n == 0 || wait_w(Lay::O_DONE, (n - 1) & 1)) && issue_u(n) && wait_w(Lay::D1_GO, n & 1))) break;
-            tc::fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_D2, tmem + T_D1 + halves(i), tc::sdesc_of<HI>(dt + i * (32 >> 4)), id_n, 1);
-            tc::commit_w(bar(Lay::N_DONE));
-            if (n > 0 && !(ok = wait_w(Lay::OUT_RD, (n - 1) & 1))) break;
-            tc::fence_after();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
-            if (!(ok = wait_w(Lay::N_GO, n & 1))) break;
-            tc::fence_after();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 + halves(i), tc::sdesc_of<HI>(dkn + i * ((16 * 128) >> 4)), id_s, 1);
-            tc::commit_w(bar(Lay::S_DONE));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + halves(i), tc::sdesc_of<HI>(dp + i * (32 >> 4)), id_n, i > 0);
-            tc::commit_w(bar(Lay::O_DONE));
+        Ring rg, ru;
+#pragma unroll 1
+        for (int n = 0; n <= nch; ++n) {  // one chunk ahead with the first
+            if (n < nch && !issue_g(n, rg)) break;
+            rg.next();
+            if (n == 0) continue;
+            if (!issue_u(n - 1, ru)) break;
+            ru.next();
         }
-        if (nch > 0) {
-            tc::commit_w(bar(Lay::END));
-            if (lane == 0) drain_bar(bar(Lay::END), 0);
-            __syncwarp();
-        }
-    } else if (warp == 2) {
-        // ---------------------------------------------------------------- MMA issuer: [K; Q] K^T
-        constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B), id_g = tc::idesc(tc::BF16, 128, C, 0, 0);
-        for (int n = 0; n < nch; ++n) {
-            if (!wait_w(Lay::KQ_FULL + n % Lay::KQS, kq_par(n))) break;
-            if (live_of(n) < C && !wait_w(Lay::KQ_ZERO, 0)) break;
-            if (n > 0 && !wait_w(Lay::KQ_FREE, (n - 1) & 1)) break;
-            tc::fence_after();
-            const uint32_t d = tc::sdesc_lo(kq(n), 16);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint64_t at = tc::sdesc_of<HI>(d + static_cast<uint32_t>(((i >> 2) * 2 * Lay::BOX + (i & 3) * 32) >> 4));
-                tc::mma_ss_w(tmem + T_KQ, at, at, id_g, i > 0);
-            }
-            tc::commit_w(bar(Lay::G_DONE));
-        }
-        if (nch > 0) {
-            tc::commit_w(bar(Lay::END2));
-            if (lane == 0) drain_bar(bar(Lay::END2), 0);
-            __syncwarp();
-        }
+        finish(Lay::END2);
     } else if (warp == 3) {
         // ---------------------------------------------------------------- decays and steps, two tokens per lane
+        Ring rg;
         const float A2 = -expf(__ldg(p.A_log + h)) * LOG2E, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
         const uint16_t *ap = p.a + static_cast<long long>(sp.bos) * p.as + h, *bp = p.beta + static_cast<long long>(sp.bos) * p.bs + h;
         uint32_t ra[2] = {0u, 0u}, rb[2] = {0u, 0u};
@@ -289,7 +319,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
         };
         fetch(0);
-        for (int n = 0; n < nch; ++n) {
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n, rg.next()) {
             const int Lv = live_of(n);
             float a[2], b[2];
 #pragma unroll
@@ -309,17 +340,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             const float all = __shfl_sync(0xffffffffu, pre, 31);
             const float g1 = pre, before = __shfl_up_sync(0xffffffffu, pre, 1), g0 = (lane ? before : 0.f) + a[0];
-            if (!wait_w(Lay::KQ_FULL + n % Lay::KQS, kq_par(n))) break;  // the buffer is free as the tile's is
-            const uint32_t o = sc(n) + 8 * lane;
+            if (!wait_w(Lay::KQ_FULL + rg.s, rg.par)) break;  // the buffer is free as the tile's is
+            const uint32_t o = sc(rg) + 8 * lane;
             SM_AT(float2, o + SC_G) = make_float2(g0, g1);
             SM_AT(float2, o + SC_B) = make_float2(b[0], b[1]);
+            const float ge = __shfl_sync(0xffffffffu, g1, lane | 7);  // at the end of the 16
+            SM_AT(float2, o + SC_CF) = make_float2(ex2_approx(ge - g0), ex2_approx(ge - g1));
             SM_AT(float2, o + SC_D) = make_float2(ex2_approx(g0), ex2_approx(g1));
             SM_AT(float2, o + SC_N) = make_float2(ex2_approx(all - g0), ex2_approx(all - g1));
-            if (lane == 0) SM_AT(float, sc(n) + SC_GAM) = ex2_approx(all);
-            arrive_w(Lay::SC_FULL + n % Lay::KQS);
+            if (lane == 0) SM_AT(float, sc(rg) + SC_GAM) = ex2_approx(all);
+            arrive_w(Lay::SC_FULL + rg.s);
         }
     } else if (warp < 12) {
         // ---------------------------------------------------------------- chain
+        Ring rg;
         const int q = warp & 3, hf = warp < 8 ? 0 : 1, v = 32 * q + lane;
         const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16);
         const uint32_t ls = lq + T_S + 64 * hf, lsb = lq + T_SB + 32 * hf, l1 = lq + T_D1 + 32 * hf, l2 = lq + T_D2 + 32 * hf;
@@ -372,19 +406,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
         };
         bool ok = true;
-        for (int n = 0; n < nch; ++n) {
+        if (nch > 0) {
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {
+                uint32_t r[32];
+                load_init(32 * g, r);
+                __syncwarp();
+                tc::st32(ls + 32 * g, r);
+            }
+            tc::wait_st();
+        }
+        // Loops are left rolled here and below: the roles' code together is larger than the instruction caches next to the
+        // schedulers, and what is fetched twice costs more than a branch.
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n, rg.next()) {
             uint32_t r[32], o[16];
             // the state as an operand
-            if (n > 0 && !(ok = wait_w(Lay::S_DONE, (n - 1) & 1))) break;
+            if (n > 0 && !(ok = wait_p(Lay::S_DONE, (n - 1) & 1))) break;
             tc::fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int g = 0; g < 2; ++g) {
-                if (n == 0) {
-                    load_init(32 * g, r);
-                } else {
-                    tc::ld32(ls + 32 * g, r);
-                    tc::wait_ld();
-                }
+                tc::ld32(ls + 32 * g, r);
+                tc::wait_ld();
                 pack(r, o);
                 tc::st16(lsb + 16 * g, o);
             }
@@ -392,39 +435,39 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before();
             arrive_w(Lay::SB_GO);
             // decayed in place
-            if (!(ok = wait_w(Lay::SC_FULL + n % Lay::KQS, kq_par(n)))) break;
-            const float gam = SM_AT(const float, sc(n) + SC_GAM);
-#pragma unroll
+            if (!(ok = wait_w(Lay::SC_FULL + rg.s, rg.par))) break;
+            const float gam = SM_AT(const float, sc(rg) + SC_GAM);
+#pragma unroll 1
             for (int g = 0; g < 2; ++g) {
-                if (n == 0) {
-                    load_init(32 * g, r);
-                } else {
-                    tc::ld32(ls + 32 * g, r);
-                    tc::wait_ld();
-                }
+                tc::ld32(ls + 32 * g, r);
+                tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(gam * __uint_as_float(r[i]));
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 x = fmul2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(gam, gam));
+                    r[i] = __float_as_uint(x.x);
+                    r[i + 1] = __float_as_uint(x.y);
+                }
                 tc::st32(ls + 32 * g, r);
             }
             // D1' over D1
-            if (!(ok = wait_w(Lay::T_FULL + n % Lay::KQS, kq_par(n)) && wait_w(Lay::D1_DONE, n & 1))) break;
+            if (!(ok = wait_w(Lay::T_FULL + rg.s, rg.par) && wait_p(Lay::D1_DONE, n & 1))) break;
             tc::fence_after();
             tc::ld32(l1, r);
             tc::wait_ld();
-            scale(r, sc(n) + SC_D + 128 * hf);
+            scale(r, sc(rg) + SC_D + 128 * hf);
             pack(r, o);
             tc::st16(l1, o);
             tc::wait_st();
             tc::fence_before();
             arrive_w(Lay::D1_GO);
             // N and N' over D2
-            if (!(ok = wait_w(Lay::N_DONE, n & 1))) break;
+            if (!(ok = wait_p(Lay::N_DONE, n & 1))) break;
             tc::fence_after();
             tc::ld32(l2, r);
             tc::wait_ld();
             pack(r, o);
             tc::st16(l2, o);
-            scale(r, sc(n) + SC_N + 128 * hf);
+            scale(r, sc(rg) + SC_N + 128 * hf);
             pack(r, o);
             tc::st16(l2 + 16, o);
             tc::wait_st();
@@ -435,7 +478,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc::fence_after();
         if (ok && nch > 0) {
             float2 z = make_float2(0.f, 0.f);  // 0 NaN and 0 inf are NaN
-#pragma unroll
+#pragma unroll 1
             for (int g = 0; g < 2; ++g) {
                 uint32_t r[32];
                 tc::ld32(ls + 32 * g, r);
@@ -448,7 +491,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         named_bar_sync(4 + q, 64);  // both halves of these rows have been looked at
         if (ok && p.fin) {
             const bool number = !(*const_cast<volatile uint32_t *>(&spoilt) >> (v / gdn::ROWS) & 1u);  // else made again at the end
-#pragma unroll
+#pragma unroll 1
             for (int g = 0; g < 2; ++g) {
                 uint32_t r[32];
                 if (nch > 0) {  // every lane of the warp takes part in the load
@@ -464,11 +507,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc::fence_before();
     } else if (warp < 16) {
         // ---------------------------------------------------------------- output
+        Ring rg;
         const int q = warp & 3;
         const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16);
-        for (int n = 0; n < nch; ++n) {
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n, rg.next()) {
             const int Lv = live_of(n);
-            const bool ok = wait_w(Lay::T_FULL + n % Lay::KQS, kq_par(n)) && wait_w(Lay::O_DONE, n & 1);
+            bool ok = true;
+            if (warp == 12) {  // its two products: all four warps have read the last chunk's
+                const uint32_t dq = tc::sdesc_lo(kq(rg), 16) + (Lay::BOX >> 4), dp = tc::sdesc_lo(pt(rg), 16);
+                ok = wait_kq(n, rg) && wait_w(Lay::SB_GO, n & 1);
+                tc::fence_after();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
+                tc::commit_w(bar(Lay::SQ_DONE));
+                ok = ok && wait_w(Lay::T_FULL + rg.s, rg.par) && wait_w(Lay::N_GO, n & 1);
+                tc::fence_after();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + halves(i), rows(dp, i), id_n, i > 0);
+                tc::commit_w(bar(Lay::O_DONE));
+            }
+            ok = ok && wait_w(Lay::T_FULL + rg.s, rg.par) && wait_w(Lay::O_DONE, n & 1);
             tc::fence_after();
             // The Q tile has been read: token i is its row i. The accumulators are loaded as warp MMA fragments (8 channels
             // x 8 tokens), so that stmatrix.trans hands a token's row its 16 bytes of eight channels.
@@ -481,7 +540,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::ld_16x256b_x4(la + T_PV, u);
                 float2 f[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = SM_AT(const float2, sc(n) + SC_O + 4 * (c0 + 8 * i + 2 * (lane & 3)));
+                for (int i = 0; i < 4; ++i) f[i] = SM_AT(const float2, sc(rg) + SC_O + 4 * (c0 + 8 * i + 2 * (lane & 3)));
                 tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -493,17 +552,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int t = c0 + 16 * i + 8 * (lane >> 4) + r;
-                    stsm_x4_t(kq(n) + (2 * (v8 >> 3) + 1) * Lay::BOX + t * 128 + (((v8 & 7) ^ r) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    stsm_x4_t(kq(rg) + (2 * (v8 >> 3) + 1) * Lay::BOX + t * 128 + (((v8 & 7) ^ r) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }
             tc::fence_before();
-            arrive_w(Lay::OUT_RD);
             tc::fence_async_smem();
             if (named_bar_or(1, 128, !ok)) break;  // all four warps leave together
             if (Lv == C) {
                 if (warp == 12 && lane == 0) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tma_store_3d(&to, kq(n) + (2 * c + 1) * Lay::BOX, 64 * c, h, sp.bos + n * C);
+                    for (int c = 0; c < 2; ++c) tma_store_3d(&to, kq(rg) + (2 * c + 1) * Lay::BOX, 64 * c, h, sp.bos + n * C);
                     bulk_commit();
                     bulk_wait_read();
                 }
@@ -513,38 +571,46 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     const long long e = static_cast<long long>(sp.bos + n * C + t) * p.os + static_cast<long long>(h) * DH + 8 * g;
                     if (!gmem_ok(e, 8, (p.total - 1) * p.os + static_cast<long long>(p.H) * DH)) continue;
                     *reinterpret_cast<uint4 *>(p.out + e) =
-                        SM_AT(const uint4, kq(n) + (2 * (g >> 3) + 1) * Lay::BOX + t * 128 + (((g & 7) ^ (t & 7)) << 4));
+                        SM_AT(const uint4, kq(rg) + (2 * (g >> 3) + 1) * Lay::BOX + t * 128 + (((g & 7) ^ (t & 7)) << 4));
                 }
             }
-            arrive_w(Lay::KQ_EMPTY + n % Lay::KQS);
+            arrive_w(Lay::KQ_EMPTY + rg.s);
         }
-        if (warp == 12 && lane == 0) bulk_wait_all();
+        if (warp == 12) {
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
+            finish(Lay::END3);
+        }
     } else {
         // ---------------------------------------------------------------- A, P and T
+        Ring rg;
         // Quarters 0 and 1 of tensor memory hold K K^T, 2 and 3 Q K^T; two warps share a quarter's columns.
         const int q = warp & 3, hf = warp < 20 ? 0 : 1, w8 = warp - 16, tid = threadIdx.x - 512;
         const int lo = q & 1, i0 = 32 * lo + lane;  // this thread's row
         const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_KQ;
         const uint32_t scr = sb + Lay::SCR;
+        auto bits = [](float x) { return __float_as_uint(x); };
         auto A = [&](int i, int j) -> float & { return SM_AT(float, scr + 4 * (i * Lay::LD + j)); };
         auto sync = [&] { named_bar_sync(2, 256); };
         const int g8 = lane >> 2, t4 = lane & 3;
-        // d += X[xr.., xc..] Y[yr.., yc..], 16 x 16 by 16 x 8, both in the scratch
+        // d += X[xr.., xc..] Y[yr.., yc..], 16 x 16 by 16 x 8, both in the scratch. What is not A itself is rounded to tf32
+        // as it is put there; A is cut off, by 2^-11 of it in the mean.
         auto product = [&](float(&d)[4], int xr, int xc, int yr, int yc) {
 #pragma unroll
             for (int k = 0; k < 16; k += 8) {
-                const uint32_t a[4] = {tf32(A(xr + g8, xc + k + t4)), tf32(A(xr + g8 + 8, xc + k + t4)), tf32(A(xr + g8, xc + k + t4 + 4)),
-                                       tf32(A(xr + g8 + 8, xc + k + t4 + 4))};
-                mma_tf32(d, a, tf32(A(yr + k + t4, yc + g8)), tf32(A(yr + k + t4 + 4, yc + g8)));
+                const uint32_t a[4] = {bits(A(xr + g8, xc + k + t4)), bits(A(xr + g8 + 8, xc + k + t4)), bits(A(xr + g8, xc + k + t4 + 4)),
+                                       bits(A(xr + g8 + 8, xc + k + t4 + 4))};
+                mma_tf32(d, a, bits(A(yr + k + t4, yc + g8)), bits(A(yr + k + t4 + 4, yc + g8)));
             }
         };
         auto put = [&](const float(&d)[4], int r, int c, float f) {
-            SM_AT(float2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_float2(f * d[0], f * d[1]);
-            SM_AT(float2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_float2(f * d[2], f * d[3]);
+            SM_AT(uint2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[0]), tf32(f * d[1]));
+            SM_AT(uint2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[2]), tf32(f * d[3]));
         };
-        for (int n = 0; n < nch; ++n) {
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n, rg.next()) {
             const int Lv = live_of(n);
-            const uint32_t s = sc(n), t0 = tt(n);
+            const uint32_t s = sc(rg), t0 = tt(rg);
             // where T[i][j] stands as an operand, times its column's step
             auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
             auto put_t = [&](const float(&d)[4], int r, int c) {
@@ -552,97 +618,116 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(uint32_t, t_at(r + g8, c + 2 * t4)) = pack_bf16(-d[0] * b.x, -d[1] * b.y);
                 SM_AT(uint32_t, t_at(r + g8 + 8, c + 2 * t4)) = pack_bf16(-d[2] * b.x, -d[3] * b.y);
             };
-            bool ok = wait_w(Lay::KQ_FULL + n % Lay::KQS, kq_par(n));
+            bool ok = wait_w(Lay::KQ_FULL + rg.s, rg.par);
             if (Lv < C) {
                 // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
                 for (int i = tid; i < (C - Lv) * 32; i += 256) {
                     const int r = Lv + (i >> 5), c = i & 31;
-                    SM_AT(uint4, kq(n) + (c >> 3) * Lay::BOX + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    SM_AT(uint4, kq(rg) + (c >> 3) * Lay::BOX + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 tc::fence_async_smem();
                 arrive_w(Lay::KQ_ZERO);
                 sync();
             }
-            if (p.l2) {  // four threads a row
-                const int r = tid >> 2, c0 = 4 * (tid & 3);
-                float2 ss[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float2 f[4];
-                        blk::unpack8(SM_AT(const uint4, kq(n) + (2 * (c0 >> 3) + m) * Lay::BOX + r * 128 + ((((c0 + c) & 7) ^ (r & 7)) << 4)), f);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) ss[m] = ffma2(f[j], f[j], ss[m]);
+            ok = ok && wait_w(Lay::SC_FULL + rg.s, rg.par);
+            // the factors of rows and columns: warps 0..3 those of 16 rows of K each, the others those of Q
+            {
+                const bool is_q = w8 >= 4;
+                const int r0 = 16 * (w8 & 3), r1 = r0 + g8 + 8 * (t4 & 1);
+                float f = 1.f;
+                if (p.l2) {
+                    // squares of norms on the diagonal of X X^T, whose operand fragments are the same registers
+                    float d[4] = {}, e[4] = {};
+                    const int r = r0 + (lane & 15), c = lane >> 4;
+                    const uint32_t at = kq(rg) + (is_q ? Lay::BOX : 0) + r * 128;
+#pragma unroll 2
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t a[4];
+                        ldsm_x4(at + (k >> 2) * 2 * Lay::BOX + (((2 * (k & 3) + c) ^ (r & 7)) << 4), a[0], a[1], a[2], a[3]);
+                        mma_bf16(d, a, a[0], a[2]);
+                        mma_bf16(e, a, a[1], a[3]);
                     }
-                float kk = ss[0].x + ss[0].y, qq = ss[1].x + ss[1].y;
-#pragma unroll
-                for (int m = 1; m < 4; m <<= 1) {
-                    kk += __shfl_xor_sync(0xffffffffu, kk, m);
-                    qq += __shfl_xor_sync(0xffffffffu, qq, m);
+                    // row g8 stands in lane t4 = g8 / 2 of d, row g8 + 8 there of e: handed to lanes t4 = 0 and 1
+                    const float u = g8 & 1 ? d[1] : d[0], w = g8 & 1 ? e[3] : e[2];
+                    const float su = __shfl_sync(0xffffffffu, u, 4 * g8 + (g8 >> 1)), sw = __shfl_sync(0xffffffffu, w, 4 * g8 + (g8 >> 1));
+                    f = rsqrtf((t4 & 1 ? sw : su) + gdn::L2_EPS);
                 }
-                if ((lane & 3) == 0) {
-                    SM_AT(float, s + SC_RK + 4 * r) = rsqrtf(kk + gdn::L2_EPS);
-                    SM_AT(float, s + SC_RQ + 4 * r) = p.scale * rsqrtf(qq + gdn::L2_EPS);
+                if (t4 < 2) {
+                    const float g = SM_AT(const float, s + SC_G + 4 * r1);
+                    if (is_q) {
+                        f *= p.scale;
+                        SM_AT(float, s + SC_FQ + 4 * r1) = f;
+                        SM_AT(float, s + SC_O + 4 * r1) = f * ex2_approx(g);
+                    } else {
+                        SM_AT(float, s + SC_FK + 4 * r1) = f * SM_AT(const float, s + SC_B + 4 * r1);
+                        SM_AT(float, s + SC_GK + 4 * r1) = p.l2 ? g - lg2_approx(f) : g;
+                        SM_AT(float, s + SC_CF + 4 * r1) *= f;
+                        SM_AT(float, s + SC_D + 4 * r1) *= -f;
+                        SM_AT(float, s + SC_N + 4 * r1) *= f;
+                    }
                 }
-            } else if (tid < C) {
-                SM_AT(float, s + SC_RK + 4 * tid) = 1.f;
-                SM_AT(float, s + SC_RQ + 4 * tid) = p.scale;
             }
-            ok = ok && wait_w(Lay::SC_FULL + n % Lay::KQS, kq_par(n));
             if (named_bar_or(2, 256, !ok)) break;  // all eight warps leave together
-            const float Gi = SM_AT(const float, s + SC_G + 4 * i0), rk = SM_AT(const float, s + SC_RK + 4 * i0);
-            const float fi = q < 2 ? SM_AT(const float, s + SC_B + 4 * i0) * rk : SM_AT(const float, s + SC_RQ + 4 * i0);
-            if (q >= 2) {
-                if (hf == 0) SM_AT(float, s + SC_O + 4 * i0) = fi * ex2_approx(Gi);
-            } else if (hf == 0) {
-                SM_AT(float, s + SC_D + 4 * i0) *= -rk;
-            } else {
-                SM_AT(float, s + SC_N + 4 * i0) *= rk;
-            }
+            const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
             ok = wait_w(Lay::G_DONE, n & 1);
             tc::fence_after();
-            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
+            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two. Away
+            // from the diagonal blocks a decay is the product of one to the end of the column's 16 and one from there.
             const int last = q < 2 ? i0 - 1 : i0;
 #pragma unroll 1
             for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
                 uint32_t r[16];
-                float w[16];
+                float2 w[8];
                 tc::ld16(lq + b, r);
+                if (lo == 1 && hf == 0) {
+                    const float rf = fi * ex2_approx(Gi - SM_AT(const float, s + SC_G + 4 * (b + 15)));
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 g = SM_AT(const float4, s + SC_G + 4 * (b + j)), k = SM_AT(const float4, s + SC_RK + 4 * (b + j));
-                    w[j] = ex2_approx(Gi - g.x) * k.x;
-                    w[j + 1] = ex2_approx(Gi - g.y) * k.y;
-                    w[j + 2] = ex2_approx(Gi - g.z) * k.z;
-                    w[j + 3] = ex2_approx(Gi - g.w) * k.w;
-                }
-                tc::wait_ld();
+                    for (int j = 0; j < 8; j += 2) {
+                        const float4 k = SM_AT(const float4, s + SC_CF + 4 * (b + 2 * j));
+                        w[j] = fmul2(make_float2(k.x, k.y), make_float2(rf, rf));
+                        w[j + 1] = fmul2(make_float2(k.z, k.w), make_float2(rf, rf));
+                    }
+                    tc::wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = b + j <= last ? fi * w[j] * __uint_as_float(r[j]) : 0.f;
-                if (q < 2) {
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + j)) = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                    for (int j = 0; j < 8; ++j) w[j] = fmul2(w[j], make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8)
-                        SM_AT(uint4, pt(n) + i0 * 128 + ((((b + j) >> 3) ^ (i0 & 7)) << 4)) =
-                            make_uint4(pack_bf16(w[j], w[j + 1]), pack_bf16(w[j + 2], w[j + 3]), pack_bf16(w[j + 4], w[j + 5]), pack_bf16(w[j + 6], w[j + 7]));
+                    for (int j = 0; j < 8; j += 2) {
+                        const float4 g = SM_AT(const float4, s + SC_GK + 4 * (b + 2 * j));
+                        w[j] = make_float2(ex2_approx(Gi - g.x), ex2_approx(Gi - g.y));
+                        w[j + 1] = make_float2(ex2_approx(Gi - g.z), ex2_approx(Gi - g.w));
+                    }
+                    tc::wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+                        if (b + 2 * j > last) w[j].x = 0.f;
+                        if (b + 2 * j + 1 > last) w[j].y = 0.f;
+                    }
+                }
+                if (q < 2) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4)
+                        SM_AT(uint4, pt(rg) + i0 * 128 + ((((b >> 3) + (j >> 2)) ^ (i0 & 7)) << 4)) =
+                            make_uint4(pack_bf16(w[j].x, w[j].y), pack_bf16(w[j + 1].x, w[j + 1].y), pack_bf16(w[j + 2].x, w[j + 2].y), pack_bf16(w[j + 3].x, w[j + 3].y));
                 }
             }
             tc::fence_before();
             arrive_w(Lay::KQ_FREE);
             if (named_bar_or(2, 256, !ok)) break;
-            // (I + A)^-1: the four diagonal blocks, a column per lane, row by row
+            // (I + A)^-1: diagonal blocks of 8, two per warp, a column per lane, row by row; then the block between them
             if (hf == 0) {
-                const int d0 = 16 * q, c = lane & 15;
-                float x[16];
+                const int d0 = 16 * q, d1 = d0 + (lane & 8), c = lane & 7;
+                float x[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     float u = i == c ? 1.f : 0.f, w = 0.f;
 #pragma unroll
                     for (int j = 0; j < i; j += 4) {
-                        const float4 a = SM_AT(const float4, scr + 4 * ((d0 + i) * Lay::LD + d0 + j));
+                        const float4 a = SM_AT(const float4, scr + 4 * ((d1 + i) * Lay::LD + d1 + j));
                         u = fmaf(-a.x, x[j], u);
                         if (j + 1 < i) w = fmaf(-a.y, x[j + 1], w);
                         if (j + 2 < i) u = fmaf(-a.z, x[j + 2], u);
@@ -652,13 +737,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 __syncwarp();
                 if (lane < 16) {
-                    const float b = SM_AT(const float, s + SC_B + 4 * (d0 + c));
+                    const float b = SM_AT(const float, s + SC_B + 4 * (d1 + c));
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        A(d0 + i, d0 + c) = x[i];
-                        SM_AT(uint16_t, t_at(d0 + i, d0 + c)) = f2bf_bits(b * x[i]);
+                    for (int i = 0; i < 8; ++i) {
+                        A(d1 + i, d1 + c) = __uint_as_float(tf32(x[i]));
+                        SM_AT(uint16_t, t_at(d1 + i, d1 + c)) = f2bf_bits(b * x[i]);
                     }
                 }
+                __syncwarp();
+                float d[4] = {}, e[4] = {};
+                const uint32_t a[4] = {bits(A(d0 + 8 + g8, d0 + t4)), 0u, bits(A(d0 + 8 + g8, d0 + t4 + 4)), 0u};
+                mma_tf32(d, a, bits(A(d0 + t4, d0 + g8)), bits(A(d0 + t4 + 4, d0 + g8)));
+                __syncwarp();
+                SM_AT(uint2, scr + 4 * ((d0 + 8 + g8) * Lay::LD + d0 + 2 * t4)) = make_uint2(tf32(d[0]), tf32(d[1]));
+                __syncwarp();
+                const uint32_t h[4] = {bits(A(d0 + 8 + g8, d0 + 8 + t4)), 0u, bits(A(d0 + 8 + g8, d0 + 8 + t4 + 4)), 0u};
+                mma_tf32(e, h, bits(A(d0 + 8 + t4, d0 + g8)), bits(A(d0 + 8 + t4 + 4, d0 + g8)));
+                __syncwarp();
+                SM_AT(uint2, scr + 4 * ((d0 + 8 + g8) * Lay::LD + d0 + 2 * t4)) = make_uint2(tf32(-e[0]), tf32(-e[1]));
+                const float2 b = SM_AT(const float2, s + SC_B + 4 * (d0 + 2 * t4));
+                SM_AT(uint32_t, t_at(d0 + 8 + g8, d0 + 2 * t4)) = pack_bf16(-e[0] * b.x, -e[1] * b.y);
             }
             sync();
             // the blocks below: -T_hi A_hl T_lo, first of 16 (eight columns per warp), then of 32
@@ -690,7 +788,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 put_t(e, 32 + mi, ni);
             }
             tc::fence_async_smem();
-            arrive_w(Lay::T_FULL + n % Lay::KQS);
+            arrive_w(Lay::T_FULL + rg.s);
         }
     }
 
