@@ -138,11 +138,46 @@ static rope::Pages pages_of(int64_t page_stride, int64_t pages, int64_t page_siz
     return {page_stride, table, static_cast<int>(width), static_cast<int>(pages), shift};
 }
 
-// Tokens per CTA: one while CTAs are fewer than the machine takes at once, up to eight.
+// Warps with a run of the cache, and the workspace with which runs may be cut inside a unit.
+static int64_t attn_workers(int sms) { return static_cast<int64_t>(sms) * attn::CTAS * attn::WARPS; }
+static size_t attn_bytes(int64_t D, int sms) { return static_cast<size_t>(attn_workers(sms)) * 2 * 16 * (D + 2) * sizeof(float); }
+
+template <int D>
+static kda_status launch_attn(const attn::AttnParams &p, cudaStream_t s)
+{
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_dev != dev) {
+        const cudaError_t e = cudaFuncSetAttribute(attn::kda_attn_step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, attn::smem_of(D));
+        if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "attention set-up failed: %s", cudaGetErrorString(e));
+        configured_dev = dev;
+    }
+    attn::kda_attn_step_kernel<D><<<(p.workers + attn::WARPS - 1) / attn::WARPS, attn::THREADS, attn::smem_of(D), s>>>(p);
+    if (const kda_status st = blk::launched("attention step"); st != KDA_OK || !p.ws) return st;
+    // few units are looked at one by one, with a block for each of their rows; many at the borders between the runs
+    const int64_t units = static_cast<int64_t>(p.S) * p.HK * p.tiles;
+    const bool by_unit = units <= p.workers;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(by_unit ? units : p.workers - 1), static_cast<unsigned>(units <= 64 ? std::min(p.rows, 16) : 1));
+    cfg.blockDim = dim3(attn::JOIN_THREADS);
+    cfg.dynamicSmemBytes = cfg.blockDim.x / 32 * (D + 2) * sizeof(float);
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its blocks look for their unit while the last runs end
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn::kda_attn_join_kernel<D>, p, static_cast<int>(by_unit));
+    if (e != cudaSuccess) return fail(KDA_ERR_LAUNCH, "attention join launch failed: %s", cudaGetErrorString(e));
+    return KDA_OK;
+}
+
+// Tokens per CTA: one while CTAs are fewer than the machine takes at once, up to MAX_TOKENS.
 static int tokens_per_cta(int64_t M, int sms)
 {
     int n = 1;
-    while (n < 8 && M > static_cast<int64_t>(sms) * 8 * n) n <<= 1;
+    while (n < rope::MAX_TOKENS && M > static_cast<int64_t>(sms) * 8 * n) n <<= 1;
     return n;
 }
 
@@ -340,7 +375,9 @@ KDA_API kda_status kda_attn_step_workspace_bytes(int64_t S, int64_t H, int64_t H
     if (!bytes) return fail(KDA_ERR_NULL, "kda_attn_step_workspace_bytes: bytes is required");
     if (S < 0 || HK < 1 || H < 1 || H % HK || (D != 64 && D != 128))
         return fail(KDA_ERR_SHAPE, "bad sizes S=%lld H=%lld HK=%lld D=%lld", (long long)S, (long long)H, (long long)HK, (long long)D);
-    *bytes = 0;
+    blk::Device d;
+    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+    *bytes = S > 0 ? mix::attn_bytes(D, d.sms) : 0;
     return KDA_OK;
 }
 
@@ -350,7 +387,7 @@ KDA_API kda_status kda_attn_step(const void *q, int64_t q_stride, const void *k_
                                  int64_t HK, int64_t D, void *workspace, size_t workspace_bytes, void *stream)
 {
     t_last_error.clear();
-    if (S < 1 || S > (1 << 24) || HK < 1 || H < 1 || H > (1 << 16) || H % HK)
+    if (S < 1 || S > (1 << 16) || HK < 1 || H < 1 || H > (1 << 16) || H % HK)
         return fail(KDA_ERR_SHAPE, "HK must divide H (S=%lld H=%lld HK=%lld)", (long long)S, (long long)H, (long long)HK);
     if (D != 64 && D != 128) return fail(KDA_ERR_SHAPE, "D must be 64 or 128 (got %lld)", (long long)D);
     if (const kda_status st = mix::check_pages(k_cache, v_cache, page_stride, pages, page_size, page_table, table_width, HK, D); st != KDA_OK) return st;
@@ -380,9 +417,20 @@ KDA_API kda_status kda_attn_step(const void *q, int64_t q_stride, const void *k_
     p.H = static_cast<int>(H);
     p.HK = static_cast<int>(HK);
     p.D = static_cast<int>(D);
-    const int64_t warps = S * H, per = attn::THREADS / 32;
-    attn::kda_attn_step_kernel<<<static_cast<unsigned>((warps + per - 1) / per), attn::THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return blk::launched("attention step");
+    p.rows = static_cast<int>(H / HK);
+    p.tiles = (p.rows + 15) / 16;
+    blk::Device d;
+    if (const kda_status st = blk::device(&d); st != KDA_OK) return st;
+    p.workers = static_cast<int>(mix::attn_workers(d.sms));
+    if (workspace) {
+        const size_t need = mix::attn_bytes(D, d.sms);
+        if (workspace_bytes < need) return fail(KDA_ERR_RANGE, "workspace of %zu bytes is smaller than the %zu this call needs", workspace_bytes, need);
+        const blk::Named ws{"workspace", blk::block(workspace, static_cast<int64_t>(need))};
+        if (const kda_status st = blk::check_apart(ws, {qr, orow, lr, kc, vc, tab, pos}); st != KDA_OK) return st;
+        p.ws = static_cast<float *>(workspace);
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return D == 64 ? mix::launch_attn<64>(p, s) : mix::launch_attn<128>(p, s);
 }
 
 }  // extern "C"

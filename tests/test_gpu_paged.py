@@ -271,7 +271,7 @@ def test_attn_step_no_number_in_sight_reaches_its_heads_alone(kda):
     kc, vc = caches(g, total, 2, page, D)
     q = randn(g, 2, 4, D)
     pos = torch.tensor(lens, device="cuda") - 1
-    clean = check_attn(kda, q, kc, vc, table, pos, 0.125)[0].clone()
+    clean = check_attn(kda, q, kc, vc, table, pos, 0.125, workspace=False)[0].clone()
     vc[int(table[0, 1]), 1, 3, 7] = float("nan")
     out = torch.empty_like(q)
     kda.attn_step(q, kc, vc, table, pos, out, 0.125)
