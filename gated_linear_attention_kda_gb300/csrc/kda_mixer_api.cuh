@@ -131,6 +131,14 @@ static kda_status check_pages(const void *k_cache, const void *v_cache, int64_t 
     return KDA_OK;
 }
 
+// go(width, interleaved) with both as constants
+template <class Go>
+static void by_width(int64_t D, bool interleaved, const Go &go)
+{
+    auto pairs = [&](auto d) { interleaved ? go(d, std::true_type()) : go(d, std::false_type()); };
+    D == 64 ? pairs(std::integral_constant<int, 64>()) : D == 128 ? pairs(std::integral_constant<int, 128>()) : pairs(std::integral_constant<int, 256>());
+}
+
 static rope::Pages pages_of(int64_t page_stride, int64_t pages, int64_t page_size, const int32_t *table, int64_t width)
 {
     int shift = 0;
@@ -173,11 +181,11 @@ static kda_status launch_attn(const attn::AttnParams &p, cudaStream_t s)
     return KDA_OK;
 }
 
-// Tokens per CTA: one while CTAs are fewer than the machine takes at once, up to MAX_TOKENS.
-static int tokens_per_cta(int64_t M, int sms)
+// Tokens per CTA: one while CTAs are fewer than the machine takes at once, up to `limit`.
+static int tokens_per_cta(int64_t M, int sms, int limit)
 {
     int n = 1;
-    while (n < rope::MAX_TOKENS && M > static_cast<int64_t>(sms) * 8 * n) n <<= 1;
+    while (n < limit && M > static_cast<int64_t>(sms) * 8 * n) n <<= 1;
     return n;
 }
 
@@ -301,15 +309,13 @@ KDA_API kda_status kda_qk_rope(const void *q, int64_t q_stride, const void *k, i
     p.M = M;
     p.H = static_cast<int>(H);
     p.HK = static_cast<int>(HK);
-    p.D = static_cast<int>(D);
-    p.tokens = mix::tokens_per_cta(M, d.sms);
+    p.tokens = mix::tokens_per_cta(M, d.sms, rope::MAX_TOKENS);
     const unsigned grid = static_cast<unsigned>((M + p.tokens - 1) / p.tokens);
     const size_t table = static_cast<size_t>(p.tokens) * (R / 2) * sizeof(float2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (interleaved)
-        rope::kda_qk_rope_kernel<true><<<grid, rope::THREADS, table, s>>>(p);
-    else
-        rope::kda_qk_rope_kernel<false><<<grid, rope::THREADS, table, s>>>(p);
+    mix::by_width(D, interleaved != 0, [&](auto d, auto inter) {
+        rope::kda_qk_rope_kernel<decltype(d)::value, decltype(inter)::value><<<grid, rope::THREADS, table, s>>>(p);
+    });
     return blk::launched("query and key rotation");
 }
 
@@ -357,15 +363,13 @@ KDA_API kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v,
     p.T = static_cast<int>(T);
     p.nseq = static_cast<int>(nseq);
     p.HK = static_cast<int>(HK);
-    p.D = static_cast<int>(D);
-    p.tokens = mix::tokens_per_cta(M, d.sms);
+    p.tokens = mix::tokens_per_cta(M, d.sms, rope::MAX_TOKENS / 2);
     const unsigned grid = static_cast<unsigned>((M + p.tokens - 1) / p.tokens);
     const size_t table = static_cast<size_t>(p.tokens) * (R / 2) * sizeof(float2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (interleaved)
-        rope::kda_kv_append_kernel<true><<<grid, rope::THREADS, table, s>>>(p);
-    else
-        rope::kda_kv_append_kernel<false><<<grid, rope::THREADS, table, s>>>(p);
+    mix::by_width(D, interleaved != 0, [&](auto d, auto inter) {
+        rope::kda_kv_append_kernel<decltype(d)::value, decltype(inter)::value><<<grid, rope::THREADS, table, s>>>(p);
+    });
     return blk::launched("cache append");
 }
 

@@ -15,8 +15,8 @@ namespace rope {
 
 constexpr int THREADS = 128;
 constexpr int MAX_D = 256;
-constexpr int BATCH = 4;       // heads of a lane group in flight
 constexpr int MAX_TOKENS = 16; // of a CTA
+constexpr int BLOCK = 4;       // tokens that a warp takes through a group of heads
 
 struct Turn {
     const int64_t *positions;  // per token
@@ -60,104 +60,100 @@ __device__ __forceinline__ float2 turn_at(int64_t position, uint64_t F)
     return make_float2(c, s);
 }
 
-__device__ __forceinline__ void load8s(const float *p, float (&f)[8])
-{
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-
-// A lane owns two vectors of eight channels of a head, of the part that is turned both members of eight pairs. First and
-// second vectors of neighbouring lanes are neighbours, so that an access covers whole sectors (32,768 tokens of 20 heads
-// of 128, 32 channels turned: 51 us so, 78 us with a lane's vectors side by side).
-struct Vectors {
-    int v0, v1;    // first channel of either
-    int c0, c1;    // first pair of either in the token's table (interleaved pairs; else c0 is both's)
+// A head is held by D / 16 neighbouring lanes, two vectors of eight channels each, of the part that is turned both members
+// of eight pairs. First and second vectors of neighbouring lanes are neighbours, so that an access covers whole sectors
+// (32,768 tokens of 20 heads of 128, 32 channels turned: 78 us with a lane's vectors side by side, 63 so).
+template <int D, bool INTER>
+struct Lane {
+    static constexpr int LANES = D / 16, HEADS = 32 / LANES;  // of a head, and heads of a warp
+    int v0, v1;    // first channel of either vector
+    int q0, q1;    // where either's turns begin in the table (interleaved pairs; else q0 is both's)
     bool t0, t1;   // turned
+    __device__ __forceinline__ explicit Lane(int R)
+    {
+        const int j = threadIdx.x % LANES, half = R / 16;  // vectors in half of the turned part
+        if (INTER) {
+            v0 = 8 * j;
+            v1 = 8 * (j + LANES);
+            q0 = j;
+            q1 = j + LANES;
+            t0 = v0 < R;
+            t1 = v1 < R;
+        } else {
+            const bool in = j < half;
+            v0 = in ? 8 * j : 8 * (j + half);
+            v1 = in ? 8 * (j + half) : 8 * (j + LANES);
+            q0 = q1 = j;
+            t0 = t1 = in;
+        }
+    }
 };
-template <bool INTER>
-__device__ __forceinline__ Vectors vectors_of(int j, int lanes, int R)
-{
-    if (INTER) return {8 * j, 8 * (j + lanes), 4 * j, 4 * (j + lanes), 8 * j < R, 8 * (j + lanes) < R};
-    const int half = R / 16;  // vectors in half of the turned part
-    if (j < half) return {8 * j, 8 * (j + half), 8 * j, 8 * j, true, true};
-    return {8 * (j + half), 8 * (j + lanes), 0, 0, false, false};
-}
 
-// Norm and turn of one head held by `lanes` neighbouring lanes; w: the head's weights or NULL; cs: the token's turns.
+// The CTA's turns: per token R / 4 quadruples (cos, cos, sin, sin) of two pairs. A lane reads those of its eight pairs (four,
+// of a vector of interleaved ones) in steps, and the quadruples of neighbouring lanes' steps lie next to each other.
 template <bool INTER>
-__device__ __forceinline__ void norm_and_turn(float (&a)[8], float (&b)[8], bool norm, float eps, float inv_d, int lanes, const float *w,
-                                              const Vectors &v, const float2 *cs)
+__device__ __forceinline__ void make_table(float *table, const Turn &t, long long tok0, int tokens)
 {
-    if (norm) {
-        float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            ss = ffma2(make_float2(a[i], a[i + 1]), make_float2(a[i], a[i + 1]), ss);
-            ss = ffma2(make_float2(b[i], b[i + 1]), make_float2(b[i], b[i + 1]), ss);
-        }
-        float sum = ss.x + ss.y;
-        for (int m = lanes >> 1; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        const float f = rsqrtf(fmaf(sum, inv_d, eps));
-        float wa[8], wb[8];
-        load8s(w + v.v0, wa);
-        load8s(w + v.v1, wb);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            a[i] *= f * wa[i];
-            b[i] *= f * wb[i];
-        }
-    }
-    if (INTER) {  // pairs inside the vectors
-        auto turn = [&](float(&x)[8], int c) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float2 t = cs[c + i / 2];
-                const float y = x[i];
-                x[i] = y * t.x - x[i + 1] * t.y;
-                x[i + 1] = x[i + 1] * t.x + y * t.y;
-            }
-        };
-        if (v.t0) turn(a, v.c0);
-        if (v.t1) turn(b, v.c1);
-    } else if (v.t0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 t = cs[v.c0 + i];
-            const float x = a[i];
-            a[i] = x * t.x - b[i] * t.y;
-            b[i] = b[i] * t.x + x * t.y;
-        }
-    }
-}
-
-// The CTA's table of cosines and sines: `tokens` rows of R / 2 pairs.
-__device__ __forceinline__ void make_table(float2 *table, const Turn &t, long long tok0, int tokens)
-{
+    constexpr int G = INTER ? 4 : 8;  // pairs of a lane's read
     const int half = t.R / 2;
     for (int i = threadIdx.x; i < half * tokens; i += blockDim.x) {
         const int tk = i / half, f = i - tk * half;
-        table[i] = turn_at(__ldg(t.positions + tok0 + tk), turns_per_step(__ldg(t.inv_freq + f)));
+        const float2 cs = turn_at(__ldg(t.positions + tok0 + tk), turns_per_step(__ldg(t.inv_freq + f)));
+        float *at = table + 4 * (tk * (half / 2) + ((f % G) >> 1) * (half / G) + f / G) + (f & 1);
+        at[0] = cs.x;
+        at[2] = cs.y;
     }
 }
 
-// A head's weights in shared memory (1 where there are none).
-__device__ __forceinline__ void keep_weights(float *dst, const float *w, int D)
+__device__ __forceinline__ void load_weights(const float *w, int c, float2 (&f)[4])
 {
-    for (int i = threadIdx.x; i < D; i += blockDim.x) dst[i] = w ? __ldg(w + i) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(1.f, 1.f);
+    if (w) blk::load8f(w + c, f);
 }
 
-// (token of the CTA, head) of a lane group, walked along without dividing
-struct Item {
-    int tk, hd;
-    __device__ __forceinline__ void next(int by, int heads)
-    {
-        hd += by;
-        while (hd >= heads) {
-            hd -= heads;
-            ++tk;
+// Norm and turn of one head; wa, wb: the lane's weights; table: the token's turns.
+template <int D, bool INTER>
+__device__ __forceinline__ void norm_and_turn(float2 (&a)[4], float2 (&b)[4], bool norm, float eps, const float2 (&wa)[4], const float2 (&wb)[4],
+                                              const Lane<D, INTER> &l, const float4 *table, int half)
+{
+    if (norm) {
+        float2 ss = fmul2(a[0], a[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) ss = ffma2(a[i], a[i], ss);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = ffma2(b[i], b[i], ss);
+        float sum = ss.x + ss.y;
+#pragma unroll
+        for (int m = D / 32; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        const float f = rsqrtf(fmaf(sum, 1.f / D, eps));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = fmul2(a[i], fmul2(wa[i], make_float2(f, f)));
+            b[i] = fmul2(b[i], fmul2(wb[i], make_float2(f, f)));
         }
     }
-};
+    if (INTER) {  // pairs inside the vectors
+        auto turn = [&](float2(&x)[4], int q) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 t = table[i * (half / 4) + q];
+                x[2 * i] = make_float2(x[2 * i].x * t.x - x[2 * i].y * t.z, x[2 * i].y * t.x + x[2 * i].x * t.z);
+                x[2 * i + 1] = make_float2(x[2 * i + 1].x * t.y - x[2 * i + 1].y * t.w, x[2 * i + 1].y * t.y + x[2 * i + 1].x * t.w);
+            }
+        };
+        if (l.t0) turn(a, l.q0);
+        if (l.t1) turn(b, l.q1);
+    } else if (l.t0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 t = table[i * (half / 8) + l.q0];
+            const float2 c = make_float2(t.x, t.y), s = make_float2(t.z, t.w), x = a[i], y = b[i];
+            a[i] = fsub2(fmul2(x, c), fmul2(y, s));
+            b[i] = ffma2(x, s, fmul2(y, c));
+        }
+    }
+}
 
 struct QkParams {
     const uint16_t *q, *k;
@@ -167,65 +163,64 @@ struct QkParams {
     Turn turn;
     HeadNorm hn;
     long long M;
-    int H, HK, D, tokens;        // tokens: of one CTA
+    int H, HK, tokens;           // tokens: of one CTA
 };
 
-template <bool INTER>
+// A CTA makes the turns of its tokens, and its warps take blocks of four tokens through groups of heads: four tokens' loads
+// are in flight, and what belongs to a head (addresses, weights) is worked out once for them.
+template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS) kda_qk_rope_kernel(const QkParams p)
 {
-    extern __shared__ float2 table[];
-    __shared__ __align__(16) float weights[2][MAX_D];
+    extern __shared__ __align__(16) float table[];
+    using L = Lane<D, INTER>;
     const long long tok0 = static_cast<long long>(blockIdx.x) * p.tokens;
-    const int n = static_cast<int>(min(static_cast<long long>(p.tokens), p.M - tok0));
-    const int lanes = p.D / 16, per = THREADS / lanes, j = threadIdx.x % lanes, heads = p.H + p.HK, units = n * heads;
-    const Vectors v = vectors_of<INTER>(j, lanes, p.turn.R);
-    const float inv_d = 1.f / static_cast<float>(p.D);
-    Item ld = {0, 0}, st;
-    ld.next(static_cast<int>(threadIdx.x) / lanes, heads);
-    st = ld;
-    uint4 x[BATCH][2];
-    auto fetch = [&]() {
+    const int n = static_cast<int>(min(static_cast<long long>(p.tokens), p.M - tok0)), half = p.turn.R / 2;
+    const int warp = threadIdx.x >> 5, mine = (threadIdx.x & 31) / L::LANES, heads = p.H + p.HK;
+    const int groups = (heads + L::HEADS - 1) / L::HEADS, units = groups * ((n + BLOCK - 1) / BLOCK);
+    const L l(p.turn.R);
+    uint4 x[BLOCK][2];
+    long long at = 0, stride = 0;
+    int hd = 0, t0 = 0;
+    auto fetch = [&](int u) {  // unit u: a group of heads, four tokens
+        t0 = u / groups * BLOCK;
+        hd = u % groups * L::HEADS + mine;
+        const bool is_q = hd < p.H;
+        stride = is_q ? p.qs : p.ks;
+        at = (tok0 + t0) * stride + (is_q ? hd : hd - p.H) * D;
+        const uint16_t *src = is_q ? p.q : p.k;
+        const long long end = (p.M - 1) * stride + (is_q ? p.H : p.HK) * D;
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
+        for (int b = 0; b < BLOCK; ++b) {
             x[b][0] = x[b][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (ld.tk < n) {
-                const bool is_q = ld.hd < p.H;
-                const long long at = is_q ? (tok0 + ld.tk) * p.qs + ld.hd * p.D : (tok0 + ld.tk) * p.ks + (ld.hd - p.H) * p.D;
-                const uint16_t *src = is_q ? p.q : p.k;
-                if (gmem_ok(at, p.D, is_q ? (p.M - 1) * p.qs + p.H * p.D : (p.M - 1) * p.ks + p.HK * p.D)) {
-                    x[b][0] = *reinterpret_cast<const uint4 *>(src + at + v.v0);
-                    x[b][1] = *reinterpret_cast<const uint4 *>(src + at + v.v1);
-                }
+            if (hd < heads && t0 + b < n && gmem_ok(at + b * stride, D, end)) {
+                x[b][0] = *reinterpret_cast<const uint4 *>(src + at + b * stride + l.v0);
+                x[b][1] = *reinterpret_cast<const uint4 *>(src + at + b * stride + l.v1);
             }
-            ld.next(per, heads);
         }
     };
-    fetch();  // ahead of the table, whose chain is long
-    make_table(table, p.turn, tok0, n);
-    if (p.hn.norm) {
-        keep_weights(weights[0], p.qw, p.D);
-        keep_weights(weights[1], p.kw, p.D);
-    }
+    if (warp < units) fetch(warp);  // ahead of the table, whose chain is long
+    make_table<INTER>(table, p.turn, tok0, n);
     __syncthreads();
-    for (int u0 = 0; u0 < units; u0 += per * BATCH) {  // every lane makes the same number of steps (the shuffles need them all)
-        if (u0 > 0) fetch();
+    for (int u = warp; u < units; u += THREADS / 32) {
+        if (u != warp) fetch(u);
+        const bool is_q = hd < p.H;
+        float2 wa[4], wb[4];
+        load_weights(is_q ? p.qw : p.kw, l.v0, wa);
+        load_weights(is_q ? p.qw : p.kw, l.v1, wb);
+        uint16_t *dst = is_q ? p.qo : p.ko;
+        const long long ostride = is_q ? p.qos : p.kos, end = (p.M - 1) * ostride + (is_q ? p.H : p.HK) * D;
+        const long long to = (tok0 + t0) * ostride + (is_q ? hd : hd - p.H) * D;
 #pragma unroll
-        for (int b = 0; b < BATCH; ++b) {
-            const bool live = st.tk < n, is_q = st.hd < p.H;
-            float f[8], g[8];
+        for (int b = 0; b < BLOCK; ++b) {
+            if (t0 + b >= n) break;  // the same for the whole warp
+            float2 f[4], g[4];
             blk::unpack8(x[b][0], f);
             blk::unpack8(x[b][1], g);
-            norm_and_turn<INTER>(f, g, p.hn.norm, p.hn.eps, inv_d, lanes, weights[is_q ? 0 : 1], v,
-                                 table + (live ? st.tk : 0) * (p.turn.R / 2));
-            if (live) {
-                const long long at = is_q ? (tok0 + st.tk) * p.qos + st.hd * p.D : (tok0 + st.tk) * p.kos + (st.hd - p.H) * p.D;
-                uint16_t *dst = is_q ? p.qo : p.ko;
-                if (gmem_ok(at, p.D, is_q ? (p.M - 1) * p.qos + p.H * p.D : (p.M - 1) * p.kos + p.HK * p.D)) {
-                    *reinterpret_cast<uint4 *>(dst + at + v.v0) = blk::pack8(f);
-                    *reinterpret_cast<uint4 *>(dst + at + v.v1) = blk::pack8(g);
-                }
+            norm_and_turn<D, INTER>(f, g, p.hn.norm, p.hn.eps, wa, wb, l, reinterpret_cast<const float4 *>(table) + (t0 + b) * (half / 2), half);
+            if (hd < heads && gmem_ok(to + b * ostride, D, end)) {
+                *reinterpret_cast<uint4 *>(dst + to + b * ostride + l.v0) = blk::pack8(f);
+                *reinterpret_cast<uint4 *>(dst + to + b * ostride + l.v1) = blk::pack8(g);
             }
-            st.next(per, heads);
         }
     }
 }
@@ -249,11 +244,11 @@ struct AppendParams {
     Pages pages;
     const int64_t *cu;
     long long M;
-    int T, nseq, HK, D, tokens;
+    int T, nseq, HK, tokens;
 };
 
 // Where a token's rows stand in the cache (of head 0), or -1 where it has none: positions below zero are padding.
-__device__ __forceinline__ long long slot_of(const AppendParams &p, long long tok)
+__device__ __forceinline__ long long slot_of(const AppendParams &p, long long tok, int D)
 {
     const int64_t pos = __ldg(p.turn.positions + tok);
     if (pos < 0) return -1;
@@ -270,66 +265,63 @@ __device__ __forceinline__ long long slot_of(const AppendParams &p, long long to
         atomicOr(&g_dev_error, DEVERR_PAGES);
         return -1;
     }
-    return page * p.pages.stride + (pos & ((1 << p.pages.shift) - 1)) * p.D;
+    return page * p.pages.stride + (pos & ((1 << p.pages.shift) - 1)) * D;
 }
 
-template <bool INTER>
+template <int D, bool INTER>
 __global__ void __launch_bounds__(THREADS) kda_kv_append_kernel(const AppendParams p)
 {
-    extern __shared__ float2 table[];
-    __shared__ __align__(16) float weights[MAX_D];
+    extern __shared__ __align__(16) float table[];
     __shared__ long long slots[MAX_TOKENS];
-    constexpr int B = BATCH / 2;  // keys and values
+    using L = Lane<D, INTER>;
+    constexpr int B = BLOCK / 2;  // tokens of a block: keys and values
     const long long tok0 = static_cast<long long>(blockIdx.x) * p.tokens;
-    const int n = static_cast<int>(min(static_cast<long long>(p.tokens), p.M - tok0));
+    const int n = static_cast<int>(min(static_cast<long long>(p.tokens), p.M - tok0)), half = p.turn.R / 2;
     if (p.cu && blockIdx.x == 0) blk::check_bounds(p.cu, p.nseq, p.M);
-    const int lanes = p.D / 16, per = THREADS / lanes, j = threadIdx.x % lanes, units = n * p.HK;
-    const Vectors v = vectors_of<INTER>(j, lanes, p.turn.R);
-    const float inv_d = 1.f / static_cast<float>(p.D);
-    const long long page_size = 1LL << p.pages.shift, cache = (p.pages.count - 1) * p.pages.stride + p.HK * page_size * p.D;
-    Item ld = {0, 0}, st;
-    ld.next(static_cast<int>(threadIdx.x) / lanes, p.HK);
-    st = ld;
+    const int warp = threadIdx.x >> 5, mine = (threadIdx.x & 31) / L::LANES;
+    const int groups = (p.HK + L::HEADS - 1) / L::HEADS, units = groups * ((n + B - 1) / B);
+    const L l(p.turn.R);
+    const long long page_size = 1LL << p.pages.shift, cache = (p.pages.count - 1) * p.pages.stride + p.HK * page_size * D;
     uint4 x[B][2], y[B][2];
-    auto fetch = [&]() {
+    int hd = 0, t0 = 0;
+    auto fetch = [&](int u) {
+        t0 = u / groups * B;
+        hd = u % groups * L::HEADS + mine;
+        const long long at = (tok0 + t0) * p.ks + hd * D, vat = (tok0 + t0) * p.vs + hd * D;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             x[b][0] = x[b][1] = y[b][0] = y[b][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (ld.tk < n) {
-                const long long at = (tok0 + ld.tk) * p.ks + ld.hd * p.D, vat = (tok0 + ld.tk) * p.vs + ld.hd * p.D;
-                if (gmem_ok(at, p.D, (p.M - 1) * p.ks + p.HK * p.D) && gmem_ok(vat, p.D, (p.M - 1) * p.vs + p.HK * p.D)) {
-                    x[b][0] = *reinterpret_cast<const uint4 *>(p.k + at + v.v0);
-                    x[b][1] = *reinterpret_cast<const uint4 *>(p.k + at + v.v1);
-                    y[b][0] = *reinterpret_cast<const uint4 *>(p.v + vat + v.v0);
-                    y[b][1] = *reinterpret_cast<const uint4 *>(p.v + vat + v.v1);
-                }
+            if (hd < p.HK && t0 + b < n && gmem_ok(at + b * p.ks, D, (p.M - 1) * p.ks + p.HK * D) && gmem_ok(vat + b * p.vs, D, (p.M - 1) * p.vs + p.HK * D)) {
+                x[b][0] = *reinterpret_cast<const uint4 *>(p.k + at + b * p.ks + l.v0);
+                x[b][1] = *reinterpret_cast<const uint4 *>(p.k + at + b * p.ks + l.v1);
+                y[b][0] = *reinterpret_cast<const uint4 *>(p.v + vat + b * p.vs + l.v0);
+                y[b][1] = *reinterpret_cast<const uint4 *>(p.v + vat + b * p.vs + l.v1);
             }
-            ld.next(per, p.HK);
         }
     };
-    fetch();  // ahead of the table and the look-up of pages, whose chains are long
-    if (threadIdx.x < n) slots[threadIdx.x] = slot_of(p, tok0 + threadIdx.x);
-    make_table(table, p.turn, tok0, n);
-    if (p.hn.norm) keep_weights(weights, p.kw, p.D);
+    if (warp < units) fetch(warp);  // ahead of the table and the look-up of pages, whose chains are long
+    if (threadIdx.x < n) slots[threadIdx.x] = slot_of(p, tok0 + threadIdx.x, D);
+    make_table<INTER>(table, p.turn, tok0, n);
+    float2 wa[4], wb[4];
+    load_weights(p.kw, l.v0, wa);
+    load_weights(p.kw, l.v1, wb);
     __syncthreads();
-    for (int u0 = 0; u0 < units; u0 += per * B) {
-        if (u0 > 0) fetch();
+    for (int u = warp; u < units; u += THREADS / 32) {
+        if (u != warp) fetch(u);
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            const long long slot = st.tk < n ? slots[st.tk] : -1;
-            float f[8], g[8];
+            if (t0 + b >= n) break;  // the same for the whole warp
+            float2 f[4], g[4];
             blk::unpack8(x[b][0], f);
             blk::unpack8(x[b][1], g);
-            norm_and_turn<INTER>(f, g, p.hn.norm, p.hn.eps, inv_d, lanes, weights, v,
-                                 table + (st.tk < n ? st.tk : 0) * (p.turn.R / 2));
-            const long long dst = slot + st.hd * page_size * p.D;
-            if (slot >= 0 && gmem_ok(dst, p.D, cache)) {
-                *reinterpret_cast<uint4 *>(p.kc + dst + v.v0) = blk::pack8(f);
-                *reinterpret_cast<uint4 *>(p.kc + dst + v.v1) = blk::pack8(g);
-                *reinterpret_cast<uint4 *>(p.vc + dst + v.v0) = y[b][0];
-                *reinterpret_cast<uint4 *>(p.vc + dst + v.v1) = y[b][1];
+            norm_and_turn<D, INTER>(f, g, p.hn.norm, p.hn.eps, wa, wb, l, reinterpret_cast<const float4 *>(table) + (t0 + b) * (half / 2), half);
+            const long long slot = slots[t0 + b], dst = slot + hd * page_size * D;
+            if (slot >= 0 && hd < p.HK && gmem_ok(dst, D, cache)) {
+                *reinterpret_cast<uint4 *>(p.kc + dst + l.v0) = blk::pack8(f);
+                *reinterpret_cast<uint4 *>(p.kc + dst + l.v1) = blk::pack8(g);
+                *reinterpret_cast<uint4 *>(p.vc + dst + l.v0) = y[b][0];
+                *reinterpret_cast<uint4 *>(p.vc + dst + l.v1) = y[b][1];
             }
-            st.next(per, p.HK);
         }
     }
 }
