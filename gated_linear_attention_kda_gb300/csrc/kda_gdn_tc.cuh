@@ -168,19 +168,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         atomicOr(&g_dev_error, DEVERR_TIMEOUT);
         flags[0] = 1;
     }
-    // the whole warp goes on only when every lane saw the phase
+    // A whole warp waits, and goes on only when every lane saw the phase. In line: a call costs 240 cycles around the 40
+    // of a wait that is over.
     auto wait_w = [&](int b, uint32_t par) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), par))) return true;
-        const bool ok = __all_sync(0xffffffffu, wait_bar_slow(bar(b), par, flags));
-        __syncwarp();
-        return ok;
-    };
-    // the same, polled for a while first: a suspended warp takes some 300 cycles to come back
-    auto wait_p = [&](int b, uint32_t par) {
-#pragma unroll 1
-        for (int i = 0; i < 256; ++i)
-            if (__all_sync(0xffffffffu, mbar_test_wait(bar(b), par))) return true;
-        return wait_w(b, par);
+        bool ok = mbar_try_wait(bar(b), par);
+        if (!ok) ok = wait_bar_slow(bar(b), par, flags);
+        return __all_sync(0xffffffffu, ok) != 0;
     };
     auto arrive_w = [&](int b) {
         __syncwarp();
@@ -241,20 +234,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
         for (int n = 0; n < nch; ++n, rg.next()) {
             const uint32_t dk = tc::sdesc_lo(kq(rg), 16), dt = tc::sdesc_lo(tt(rg), 16), dkn = tc::sdesc_lo(kq(rg), 2 * Lay::BOX);
-            if (!wait_kq(n, rg) || !wait_p(Lay::SB_GO, n & 1)) break;
+            if (!wait_kq(n, rg) || !wait_w(Lay::SB_GO, n & 1)) break;
             tc::fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_D1, tmem + T_SB + 8 * i, kmaj(dk, i), id_n, i > 0);
             tc::commit_w(bar(Lay::D1_DONE));
-            if (!wait_w(Lay::U_DONE, n & 1) || !wait_p(Lay::D1_GO, n & 1)) break;
+            if (!wait_w(Lay::U_DONE, n & 1) || !wait_w(Lay::D1_GO, n & 1)) break;
             tc::fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_D2, tmem + T_D1 + halves(i), rows(dt, i), id_n, 1);
             tc::commit_w(bar(Lay::N_DONE));
             // (with the product of this state and Q done, S_DONE frees its copy too)
-            if (!wait_w(Lay::SQ_DONE, n & 1) || !wait_p(Lay::N_GO, n & 1)) break;
+            if (!wait_w(Lay::SQ_DONE, n & 1) || !wait_w(Lay::N_GO, n & 1)) break;
             tc::fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 + halves(i), nmaj(dkn, i), id_s, 1);
             tc::commit_w(bar(Lay::S_DONE));
         }
@@ -266,7 +259,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (n > 0 && !wait_w(Lay::KQ_FREE, (n - 1) & 1)) return false;
             tc::fence_after();
             const uint32_t d = tc::sdesc_lo(kq(rg), 16);
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_KQ, kmaj(d, i), kmaj(d, i), id_n, i > 0);
             tc::commit_w(bar(Lay::G_DONE));
             return true;
@@ -286,7 +279,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (n > 0 && (!wait_w(Lay::O_DONE, (n - 1) & 1) || !wait_w(Lay::S_DONE, (n - 1) & 1))) return false;
             tc::fence_after();
             const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(rg), 16);
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ss_w(tmem + T_D2, nmaj(dv, i), rows(dt, i), id_u, i > 0);
             tc::commit_w(bar(Lay::U_DONE));
             tc::commit_w(bar(Lay::V_EMPTY + n % Lay::VS));
@@ -422,7 +415,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int n = 0; n < nch; ++n, rg.next()) {
             uint32_t r[32], o[16];
             // the state as an operand
-            if (n > 0 && !(ok = wait_p(Lay::S_DONE, (n - 1) & 1))) break;
+            if (n > 0 && !(ok = wait_w(Lay::S_DONE, (n - 1) & 1))) break;
             tc::fence_after();
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
@@ -450,7 +443,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::st32(ls + 32 * g, r);
             }
             // D1' over D1
-            if (!(ok = wait_w(Lay::T_FULL + rg.s, rg.par) && wait_p(Lay::D1_DONE, n & 1))) break;
+            if (!(ok = wait_w(Lay::T_FULL + rg.s, rg.par) && wait_w(Lay::D1_DONE, n & 1))) break;
             tc::fence_after();
             tc::ld32(l1, r);
             tc::wait_ld();
@@ -461,7 +454,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before();
             arrive_w(Lay::D1_GO);
             // N and N' over D2
-            if (!(ok = wait_p(Lay::N_DONE, n & 1))) break;
+            if (!(ok = wait_w(Lay::N_DONE, n & 1))) break;
             tc::fence_after();
             tc::ld32(l2, r);
             tc::wait_ld();
@@ -518,12 +511,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const uint32_t dq = tc::sdesc_lo(kq(rg), 16) + (Lay::BOX >> 4), dp = tc::sdesc_lo(pt(rg), 16);
                 ok = wait_kq(n, rg) && wait_w(Lay::SB_GO, n & 1);
                 tc::fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
                 tc::commit_w(bar(Lay::SQ_DONE));
                 ok = ok && wait_w(Lay::T_FULL + rg.s, rg.par) && wait_w(Lay::N_GO, n & 1);
                 tc::fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + halves(i), rows(dp, i), id_n, i > 0);
                 tc::commit_w(bar(Lay::O_DONE));
             }
