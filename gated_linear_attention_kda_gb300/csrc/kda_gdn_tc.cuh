@@ -35,7 +35,7 @@
 //   warp 3       running sums of the decays, steps
 //   warps 4-11   chain: bf16 state, D1', N and N', decay (value channel, half of the columns each)
 //   warps 12-15  output (value channel), transposed through the chunk's Q tile
-//   warps 16-23  norms of queries and keys, A, P and T of a chunk
+//   warps 16-23  A, P and T of a chunk; warps 20-23 norms of queries and keys, one chunk ahead where they can
 #pragma once
 #include "kda_gdn_step.cuh"
 #include "kda_ssm_tc.cuh"
@@ -52,10 +52,8 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t T_S = 0, T_SB = 128, T_D1 = 192, T_SQ = 256, T_D2 = 320, T_PV = 384, T_KQ = 448;
 
 // scalars of a chunk: running log2 sums, steps, 2^G (then the factors of D1'), 2^(G_63 - G) (then those of N'), the
-// output's factors; by key column G less log2 1 / |k|, and 2^(G at the end of its 16 - G) / |k|; by row b / |k| and
-// scale / |q|; the chunk's whole decay
-constexpr int SC_G = 0, SC_B = 256, SC_D = 512, SC_N = 768, SC_O = 1024, SC_GK = 1280, SC_CF = 1536, SC_FK = 1792, SC_FQ = 2048, SC_GAM = 2304,
-              SC_BYTES = 2320;
+// output's factors; by key column G less log2 1 / |k|; by row b / |k| and scale / |q|; the chunk's whole decay
+constexpr int SC_G = 0, SC_B = 256, SC_D = 512, SC_N = 768, SC_O = 1024, SC_GK = 1280, SC_FK = 1536, SC_FQ = 1792, SC_GAM = 2048, SC_BYTES = 2064;
 
 struct Layout {
     static constexpr int BOX = C * 128;             // 64 channels x 64 rows, 128-byte swizzle
@@ -98,6 +96,33 @@ __device__ __forceinline__ uint32_t tf32(float x)
     uint32_t r;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
     return r;
+}
+
+// Waits for a phase, up to WAIT_LIMIT polls or until another role has set the flag at shared address `flag`; sets it
+// when it gives up.
+__device__ __forceinline__ bool wait_or_flag(uint32_t b, uint32_t par, uint32_t flag)
+{
+    if (!smem_ok(b, 8)) return false;
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 i, f;\n\tmov.u32 i, 0;\n"
+                 "W%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t@p bra D%=;\n\t"
+                 "ld.volatile.shared.u32 f, [%3];\n\tadd.u32 i, i, 1;\n\tsetp.ne.u32 q, f, 0;\n\t@q bra D%=;\n\t"
+                 "setp.lt.u32 q, i, %5;\n\t@q bra W%=;\n"
+                 "D%=:\n\t@!p st.volatile.shared.u32 [%3], 1;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(b), "r"(par), "r"(flag), "r"(WAIT_HINT_NS), "r"(static_cast<uint32_t>(WAIT_LIMIT))
+                 : "memory");
+    return ok != 0;
+}
+
+// log(1 + 2^(u log2 e)). Away from 0 by the hardware's logarithm, off by 2^-22; where e^u is below 1/32, whose logarithm of
+// 1 + e^u would lose what it is there for, by the series, which leaves out e^4 / 5 of it, 2^-22. The few instructions count
+// for the kernel's size. NaN comes through.
+__device__ __forceinline__ float softplus_fast(float u)
+{
+    const float e = ex2_approx(-fabsf(u) * LOG2E), small = e * fmaf(e, fmaf(e, fmaf(e, -0.25f, 1.f / 3.f), -0.5f), 1.f);
+    const float l = e < 0.03125f ? small : lg2_approx(1.f + e) * (1.f / LOG2E);
+    return u > 0.f ? u + l : l;
 }
 
 // The rows of a sequence that hold no numbers at its end, made again: rows 8 g .. 8 g + 7 for every set bit of `groups`.
@@ -151,7 +176,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         for (int i : {Lay::G_DONE, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::SQ_DONE, Lay::U_DONE, Lay::END, Lay::END2, Lay::END3})
             mbar_init(bar(i), 1);
-        for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO, Lay::KQ_FREE, Lay::KQ_ZERO}) mbar_init(bar(i), 8);
+        mbar_init(bar(Lay::KQ_ZERO), 4);
+        for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO, Lay::KQ_FREE}) mbar_init(bar(i), 8);
         flags[0] = 0;
         spoilt = 0u;
         fence_mbar_init();
@@ -164,17 +190,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc::fence_after();
     // the allocation is the whole tensor memory, so it starts at address 0
     constexpr uint32_t tmem = 0;
-    if (*reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR) != tmem && threadIdx.x == 0) {
-        atomicOr(&g_dev_error, DEVERR_TIMEOUT);
-        flags[0] = 1;
-    }
-    // A whole warp waits, and goes on only when every lane saw the phase. In line: a call costs 240 cycles around the 40
-    // of a wait that is over.
-    auto wait_w = [&](int b, uint32_t par) {
-        bool ok = mbar_try_wait(bar(b), par);
-        if (!ok) ok = wait_bar_slow(bar(b), par, flags);
-        return __all_sync(0xffffffffu, ok) != 0;
-    };
+    if (*reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR) != tmem && threadIdx.x == 0) flags[0] = 1;
+    // A whole warp waits, and goes on only when every lane saw the phase; after WAIT_LIMIT polls, or when another role has
+    // given up, all give up (the flag becomes an error at the kernel's end). In line, as a call costs 240 cycles, and short.
+    const uint32_t flag = sb + Lay::FLAGS;
+    auto wait_w = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, wait_or_flag(bar(b), par, flag)) != 0; };
     auto arrive_w = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
@@ -274,9 +294,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::fence_async_smem();
                 __syncwarp();
             }
-            if (!wait_w(Lay::T_FULL + rg.s, rg.par)) return false;
             // both products of the last chunk's N, whose columns these are, have been made
             if (n > 0 && (!wait_w(Lay::O_DONE, (n - 1) & 1) || !wait_w(Lay::S_DONE, (n - 1) & 1))) return false;
+            if (!wait_w(Lay::T_FULL + rg.s, rg.par)) return false;
             tc::fence_after();
             const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(rg), 16);
 #pragma unroll 1
@@ -320,9 +340,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int i = 0; i < 2; ++i) {
                 const bool live = 2 * lane + i < Lv;
                 // held at the least decay by a comparison that lets NaN through (fmaxf would not)
-                const float u = A2 * gdn::softplus(__uint_as_float(ra[i] << 16) + bias);
+                const float u = A2 * softplus_fast(__uint_as_float(ra[i] << 16) + bias);
                 a[i] = !live ? 0.f : u < ssm::MIN_LOG2_DECAY ? ssm::MIN_LOG2_DECAY : u;
-                b[i] = live ? gdn::sigmoid(__uint_as_float(rb[i] << 16)) : 0.f;
+                b[i] = live ? blk::sigmoid_fast(__uint_as_float(rb[i] << 16)) : 0.f;
             }
             fetch(n + 1);
             float pre = a[0] + a[1];
@@ -337,8 +357,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const uint32_t o = sc(rg) + 8 * lane;
             SM_AT(float2, o + SC_G) = make_float2(g0, g1);
             SM_AT(float2, o + SC_B) = make_float2(b[0], b[1]);
-            const float ge = __shfl_sync(0xffffffffu, g1, lane | 7);  // at the end of the 16
-            SM_AT(float2, o + SC_CF) = make_float2(ex2_approx(ge - g0), ex2_approx(ge - g1));
             SM_AT(float2, o + SC_D) = make_float2(ex2_approx(g0), ex2_approx(g1));
             SM_AT(float2, o + SC_N) = make_float2(ex2_approx(all - g0), ex2_approx(all - g1));
             if (lane == 0) SM_AT(float, sc(rg) + SC_GAM) = ex2_approx(all);
@@ -443,7 +461,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::st32(ls + 32 * g, r);
             }
             // D1' over D1
-            if (!(ok = wait_w(Lay::T_FULL + rg.s, rg.par) && wait_w(Lay::D1_DONE, n & 1))) break;
+            if (!(ok = wait_w(Lay::D1_DONE, n & 1) && wait_w(Lay::T_FULL + rg.s, rg.par))) break;
             tc::fence_after();
             tc::ld32(l1, r);
             tc::wait_ld();
@@ -578,7 +596,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // ---------------------------------------------------------------- A, P and T
         Ring rg;
         // Quarters 0 and 1 of tensor memory hold K K^T, 2 and 3 Q K^T; two warps share a quarter's columns.
-        const int q = warp & 3, hf = warp < 20 ? 0 : 1, w8 = warp - 16, tid = threadIdx.x - 512;
+        const int q = warp & 3, hf = warp < 20 ? 0 : 1, w8 = warp - 16;
         const int lo = q & 1, i0 = 32 * lo + lane;  // this thread's row
         const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_KQ;
         const uint32_t scr = sb + Lay::SCR;
@@ -600,9 +618,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             SM_AT(uint2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[0]), tf32(f * d[1]));
             SM_AT(uint2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[2]), tf32(f * d[3]));
         };
+        // The factors of rows and columns of a chunk, a row of K or Q per thread of warps 4..7. One chunk ahead, while the
+        // other warps invert, if its tile is there by then; else where the chunk begins.
+        auto factors = [&](int n, const Ring &g) {
+            const int Lv = live_of(n), r = 32 * (w8 & 1) + lane;
+            const bool is_q = w8 >= 6;
+            const uint32_t s = sc(g) + 4 * r, at = kq(g) + (is_q ? Lay::BOX : 0) + r * 128;
+            auto vec = [&](int c) { return at + (c >> 3) * 2 * Lay::BOX + (((c & 7) ^ (r & 7)) << 4); };
+            if (Lv < C) {
+                // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
+                if (r >= Lv)
+#pragma unroll 1
+                    for (int c = 0; c < 16; ++c) SM_AT(uint4, vec(c)) = make_uint4(0u, 0u, 0u, 0u);
+                tc::fence_async_smem();
+                arrive_w(Lay::KQ_ZERO);
+            }
+            float f = 1.f;
+            if (p.l2) {
+                float2 ss = make_float2(0.f, 0.f);
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    float2 x[4];
+                    blk::unpack8(SM_AT(const uint4, vec(c)), x);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) ss = ffma2(x[j], x[j], ss);
+                }
+                f = rsqrtf(ss.x + ss.y + gdn::L2_EPS);
+            }
+            const float G = SM_AT(const float, s + SC_G);
+            if (is_q) {
+                f *= p.scale;
+                SM_AT(float, s + SC_FQ) = f;
+                SM_AT(float, s + SC_O) = f * ex2_approx(G);
+            } else {
+                const float b = SM_AT(const float, s + SC_B), fd = SM_AT(const float, s + SC_D), fn = SM_AT(const float, s + SC_N);
+                SM_AT(float, s + SC_FK) = f * b;
+                SM_AT(float, s + SC_GK) = p.l2 ? G - lg2_approx(f) : G;
+                SM_AT(float, s + SC_D) = -fd * f;
+                SM_AT(float, s + SC_N) = fn * f;
+            }
+        };
+        bool ahead = false;  // this warp's part of the next chunk's factors is there
 #pragma unroll 1
         for (int n = 0; n < nch; ++n, rg.next()) {
-            const int Lv = live_of(n);
             const uint32_t s = sc(rg), t0 = tt(rg);
             // where T[i][j] stands as an operand, times its column's step
             auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
@@ -611,92 +669,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(uint32_t, t_at(r + g8, c + 2 * t4)) = pack_bf16(-d[0] * b.x, -d[1] * b.y);
                 SM_AT(uint32_t, t_at(r + g8 + 8, c + 2 * t4)) = pack_bf16(-d[2] * b.x, -d[3] * b.y);
             };
-            bool ok = wait_w(Lay::KQ_FULL + rg.s, rg.par);
-            if (Lv < C) {
-                // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
-                for (int i = tid; i < (C - Lv) * 32; i += 256) {
-                    const int r = Lv + (i >> 5), c = i & 31;
-                    SM_AT(uint4, kq(rg) + (c >> 3) * Lay::BOX + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                tc::fence_async_smem();
-                arrive_w(Lay::KQ_ZERO);
-                sync();
-            }
-            ok = ok && wait_w(Lay::SC_FULL + rg.s, rg.par);
-            // the factors of rows and columns: warps 0..3 those of 16 rows of K each, the others those of Q
-            {
-                const bool is_q = w8 >= 4;
-                const int r0 = 16 * (w8 & 3), r1 = r0 + g8 + 8 * (t4 & 1);
-                float f = 1.f;
-                if (p.l2) {
-                    // squares of norms on the diagonal of X X^T, whose operand fragments are the same registers
-                    float d[4] = {}, e[4] = {};
-                    const int r = r0 + (lane & 15), c = lane >> 4;
-                    const uint32_t at = kq(rg) + (is_q ? Lay::BOX : 0) + r * 128;
-#pragma unroll 2
-                    for (int k = 0; k < 8; ++k) {
-                        uint32_t a[4];
-                        ldsm_x4(at + (k >> 2) * 2 * Lay::BOX + (((2 * (k & 3) + c) ^ (r & 7)) << 4), a[0], a[1], a[2], a[3]);
-                        mma_bf16(d, a, a[0], a[2]);
-                        mma_bf16(e, a, a[1], a[3]);
-                    }
-                    // row g8 stands in lane t4 = g8 / 2 of d, row g8 + 8 there of e: handed to lanes t4 = 0 and 1
-                    const float u = g8 & 1 ? d[1] : d[0], w = g8 & 1 ? e[3] : e[2];
-                    const float su = __shfl_sync(0xffffffffu, u, 4 * g8 + (g8 >> 1)), sw = __shfl_sync(0xffffffffu, w, 4 * g8 + (g8 >> 1));
-                    f = rsqrtf((t4 & 1 ? sw : su) + gdn::L2_EPS);
-                }
-                if (t4 < 2) {
-                    const float g = SM_AT(const float, s + SC_G + 4 * r1);
-                    if (is_q) {
-                        f *= p.scale;
-                        SM_AT(float, s + SC_FQ + 4 * r1) = f;
-                        SM_AT(float, s + SC_O + 4 * r1) = f * ex2_approx(g);
-                    } else {
-                        SM_AT(float, s + SC_FK + 4 * r1) = f * SM_AT(const float, s + SC_B + 4 * r1);
-                        SM_AT(float, s + SC_GK + 4 * r1) = p.l2 ? g - lg2_approx(f) : g;
-                        SM_AT(float, s + SC_CF + 4 * r1) *= f;
-                        SM_AT(float, s + SC_D + 4 * r1) *= -f;
-                        SM_AT(float, s + SC_N + 4 * r1) *= f;
-                    }
-                }
+            bool ok = true;
+            if (hf == 1 && !ahead) {
+                ok = wait_w(Lay::KQ_FULL + rg.s, rg.par) && wait_w(Lay::SC_FULL + rg.s, rg.par);
+                if (ok) factors(n, rg);
             }
             if (named_bar_or(2, 256, !ok)) break;  // all eight warps leave together
             const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
             ok = wait_w(Lay::G_DONE, n & 1);
             tc::fence_after();
-            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two. Away
-            // from the diagonal blocks a decay is the product of one to the end of the column's 16 and one from there.
+            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
             const int last = q < 2 ? i0 - 1 : i0;
 #pragma unroll 1
             for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
                 uint32_t r[16];
                 float2 w[8];
                 tc::ld16(lq + b, r);
-                if (lo == 1 && hf == 0) {
-                    const float rf = fi * ex2_approx(Gi - SM_AT(const float, s + SC_G + 4 * (b + 15)));
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float4 k = SM_AT(const float4, s + SC_CF + 4 * (b + 2 * j));
-                        w[j] = fmul2(make_float2(k.x, k.y), make_float2(rf, rf));
-                        w[j + 1] = fmul2(make_float2(k.z, k.w), make_float2(rf, rf));
-                    }
-                    tc::wait_ld();
+                for (int j = 0; j < 8; j += 2) {
+                    const float4 g = SM_AT(const float4, s + SC_GK + 4 * (b + 2 * j));
+                    w[j] = make_float2(ex2_approx(Gi - g.x), ex2_approx(Gi - g.y));
+                    w[j + 1] = make_float2(ex2_approx(Gi - g.z), ex2_approx(Gi - g.w));
+                }
+                tc::wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = fmul2(w[j], make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float4 g = SM_AT(const float4, s + SC_GK + 4 * (b + 2 * j));
-                        w[j] = make_float2(ex2_approx(Gi - g.x), ex2_approx(Gi - g.y));
-                        w[j + 1] = make_float2(ex2_approx(Gi - g.z), ex2_approx(Gi - g.w));
-                    }
-                    tc::wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-                        if (b + 2 * j > last) w[j].x = 0.f;
-                        if (b + 2 * j + 1 > last) w[j].y = 0.f;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+                    if (b + 2 * j > last) w[j].x = 0.f;
+                    if (b + 2 * j + 1 > last) w[j].y = 0.f;
                 }
                 if (q < 2) {
 #pragma unroll
@@ -750,6 +750,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(uint2, scr + 4 * ((d0 + 8 + g8) * Lay::LD + d0 + 2 * t4)) = make_uint2(tf32(-e[0]), tf32(-e[1]));
                 const float2 b = SM_AT(const float2, s + SC_B + 4 * (d0 + 2 * t4));
                 SM_AT(uint32_t, t_at(d0 + 8 + g8, d0 + 2 * t4)) = pack_bf16(-e[0] * b.x, -e[1] * b.y);
+            } else if (n + 1 < nch) {
+                Ring g = rg;
+                g.next();
+                ahead = __all_sync(0xffffffffu, mbar_test_wait(bar(Lay::KQ_FULL + g.s), g.par) && mbar_test_wait(bar(Lay::SC_FULL + g.s), g.par));
+                if (ahead) factors(n + 1, g);
             }
             sync();
             // the blocks below: -T_hi A_hl T_lo, first of 16 (eight columns per warp), then of 32
@@ -787,6 +792,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     tc::fence_before();
     __syncthreads();
+    if (*flags && threadIdx.x == 0) atomicOr(&g_dev_error, DEVERR_TIMEOUT);
     const uint32_t groups = spoilt;
     if (groups) redo_rows(p, seq, h, sp, groups);
     if (warp == 0) {
