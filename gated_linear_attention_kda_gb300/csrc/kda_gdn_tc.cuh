@@ -98,21 +98,20 @@ __device__ __forceinline__ uint32_t tf32(float x)
     return r;
 }
 
-// Waits for a phase, up to WAIT_LIMIT polls or until another role has set the flag at shared address `flag`; sets it
-// when it gives up.
-__device__ __forceinline__ bool wait_or_flag(uint32_t b, uint32_t par, uint32_t flag)
+// Waits for a phase, up to WAIT_LIMIT polls or until some role has given up, which the flag at shared address `flag` tells;
+// sets it on giving up. The roles go on all the same, so that every barrier keeps its count and the CTA comes to its end
+// (a wait then lasts one poll): what they make is void, and the flag becomes an error. This keeps a wait short: see the
+// note on code size below.
+__device__ __forceinline__ void wait_or_flag(uint32_t b, uint32_t par, uint32_t flag)
 {
-    if (!smem_ok(b, 8)) return false;
-    uint32_t ok;
+    if (!smem_ok(b, 8)) return;
     asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 i, f;\n\tmov.u32 i, 0;\n"
-                 "W%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t@p bra D%=;\n\t"
-                 "ld.volatile.shared.u32 f, [%3];\n\tadd.u32 i, i, 1;\n\tsetp.ne.u32 q, f, 0;\n\t@q bra D%=;\n\t"
-                 "setp.lt.u32 q, i, %5;\n\t@q bra W%=;\n"
-                 "D%=:\n\t@!p st.volatile.shared.u32 [%3], 1;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(b), "r"(par), "r"(flag), "r"(WAIT_HINT_NS), "r"(static_cast<uint32_t>(WAIT_LIMIT))
+                 "W%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1, %3;\n\t@p bra D%=;\n\t"
+                 "ld.volatile.shared.u32 f, [%2];\n\tadd.u32 i, i, 1;\n\tsetp.ne.u32 q, f, 0;\n\t@q bra D%=;\n\t"
+                 "setp.lt.u32 q, i, %4;\n\t@q bra W%=;\n"
+                 "D%=:\n\t@!p st.volatile.shared.u32 [%2], 1;\n\t}" ::"r"(b),
+                 "r"(par), "r"(flag), "r"(WAIT_HINT_NS), "r"(static_cast<uint32_t>(WAIT_LIMIT))
                  : "memory");
-    return ok != 0;
 }
 
 // log(1 + 2^(u log2 e)). Away from 0 by the hardware's logarithm, off by 2^-22; where e^u is below 1/32, whose logarithm of
@@ -191,10 +190,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // the allocation is the whole tensor memory, so it starts at address 0
     constexpr uint32_t tmem = 0;
     if (*reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR) != tmem && threadIdx.x == 0) flags[0] = 1;
-    // A whole warp waits, and goes on only when every lane saw the phase; after WAIT_LIMIT polls, or when another role has
-    // given up, all give up (the flag becomes an error at the kernel's end). In line, as a call costs 240 cycles, and short.
     const uint32_t flag = sb + Lay::FLAGS;
-    auto wait_w = [&](int b, uint32_t par) { return __all_sync(0xffffffffu, wait_or_flag(bar(b), par, flag)) != 0; };
+    auto wait_w = [&](int b, uint32_t par) {
+        wait_or_flag(bar(b), par, flag);
+        __syncwarp();
+    };
     auto arrive_w = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto halves = [](int i) { return static_cast<uint32_t>(32 * (i >> 1) + 8 * (i & 1)); };
     // a [K; Q] tile is there, with the rows past the sequence's end cleared
     auto wait_kq = [&](int n, const Ring &g) {
-        return wait_w(Lay::KQ_FULL + g.s, g.par) && (live_of(n) == C || wait_w(Lay::KQ_ZERO, 0));
+        wait_w(Lay::KQ_FULL + g.s, g.par);
+        if (live_of(n) < C) wait_w(Lay::KQ_ZERO, 0);
     };
     // the products of an issuer that are still on their way when its loop is left
     auto finish = [&](int b) {
@@ -230,7 +231,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
             for (int n = 0; n < nch; ++n, rg.next()) {
                 const int tok = sp.bos + n * C, full = Lay::KQ_FULL + rg.s, vfull = Lay::V_FULL + n % Lay::VS;
-                if (!wait_bar(bar(Lay::KQ_EMPTY + rg.s), rg.par ^ 1, flags)) break;
+                wait_or_flag(bar(Lay::KQ_EMPTY + rg.s), rg.par ^ 1, flag);
+                if (*flags) break;
                 mbar_arrive_expect_tx(bar(full), Lay::KQT);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -238,7 +240,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tma_load_3d(kq(rg) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
                 }
                 ++nk;
-                if (!wait_bar(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flags)) break;
+                wait_or_flag(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flag);
+                if (*flags) break;
                 mbar_arrive_expect_tx(bar(vfull), Lay::VT);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) tma_load_3d(vt(n) + c * Lay::BOX, &tv, 64 * c, h, tok, bar(vfull));
@@ -254,18 +257,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
         for (int n = 0; n < nch; ++n, rg.next()) {
             const uint32_t dk = tc::sdesc_lo(kq(rg), 16), dt = tc::sdesc_lo(tt(rg), 16), dkn = tc::sdesc_lo(kq(rg), 2 * Lay::BOX);
-            if (!wait_kq(n, rg) || !wait_w(Lay::SB_GO, n & 1)) break;
+            wait_kq(n, rg);
+            wait_w(Lay::SB_GO, n & 1);
             tc::fence_after();
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_D1, tmem + T_SB + 8 * i, kmaj(dk, i), id_n, i > 0);
             tc::commit_w(bar(Lay::D1_DONE));
-            if (!wait_w(Lay::U_DONE, n & 1) || !wait_w(Lay::D1_GO, n & 1)) break;
+            wait_w(Lay::U_DONE, n & 1);
+            wait_w(Lay::D1_GO, n & 1);
             tc::fence_after();
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_D2, tmem + T_D1 + halves(i), rows(dt, i), id_n, 1);
             tc::commit_w(bar(Lay::N_DONE));
             // (with the product of this state and Q done, S_DONE frees its copy too)
-            if (!wait_w(Lay::SQ_DONE, n & 1) || !wait_w(Lay::N_GO, n & 1)) break;
+            wait_w(Lay::SQ_DONE, n & 1);
+            wait_w(Lay::N_GO, n & 1);
             tc::fence_after();
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 + halves(i), nmaj(dkn, i), id_s, 1);
@@ -275,17 +281,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else if (warp == 2) {
         // ---------------------------------------------------------------- MMA issuer: [K; Q] K^T, V^T T^T
         auto issue_g = [&](int n, const Ring &rg) {
-            if (!wait_kq(n, rg)) return false;
-            if (n > 0 && !wait_w(Lay::KQ_FREE, (n - 1) & 1)) return false;
+            wait_kq(n, rg);
+            if (n > 0) wait_w(Lay::KQ_FREE, (n - 1) & 1);
             tc::fence_after();
             const uint32_t d = tc::sdesc_lo(kq(rg), 16);
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_KQ, kmaj(d, i), kmaj(d, i), id_n, i > 0);
             tc::commit_w(bar(Lay::G_DONE));
-            return true;
         };
         auto issue_u = [&](int n, const Ring &rg) {
-            if (!wait_w(Lay::V_FULL + n % Lay::VS, (n / Lay::VS) & 1)) return false;
+            wait_w(Lay::V_FULL + n % Lay::VS, (n / Lay::VS) & 1);
             if (const int Lv = live_of(n); Lv < C) {  // as the rows of K and Q past the end, which other warps clear
                 for (int i = lane; i < (C - Lv) * 16; i += 32) {
                     const int r = Lv + (i >> 4), c = i & 15;
@@ -295,23 +300,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 __syncwarp();
             }
             // both products of the last chunk's N, whose columns these are, have been made
-            if (n > 0 && (!wait_w(Lay::O_DONE, (n - 1) & 1) || !wait_w(Lay::S_DONE, (n - 1) & 1))) return false;
-            if (!wait_w(Lay::T_FULL + rg.s, rg.par)) return false;
+            if (n > 0) {
+                wait_w(Lay::O_DONE, (n - 1) & 1);
+                wait_w(Lay::S_DONE, (n - 1) & 1);
+            }
+            wait_w(Lay::T_FULL + rg.s, rg.par);
             tc::fence_after();
             const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(rg), 16);
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ss_w(tmem + T_D2, nmaj(dv, i), rows(dt, i), id_u, i > 0);
             tc::commit_w(bar(Lay::U_DONE));
             tc::commit_w(bar(Lay::V_EMPTY + n % Lay::VS));
-            return true;
         };
         Ring rg, ru;
 #pragma unroll 1
         for (int n = 0; n <= nch; ++n) {  // one chunk ahead with the first
-            if (n < nch && !issue_g(n, rg)) break;
+            if (n < nch) issue_g(n, rg);
             rg.next();
             if (n == 0) continue;
-            if (!issue_u(n - 1, ru)) break;
+            issue_u(n - 1, ru);
             ru.next();
         }
         finish(Lay::END2);
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             const float all = __shfl_sync(0xffffffffu, pre, 31);
             const float g1 = pre, before = __shfl_up_sync(0xffffffffu, pre, 1), g0 = (lane ? before : 0.f) + a[0];
-            if (!wait_w(Lay::KQ_FULL + rg.s, rg.par)) break;  // the buffer is free as the tile's is
+            wait_w(Lay::KQ_FULL + rg.s, rg.par);  // the buffer is free as the tile's is
             const uint32_t o = sc(rg) + 8 * lane;
             SM_AT(float2, o + SC_G) = make_float2(g0, g1);
             SM_AT(float2, o + SC_B) = make_float2(b[0], b[1]);
@@ -416,7 +423,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 r[i] = __float_as_uint(x.x); r[i + 1] = __float_as_uint(x.y); r[i + 2] = __float_as_uint(y.x); r[i + 3] = __float_as_uint(y.y);
             }
         };
-        bool ok = true;
         if (nch > 0) {
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int n = 0; n < nch; ++n, rg.next()) {
             uint32_t r[32], o[16];
             // the state as an operand
-            if (n > 0 && !(ok = wait_w(Lay::S_DONE, (n - 1) & 1))) break;
+            if (n > 0) wait_w(Lay::S_DONE, (n - 1) & 1);
             tc::fence_after();
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
@@ -446,7 +452,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before();
             arrive_w(Lay::SB_GO);
             // decayed in place
-            if (!(ok = wait_w(Lay::SC_FULL + rg.s, rg.par))) break;
+            wait_w(Lay::SC_FULL + rg.s, rg.par);
             const float gam = SM_AT(const float, sc(rg) + SC_GAM);
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
@@ -461,7 +467,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::st32(ls + 32 * g, r);
             }
             // D1' over D1
-            if (!(ok = wait_w(Lay::D1_DONE, n & 1) && wait_w(Lay::T_FULL + rg.s, rg.par))) break;
+            wait_w(Lay::D1_DONE, n & 1);
+            wait_w(Lay::T_FULL + rg.s, rg.par);
             tc::fence_after();
             tc::ld32(l1, r);
             tc::wait_ld();
@@ -472,7 +479,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before();
             arrive_w(Lay::D1_GO);
             // N and N' over D2
-            if (!(ok = wait_w(Lay::N_DONE, n & 1))) break;
+            wait_w(Lay::N_DONE, n & 1);
             tc::fence_after();
             tc::ld32(l2, r);
             tc::wait_ld();
@@ -485,9 +492,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before();
             arrive_w(Lay::N_GO);
         }
-        if (ok && nch > 0) ok = wait_w(Lay::S_DONE, (nch - 1) & 1);
+        if (nch > 0) wait_w(Lay::S_DONE, (nch - 1) & 1);
         tc::fence_after();
-        if (ok && nch > 0) {
+        if (nch > 0) {
             float2 z = make_float2(0.f, 0.f);  // 0 NaN and 0 inf are NaN
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (!(z.x + z.y == 0.f)) atomicOr(&spoilt, 1u << (v / gdn::ROWS));
         }
         named_bar_sync(4 + q, 64);  // both halves of these rows have been looked at
-        if (ok && p.fin) {
+        if (p.fin) {
             const bool number = !(*const_cast<volatile uint32_t *>(&spoilt) >> (v / gdn::ROWS) & 1u);  // else made again at the end
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
@@ -524,21 +531,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
         for (int n = 0; n < nch; ++n, rg.next()) {
             const int Lv = live_of(n);
-            bool ok = true;
             if (warp == 12) {  // its two products: all four warps have read the last chunk's
                 const uint32_t dq = tc::sdesc_lo(kq(rg), 16) + (Lay::BOX >> 4), dp = tc::sdesc_lo(pt(rg), 16);
-                ok = wait_kq(n, rg) && wait_w(Lay::SB_GO, n & 1);
+                wait_kq(n, rg);
+                wait_w(Lay::SB_GO, n & 1);
                 tc::fence_after();
 #pragma unroll 1
                 for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
                 tc::commit_w(bar(Lay::SQ_DONE));
-                ok = ok && wait_w(Lay::T_FULL + rg.s, rg.par) && wait_w(Lay::N_GO, n & 1);
+                wait_w(Lay::T_FULL + rg.s, rg.par);
+                wait_w(Lay::N_GO, n & 1);
                 tc::fence_after();
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + halves(i), rows(dp, i), id_n, i > 0);
                 tc::commit_w(bar(Lay::O_DONE));
             }
-            ok = ok && wait_w(Lay::T_FULL + rg.s, rg.par) && wait_w(Lay::O_DONE, n & 1);
+            wait_w(Lay::T_FULL + rg.s, rg.par);
+            wait_w(Lay::O_DONE, n & 1);
             tc::fence_after();
             // The Q tile has been read: token i is its row i. The accumulators are loaded as warp MMA fragments (8 channels
             // x 8 tokens), so that stmatrix.trans hands a token's row its 16 bytes of eight channels.
@@ -568,7 +577,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             tc::fence_before();
             tc::fence_async_smem();
-            if (named_bar_or(1, 128, !ok)) break;  // all four warps leave together
+            named_bar_sync(1, 128);
             if (Lv == C) {
                 if (warp == 12 && lane == 0) {
 #pragma unroll
@@ -618,9 +627,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             SM_AT(uint2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[0]), tf32(f * d[1]));
             SM_AT(uint2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[2]), tf32(f * d[3]));
         };
-        // The factors of rows and columns of a chunk, a row of K or Q per thread of warps 4..7. One chunk ahead, while the
-        // other warps invert, if its tile is there by then; else where the chunk begins.
+        // The factors of rows and columns of chunk n, a row of K or Q per thread of warps 4..7: one chunk ahead, while the
+        // others invert.
         auto factors = [&](int n, const Ring &g) {
+            wait_w(Lay::KQ_FULL + g.s, g.par);
+            wait_w(Lay::SC_FULL + g.s, g.par);
             const int Lv = live_of(n), r = 32 * (w8 & 1) + lane;
             const bool is_q = w8 >= 6;
             const uint32_t s = sc(g) + 4 * r, at = kq(g) + (is_q ? Lay::BOX : 0) + r * 128;
@@ -658,9 +669,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(float, s + SC_N) = fn * f;
             }
         };
-        bool ahead = false;  // this warp's part of the next chunk's factors is there
+        Ring nx;
 #pragma unroll 1
-        for (int n = 0; n < nch; ++n, rg.next()) {
+        for (int n = -1; n < nch; ++n) {  // (chunk -1: the first chunk's factors alone)
             const uint32_t s = sc(rg), t0 = tt(rg);
             // where T[i][j] stands as an operand, times its column's step
             auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
@@ -669,50 +680,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(uint32_t, t_at(r + g8, c + 2 * t4)) = pack_bf16(-d[0] * b.x, -d[1] * b.y);
                 SM_AT(uint32_t, t_at(r + g8 + 8, c + 2 * t4)) = pack_bf16(-d[2] * b.x, -d[3] * b.y);
             };
-            bool ok = true;
-            if (hf == 1 && !ahead) {
-                ok = wait_w(Lay::KQ_FULL + rg.s, rg.par) && wait_w(Lay::SC_FULL + rg.s, rg.par);
-                if (ok) factors(n, rg);
-            }
-            if (named_bar_or(2, 256, !ok)) break;  // all eight warps leave together
-            const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
-            ok = wait_w(Lay::G_DONE, n & 1);
-            tc::fence_after();
-            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
-            const int last = q < 2 ? i0 - 1 : i0;
+            if (n >= 0) {
+                sync();
+                const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
+                wait_w(Lay::G_DONE, n & 1);
+                tc::fence_after();
+                // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
+                const int last = q < 2 ? i0 - 1 : i0;
 #pragma unroll 1
-            for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
-                uint32_t r[16];
-                float2 w[8];
-                tc::ld16(lq + b, r);
+                for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
+                    uint32_t r[16];
+                    float2 w[8];
+                    tc::ld16(lq + b, r);
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float4 g = SM_AT(const float4, s + SC_GK + 4 * (b + 2 * j));
-                    w[j] = make_float2(ex2_approx(Gi - g.x), ex2_approx(Gi - g.y));
-                    w[j + 1] = make_float2(ex2_approx(Gi - g.z), ex2_approx(Gi - g.w));
+                    for (int j = 0; j < 8; j += 2) {
+                        const float4 g = SM_AT(const float4, s + SC_GK + 4 * (b + 2 * j));
+                        w[j] = make_float2(ex2_approx(Gi - g.x), ex2_approx(Gi - g.y));
+                        w[j + 1] = make_float2(ex2_approx(Gi - g.z), ex2_approx(Gi - g.w));
+                    }
+                    tc::wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+                        if (b + 2 * j > last) w[j].x = 0.f;
+                        if (b + 2 * j + 1 > last) w[j].y = 0.f;
+                    }
+                    if (q < 2) {
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4)
+                            SM_AT(uint4, pt(rg) + i0 * 128 + ((((b >> 3) + (j >> 2)) ^ (i0 & 7)) << 4)) =
+                                make_uint4(pack_bf16(w[j].x, w[j].y), pack_bf16(w[j + 1].x, w[j + 1].y), pack_bf16(w[j + 2].x, w[j + 2].y), pack_bf16(w[j + 3].x, w[j + 3].y));
+                    }
                 }
-                tc::wait_ld();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-                    if (b + 2 * j > last) w[j].x = 0.f;
-                    if (b + 2 * j + 1 > last) w[j].y = 0.f;
-                }
-                if (q < 2) {
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; j += 4)
-                        SM_AT(uint4, pt(rg) + i0 * 128 + ((((b >> 3) + (j >> 2)) ^ (i0 & 7)) << 4)) =
-                            make_uint4(pack_bf16(w[j].x, w[j].y), pack_bf16(w[j + 1].x, w[j + 1].y), pack_bf16(w[j + 2].x, w[j + 2].y), pack_bf16(w[j + 3].x, w[j + 3].y));
-                }
+                tc::fence_before();
+                arrive_w(Lay::KQ_FREE);
+                sync();
             }
-            tc::fence_before();
-            arrive_w(Lay::KQ_FREE);
-            if (named_bar_or(2, 256, !ok)) break;
             // (I + A)^-1: diagonal blocks of 8, two per warp, a column per lane, row by row; then the block between them
-            if (hf == 0) {
+            if (hf == 1) {
+                if (n + 1 < nch) factors(n + 1, nx);
+            } else if (n >= 0) {
                 const int d0 = 16 * q, d1 = d0 + (lane & 8), c = lane & 7;
                 float x[8];
 #pragma unroll
@@ -750,12 +760,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(uint2, scr + 4 * ((d0 + 8 + g8) * Lay::LD + d0 + 2 * t4)) = make_uint2(tf32(-e[0]), tf32(-e[1]));
                 const float2 b = SM_AT(const float2, s + SC_B + 4 * (d0 + 2 * t4));
                 SM_AT(uint32_t, t_at(d0 + 8 + g8, d0 + 2 * t4)) = pack_bf16(-e[0] * b.x, -e[1] * b.y);
-            } else if (n + 1 < nch) {
-                Ring g = rg;
-                g.next();
-                ahead = __all_sync(0xffffffffu, mbar_test_wait(bar(Lay::KQ_FULL + g.s), g.par) && mbar_test_wait(bar(Lay::SC_FULL + g.s), g.par));
-                if (ahead) factors(n + 1, g);
             }
+            nx.next();
+            if (n < 0) continue;
             sync();
             // the blocks below: -T_hi A_hl T_lo, first of 16 (eight columns per warp), then of 32
             if (hf == 0) {
@@ -787,6 +794,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             tc::fence_async_smem();
             arrive_w(Lay::T_FULL + rg.s);
+            rg.next();
         }
     }
 
