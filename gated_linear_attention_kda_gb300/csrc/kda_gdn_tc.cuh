@@ -34,7 +34,7 @@
 //   warp 2       MMA issuer: [K; Q] K^T
 //   warp 3       running sums of the decays, steps
 //   warps 4-11   chain: bf16 state, D1', N and N', decay (value channel, half of the columns each)
-//   warps 12-15  output (value channel), transposed through the chunk's Q tile
+//   warps 12-15  output (value channel), transposed on the way through shared memory; its MMAs
 //   warps 16-23  A, P and T of a chunk; warps 20-23 norms of queries and keys, one chunk ahead where they can
 #pragma once
 #include "kda_gdn_step.cuh"
@@ -66,7 +66,8 @@ struct Layout {
     static constexpr int T = P + KQS * BOX;
     static constexpr int SCR = T + KQS * BOX;
     static constexpr int SC = SCR + C * LD * 4;
-    static constexpr int BAR = SC + KQS * SC_BYTES;
+    static constexpr int OUT = (SC + 4 * SC_BYTES + 1023) / 1024 * 1024;  // a chunk's output, [token][channel]
+    static constexpr int BAR = OUT + VT;
     static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 8, SC_FULL = 10, T_FULL = 13, G_DONE = 16, KQ_FREE = 17,
                          KQ_ZERO = 18, SB_GO = 19, D1_DONE = 20, D1_GO = 21, N_DONE = 22, N_GO = 23, S_DONE = 24, O_DONE = 25,
                          SQ_DONE = 26, U_DONE = 27, END = 28, END2 = 29, END3 = 30, NBARS = 31;
@@ -98,19 +99,18 @@ __device__ __forceinline__ uint32_t tf32(float x)
     return r;
 }
 
-// Waits for a phase, up to WAIT_LIMIT polls or until some role has given up, which the flag at shared address `flag` tells;
-// sets it on giving up. The roles go on all the same, so that every barrier keeps its count and the CTA comes to its end
-// (a wait then lasts one poll): what they make is void, and the flag becomes an error. This keeps a wait short: see the
-// note on code size below.
+// Waits for a phase. The producer waits for every chunk's buffers in turn, with a limit, and sets the flag at shared
+// address `flag` when one does not come back; the others wait until their phase comes or that flag is set, and go on all
+// the same, so that every barrier keeps its count and the CTA comes to its end (a wait then lasts one poll): what they make
+// is void, and the flag becomes an error. This keeps a wait short: see the note on code size below.
 __device__ __forceinline__ void wait_or_flag(uint32_t b, uint32_t par, uint32_t flag)
 {
     if (!smem_ok(b, 8)) return;
-    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 i, f;\n\tmov.u32 i, 0;\n"
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 f;\n"
                  "W%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1, %3;\n\t@p bra D%=;\n\t"
-                 "ld.volatile.shared.u32 f, [%2];\n\tadd.u32 i, i, 1;\n\tsetp.ne.u32 q, f, 0;\n\t@q bra D%=;\n\t"
-                 "setp.lt.u32 q, i, %4;\n\t@q bra W%=;\n"
-                 "D%=:\n\t@!p st.volatile.shared.u32 [%2], 1;\n\t}" ::"r"(b),
-                 "r"(par), "r"(flag), "r"(WAIT_HINT_NS), "r"(static_cast<uint32_t>(WAIT_LIMIT))
+                 "ld.volatile.shared.u32 f, [%2];\n\tsetp.eq.u32 p, f, 0;\n\t@p bra W%=;\n"
+                 "D%=:\n\t}" ::"r"(b),
+                 "r"(par), "r"(flag), "r"(WAIT_HINT_NS)
                  : "memory");
 }
 
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto vt = [&](int n) { return sb + Lay::V + (n % Lay::VS) * Lay::VT; };
     auto pt = [&](const Ring &g) { return sb + Lay::P + g.s * Lay::BOX; };
     auto tt = [&](const Ring &g) { return sb + Lay::T + g.s * Lay::BOX; };
-    auto sc = [&](const Ring &g) { return sb + Lay::SC + g.s * SC_BYTES; };
+    auto sc = [&](int n) { return sb + Lay::SC + (n & 3) * SC_BYTES; };
     auto live_of = [&](int n) { return min(C, sp.len - n * C); };
 
     if (warp == 0) {
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (threadIdx.x == 32) {
         for (int i = 0; i < Lay::KQS; ++i) {
             mbar_init(bar(Lay::KQ_FULL + i), 1);
-            mbar_init(bar(Lay::KQ_EMPTY + i), 4);
+            mbar_init(bar(Lay::KQ_EMPTY + i), 2);
             mbar_init(bar(Lay::SC_FULL + i), 1);
             mbar_init(bar(Lay::T_FULL + i), 8);
         }
@@ -231,8 +231,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
             for (int n = 0; n < nch; ++n, rg.next()) {
                 const int tok = sp.bos + n * C, full = Lay::KQ_FULL + rg.s, vfull = Lay::V_FULL + n % Lay::VS;
-                wait_or_flag(bar(Lay::KQ_EMPTY + rg.s), rg.par ^ 1, flag);
-                if (*flags) break;
+                if (!wait_bar(bar(Lay::KQ_EMPTY + rg.s), rg.par ^ 1, flags)) break;
                 mbar_arrive_expect_tx(bar(full), Lay::KQT);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -240,8 +239,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tma_load_3d(kq(rg) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
                 }
                 ++nk;
-                wait_or_flag(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flag);
-                if (*flags) break;
+                if (!wait_bar(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flags)) break;
                 mbar_arrive_expect_tx(bar(vfull), Lay::VT);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) tma_load_3d(vt(n) + c * Lay::BOX, &tv, 64 * c, h, tok, bar(vfull));
@@ -250,6 +248,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // no copy is in flight when the CTA ends, whichever way the loop was left
             for (int m = max(nk - Lay::KQS, 0); m < nk; ++m) drain_bar(bar(Lay::KQ_FULL + m % Lay::KQS), (m / Lay::KQS) & 1);
             for (int m = max(nv - Lay::VS, 0); m < nv; ++m) drain_bar(bar(Lay::V_FULL + m % Lay::VS), (m / Lay::VS) & 1);
+            // and the watch over the others' waits lasts until the last chunk's output
+            for (int m = max(nk - Lay::KQS, 0); m < nk; ++m) wait_bar(bar(Lay::KQ_EMPTY + m % Lay::KQS), (m / Lay::KQS) & 1, flags);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer: chain (whole warp)
@@ -274,8 +274,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             wait_w(Lay::N_GO, n & 1);
             tc::fence_after();
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 + halves(i), nmaj(dkn, i), id_s, 1);
+            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 * i + 8, nmaj(dkn, i), id_s, 1);
             tc::commit_w(bar(Lay::S_DONE));
+            tc::commit_w(bar(Lay::KQ_EMPTY + rg.s));
         }
         finish(Lay::END);
     } else if (warp == 2) {
@@ -360,13 +361,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             const float all = __shfl_sync(0xffffffffu, pre, 31);
             const float g1 = pre, before = __shfl_up_sync(0xffffffffu, pre, 1), g0 = (lane ? before : 0.f) + a[0];
-            wait_w(Lay::KQ_FULL + rg.s, rg.par);  // the buffer is free as the tile's is
-            const uint32_t o = sc(rg) + 8 * lane;
+            wait_w(Lay::KQ_EMPTY + rg.s, rg.par ^ 1);  // its buffer is free with that of the tile three chunks back
+            const uint32_t o = sc(n) + 8 * lane;
             SM_AT(float2, o + SC_G) = make_float2(g0, g1);
             SM_AT(float2, o + SC_B) = make_float2(b[0], b[1]);
             SM_AT(float2, o + SC_D) = make_float2(ex2_approx(g0), ex2_approx(g1));
             SM_AT(float2, o + SC_N) = make_float2(ex2_approx(all - g0), ex2_approx(all - g1));
-            if (lane == 0) SM_AT(float, sc(rg) + SC_GAM) = ex2_approx(all);
+            if (lane == 0) SM_AT(float, sc(n) + SC_GAM) = ex2_approx(all);
             arrive_w(Lay::SC_FULL + rg.s);
         }
     } else if (warp < 12) {
@@ -409,18 +410,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
             }
         };
-        auto pack = [](const uint32_t(&r)[32], uint32_t(&o)[16]) {
+        // 16 columns as 8 of an operand, as they are or times the factors at `at`
+        auto pack = [](const uint32_t(&r)[16], uint32_t(&o)[8]) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+            for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
         };
-        // 32 columns times the factors at `at`
-        auto scale = [&](uint32_t(&r)[32], uint32_t at) {
+        auto pack_scaled = [&](const uint32_t(&r)[16], uint32_t(&o)[8], uint32_t at) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
                 const float4 f = SM_AT(const float4, at + 4 * i);
                 const float2 x = fmul2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(f.x, f.y));
                 const float2 y = fmul2(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), make_float2(f.z, f.w));
-                r[i] = __float_as_uint(x.x); r[i + 1] = __float_as_uint(x.y); r[i + 2] = __float_as_uint(y.x); r[i + 3] = __float_as_uint(y.y);
+                o[i / 2] = pack_bf16(x.x, x.y);
+                o[i / 2 + 1] = pack_bf16(y.x, y.y);
             }
         };
         if (nch > 0) {
@@ -437,57 +439,61 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // schedulers, and what is fetched twice costs more than a branch.
 #pragma unroll 1
         for (int n = 0; n < nch; ++n, rg.next()) {
-            uint32_t r[32], o[16];
+            uint32_t r[16], o[8];
             // the state as an operand
             if (n > 0) wait_w(Lay::S_DONE, (n - 1) & 1);
             tc::fence_after();
 #pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                tc::ld32(ls + 32 * g, r);
+            for (int g = 0; g < 4; ++g) {
+                tc::ld16(ls + 16 * g, r);
                 tc::wait_ld();
                 pack(r, o);
-                tc::st16(lsb + 16 * g, o);
+                tc::st8(lsb + 8 * g, o);
             }
             tc::wait_st();
             tc::fence_before();
             arrive_w(Lay::SB_GO);
             // decayed in place
             wait_w(Lay::SC_FULL + rg.s, rg.par);
-            const float gam = SM_AT(const float, sc(rg) + SC_GAM);
+            const float gam = SM_AT(const float, sc(n) + SC_GAM);
 #pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                tc::ld32(ls + 32 * g, r);
+            for (int g = 0; g < 4; ++g) {
+                tc::ld16(ls + 16 * g, r);
                 tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
+                for (int i = 0; i < 16; i += 2) {
                     const float2 x = fmul2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(gam, gam));
                     r[i] = __float_as_uint(x.x);
                     r[i + 1] = __float_as_uint(x.y);
                 }
-                tc::st32(ls + 32 * g, r);
+                tc::st16(ls + 16 * g, r);
             }
             // D1' over D1
             wait_w(Lay::D1_DONE, n & 1);
             wait_w(Lay::T_FULL + rg.s, rg.par);
             tc::fence_after();
-            tc::ld32(l1, r);
-            tc::wait_ld();
-            scale(r, sc(rg) + SC_D + 128 * hf);
-            pack(r, o);
-            tc::st16(l1, o);
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {
+                tc::ld16(l1 + 16 * g, r);
+                tc::wait_ld();
+                pack_scaled(r, o, sc(n) + SC_D + 128 * hf + 64 * g);
+                tc::st8(l1 + 8 * g, o);
+            }
             tc::wait_st();
             tc::fence_before();
             arrive_w(Lay::D1_GO);
             // N and N' over D2
             wait_w(Lay::N_DONE, n & 1);
             tc::fence_after();
-            tc::ld32(l2, r);
-            tc::wait_ld();
-            pack(r, o);
-            tc::st16(l2, o);
-            scale(r, sc(rg) + SC_N + 128 * hf);
-            pack(r, o);
-            tc::st16(l2 + 16, o);
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {
+                tc::ld16(l2 + 16 * g, r);
+                tc::wait_ld();
+                pack(r, o);
+                tc::st8(l2 + 16 * g, o);
+                pack_scaled(r, o, sc(n) + SC_N + 128 * hf + 64 * g);
+                tc::st8(l2 + 16 * g + 8, o);
+            }
             tc::wait_st();
             tc::fence_before();
             arrive_w(Lay::N_GO);
@@ -543,14 +549,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 wait_w(Lay::N_GO, n & 1);
                 tc::fence_after();
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + halves(i), rows(dp, i), id_n, i > 0);
+                for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + 16 * i, rows(dp, i), id_n, i > 0);
                 tc::commit_w(bar(Lay::O_DONE));
+                tc::commit_w(bar(Lay::KQ_EMPTY + rg.s));
+                if (lane == 0) bulk_wait_read();  // the last chunk's store is done with the buffer
+                __syncwarp();
             }
             wait_w(Lay::T_FULL + rg.s, rg.par);
             wait_w(Lay::O_DONE, n & 1);
+            named_bar_sync(1, 128);
             tc::fence_after();
-            // The Q tile has been read: token i is its row i. The accumulators are loaded as warp MMA fragments (8 channels
-            // x 8 tokens), so that stmatrix.trans hands a token's row its 16 bytes of eight channels.
+            // The accumulators are loaded as warp MMA fragments (8 channels x 8 tokens), so that stmatrix.trans hands a token's
+            // row its 16 bytes of eight channels.
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {  // 16 channels x 32 tokens
                 const int lh = g >> 1, c0 = 32 * (g & 1);
@@ -560,7 +570,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 tc::ld_16x256b_x4(la + T_PV, u);
                 float2 f[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = SM_AT(const float2, sc(rg) + SC_O + 4 * (c0 + 8 * i + 2 * (lane & 3)));
+                for (int i = 0; i < 4; ++i) f[i] = SM_AT(const float2, sc(n) + SC_O + 4 * (c0 + 8 * i + 2 * (lane & 3)));
                 tc::wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -572,7 +582,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int t = c0 + 16 * i + 8 * (lane >> 4) + r;
-                    stsm_x4_t(kq(rg) + (2 * (v8 >> 3) + 1) * Lay::BOX + t * 128 + (((v8 & 7) ^ r) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    stsm_x4_t(sb + Lay::OUT + (v8 >> 3) * Lay::BOX + t * 128 + (((v8 & 7) ^ r) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }
             tc::fence_before();
@@ -581,9 +591,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (Lv == C) {
                 if (warp == 12 && lane == 0) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tma_store_3d(&to, kq(rg) + (2 * c + 1) * Lay::BOX, 64 * c, h, sp.bos + n * C);
+                    for (int c = 0; c < 2; ++c) tma_store_3d(&to, sb + Lay::OUT + c * Lay::BOX, 64 * c, h, sp.bos + n * C);
                     bulk_commit();
-                    bulk_wait_read();
                 }
             } else {
                 for (int i = threadIdx.x - 384; i < Lv * 16; i += 128) {
@@ -591,10 +600,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     const long long e = static_cast<long long>(sp.bos + n * C + t) * p.os + static_cast<long long>(h) * DH + 8 * g;
                     if (!gmem_ok(e, 8, (p.total - 1) * p.os + static_cast<long long>(p.H) * DH)) continue;
                     *reinterpret_cast<uint4 *>(p.out + e) =
-                        SM_AT(const uint4, kq(rg) + (2 * (g >> 3) + 1) * Lay::BOX + t * 128 + (((g & 7) ^ (t & 7)) << 4));
+                        SM_AT(const uint4, sb + Lay::OUT + (g >> 3) * Lay::BOX + t * 128 + (((g & 7) ^ (t & 7)) << 4));
                 }
             }
-            arrive_w(Lay::KQ_EMPTY + rg.s);
         }
         if (warp == 12) {
             if (lane == 0) bulk_wait_all();
@@ -634,7 +642,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             wait_w(Lay::SC_FULL + g.s, g.par);
             const int Lv = live_of(n), r = 32 * (w8 & 1) + lane;
             const bool is_q = w8 >= 6;
-            const uint32_t s = sc(g) + 4 * r, at = kq(g) + (is_q ? Lay::BOX : 0) + r * 128;
+            const uint32_t s = sc(n) + 4 * r, at = kq(g) + (is_q ? Lay::BOX : 0) + r * 128;
             auto vec = [&](int c) { return at + (c >> 3) * 2 * Lay::BOX + (((c & 7) ^ (r & 7)) << 4); };
             if (Lv < C) {
                 // rows past the end hold another sequence's tokens: zero, so that a NaN there meets no product
@@ -672,7 +680,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Ring nx;
 #pragma unroll 1
         for (int n = -1; n < nch; ++n) {  // (chunk -1: the first chunk's factors alone)
-            const uint32_t s = sc(rg), t0 = tt(rg);
+            const uint32_t s = sc(n), t0 = tt(rg);
             // where T[i][j] stands as an operand, times its column's step
             auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
             auto put_t = [&](const float(&d)[4], int r, int c) {
@@ -719,33 +727,35 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 arrive_w(Lay::KQ_FREE);
                 sync();
             }
-            // (I + A)^-1: diagonal blocks of 8, two per warp, a column per lane, row by row; then the block between them
+            // (I + A)^-1: diagonal blocks of 8, two per warp, a row per lane; then the block between them
             if (hf == 1) {
                 if (n + 1 < nch) factors(n + 1, nx);
             } else if (n >= 0) {
                 const int d0 = 16 * q, d1 = d0 + (lane & 8), c = lane & 7;
+                // row c of the inverse, x (I + A) = e_c, from its last column to its first
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float u = i == c ? 1.f : 0.f, w = 0.f;
+                for (int j = 7; j >= 0; --j) {
+                    float u = j == c ? 1.f : 0.f, w = 0.f;
 #pragma unroll
-                    for (int j = 0; j < i; j += 4) {
-                        const float4 a = SM_AT(const float4, scr + 4 * ((d1 + i) * Lay::LD + d1 + j));
-                        u = fmaf(-a.x, x[j], u);
-                        if (j + 1 < i) w = fmaf(-a.y, x[j + 1], w);
-                        if (j + 2 < i) u = fmaf(-a.z, x[j + 2], u);
-                        if (j + 3 < i) w = fmaf(-a.w, x[j + 3], w);
-                    }
-                    x[i] = u + w;
+                    for (int i = j + 1; i < 8; ++i)
+                        if ((i - j) & 1)
+                            u = fmaf(-A(d1 + i, d1 + j), x[i], u);
+                        else
+                            w = fmaf(-A(d1 + i, d1 + j), x[i], w);
+                    x[j] = u + w;
                 }
                 __syncwarp();
                 if (lane < 16) {
-                    const float b = SM_AT(const float, s + SC_B + 4 * (d1 + c));
+                    uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        A(d1 + i, d1 + c) = __uint_as_float(tf32(x[i]));
-                        SM_AT(uint16_t, t_at(d1 + i, d1 + c)) = f2bf_bits(b * x[i]);
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 b = SM_AT(const float4, s + SC_B + 4 * (d1 + j));
+                        SM_AT(uint4, scr + 4 * ((d1 + c) * Lay::LD + d1 + j)) = make_uint4(tf32(x[j]), tf32(x[j + 1]), tf32(x[j + 2]), tf32(x[j + 3]));
+                        o[j / 2] = pack_bf16(x[j] * b.x, x[j + 1] * b.y);
+                        o[j / 2 + 1] = pack_bf16(x[j + 2] * b.z, x[j + 3] * b.w);
                     }
+                    SM_AT(uint4, t_at(d1 + c, d1)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 __syncwarp();
                 float d[4] = {}, e[4] = {};
