@@ -30,12 +30,12 @@
 //
 // Warp roles (768 threads):
 //   warp 0       TMA producer (lane 0): [K; Q] tiles three deep, V tiles two
-//   warp 1       MMA issuer: everything on the chain, and the output
-//   warp 2       MMA issuer: [K; Q] K^T
-//   warp 3       running sums of the decays, steps
+//   warp 1       MMA issuer: the chain
+//   warp 2       MMA issuer: [K; Q] K^T, V^T T^T
+//   warp 3       MMA issuer: output; running sums of the decays, steps
 //   warps 4-11   chain: bf16 state, D1', N and N', decay (value channel, half of the columns each)
-//   warps 12-15  output (value channel), transposed on the way through shared memory; its MMAs
-//   warps 16-23  A, P and T of a chunk; warps 20-23 norms of queries and keys, one chunk ahead where they can
+//   warps 12-15  output (value channel), transposed on the way through shared memory; norms of queries and keys
+//   warps 16-23  A, P and T of a chunk
 #pragma once
 #include "kda_gdn_step.cuh"
 #include "kda_ssm_tc.cuh"
@@ -70,7 +70,7 @@ struct Layout {
     static constexpr int BAR = OUT + VT;
     static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 8, SC_FULL = 10, T_FULL = 13, G_DONE = 16, KQ_FREE = 17,
                          KQ_ZERO = 18, SB_GO = 19, D1_DONE = 20, D1_GO = 21, N_DONE = 22, N_GO = 23, S_DONE = 24, O_DONE = 25,
-                         SQ_DONE = 26, U_DONE = 27, END = 28, END2 = 29, END3 = 30, NBARS = 31;
+                         SQ_DONE = 26, U_DONE = 27, OUT_RD = 28, FACT = 29, END = 32, END2 = 33, END3 = 34, NBARS = 35;
     static constexpr int TMEMPTR = (BAR + NBARS * 8 + 15) / 16 * 16;
     static constexpr int FLAGS = TMEMPTR + 16;
     static constexpr int ALLOC = FLAGS + 16 + 1024;
@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(bar(Lay::KQ_EMPTY + i), 2);
             mbar_init(bar(Lay::SC_FULL + i), 1);
             mbar_init(bar(Lay::T_FULL + i), 8);
+            mbar_init(bar(Lay::FACT + i), 4);
         }
         for (int i = 0; i < Lay::VS; ++i) {
             mbar_init(bar(Lay::V_FULL + i), 1);
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int i : {Lay::G_DONE, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::SQ_DONE, Lay::U_DONE, Lay::END, Lay::END2, Lay::END3})
             mbar_init(bar(i), 1);
         mbar_init(bar(Lay::KQ_ZERO), 4);
+        mbar_init(bar(Lay::OUT_RD), 4);
         for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO, Lay::KQ_FREE}) mbar_init(bar(i), 8);
         flags[0] = 0;
         spoilt = 0u;
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         finish(Lay::END2);
     } else if (warp == 3) {
-        // ---------------------------------------------------------------- decays and steps, two tokens per lane
+        // ---------------------------------------------------------------- decays and steps, two tokens per lane; output MMAs
         Ring rg;
         const float A2 = -expf(__ldg(p.A_log + h)) * LOG2E, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
         const uint16_t *ap = p.a + static_cast<long long>(sp.bos) * p.as + h, *bp = p.beta + static_cast<long long>(sp.bos) * p.bs + h;
@@ -340,36 +342,59 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
         };
         fetch(0);
+        Ring rs;  // of the scalars, three chunks ahead
 #pragma unroll 1
-        for (int n = 0; n < nch; ++n, rg.next()) {
-            const int Lv = live_of(n);
-            float a[2], b[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool live = 2 * lane + i < Lv;
-                // held at the least decay by a comparison that lets NaN through (fmaxf would not)
-                const float u = A2 * softplus_fast(__uint_as_float(ra[i] << 16) + bias);
-                a[i] = !live ? 0.f : u < ssm::MIN_LOG2_DECAY ? ssm::MIN_LOG2_DECAY : u;
-                b[i] = live ? blk::sigmoid_fast(__uint_as_float(rb[i] << 16)) : 0.f;
+        for (int n = -Lay::KQS; n < nch; ++n) {
+            if (n >= 0) {
+                const uint32_t dq = tc::sdesc_lo(kq(rg), 16) + (Lay::BOX >> 4), dp = tc::sdesc_lo(pt(rg), 16);
+                wait_kq(n, rg);
+                if (n > 0) wait_w(Lay::OUT_RD, (n - 1) & 1);
+                wait_w(Lay::SB_GO, n & 1);
+                tc::fence_after();
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
+                tc::commit_w(bar(Lay::SQ_DONE));
+                wait_w(Lay::T_FULL + rg.s, rg.par);
+                wait_w(Lay::N_GO, n & 1);
+                tc::fence_after();
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + 16 * i, rows(dp, i), id_n, i > 0);
+                tc::commit_w(bar(Lay::O_DONE));
+                tc::commit_w(bar(Lay::KQ_EMPTY + rg.s));
+                rg.next();
             }
-            fetch(n + 1);
-            float pre = a[0] + a[1];
+            if (const int m = n + Lay::KQS; m < nch) {
+                const int Lv = live_of(m);
+                float a[2], b[2];
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, pre, m);
-                if (lane >= m) pre += u;
+                for (int i = 0; i < 2; ++i) {
+                    const bool live = 2 * lane + i < Lv;
+                    // held at the least decay by a comparison that lets NaN through (fmaxf would not)
+                    const float u = A2 * softplus_fast(__uint_as_float(ra[i] << 16) + bias);
+                    a[i] = !live ? 0.f : u < ssm::MIN_LOG2_DECAY ? ssm::MIN_LOG2_DECAY : u;
+                    b[i] = live ? blk::sigmoid_fast(__uint_as_float(rb[i] << 16)) : 0.f;
+                }
+                fetch(m + 1);
+                float pre = a[0] + a[1];
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const float u = __shfl_up_sync(0xffffffffu, pre, d);
+                    if (lane >= d) pre += u;
+                }
+                const float all = __shfl_sync(0xffffffffu, pre, 31);
+                const float g1 = pre, before = __shfl_up_sync(0xffffffffu, pre, 1), g0 = (lane ? before : 0.f) + a[0];
+                wait_w(Lay::KQ_EMPTY + rs.s, rs.par ^ 1);  // its buffer is free with that of the tile three chunks back
+                const uint32_t o = sc(m) + 8 * lane;
+                SM_AT(float2, o + SC_G) = make_float2(g0, g1);
+                SM_AT(float2, o + SC_B) = make_float2(b[0], b[1]);
+                SM_AT(float2, o + SC_D) = make_float2(ex2_approx(g0), ex2_approx(g1));
+                SM_AT(float2, o + SC_N) = make_float2(ex2_approx(all - g0), ex2_approx(all - g1));
+                if (lane == 0) SM_AT(float, sc(m) + SC_GAM) = ex2_approx(all);
+                arrive_w(Lay::SC_FULL + rs.s);
+                rs.next();
             }
-            const float all = __shfl_sync(0xffffffffu, pre, 31);
-            const float g1 = pre, before = __shfl_up_sync(0xffffffffu, pre, 1), g0 = (lane ? before : 0.f) + a[0];
-            wait_w(Lay::KQ_EMPTY + rg.s, rg.par ^ 1);  // its buffer is free with that of the tile three chunks back
-            const uint32_t o = sc(n) + 8 * lane;
-            SM_AT(float2, o + SC_G) = make_float2(g0, g1);
-            SM_AT(float2, o + SC_B) = make_float2(b[0], b[1]);
-            SM_AT(float2, o + SC_D) = make_float2(ex2_approx(g0), ex2_approx(g1));
-            SM_AT(float2, o + SC_N) = make_float2(ex2_approx(all - g0), ex2_approx(all - g1));
-            if (lane == 0) SM_AT(float, sc(n) + SC_GAM) = ex2_approx(all);
-            arrive_w(Lay::SC_FULL + rg.s);
         }
+        finish(Lay::END3);
     } else if (warp < 12) {
         // ---------------------------------------------------------------- chain
         Ring rg;
@@ -534,114 +559,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Ring rg;
         const int q = warp & 3;
         const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16);
-#pragma unroll 1
-        for (int n = 0; n < nch; ++n, rg.next()) {
-            const int Lv = live_of(n);
-            if (warp == 12) {  // its two products: all four warps have read the last chunk's
-                const uint32_t dq = tc::sdesc_lo(kq(rg), 16) + (Lay::BOX >> 4), dp = tc::sdesc_lo(pt(rg), 16);
-                wait_kq(n, rg);
-                wait_w(Lay::SB_GO, n & 1);
-                tc::fence_after();
-#pragma unroll 1
-                for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
-                tc::commit_w(bar(Lay::SQ_DONE));
-                wait_w(Lay::T_FULL + rg.s, rg.par);
-                wait_w(Lay::N_GO, n & 1);
-                tc::fence_after();
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + 16 * i, rows(dp, i), id_n, i > 0);
-                tc::commit_w(bar(Lay::O_DONE));
-                tc::commit_w(bar(Lay::KQ_EMPTY + rg.s));
-                if (lane == 0) bulk_wait_read();  // the last chunk's store is done with the buffer
-                __syncwarp();
-            }
-            wait_w(Lay::T_FULL + rg.s, rg.par);
-            wait_w(Lay::O_DONE, n & 1);
-            named_bar_sync(1, 128);
-            tc::fence_after();
-            // The accumulators are loaded as warp MMA fragments (8 channels x 8 tokens), so that stmatrix.trans hands a token's
-            // row its 16 bytes of eight channels.
-#pragma unroll 1
-            for (int g = 0; g < 4; ++g) {  // 16 channels x 32 tokens
-                const int lh = g >> 1, c0 = 32 * (g & 1);
-                const uint32_t la = lq + (static_cast<uint32_t>(16 * lh) << 16) + c0;
-                uint32_t s[16], u[16], o[8];
-                tc::ld_16x256b_x4(la + T_SQ, s);
-                tc::ld_16x256b_x4(la + T_PV, u);
-                float2 f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = SM_AT(const float2, sc(n) + SC_O + 4 * (c0 + 8 * i + 2 * (lane & 3)));
-                tc::wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 y = ffma2(f[i >> 1], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
-                                           make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
-                    o[i] = pack_bf16(y.x, y.y);
-                }
-                const int v8 = 4 * q + 2 * lh + ((lane >> 3) & 1), r = lane & 7;  // eight channels and token row of this lane's address
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int t = c0 + 16 * i + 8 * (lane >> 4) + r;
-                    stsm_x4_t(sb + Lay::OUT + (v8 >> 3) * Lay::BOX + t * 128 + (((v8 & 7) ^ r) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                }
-            }
-            tc::fence_before();
-            tc::fence_async_smem();
-            named_bar_sync(1, 128);
-            if (Lv == C) {
-                if (warp == 12 && lane == 0) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) tma_store_3d(&to, sb + Lay::OUT + c * Lay::BOX, 64 * c, h, sp.bos + n * C);
-                    bulk_commit();
-                }
-            } else {
-                for (int i = threadIdx.x - 384; i < Lv * 16; i += 128) {
-                    const int t = i >> 4, g = i & 15;
-                    const long long e = static_cast<long long>(sp.bos + n * C + t) * p.os + static_cast<long long>(h) * DH + 8 * g;
-                    if (!gmem_ok(e, 8, (p.total - 1) * p.os + static_cast<long long>(p.H) * DH)) continue;
-                    *reinterpret_cast<uint4 *>(p.out + e) =
-                        SM_AT(const uint4, sb + Lay::OUT + (g >> 3) * Lay::BOX + t * 128 + (((g & 7) ^ (t & 7)) << 4));
-                }
-            }
-        }
-        if (warp == 12) {
-            if (lane == 0) bulk_wait_all();
-            __syncwarp();
-            finish(Lay::END3);
-        }
-    } else {
-        // ---------------------------------------------------------------- A, P and T
-        Ring rg;
-        // Quarters 0 and 1 of tensor memory hold K K^T, 2 and 3 Q K^T; two warps share a quarter's columns.
-        const int q = warp & 3, hf = warp < 20 ? 0 : 1, w8 = warp - 16;
-        const int lo = q & 1, i0 = 32 * lo + lane;  // this thread's row
-        const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_KQ;
-        const uint32_t scr = sb + Lay::SCR;
-        auto bits = [](float x) { return __float_as_uint(x); };
-        auto A = [&](int i, int j) -> float & { return SM_AT(float, scr + 4 * (i * Lay::LD + j)); };
-        auto sync = [&] { named_bar_sync(2, 256); };
-        const int g8 = lane >> 2, t4 = lane & 3;
-        // d += X[xr.., xc..] Y[yr.., yc..], 16 x 16 by 16 x 8, both in the scratch. What is not A itself is rounded to tf32
-        // as it is put there; A is cut off, by 2^-11 of it in the mean.
-        auto product = [&](float(&d)[4], int xr, int xc, int yr, int yc) {
-#pragma unroll
-            for (int k = 0; k < 16; k += 8) {
-                const uint32_t a[4] = {bits(A(xr + g8, xc + k + t4)), bits(A(xr + g8 + 8, xc + k + t4)), bits(A(xr + g8, xc + k + t4 + 4)),
-                                       bits(A(xr + g8 + 8, xc + k + t4 + 4))};
-                mma_tf32(d, a, bits(A(yr + k + t4, yc + g8)), bits(A(yr + k + t4 + 4, yc + g8)));
-            }
-        };
-        auto put = [&](const float(&d)[4], int r, int c, float f) {
-            SM_AT(uint2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[0]), tf32(f * d[1]));
-            SM_AT(uint2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[2]), tf32(f * d[3]));
-        };
-        // The factors of rows and columns of chunk n, a row of K or Q per thread of warps 4..7: one chunk ahead, while the
-        // others invert.
+        // The factors of rows and columns of a chunk, a row of K or Q per thread, two chunks ahead
         auto factors = [&](int n, const Ring &g) {
             wait_w(Lay::KQ_FULL + g.s, g.par);
             wait_w(Lay::SC_FULL + g.s, g.par);
-            const int Lv = live_of(n), r = 32 * (w8 & 1) + lane;
-            const bool is_q = w8 >= 6;
+            const int Lv = live_of(n), r = 32 * (q & 1) + lane;
+            const bool is_q = q >= 2;
             const uint32_t s = sc(n) + 4 * r, at = kq(g) + (is_q ? Lay::BOX : 0) + r * 128;
             auto vec = [&](int c) { return at + (c >> 3) * 2 * Lay::BOX + (((c & 7) ^ (r & 7)) << 4); };
             if (Lv < C) {
@@ -676,10 +599,99 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(float, s + SC_D) = -fd * f;
                 SM_AT(float, s + SC_N) = fn * f;
             }
+            arrive_w(Lay::FACT + g.s);
         };
-        Ring nx;
+        Ring ra;
 #pragma unroll 1
-        for (int n = -1; n < nch; ++n) {  // (chunk -1: the first chunk's factors alone)
+        for (int n = -2; n < nch; ++n) {
+            if (n + 2 < nch) factors(n + 2, ra);
+            ra.next();
+            if (n < 0) continue;
+            const int Lv = live_of(n);
+            if (warp == 12) {
+                if (lane == 0) bulk_wait_read();  // the last chunk's store is done with the buffer
+                __syncwarp();
+            }
+            wait_w(Lay::T_FULL + rg.s, rg.par);
+            wait_w(Lay::O_DONE, n & 1);
+            named_bar_sync(1, 128);
+            tc::fence_after();
+            // The accumulators are loaded as warp MMA fragments (8 channels x 8 tokens), so that stmatrix.trans hands a token's
+            // row its 16 bytes of eight channels.
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {  // 16 channels x 32 tokens
+                const int lh = g >> 1, c0 = 32 * (g & 1);
+                const uint32_t la = lq + (static_cast<uint32_t>(16 * lh) << 16) + c0;
+                uint32_t s[16], u[16], o[8];
+                tc::ld_16x256b_x4(la + T_SQ, s);
+                tc::ld_16x256b_x4(la + T_PV, u);
+                float2 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = SM_AT(const float2, sc(n) + SC_O + 4 * (c0 + 8 * i + 2 * (lane & 3)));
+                tc::wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 y = ffma2(f[i >> 1], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                           make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
+                    o[i] = pack_bf16(y.x, y.y);
+                }
+                const int v8 = 4 * q + 2 * lh + ((lane >> 3) & 1), r = lane & 7;  // eight channels and token row of this lane's address
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = c0 + 16 * i + 8 * (lane >> 4) + r;
+                    stsm_x4_t(sb + Lay::OUT + (v8 >> 3) * Lay::BOX + t * 128 + (((v8 & 7) ^ r) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            tc::fence_before();
+            arrive_w(Lay::OUT_RD);
+            tc::fence_async_smem();
+            named_bar_sync(1, 128);
+            if (Lv == C) {
+                if (warp == 12 && lane == 0) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tma_store_3d(&to, sb + Lay::OUT + c * Lay::BOX, 64 * c, h, sp.bos + n * C);
+                    bulk_commit();
+                }
+            } else {
+                for (int i = threadIdx.x - 384; i < Lv * 16; i += 128) {
+                    const int t = i >> 4, g = i & 15;
+                    const long long e = static_cast<long long>(sp.bos + n * C + t) * p.os + static_cast<long long>(h) * DH + 8 * g;
+                    if (!gmem_ok(e, 8, (p.total - 1) * p.os + static_cast<long long>(p.H) * DH)) continue;
+                    *reinterpret_cast<uint4 *>(p.out + e) =
+                        SM_AT(const uint4, sb + Lay::OUT + (g >> 3) * Lay::BOX + t * 128 + (((g & 7) ^ (t & 7)) << 4));
+                }
+            }
+            rg.next();
+        }
+        if (warp == 12 && lane == 0) bulk_wait_all();
+    } else {
+        // ---------------------------------------------------------------- A, P and T
+        Ring rg;
+        // Quarters 0 and 1 of tensor memory hold K K^T, 2 and 3 Q K^T; two warps share a quarter's columns.
+        const int q = warp & 3, hf = warp < 20 ? 0 : 1, w8 = warp - 16;
+        const int lo = q & 1, i0 = 32 * lo + lane;  // this thread's row
+        const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_KQ;
+        const uint32_t scr = sb + Lay::SCR;
+        auto bits = [](float x) { return __float_as_uint(x); };
+        auto A = [&](int i, int j) -> float & { return SM_AT(float, scr + 4 * (i * Lay::LD + j)); };
+        auto sync = [&] { named_bar_sync(2, 256); };
+        const int g8 = lane >> 2, t4 = lane & 3;
+        // d += X[xr.., xc..] Y[yr.., yc..], 16 x 16 by 16 x 8, both in the scratch. What is not A itself is rounded to tf32
+        // as it is put there; A is cut off, by 2^-11 of it in the mean.
+        auto product = [&](float(&d)[4], int xr, int xc, int yr, int yc) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 8) {
+                const uint32_t a[4] = {bits(A(xr + g8, xc + k + t4)), bits(A(xr + g8 + 8, xc + k + t4)), bits(A(xr + g8, xc + k + t4 + 4)),
+                                       bits(A(xr + g8 + 8, xc + k + t4 + 4))};
+                mma_tf32(d, a, bits(A(yr + k + t4, yc + g8)), bits(A(yr + k + t4 + 4, yc + g8)));
+            }
+        };
+        auto put = [&](const float(&d)[4], int r, int c, float f) {
+            SM_AT(uint2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[0]), tf32(f * d[1]));
+            SM_AT(uint2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[2]), tf32(f * d[3]));
+        };
+#pragma unroll 1
+        for (int n = 0; n < nch; ++n, rg.next()) {
             const uint32_t s = sc(n), t0 = tt(rg);
             // where T[i][j] stands as an operand, times its column's step
             auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
@@ -688,49 +700,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(uint32_t, t_at(r + g8, c + 2 * t4)) = pack_bf16(-d[0] * b.x, -d[1] * b.y);
                 SM_AT(uint32_t, t_at(r + g8 + 8, c + 2 * t4)) = pack_bf16(-d[2] * b.x, -d[3] * b.y);
             };
-            if (n >= 0) {
-                sync();
-                const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
-                wait_w(Lay::G_DONE, n & 1);
-                tc::fence_after();
-                // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
-                const int last = q < 2 ? i0 - 1 : i0;
+            wait_w(Lay::FACT + rg.s, rg.par);
+            const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
+            wait_w(Lay::G_DONE, n & 1);
+            tc::fence_after();
+            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
+            const int last = q < 2 ? i0 - 1 : i0;
 #pragma unroll 1
-                for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
-                    uint32_t r[16];
-                    float2 w[8];
-                    tc::ld16(lq + b, r);
+            for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
+                uint32_t r[16];
+                float2 w[8];
+                tc::ld16(lq + b, r);
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float4 g = SM_AT(const float4, s + SC_GK + 4 * (b + 2 * j));
-                        w[j] = make_float2(ex2_approx(Gi - g.x), ex2_approx(Gi - g.y));
-                        w[j + 1] = make_float2(ex2_approx(Gi - g.z), ex2_approx(Gi - g.w));
-                    }
-                    tc::wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-                        if (b + 2 * j > last) w[j].x = 0.f;
-                        if (b + 2 * j + 1 > last) w[j].y = 0.f;
-                    }
-                    if (q < 2) {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; j += 4)
-                            SM_AT(uint4, pt(rg) + i0 * 128 + ((((b >> 3) + (j >> 2)) ^ (i0 & 7)) << 4)) =
-                                make_uint4(pack_bf16(w[j].x, w[j].y), pack_bf16(w[j + 1].x, w[j + 1].y), pack_bf16(w[j + 2].x, w[j + 2].y), pack_bf16(w[j + 3].x, w[j + 3].y));
-                    }
+                for (int j = 0; j < 8; j += 2) {
+                    const float4 g = SM_AT(const float4, s + SC_GK + 4 * (b + 2 * j));
+                    w[j] = make_float2(ex2_approx(Gi - g.x), ex2_approx(Gi - g.y));
+                    w[j + 1] = make_float2(ex2_approx(Gi - g.z), ex2_approx(Gi - g.w));
                 }
-                tc::fence_before();
-                arrive_w(Lay::KQ_FREE);
-                sync();
+                tc::wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+                    if (b + 2 * j > last) w[j].x = 0.f;
+                    if (b + 2 * j + 1 > last) w[j].y = 0.f;
+                }
+                if (q < 2) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4)
+                        SM_AT(uint4, pt(rg) + i0 * 128 + ((((b >> 3) + (j >> 2)) ^ (i0 & 7)) << 4)) =
+                            make_uint4(pack_bf16(w[j].x, w[j].y), pack_bf16(w[j + 1].x, w[j + 1].y), pack_bf16(w[j + 2].x, w[j + 2].y), pack_bf16(w[j + 3].x, w[j + 3].y));
+                }
             }
+            tc::fence_before();
+            arrive_w(Lay::KQ_FREE);
+            sync();
             // (I + A)^-1: diagonal blocks of 8, two per warp, a row per lane; then the block between them
-            if (hf == 1) {
-                if (n + 1 < nch) factors(n + 1, nx);
-            } else if (n >= 0) {
+            if (hf == 0) {
                 const int d0 = 16 * q, d1 = d0 + (lane & 8), c = lane & 7;
                 // row c of the inverse, x (I + A) = e_c, from its last column to its first
                 float x[8];
@@ -771,8 +779,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const float2 b = SM_AT(const float2, s + SC_B + 4 * (d0 + 2 * t4));
                 SM_AT(uint32_t, t_at(d0 + 8 + g8, d0 + 2 * t4)) = pack_bf16(-e[0] * b.x, -e[1] * b.y);
             }
-            nx.next();
-            if (n < 0) continue;
             sync();
             // the blocks below: -T_hi A_hl T_lo, first of 16 (eight columns per warp), then of 32
             if (hf == 0) {
@@ -804,7 +810,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             tc::fence_async_smem();
             arrive_w(Lay::T_FULL + rg.s);
-            rg.next();
         }
     }
 
