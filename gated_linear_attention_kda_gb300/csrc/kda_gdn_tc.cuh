@@ -35,7 +35,7 @@
 //   warp 3       MMA issuer: output; running sums of the decays, steps
 //   warps 4-11   chain: bf16 state, D1', N and N', decay (value channel, half of the columns each)
 //   warps 12-15  output (value channel), transposed on the way through shared memory; norms of queries and keys
-//   warps 16-23  A, P and T of a chunk
+//   warps 16-23  A, P and T of a chunk, two groups in turn
 #pragma once
 #include "kda_gdn_step.cuh"
 #include "kda_ssm_tc.cuh"
@@ -59,18 +59,20 @@ struct Layout {
     static constexpr int BOX = C * 128;             // 64 channels x 64 rows, 128-byte swizzle
     static constexpr int KQS = 3, KQT = 4 * BOX;    // a tile: per 64 channels the rows of K, then those of Q
     static constexpr int VS = 2, VT = 2 * BOX;
-    static constexpr int LD = 68;                   // floats per row of the inverse's scratch
+    static constexpr int TS = 2;                    // T tiles
+    // the inverse's scratch, fp32, one per group: rows 0..31 need 32 columns, the others 64 (and four more for the banks)
+    static constexpr int LD0 = 36, LD1 = 68, SCRATCH = 32 * (LD0 + LD1) * 4;
     static constexpr int KQ = 0;
     static constexpr int V = KQ + KQS * KQT;
     static constexpr int P = V + VS * VT;           // scores [i][j] and T [i][j], bf16, 128-byte rows
     static constexpr int T = P + KQS * BOX;
-    static constexpr int SCR = T + KQS * BOX;
-    static constexpr int SC = SCR + C * LD * 4;
+    static constexpr int SCR = T + TS * BOX;
+    static constexpr int SC = SCR + 2 * SCRATCH;
     static constexpr int OUT = (SC + 4 * SC_BYTES + 1023) / 1024 * 1024;  // a chunk's output, [token][channel]
     static constexpr int BAR = OUT + VT;
-    static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 8, SC_FULL = 10, T_FULL = 13, G_DONE = 16, KQ_FREE = 17,
+    static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 8, SC_FULL = 10, T_FULL = 13, G_DONE = 35, KQ_FREE = 17,
                          KQ_ZERO = 18, SB_GO = 19, D1_DONE = 20, D1_GO = 21, N_DONE = 22, N_GO = 23, S_DONE = 24, O_DONE = 25,
-                         SQ_DONE = 26, U_DONE = 27, OUT_RD = 28, FACT = 29, END = 32, END2 = 33, END3 = 34, NBARS = 35;
+                         SQ_DONE = 26, U_DONE = 27, OUT_RD = 28, FACT = 29, END = 32, END2 = 33, END3 = 34, T_EMPTY = 37, NBARS = 39;
     static constexpr int TMEMPTR = (BAR + NBARS * 8 + 15) / 16 * 16;
     static constexpr int FLAGS = TMEMPTR + 16;
     static constexpr int ALLOC = FLAGS + 16 + 1024;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto kq = [&](const Ring &g) { return sb + Lay::KQ + g.s * Lay::KQT; };
     auto vt = [&](int n) { return sb + Lay::V + (n % Lay::VS) * Lay::VT; };
     auto pt = [&](const Ring &g) { return sb + Lay::P + g.s * Lay::BOX; };
-    auto tt = [&](const Ring &g) { return sb + Lay::T + g.s * Lay::BOX; };
+    auto tt = [&](int n) { return sb + Lay::T + (n & 1) * Lay::BOX; };
     auto sc = [&](int n) { return sb + Lay::SC + (n & 3) * SC_BYTES; };
     auto live_of = [&](int n) { return min(C, sp.len - n * C); };
 
@@ -167,24 +169,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(bar(Lay::KQ_FULL + i), 1);
             mbar_init(bar(Lay::KQ_EMPTY + i), 2);
             mbar_init(bar(Lay::SC_FULL + i), 1);
-            mbar_init(bar(Lay::T_FULL + i), 8);
+            mbar_init(bar(Lay::T_FULL + i), 4);
             mbar_init(bar(Lay::FACT + i), 4);
         }
         for (int i = 0; i < Lay::VS; ++i) {
             mbar_init(bar(Lay::V_FULL + i), 1);
             mbar_init(bar(Lay::V_EMPTY + i), 1);
         }
-        for (int i : {Lay::G_DONE, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::SQ_DONE, Lay::U_DONE, Lay::END, Lay::END2, Lay::END3})
+        for (int i : {Lay::G_DONE, Lay::G_DONE + 1, Lay::T_EMPTY, Lay::T_EMPTY + 1, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::SQ_DONE, Lay::U_DONE, Lay::END, Lay::END2, Lay::END3})
             mbar_init(bar(i), 1);
         mbar_init(bar(Lay::KQ_ZERO), 4);
         mbar_init(bar(Lay::OUT_RD), 4);
-        for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO, Lay::KQ_FREE}) mbar_init(bar(i), 8);
+        mbar_init(bar(Lay::KQ_FREE), 4);
+        for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO}) mbar_init(bar(i), 8);
         flags[0] = 0;
         spoilt = 0u;
         fence_mbar_init();
     }
     // the parts of P and T above their diagonal blocks are zero for good
-    for (int i = threadIdx.x; i < 2 * Lay::KQS * Lay::BOX / 16; i += NTHREADS) SM_AT(uint4, sb + Lay::P + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < (Lay::KQS + Lay::TS) * Lay::BOX / 16; i += NTHREADS) SM_AT(uint4, sb + Lay::P + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
     tc::fence_before();
     __syncthreads();
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         Ring rg;
 #pragma unroll 1
         for (int n = 0; n < nch; ++n, rg.next()) {
-            const uint32_t dk = tc::sdesc_lo(kq(rg), 16), dt = tc::sdesc_lo(tt(rg), 16), dkn = tc::sdesc_lo(kq(rg), 2 * Lay::BOX);
+            const uint32_t dk = tc::sdesc_lo(kq(rg), 16), dt = tc::sdesc_lo(tt(n), 16), dkn = tc::sdesc_lo(kq(rg), 2 * Lay::BOX);
             wait_kq(n, rg);
             wait_w(Lay::SB_GO, n & 1);
             tc::fence_after();
@@ -271,6 +274,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_D2, tmem + T_D1 + halves(i), rows(dt, i), id_n, 1);
             tc::commit_w(bar(Lay::N_DONE));
+            tc::commit_w(bar(Lay::T_EMPTY + (n & 1)));
             // (with the product of this state and Q done, S_DONE frees its copy too)
             wait_w(Lay::SQ_DONE, n & 1);
             wait_w(Lay::N_GO, n & 1);
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const uint32_t d = tc::sdesc_lo(kq(rg), 16);
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) tc::mma_ss_w(tmem + T_KQ, kmaj(d, i), kmaj(d, i), id_n, i > 0);
-            tc::commit_w(bar(Lay::G_DONE));
+            tc::commit_w(bar(Lay::G_DONE + (n & 1)));  // either group sees every phase of its own
         };
         auto issue_u = [&](int n, const Ring &rg) {
             wait_w(Lay::V_FULL + n % Lay::VS, (n / Lay::VS) & 1);
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             wait_w(Lay::T_FULL + rg.s, rg.par);
             tc::fence_after();
-            const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(rg), 16);
+            const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(n), 16);
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ss_w(tmem + T_D2, nmaj(dv, i), rows(dt, i), id_u, i > 0);
             tc::commit_w(bar(Lay::U_DONE));
@@ -667,32 +671,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else {
         // ---------------------------------------------------------------- A, P and T
         Ring rg;
-        // Quarters 0 and 1 of tensor memory hold K K^T, 2 and 3 Q K^T; two warps share a quarter's columns.
-        const int q = warp & 3, hf = warp < 20 ? 0 : 1, w8 = warp - 16;
+        // Two groups of four warps take turns. Quarters 0 and 1 of tensor memory hold K K^T, 2 and 3 Q K^T.
+        const int q = warp & 3, grp = (warp - 16) >> 2;
         const int lo = q & 1, i0 = 32 * lo + lane;  // this thread's row
         const uint32_t lq = tmem + (static_cast<uint32_t>(32 * q) << 16) + T_KQ;
-        const uint32_t scr = sb + Lay::SCR;
+        const uint32_t scr = sb + Lay::SCR + grp * Lay::SCRATCH;
         auto bits = [](float x) { return __float_as_uint(x); };
-        auto A = [&](int i, int j) -> float & { return SM_AT(float, scr + 4 * (i * Lay::LD + j)); };
-        auto sync = [&] { named_bar_sync(2, 256); };
+        auto at = [&](int i, int j) { return scr + 4 * ((i < 32 ? i * Lay::LD0 : 32 * Lay::LD0 + (i - 32) * Lay::LD1) + j); };
+        auto A = [&](int i, int j) -> float & { return SM_AT(float, at(i, j)); };
+        auto sync = [&] { named_bar_sync(2 + grp, 128); };
         const int g8 = lane >> 2, t4 = lane & 3;
         // d += X[xr.., xc..] Y[yr.., yc..], 16 x 16 by 16 x 8, both in the scratch. What is not A itself is rounded to tf32
         // as it is put there; A is cut off, by 2^-11 of it in the mean.
         auto product = [&](float(&d)[4], int xr, int xc, int yr, int yc) {
+            const uint32_t x = at(xr + g8, xc + t4), xd = 32 * (xr < 32 ? Lay::LD0 : Lay::LD1), y = at(yr + t4, yc + g8), yd = 16 * (yr < 32 ? Lay::LD0 : Lay::LD1);
 #pragma unroll
-            for (int k = 0; k < 16; k += 8) {
-                const uint32_t a[4] = {bits(A(xr + g8, xc + k + t4)), bits(A(xr + g8 + 8, xc + k + t4)), bits(A(xr + g8, xc + k + t4 + 4)),
-                                       bits(A(xr + g8 + 8, xc + k + t4 + 4))};
-                mma_tf32(d, a, bits(A(yr + k + t4, yc + g8)), bits(A(yr + k + t4 + 4, yc + g8)));
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t a[4] = {SM_AT(uint32_t, x + 32 * k), SM_AT(uint32_t, x + xd + 32 * k), SM_AT(uint32_t, x + 32 * k + 16), SM_AT(uint32_t, x + xd + 32 * k + 16)};
+                mma_tf32(d, a, SM_AT(uint32_t, y + 2 * k * yd), SM_AT(uint32_t, y + (2 * k + 1) * yd));
             }
         };
         auto put = [&](const float(&d)[4], int r, int c, float f) {
-            SM_AT(uint2, scr + 4 * ((r + g8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[0]), tf32(f * d[1]));
-            SM_AT(uint2, scr + 4 * ((r + g8 + 8) * Lay::LD + c + 2 * t4)) = make_uint2(tf32(f * d[2]), tf32(f * d[3]));
+            SM_AT(uint2, at(r + g8, c + 2 * t4)) = make_uint2(tf32(f * d[0]), tf32(f * d[1]));
+            SM_AT(uint2, at(r + g8 + 8, c + 2 * t4)) = make_uint2(tf32(f * d[2]), tf32(f * d[3]));
         };
+        if (grp) rg.next();
 #pragma unroll 1
-        for (int n = 0; n < nch; ++n, rg.next()) {
-            const uint32_t s = sc(n), t0 = tt(rg);
+        for (int n = grp; n < nch; n += 2) {
+            const uint32_t s = sc(n), t0 = tt(n);
             // where T[i][j] stands as an operand, times its column's step
             auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
             auto put_t = [&](const float(&d)[4], int r, int c) {
@@ -702,12 +708,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             };
             wait_w(Lay::FACT + rg.s, rg.par);
             const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
-            wait_w(Lay::G_DONE, n & 1);
+            wait_w(Lay::G_DONE + (n & 1), (n >> 1) & 1);
             tc::fence_after();
-            // A and P up to their diagonal, 16 columns at a time: rows 0..31 have one block per warp, the others two
+            // A and P up to their diagonal, 16 columns at a time
             const int last = q < 2 ? i0 - 1 : i0;
 #pragma unroll 1
-            for (int b = (lo + 1) * 16 * hf; b < (lo + 1) * 16 * (hf + 1); b += 16) {
+            for (int b = 0; b < 32 * (lo + 1); b += 16) {
                 uint32_t r[16];
                 float2 w[8];
                 tc::ld16(lq + b, r);
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 if (q < 2) {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) SM_AT(float4, scr + 4 * (i0 * Lay::LD + b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
+                    for (int j = 0; j < 8; j += 2) SM_AT(float4, at(i0, b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; j += 4)
@@ -737,10 +743,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before();
             arrive_w(Lay::KQ_FREE);
             sync();
+            wait_w(Lay::T_EMPTY + (n & 1), ((n >> 1) & 1) ^ 1);  // T's buffer has been read up two chunks back
             // (I + A)^-1: diagonal blocks of 8, two per warp, a row per lane; then the block between them
-            if (hf == 0) {
+            {
                 const int d0 = 16 * q, d1 = d0 + (lane & 8), c = lane & 7;
                 // row c of the inverse, x (I + A) = e_c, from its last column to its first
+                const uint32_t ad = at(d1, d1), ld = 4 * (q < 2 ? Lay::LD0 : Lay::LD1);
                 float x[8];
 #pragma unroll
                 for (int j = 7; j >= 0; --j) {
@@ -748,9 +756,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                     for (int i = j + 1; i < 8; ++i)
                         if ((i - j) & 1)
-                            u = fmaf(-A(d1 + i, d1 + j), x[i], u);
+                            u = fmaf(-SM_AT(const float, ad + i * ld + 4 * j), x[i], u);
                         else
-                            w = fmaf(-A(d1 + i, d1 + j), x[i], w);
+                            w = fmaf(-SM_AT(const float, ad + i * ld + 4 * j), x[i], w);
                     x[j] = u + w;
                 }
                 __syncwarp();
@@ -759,7 +767,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 8; j += 4) {
                         const float4 b = SM_AT(const float4, s + SC_B + 4 * (d1 + j));
-                        SM_AT(uint4, scr + 4 * ((d1 + c) * Lay::LD + d1 + j)) = make_uint4(tf32(x[j]), tf32(x[j + 1]), tf32(x[j + 2]), tf32(x[j + 3]));
+                        SM_AT(uint4, at(d1 + c, d1 + j)) = make_uint4(tf32(x[j]), tf32(x[j + 1]), tf32(x[j + 2]), tf32(x[j + 3]));
                         o[j / 2] = pack_bf16(x[j] * b.x, x[j + 1] * b.y);
                         o[j / 2 + 1] = pack_bf16(x[j + 2] * b.z, x[j + 3] * b.w);
                     }
@@ -770,18 +778,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const uint32_t a[4] = {bits(A(d0 + 8 + g8, d0 + t4)), 0u, bits(A(d0 + 8 + g8, d0 + t4 + 4)), 0u};
                 mma_tf32(d, a, bits(A(d0 + t4, d0 + g8)), bits(A(d0 + t4 + 4, d0 + g8)));
                 __syncwarp();
-                SM_AT(uint2, scr + 4 * ((d0 + 8 + g8) * Lay::LD + d0 + 2 * t4)) = make_uint2(tf32(d[0]), tf32(d[1]));
+                SM_AT(uint2, at(d0 + 8 + g8, d0 + 2 * t4)) = make_uint2(tf32(d[0]), tf32(d[1]));
                 __syncwarp();
                 const uint32_t h[4] = {bits(A(d0 + 8 + g8, d0 + 8 + t4)), 0u, bits(A(d0 + 8 + g8, d0 + 8 + t4 + 4)), 0u};
                 mma_tf32(e, h, bits(A(d0 + 8 + t4, d0 + g8)), bits(A(d0 + 8 + t4 + 4, d0 + g8)));
                 __syncwarp();
-                SM_AT(uint2, scr + 4 * ((d0 + 8 + g8) * Lay::LD + d0 + 2 * t4)) = make_uint2(tf32(-e[0]), tf32(-e[1]));
+                SM_AT(uint2, at(d0 + 8 + g8, d0 + 2 * t4)) = make_uint2(tf32(-e[0]), tf32(-e[1]));
                 const float2 b = SM_AT(const float2, s + SC_B + 4 * (d0 + 2 * t4));
                 SM_AT(uint32_t, t_at(d0 + 8 + g8, d0 + 2 * t4)) = pack_bf16(-e[0] * b.x, -e[1] * b.y);
             }
             sync();
             // the blocks below: -T_hi A_hl T_lo, first of 16 (eight columns per warp), then of 32
-            if (hf == 0) {
+            {
                 const int c0 = 32 * (q & 1), r0 = c0 + 16, n8 = 8 * (q >> 1);
                 float d[4] = {}, e[4] = {};
                 product(d, r0, c0, c0, c0 + n8);
@@ -794,22 +802,31 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             sync();
             {
-                const int mi = 16 * (w8 >> 2), ni = 8 * (w8 & 3);
-                float d[4] = {}, e[4] = {};
-                for (int k = ni & 16; k < 32; k += 16) {
-                    const bool below = k > (ni & 16);  // the block below the diagonal ones stands above them
-                    product(d, 32 + mi, k, below ? 0 : k, below ? 16 + ni : ni);
-                }
-                put(d, mi, 32 + ni, 1.f);
+                const int mi = 16 * (q >> 1), n0 = 8 * (q & 1);  // columns n0 .. and n0 + 16 ..
+                float d[2][4] = {}, e[2][4] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    for (int k = 16 * h; k < 32; k += 16) {
+                        const bool below = k > 16 * h;  // the block below the diagonal ones stands above them
+                        product(d[h], 32 + mi, k, below ? 0 : k, below ? 16 + n0 : n0 + 16 * h);
+                    }
                 sync();
-                for (int k = 0; k <= mi; k += 16) {
-                    const bool below = k < mi;
-                    product(e, below ? 32 : 32 + mi, below ? 48 : 32 + k, k, 32 + ni);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) put(d[h], 32 + mi, n0 + 16 * h, 1.f);  // over A, which has been read
+                sync();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    for (int k = 0; k <= mi; k += 16) {
+                        const bool below = k < mi;
+                        product(e[h], below ? 32 : 32 + mi, below ? 48 : 32 + k, 32 + k, n0 + 16 * h);
+                    }
+                    put_t(e[h], 32 + mi, n0 + 16 * h);
                 }
-                put_t(e, 32 + mi, ni);
             }
             tc::fence_async_smem();
             arrive_w(Lay::T_FULL + rg.s);
+            rg.next();
+            rg.next();
         }
     }
 
