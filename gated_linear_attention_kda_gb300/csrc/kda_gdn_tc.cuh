@@ -244,6 +244,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tma_load_3d(kq(rg) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
                 }
                 ++nk;
+                // a tile's buffer is free late, so the next ones are on their way to L2 by then
+                if (n + Lay::KQS < nch) {
+                    const int ahead = tok + Lay::KQS * C;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tma_prefetch_3d(&tk, 64 * c, hk, ahead);
+                        tma_prefetch_3d(&tq, 64 * c, hk, ahead);
+                        tma_prefetch_3d(&tv, 64 * c, h, ahead);
+                    }
+                }
                 if (!wait_bar(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flags)) break;
                 mbar_arrive_expect_tx(bar(vfull), Lay::VT);
 #pragma unroll
@@ -711,7 +721,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             wait_w(Lay::G_DONE + (n & 1), (n >> 1) & 1);
             tc::fence_after();
             // A and P up to their diagonal, 16 columns at a time
-            const int last = q < 2 ? i0 - 1 : i0;
 #pragma unroll 1
             for (int b = 0; b < 32 * (lo + 1); b += 16) {
                 uint32_t r[16];
@@ -725,15 +734,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 tc::wait_ld();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-                    if (b + 2 * j > last) w[j].x = 0.f;
-                    if (b + 2 * j + 1 > last) w[j].y = 0.f;
-                }
+                for (int j = 0; j < 8; ++j) w[j] = fmul2(fmul2(w[j], make_float2(fi, fi)), make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
                 if (q < 2) {
+                    // of what is not below the diagonal, only the upper right 8 x 8 of a diagonal block is read: zero
+                    const bool off = (i0 & ~7) == b;
+#pragma unroll
+                    for (int j = 4; j < 8; ++j) w[j] = off ? make_float2(0.f, 0.f) : w[j];
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) SM_AT(float4, at(i0, b + 2 * j)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
                 } else {
+                    if (b >= 32 * lo) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (b + 2 * j > i0) w[j].x = 0.f;
+                            if (b + 2 * j + 1 > i0) w[j].y = 0.f;
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; j += 4)
                         SM_AT(uint4, pt(rg) + i0 * 128 + ((((b >> 3) + (j >> 2)) ^ (i0 & 7)) << 4)) =

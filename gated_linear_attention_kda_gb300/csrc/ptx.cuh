@@ -97,6 +97,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
                  : "memory");
 }
 
+// The same box into L2 only, ahead of its load.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *m, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1),
+                 "r"(c2)
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- named barriers
 // TMA tile store from shared memory (bulk-group completion); coordinates as for tma_load_3d.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, uint32_t src, int c0, int c1, int c2)
