@@ -89,8 +89,10 @@ struct Runs {
     // the run that holds slice x
     __device__ __forceinline__ uint32_t of(long long x) const
     {
-        uint32_t w = min(static_cast<uint32_t>(quotient(x, each)), count - 1);  // too far by what the rest adds
-        while (start(w) > x) --w;
+        // nearly: a float's rounding is off by less than one of a few thousand runs
+        uint32_t w = min(static_cast<uint32_t>(__fdividef(static_cast<float>(x) * static_cast<float>(count), static_cast<float>(total))), count - 1);
+        while (w > 0 && start(w) > x) --w;
+        while (w + 1 < count && start(w + 1) <= x) ++w;
         return w;
     }
 };
