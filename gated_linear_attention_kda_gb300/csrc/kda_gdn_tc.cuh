@@ -112,7 +112,7 @@ __device__ __forceinline__ void wait_or_flag(uint32_t b, uint32_t par, uint32_t 
                  "W%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1, %3;\n\t@p bra D%=;\n\t"
                  "ld.volatile.shared.u32 f, [%2];\n\tsetp.eq.u32 p, f, 0;\n\t@p bra W%=;\n"
                  "D%=:\n\t}" ::"r"(b),
-                 "r"(par), "r"(flag), "r"(WAIT_HINT_NS)
+                 "r"(par), "r"(flag), "r"(2000)  // ns that a poll may last
                  : "memory");
 }
 
