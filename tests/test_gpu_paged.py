@@ -362,3 +362,87 @@ def test_one_layers_step_in_a_graph(kda):
         assert (qr.double() - y).abs().max() <= 2.0 ** -7 * y.abs().max()
         exp, _, mag, size = ref.attn_step(qr, kc, vc, table, pos, D ** -0.5)
         assert ((out.double() - exp).abs() <= 2.0 ** -8 * exp.abs() + (2.0 ** -8 + 2.0 ** -16 * size[..., None]) * mag).all()
+
+
+def test_two_graphs_may_share_a_workspace(kda):
+    """Captured calls replayed one after the other on one stream, each over its own cache."""
+    g, H, HK, D = gen(18), 8, 2, 64
+    ws = torch.empty(kda.attn_step_workspace_bytes(4, H, HK, D), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for lens, page in (([900, 3, 40, 0], 16), ([5000], 128)):
+        table, total = pages(g, lens, page)
+        kc, vc = caches(g, total, HK, page, D)
+        q, pos = randn(g, len(lens), H, D), torch.tensor(lens, device="cuda") - 1
+        out, ls = torch.empty_like(q), torch.empty(len(lens), H, device="cuda")
+        kda.attn_step(q, kc, vc, table, pos, out, 0.125, ls, ws)
+        torch.cuda.synchronize()
+        want = out.clone(), ls.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            kda.attn_step(q, kc, vc, table, pos, out, 0.125, ls, ws)
+        graphs.append((graph, out, ls, want, (kc, vc, q)))
+    for _ in range(3):
+        for graph, out, ls, _, _ in graphs:
+            out.zero_()
+            ls.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    kda.check_device_status()
+    for _, out, ls, want, _ in graphs:
+        assert torch.equal(out, want[0]) and torch.equal(ls, want[1])
+
+
+def test_attn_step_same_call_same_bits(kda):
+    """Cuts follow the lengths alone and are joined in order: a call repeats its bits, also on another stream."""
+    g = gen(19)
+    lens = [3000, 17, 640]
+    table, total = pages(g, lens, 32)
+    kc, vc = caches(g, total, 4, 32, 128)
+    q, pos = randn(g, 3, 16, 128), torch.tensor(lens, device="cuda") - 1
+    ws = torch.empty(kda.attn_step_workspace_bytes(3, 16, 4, 128), dtype=torch.uint8, device="cuda")
+    outs = []
+    side = torch.cuda.Stream()
+    for s in (torch.cuda.current_stream(), side, side, torch.cuda.current_stream()):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            out = torch.empty_like(q)
+            kda.attn_step(q, kc, vc, table, pos, out, 0.09, workspace=ws)
+        torch.cuda.synchronize()
+        outs.append(out)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_workspace_too_small_is_refused(kda):
+    g = gen(20)
+    table, total = pages(g, [5], 8)
+    kc, vc = caches(g, total, 1, 8, 64)
+    q, pos = randn(g, 1, 1, 64), torch.tensor([4], device="cuda")
+    n = kda.attn_step_workspace_bytes(1, 1, 1, 64)
+    assert n > 0 and kda.attn_step_workspace_bytes(500, 64, 8, 64) == n  # whatever the sizes
+    with pytest.raises(ValueError, match="workspace of"):
+        kda.attn_step(q, kc, vc, table, pos, q.clone(), 1.0, workspace=torch.empty(n - 16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_attn_step_random_shapes(kda, seed):
+    import random
+    r = random.Random(seed)
+    S, HK, D, page = r.randint(1, 9), r.choice([1, 2, 3, 8]), r.choice([64, 128]), r.choice([8, 16, 64, 256])
+    lens = [r.choice([0, 1, 15, 16, 17, r.randint(1, 3000)]) for _ in range(S)]
+    g = gen(100 + seed)
+    table, total = pages(g, lens, page)
+    kc, vc = caches(g, total, HK, page, D, joint=r.random() < 0.5)
+    check_attn(kda, randn(g, S, HK * r.choice([1, 3, 8, 17]), D), kc, vc, table, torch.tensor(lens, device="cuda") - 1, D ** -0.5, r.random() < 0.8, r.random() < 0.7)
+
+
+def test_layers_hand_their_states_from_a_prompt_to_steps(kda):
+    """examples/delta_attention_layers.py: prompts, then single tokens, against one longer prompt. Prompts go through the
+    chunks of the delta rule (seven roundings), steps through fp32; convolution, norms, projections, weights and outputs
+    round alike in number but not in place. Some sixteen roundings of at most 2^-8 that add as squares."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "delta_attention_layers.py")
+    spec = importlib.util.spec_from_file_location("delta_attention_layers", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.main() <= 4 * 2.0 ** -8
