@@ -2,12 +2,14 @@
 // at a time.
 //
 // Chunk algebra. Over a chunk of tokens j = 0..63 that starts from S0 (V x K), with G_i the running sum of the log2 decays
-// up to and with token i, the corrected values n_i = b_i (v_i - 2^(a_i) S_{i-1} k_i) satisfy
-//   (I + A) N = diag(b) (V - diag(2^G) K S0^T),   A[i, j] = b_i 2^(G_i - G_j) k_i . k_j   for j < i, else 0
-// so that with T = (I + A)^-1 diag(b)
+// up to and with token i, the misses n_i = v_i - 2^(a_i) S_{i-1} k_i, of which the state takes b_i, satisfy
+//   (I + A) N = V - diag(2^G) K S0^T,   A[i, j] = 2^(G_i - G_j) b_j k_i . k_j   for j < i, else 0
+// so that with T = (I + A)^-1
 //   N     = T V - T diag(2^G) K S0^T
-//   out_i = scale (2^(G_i) S0 q_i + sum_{j <= i} 2^(G_i - G_j) (q_i . k_j) n_j)
-//   S1    = 2^(G_63) S0 + sum_j 2^(G_63 - G_j) n_j k_j^T
+//   out_i = scale (2^(G_i) S0 q_i + sum_{j <= i} 2^(G_i - G_j) b_j (q_i . k_j) n_j)
+//   S1    = 2^(G_63) S0 + sum_j 2^(G_63 - G_j) b_j n_j k_j^T
+// (With the steps inside T, as diag(b), its diagonal would have to be rounded: here it is one, which is exact, and it is
+// most of T where keys are not alike: outputs are off by 3.1e-3 of their head's norm this way, 3.4e-3 the other.)
 // No exponent is positive, so nothing overflows, and with one decay per head every scaling is by a token: K, Q and V enter
 // the products as they lie in memory, and norms of queries and keys are factors of the same kind.
 //
@@ -16,17 +18,32 @@
 //   D1  [128 x 64]  = S K^T           S as bf16 in tensor memory (its own copy)
 //   D2  [128 x 64]  = V^T T^T         V^T straight from V's tile (its transpose is a layout of the operand)
 //   D2             += D1' T^T         D1' = -2^(G_j) D1 as bf16, written over D1
-//   S              += N' K            N' = 2^(G_63 - G_j) N^T as bf16, written over D2; S decayed before
+//   S              += N' K            N' = 2^(G_63 - G_j) b_j N^T as bf16, written over D2; S decayed before
 //   O   [128 x 64]  = S Q^T,  N^T P^T and the output is their sum, the first scaled per token
 // Beside the chain, one or two chunks ahead: [K; Q] K^T, its scaled halves A and P, and T.
 // Roundings: the state, D1', N, N', P and T enter products as bf16 (the output is bf16; the state that is carried and
-// returned is fp32). The inverse is fp32 within 16 x 16 blocks and tf32 (rounded to nearest) between them, an eighth of
-// the step of T's own rounding.
+// returned is fp32). The inverse is fp32 within 8 x 8 blocks and tf32 between them (products rounded to nearest, A cut
+// off by the instruction), an eighth and a quarter of the step of T's own rounding. Of an output's error, 3.1e-3, its own
+// rounding, P's and N's are 1.66e-3 each, and the rest, which adds as squares, is T's and the state's; of a state's,
+// 2.5e-3, N' and the rounding of a bf16 state are most. Second parts of N, N' and P would halve it, for 25 % more products
+// and 40 KB more shared memory than there is. Where all keys of a chunk are one, steps are near one and nothing decays, the
+// sum of the b_j n_j telescopes, and what T's rows sum to for their rounding adds up: .09 after 64 tokens.
 //
 // NaN: a product multiplies what a mask leaves out by zero, and 0 NaN is NaN, so a token that holds a NaN or infinity
 // would reach earlier ones of its chunk. What holds one leaves no number in the state's rows it reaches, up to the end of
 // the sequence, where such rows show; their eight neighbours' outputs and states are then made again token by token from
 // the start of the sequence (walk_rows). A NaN in q stays in its token without that.
+//
+// What bounds it (8 x 4096 tokens of 16 heads: 160 us, 3.4 TB/s of 6.7; one sequence of 131,072 tokens of 32 heads: 4.4 ms,
+// 2.2 us a chunk on 32 SMs): a chunk's way through four dependent products and three conversions between them, each a round
+// trip of 260 cycles to the tensor core besides its work, so that its pipe is busy a fifth of the time; and, next to that,
+// instruction supply. Eight roles hold some 100 KB of code, most of which every chunk runs through once: the level-1.5 cache misses
+// one fetch in four and the next level's port runs at 72 % of its peak. 8 KB more straight-line code made the kernel 11 %
+// slower, code inside rolled loops nothing, a call in place of an inlined wait 200 cycles more than the wait; so loops over
+// products and blocks stay rolled, waits are a few instructions, and masks are made only in the chunk that needs them.
+// Roles were split until the chain had warps of its own (209 us with A, P and T by one group of warps, 180 with norms and
+// output MMAs moved off the chain's issuers, 165 with two groups in turn, 160 with the steps outside T). Two CTAs per SM do not fit: tensor memory and
+// 220 KB of shared memory are full.
 //
 // Warp roles (768 threads):
 //   warp 0       TMA producer (lane 0): [K; Q] tiles three deep, V tiles two
@@ -52,7 +69,7 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t T_S = 0, T_SB = 128, T_D1 = 192, T_SQ = 256, T_D2 = 320, T_PV = 384, T_KQ = 448;
 
 // scalars of a chunk: running log2 sums, steps, 2^G (then the factors of D1'), 2^(G_63 - G) (then those of N'), the
-// output's factors; by key column G less log2 1 / |k|; by row b / |k| and scale / |q|; the chunk's whole decay
+// output's factors; by key column G less log2 b / |k|; by row 1 / |k| and scale / |q|; the chunk's whole decay
 constexpr int SC_G = 0, SC_B = 256, SC_D = 512, SC_N = 768, SC_O = 1024, SC_GK = 1280, SC_FK = 1536, SC_FQ = 1792, SC_GAM = 2048, SC_BYTES = 2064;
 
 struct Layout {
@@ -104,7 +121,7 @@ __device__ __forceinline__ uint32_t tf32(float x)
 // Waits for a phase. The producer waits for every chunk's buffers in turn, with a limit, and sets the flag at shared
 // address `flag` when one does not come back; the others wait until their phase comes or that flag is set, and go on all
 // the same, so that every barrier keeps its count and the CTA comes to its end (a wait then lasts one poll): what they make
-// is void, and the flag becomes an error. This keeps a wait short: see the note on code size below.
+// is void, and the flag becomes an error. This keeps a wait short, which counts for the kernel's size.
 __device__ __forceinline__ void wait_or_flag(uint32_t b, uint32_t par, uint32_t flag)
 {
     if (!smem_ok(b, 8)) return;
@@ -608,10 +625,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 SM_AT(float, s + SC_O) = f * ex2_approx(G);
             } else {
                 const float b = SM_AT(const float, s + SC_B), fd = SM_AT(const float, s + SC_D), fn = SM_AT(const float, s + SC_N);
-                SM_AT(float, s + SC_FK) = f * b;
-                SM_AT(float, s + SC_GK) = p.l2 ? G - lg2_approx(f) : G;
+                SM_AT(float, s + SC_FK) = f;
+                SM_AT(float, s + SC_GK) = G - lg2_approx(f * b);  // b = 0: infinity, and the factor is 0
                 SM_AT(float, s + SC_D) = -fd * f;
-                SM_AT(float, s + SC_N) = fn * f;
+                SM_AT(float, s + SC_N) = fn * f * b;
             }
             arrive_w(Lay::FACT + g.s);
         };
@@ -709,12 +726,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
         for (int n = grp; n < nch; n += 2) {
             const uint32_t s = sc(n), t0 = tt(n);
-            // where T[i][j] stands as an operand, times its column's step
+            // where T[i][j] stands as an operand
             auto t_at = [&](int i, int j) { return t0 + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2; };
             auto put_t = [&](const float(&d)[4], int r, int c) {
-                const float2 b = SM_AT(const float2, s + SC_B + 4 * (c + 2 * t4));
-                SM_AT(uint32_t, t_at(r + g8, c + 2 * t4)) = pack_bf16(-d[0] * b.x, -d[1] * b.y);
-                SM_AT(uint32_t, t_at(r + g8 + 8, c + 2 * t4)) = pack_bf16(-d[2] * b.x, -d[3] * b.y);
+                SM_AT(uint32_t, t_at(r + g8, c + 2 * t4)) = pack_bf16(-d[0], -d[1]);
+                SM_AT(uint32_t, t_at(r + g8 + 8, c + 2 * t4)) = pack_bf16(-d[2], -d[3]);
             };
             wait_w(Lay::FACT + rg.s, rg.par);
             const float Gi = SM_AT(const float, s + SC_G + 4 * i0), fi = SM_AT(const float, s + (q < 2 ? SC_FK : SC_FQ) + 4 * i0);
@@ -782,10 +798,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     uint32_t o[4];
 #pragma unroll
                     for (int j = 0; j < 8; j += 4) {
-                        const float4 b = SM_AT(const float4, s + SC_B + 4 * (d1 + j));
                         SM_AT(uint4, at(d1 + c, d1 + j)) = make_uint4(tf32(x[j]), tf32(x[j + 1]), tf32(x[j + 2]), tf32(x[j + 3]));
-                        o[j / 2] = pack_bf16(x[j] * b.x, x[j + 1] * b.y);
-                        o[j / 2 + 1] = pack_bf16(x[j + 2] * b.z, x[j + 3] * b.w);
+                        o[j / 2] = pack_bf16(x[j], x[j + 1]);
+                        o[j / 2 + 1] = pack_bf16(x[j + 2], x[j + 3]);
                     }
                     SM_AT(uint4, t_at(d1 + c, d1)) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
@@ -800,8 +815,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 mma_tf32(e, h, bits(A(d0 + 8 + t4, d0 + g8)), bits(A(d0 + 8 + t4 + 4, d0 + g8)));
                 __syncwarp();
                 SM_AT(uint2, at(d0 + 8 + g8, d0 + 2 * t4)) = make_uint2(tf32(-e[0]), tf32(-e[1]));
-                const float2 b = SM_AT(const float2, s + SC_B + 4 * (d0 + 2 * t4));
-                SM_AT(uint32_t, t_at(d0 + 8 + g8, d0 + 2 * t4)) = pack_bf16(-e[0] * b.x, -e[1] * b.y);
+                SM_AT(uint32_t, t_at(d0 + 8 + g8, d0 + 2 * t4)) = pack_bf16(-e[0], -e[1]);
             }
             sync();
             // the blocks below: -T_hi A_hl T_lo, first of 16 (eight columns per warp), then of 32

@@ -308,20 +308,20 @@ def test_gdn_many_states_than_sms(kda):
 
 def test_gdn_repeated_keys(kda):
     """The worst that the roundings meet: one key for all tokens, steps b near one and no decay. A head's state is then k s^T
-    with s the last value almost, and s_i = s_0 + sum_{j <= i} N_j, N_j = sum_l T[j, l] (v_l - s_0) telescopes: what N_j adds
-    N_{j+1} takes back. The inverse is known, T[j, j] = b and T[j, l] = -b^2 (1 - b)^(j - l - 1), so its rounding to bf16 is
-    too. Its rows no longer sum to about nothing: with b = sigmoid(6) what is off is .0025 of s_0 a token, .15 of it after a
-    chunk. That has to be all beside the roundings of N and of P, 1.66e-3 of |N_j| = 2^0.5 |v| each in the mean square, which
+    with s the last value almost, and s_i = s_0 + sum_{j <= i} b n_j, n_j = sum_l T[j, l] (v_l - s_0) telescopes: what n_j
+    adds n_{j+1} takes back. The inverse is known, T[j, j] = 1 and T[j, l] = -b (1 - b)^(j - l - 1), so its rounding to bf16 is
+    too. Its rows no longer sum to about nothing: with b = sigmoid(6) what is off is .0014 of s_0 a token, .09 of it after a
+    chunk. That has to be all beside the roundings of N and of P, 1.66e-3 of |n_j| = 2^0.5 |v| each in the mean square, which
     add up over i <= 64 tokens: 1.66e-3 (2 * 2 * 64)^0.5 = .0266, on top of REL."""
     d = make(1, 200, 2, 1, seed=41, gate=-20.0)
     d["k"][:] = d["k"][:, :1].clone()
     d["beta"][:] = 6.0
     out, fin = run(kda, d)
     exp, efin = want(d)
-    assert (out.double() - exp).norm() <= .15 * exp.norm()
+    assert (out.double() - exp).norm() <= .1 * exp.norm()
     b = torch.sigmoid(torch.tensor(6.0, dtype=torch.float64))
     m = torch.arange(64)[:, None] - torch.arange(64)
-    T = torch.where(m == 0, b, torch.where(m > 0, -b * b * (1 - b) ** (m - 1).clamp(min=0), 0.0)).to(BF16).double().cuda()
+    T = torch.where(m == 0, 1.0, torch.where(m > 0, -b * (1 - b) ** (m - 1).clamp(min=0), 0.0)).to(BF16).double().cuda()
     k, q = d["k"].double()[0, :, 0], d["q"].double()[0, :, 0]
     kk = k / k.pow(2).sum(-1, keepdim=True).add(1e-6).sqrt()
     qq = q / q.pow(2).sum(-1, keepdim=True).add(1e-6).sqrt()
@@ -330,7 +330,7 @@ def test_gdn_repeated_keys(kda):
         s, rows = torch.zeros(128, dtype=torch.float64, device="cuda"), []
         for c in range(0, 200, 64):
             x = v[c:c + 64, h] - s
-            at = s + (T[:len(x), :len(x)] @ x).cumsum(0)
+            at = s + b.cuda() * (T[:len(x), :len(x)] @ x).cumsum(0)
             rows.append(p[c:c + 64, None] * at)
             s = at[-1]
         rows = torch.cat(rows)
