@@ -6,6 +6,8 @@
 // are taken from the old row, together. A warp owns ROWS rows, four of the 128 key channels per lane, in fp32 registers
 // from the first token to the last; the 2 ROWS sums go through a reduce-scatter butterfly (sixteen exchanges for eight
 // rows), after which the rows' n are handed back to all lanes.
+// Bound by the state's bytes for single tokens: 128 sequences of 16 heads, 268 MB of fp32 state read and written, take
+// 40.5 us on the device, 6.6 TB/s, what a copy reaches. Over more tokens the sums bound it, 0.35 us a token and more.
 #pragma once
 #include "blk_common.cuh"
 

@@ -7,6 +7,8 @@
 // a radian. The turn is therefore counted in whole turns, as a 64-bit fixed-point fraction: inv_freq / (2 pi) is an
 // integer F of 2^-64 turns, position F wraps as turns do, and its upper 32 bits are the angle. F is off by at most one
 // unit, so a position below 2^31 is off by less than 2^-33 turns; no 64-bit floating point is needed.
+// Bound by HBM where there are many tokens: 32,768 of 20 heads of 128 take 63.5 us, 5.3 TB/s; 65,519 packed ones appended
+// with 8 key heads of 128, .54 GB, 92 us, 5.8 TB/s. For single tokens the launch and one chain of loads are all: 6 us.
 #pragma once
 #include "blk_common.cuh"
 
