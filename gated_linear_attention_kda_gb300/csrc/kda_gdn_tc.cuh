@@ -36,11 +36,11 @@
 //
 // What bounds it (8 x 4096 tokens of 16 heads: 160 us, 3.4 TB/s of 6.7; one sequence of 131,072 tokens of 32 heads: 4.4 ms,
 // 2.2 us a chunk on 32 SMs): a chunk's way through four dependent products and three conversions between them, each a round
-// trip of 260 cycles to the tensor core besides its work, so that its pipe is busy a fifth of the time; and, next to that,
-// instruction supply. Eight roles hold some 100 KB of code, most of which every chunk runs through once: the level-1.5 cache misses
-// one fetch in four and the next level's port runs at 72 % of its peak. 8 KB more straight-line code made the kernel 11 %
-// slower, code inside rolled loops nothing, a call in place of an inlined wait 200 cycles more than the wait; so loops over
-// products and blocks stay rolled, waits are a few instructions, and masks are made only in the chunk that needs them.
+// trip of 260 cycles to the tensor core besides its work, so that its pipe is busy 30 % of the time; and, next to that,
+// instruction supply. Eight roles hold some 100 KB of code, most of which every chunk runs through once: the SM's own cache
+// misses one fetch in seven and the port of the one behind it runs at 83 % of its peak. 8 KB more straight-line code made
+// the kernel 11 % slower, code inside rolled loops nothing, a call in place of an inlined wait 200 cycles more than the wait;
+// so loops over products and blocks stay rolled, waits are a few instructions, and masks are made only where they are read.
 // Roles were split until the chain had warps of its own (209 us with A, P and T by one group of warps, 180 with norms and
 // output MMAs moved off the chain's issuers, 165 with two groups in turn, 160 with the steps outside T). Two CTAs per SM do not fit: tensor memory and
 // 220 KB of shared memory are full.
