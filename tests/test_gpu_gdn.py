@@ -336,3 +336,21 @@ def test_gdn_repeated_keys(kda):
         rows = torch.cat(rows)
         assert (out[0, :, h].double() - rows).norm() <= (REL + .0266) * rows.norm()
         assert (fin[0, h].double() - torch.outer(s, kk[0])).norm() <= (REL + .0266) * s.norm()
+
+
+@pytest.mark.parametrize("beta", [-200.0, -60.0, 60.0, float("inf"), float("-inf")])
+@pytest.mark.parametrize("l2", [True, False])
+def test_gdn_steps_at_their_ends(kda, beta, l2):
+    """Steps of 0 and 1 among ordinary ones: a step of 0 leaves the state to its decay, and no logarithm of it shows."""
+    d = make(1, 150, 2, 1, seed=43, init=F32, l2=l2)
+    d["beta"][:, ::3] = beta
+    out, fin = run(kda, d)
+    exp, efin = want(d)
+    check(out, fin, exp, efin, [(0, 150)])
+    d["beta"][:] = beta
+    out, fin = run(kda, d)
+    exp, efin = want(d)
+    if beta < 0:  # outputs are the decayed state's alone
+        assert torch.isfinite(out).all() and (fin.double() - efin).norm() <= REL * efin.norm() + 1e-30
+    else:
+        check(out, fin, exp, efin, [(0, 150)])
