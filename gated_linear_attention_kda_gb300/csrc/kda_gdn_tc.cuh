@@ -38,16 +38,18 @@
 // 2.1 us a chunk on 32 SMs). Three loops of 4,500 to 4,700 cycles a chunk, about even by the clocks of their steps: the chain
 // (S to bf16 500, D1 1,350, D1' 400, N 1,100, N' 450, S 700); the scores' one accumulator (product 1,600 from the wait on,
 // read 3,050 by the warps with four blocks of columns); and, over two chunks, a tile's way from its load over the norms and
-// the scores to T (inverse 3,500). The tensor pipe is busy 30 % of the time. Next to that, instruction supply: eight roles
-// hold some 100 KB of code, most of which every chunk runs through once; the SM's own cache misses one fetch in seven and the
+// the scores to T (inverse 3,500). The tensor pipe is busy 30 % of the time. Next to that, instruction supply: the
+// roles' loops hold some 40 KB of code (chain and its issuer 9, the other issuers and decays 9, output and norms 10, A, P
+// and T 13), which every chunk runs through once; the SM's own cache misses one fetch in seven and the
 // port of the one behind it runs at 83 % of its peak. 8 KB more straight-line code on the chain made the kernel 11 % slower,
-// a call in place of an inlined wait 200 cycles more than the wait; so loops over products stay rolled, waits are a few
-// instructions, and masks are made only where they are read. Against 162 us in one run: the inverse's products rolled as
-// well 164 to 176; scores read a block ahead of their use, which frees the accumulator sooner, 176; their factors outside
-// diagonal blocks as a row's times a column's, which saves 30 of 64 exponentials, 184.
+// unrolling the eight products of one issuer 5 %, a call in place of an inlined wait costs 200 cycles more than the wait; so
+// loops over products stay rolled, waits are a few instructions, and masks are made only where they are read. Against 162 us
+// in one run: the inverse's products rolled as well 164 to 176; scores read a block ahead of their use, which frees the
+// accumulator sooner, 176; their factors outside diagonal blocks as a row's times a column's, which saves 30 of 64
+// exponentials, 184.
 // Roles were split until the chain had warps of its own (209 us with A, P and T by one group of warps, 180 with norms and
-// output MMAs moved off the chain's issuers, 165 with two groups in turn, 160 with the steps outside T). Two CTAs per SM do not fit: tensor memory and
-// 220 KB of shared memory are full.
+// output MMAs moved off the chain's issuers, 165 with two groups in turn, 160 with the steps outside T). Two CTAs per SM do
+// not fit: tensor memory and 220 KB of shared memory are full.
 //
 // Warp roles (768 threads):
 //   warp 0       TMA producer (lane 0): [K; Q] tiles three deep, V tiles two
