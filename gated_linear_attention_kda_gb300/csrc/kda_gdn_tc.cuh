@@ -149,8 +149,8 @@ __device__ __forceinline__ float softplus_fast(float u)
     return u > 0.f ? u + l : l;
 }
 
-// The rows of a sequence that hold no numbers at its end, made again: rows 8 g .. 8 g + 7 for every set bit of `groups`.
-__device__ __noinline__ void redo_rows(const GdnParams &p, int seq, int h, const Span &sp, uint32_t groups)
+// Rows of a sequence token by token: rows 8 g .. 8 g + 7 for every set bit of `groups`.
+__device__ __noinline__ void walk_groups(const GdnParams &p, int seq, int h, const Span &sp, uint32_t groups)
 {
     for (int g = threadIdx.x >> 5; g < DH / gdn::ROWS; g += NTHREADS / 32)
         if (groups >> g & 1) gdn::walk_rows(p, seq, h, sp, gdn::ROWS * g);
@@ -169,8 +169,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int h = blockIdx.x % p.H, slot = blockIdx.x / p.H, hk = h / (p.H / p.HK);
     const int seq = p.cu && p.nseq <= LPT_MAX_SEQS ? ssmtc::longest_first(p, slot) : slot;
     if (p.cu && blockIdx.x == 0) blk::check_bounds(p.cu, p.nseq, p.total);
-    const Span sp = gdn::gdn_span(p, seq);
+    Span sp = gdn::gdn_span(p, seq);
     if (!sp.ok) return;  // CTA-uniform, before any tensor memory is taken
+    if (sp.len <= gdn::STEP_TOKENS) {  // as uniform; a packed call's short sequences are answered as they are alone
+        if (!p.split) walk_groups(p, seq, h, sp, (1u << (DH / gdn::ROWS)) - 1u);
+        return;
+    }
+    // (the compiler is not told that there are chunks: with that it lays the loops out another way, 2.5 % slower)
+    asm volatile("" : "+r"(sp.len));
     const int nch = (sp.len + C - 1) / C;
 
     volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
@@ -242,7 +248,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     // the products of an issuer that are still on their way when its loop is left
     auto finish = [&](int b) {
-        if (nch == 0) return;
         tc::commit_w(bar(b));
         if (lane == 0) drain_bar(bar(b), 0);
         __syncwarp();
@@ -487,16 +492,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 o[i / 2 + 1] = pack_bf16(y.x, y.y);
             }
         };
-        if (nch > 0) {
 #pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                uint32_t r[32];
-                load_init(32 * g, r);
-                __syncwarp();
-                tc::st32(ls + 32 * g, r);
-            }
-            tc::wait_st();
+        for (int g = 0; g < 2; ++g) {
+            uint32_t r[32];
+            load_init(32 * g, r);
+            __syncwarp();
+            tc::st32(ls + 32 * g, r);
         }
+        tc::wait_st();
         // Loops are left rolled here and below: the roles' code together is larger than the instruction caches next to the
         // schedulers, and what is fetched twice costs more than a branch.
 #pragma unroll 1
@@ -560,32 +563,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::fence_before();
             arrive_w(Lay::N_GO);
         }
-        if (nch > 0) wait_w(Lay::S_DONE, (nch - 1) & 1);
+        wait_w(Lay::S_DONE, (nch - 1) & 1);
         tc::fence_after();
-        if (nch > 0) {
-            float2 z = make_float2(0.f, 0.f);  // 0 NaN and 0 inf are NaN
+        float2 z = make_float2(0.f, 0.f);  // 0 NaN and 0 inf are NaN
 #pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
-                uint32_t r[32];
-                tc::ld32(ls + 32 * g, r);
-                tc::wait_ld();
+        for (int g = 0; g < 2; ++g) {
+            uint32_t r[32];
+            tc::ld32(ls + 32 * g, r);
+            tc::wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) z = ffma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(0.f, 0.f), z);
-            }
-            if (!(z.x + z.y == 0.f)) atomicOr(&spoilt, 1u << (v / gdn::ROWS));
+            for (int i = 0; i < 32; i += 2) z = ffma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(0.f, 0.f), z);
         }
+        if (!(z.x + z.y == 0.f)) atomicOr(&spoilt, 1u << (v / gdn::ROWS));
         named_bar_sync(4 + q, 64);  // both halves of these rows have been looked at
         if (p.fin) {
             const bool number = !(*const_cast<volatile uint32_t *>(&spoilt) >> (v / gdn::ROWS) & 1u);  // else made again at the end
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
                 uint32_t r[32];
-                if (nch > 0) {  // every lane of the warp takes part in the load
-                    tc::ld32(ls + 32 * g, r);
-                    tc::wait_ld();
-                } else {
-                    load_init(32 * g, r);
-                }
+                tc::ld32(ls + 32 * g, r);  // every lane of the warp takes part in the load
+                tc::wait_ld();
                 if (number) store_fin(32 * g, r);
                 __syncwarp();
             }
@@ -870,7 +867,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __syncthreads();
     if (*flags && threadIdx.x == 0) atomicOr(&g_dev_error, DEVERR_TIMEOUT);
     const uint32_t groups = spoilt;
-    if (groups) redo_rows(p, seq, h, sp, groups);
+    if (groups) walk_groups(p, seq, h, sp, groups);
     if (warp == 0) {
         __syncwarp();
         tc::fence_after();

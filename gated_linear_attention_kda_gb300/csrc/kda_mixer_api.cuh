@@ -81,11 +81,6 @@ static kda_status launch_gdn_steps(const gdn::GdnParams &p, cudaStream_t s)
     return blk::launched("gated delta rule step");
 }
 
-// Up to this many tokens per sequence the token-by-token kernel answers sooner than the chunked one, at every size. us for
-// 8 tokens: 6.7 against 12.6 (1 sequence of 8 heads), 10.6 against 13.9 (8 of 16), 59 against 93 (64 of 16); for 12: 14.3
-// against 13.8 (8 of 16); for 16: 11.4 against 12.9, and 105 against 93 (64 of 16). It is also the more exact one.
-constexpr int64_t STEP_TOKENS = 8;
-
 static kda_status launch_gdn_tc(const gdn::GdnParams &p, cudaStream_t s)
 {
     CUtensorMap mq, mk, mv, mo;
@@ -235,7 +230,15 @@ KDA_API kda_status kda_gdn(const void *q, int64_t q_stride, const void *k, int64
     if (const kda_status st = bufs.check_out({"initial_state", state_block(initial_state, initial_dtype)}); st != KDA_OK) return st;
     if (const kda_status st = bufs.check_state({"final_state", state_block(final_state, final_dtype)}); st != KDA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return total <= (cu_seqlens ? 1 : nseq) * mix::STEP_TOKENS ? mix::launch_gdn_steps(p, s) : mix::launch_gdn_tc(p, s);
+    if (total <= (cu_seqlens ? 1 : nseq) * gdn::STEP_TOKENS) return mix::launch_gdn_steps(p, s);
+    // A packed call's short sequences are walked by the chunk kernel's CTAs, one to an SM, or, where the lengths are short in
+    // the mean, by a launch of their own ahead of it. us for 128 sequences of 16 heads, by the one and the other: single tokens
+    // 106, 52; 8 tokens each 227, 130; these and one of 1024 tokens 227, 175; 9 tokens each, where none is short, 134, 143. One of
+    // 4096 tokens and 128 single ones: 157 by the CTAs, no more than the 4096 alone.
+    p.split = cu_seqlens && total <= nseq * 2 * gdn::STEP_TOKENS;
+    if (p.split)
+        if (const kda_status st = mix::launch_gdn_steps(p, s); st != KDA_OK) return st;
+    return mix::launch_gdn_tc(p, s);
 }
 
 KDA_API kda_status kda_gdn_step(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,

@@ -56,8 +56,8 @@ def gdn(q, k, v, a, beta, scale, out, A_log, dt_bias=None, initial_state=None, f
     """Gated delta rule ``kda_gdn``: ``q``, ``k`` bf16 [B, T, HK, 128], ``v``, ``out`` bf16 [B, T, H, 128]
     (HK divides H; token-strided views allowed), ``a`` (before ``dt_bias`` and softplus) and ``beta``
     (before the sigmoid) bf16 [B, T, H], ``A_log``, ``dt_bias`` fp32 [H], states bf16/fp32
-    [B|N, H, 128, 128]. ``qk_l2norm`` normalises q and k per (token, head). Sequences of up to 8 tokens (packed
-    calls of up to 8) run in fp32, longer ones in chunks with bf16 operands. Returns ``(out, final_state)``."""
+    [B|N, H, 128, 128]. ``qk_l2norm`` normalises q and k per (token, head). Sequences of up to 8 tokens
+    run in fp32, longer ones in chunks with bf16 operands. Returns ``(out, final_state)``."""
     dev = _device("v", v, (4,), "[B, T, H, 128]")
     B, T = v.shape[:2]
     head, H, HK, K, V = _gdn_args(q, k, v, a, beta, scale, out, A_log, dt_bias, 2, dev)

@@ -531,8 +531,8 @@ KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void
  *   cu_seqlens, N  as kda_fwd's varlen mode (B == 1).
  *   flags    0 or KDA_FLAG_QK_L2NORM: q and k are used as
  *            x / sqrt(sum x^2 + 1e-6), formed in fp32.
- * Sequences of at most 8 tokens (varlen mode: calls of at most 8) go token by
- * token in fp32. Longer ones go 64 tokens at a time: operands of the products
+ * Sequences of at most 8 tokens go token by token in fp32, beside longer ones of a
+ * packed call as alone. Longer ones go 64 tokens at a time: operands of the products
  * (state, inverse, corrected values, scores) are bf16, sums, decays and the
  * carried state fp32; a head's outputs are off by about 3.1e-3 of their norm,
  * and a token's decay is held at 2^-160 at least. Where keys repeat, steps b are
