@@ -18,24 +18,32 @@
 //   D1  [128 x 64]  = S K^T           S as bf16 in tensor memory (its own copy)
 //   D2  [128 x 64]  = V^T T^T         V^T straight from V's tile (its transpose is a layout of the operand)
 //   D2             += D1' T^T         D1' = -2^(G_j) D1 as bf16, written over D1
-//   S              += N' K            N' = 2^(G_63 - G_j) b_j N^T as bf16, written over D2; S decayed before
-//   O   [128 x 64]  = S Q^T,  N^T P^T and the output is their sum, the first scaled per token
-// Beside the chain, one or two chunks ahead: [K; Q] K^T, its scaled halves A and P, and T.
-// Roundings: the state, D1', N, N', P and T enter products as bf16 (the output is bf16; the state that is carried and
-// returned is fp32). The inverse is fp32 within 8 x 8 blocks and tf32 between them (products rounded to nearest, A cut
-// off by the instruction), an eighth and a quarter of the step of T's own rounding. Of an output's error, 3.1e-3, its own
-// rounding, P's and N's are 1.66e-3 each, and the rest, which adds as squares, is T's and the state's; of a state's,
-// 2.5e-3, N' and the rounding of a bf16 state are most. Second parts of N, N' and P would halve it, for 25 % more products
-// and 40 KB more shared memory than there is. Where all keys of a chunk are one, steps are near one and nothing decays, the
-// sum of the b_j n_j telescopes, and what T's rows sum to for their rounding adds up: .09 after 64 tokens.
+//   S              += N' K            N' = 2^(G_63 - G_j) b_j N^T as bf16, written over D1'; S decayed before
+//   O   [128 x 64]  = S Q^T,  N^T P^T and the output is their sum, the first scaled per token; N as it lies in D2, tf32
+// Beside the chain, one or two chunks ahead: [K; Q] K^T, its scaled halves A and P, and T. D1' T^T and N^T P^T take 16 tokens j
+// at a time, each for the outputs i from there on: T and P are zero before.
+// Roundings: the state, D1', N' and T enter products as bf16, N and P as tf32, cut off by the instruction (the output is
+// bf16; the state that is carried and returned is fp32). The inverse is fp32 within 8 x 8 blocks and tf32 between them
+// (products rounded to nearest, A cut off by the instruction), an eighth and a quarter of the step of T's own rounding.
+// What they make depends on the keys. Where these have a common direction, an output is a sum of P[i, j] n_j that take each
+// other back (where all are one and steps near one it telescopes), and what each term is off by adds up. With N and P as
+// bf16 outputs were off by 3.1e-3 of a head's norm for independent keys, and by 5.8e-3, 9.3e-3, 1.3e-2 for keys with a cosine of
+// .3, .6, .9 between them (steps about .5, decays about .99); in tf32 they are by 2.8e-3, 3.0e-3, 4.3e-3, 6.0e-3, of which the
+// output's own rounding is 1.66e-3, and the rest mostly T's and the state's. That costs twice P's shared memory (V has one
+// buffer for it), and 3 % where one sequence's chain is all (4.42 to 4.57 ms for 131,072 tokens of 32 heads), 1 % for 8 x
+// 4096 tokens; packed prompts take 1 % less, as N is no longer converted. A second bf16 part of T would bring them to 2.5e-3
+// throughout, and one of N' states from 2.2e-3 to 4.3e-3 to below 2.4e-3 (by an emulation): 128 and 256 cycles of products on
+// the chain. Where all keys of a chunk are one, steps are near one and nothing decays, what T's rows sum to for
+// their rounding adds up: .09 after 64 tokens.
 //
 // NaN: a product multiplies what a mask leaves out by zero, and 0 NaN is NaN, so a token that holds a NaN or infinity
 // would reach earlier ones of its chunk. What holds one leaves no number in the state's rows it reaches, up to the end of
 // the sequence, where such rows show; their eight neighbours' outputs and states are then made again token by token from
 // the start of the sequence (walk_rows). A NaN in q stays in its token without that.
 //
-// What bounds it (8 x 4096 tokens of 16 heads: 160 us, 3.4 TB/s of 6.7; one sequence of 131,072 tokens of 32 heads: 4.4 ms,
-// 2.1 us a chunk on 32 SMs). Three loops of 4,500 to 4,700 cycles a chunk, about even by the clocks of their steps: the chain
+// What bounds it (8 x 4096 tokens of 16 heads: 163 us, 3.3 TB/s of 6.7; one sequence of 131,072 tokens of 32 heads: 4.6 ms,
+// 2.2 us a chunk on 32 SMs; cycles as counted at 160 us, before N and P were tf32). Three loops of 4,500 to 4,700 cycles a
+// chunk, about even by the clocks of their steps: the chain
 // (S to bf16 500, D1 1,350, D1' 400, N 1,100, N' 450, S 700); the scores' one accumulator (product 1,600 from the wait on,
 // read 3,050 by the warps with four blocks of columns); and, over two chunks, a tile's way from its load over the norms and
 // the scores to T (inverse 3,500). The tensor pipe is busy 30 % of the time. Next to that, instruction supply: the
@@ -52,7 +60,7 @@
 // not fit: tensor memory and 220 KB of shared memory are full.
 //
 // Warp roles (768 threads):
-//   warp 0       TMA producer (lane 0): [K; Q] tiles three deep, V tiles two
+//   warp 0       TMA producer (lane 0): [K; Q] tiles three deep, V's one
 //   warp 1       MMA issuer: the chain
 //   warp 2       MMA issuer: [K; Q] K^T, V^T T^T
 //   warp 3       MMA issuer: output; running sums of the decays, steps
@@ -81,26 +89,27 @@ constexpr int SC_G = 0, SC_B = 256, SC_D = 512, SC_N = 768, SC_O = 1024, SC_GK =
 struct Layout {
     static constexpr int BOX = C * 128;             // 64 channels x 64 rows, 128-byte swizzle
     static constexpr int KQS = 3, KQT = 4 * BOX;    // a tile: per 64 channels the rows of K, then those of Q
-    static constexpr int VS = 2, VT = 2 * BOX;
+    static constexpr int VT = 2 * BOX;              // one tile of V
+    static constexpr int PS = KQS, PT = 2 * BOX;    // score tiles, fp32: per 32 columns 64 rows of 128 bytes
     static constexpr int TS = 2;                    // T tiles
     // the inverse's scratch, fp32, one per group: rows 0..31 need 32 columns, the others 64 (and four more for the banks)
     static constexpr int LD0 = 36, LD1 = 68, SCRATCH = 32 * (LD0 + LD1) * 4;
     static constexpr int KQ = 0;
     static constexpr int V = KQ + KQS * KQT;
-    static constexpr int P = V + VS * VT;           // scores [i][j] and T [i][j], bf16, 128-byte rows
-    static constexpr int T = P + KQS * BOX;
+    static constexpr int P = V + VT;                // scores [i][j]
+    static constexpr int T = P + PS * PT;           // T [i][j], bf16, 128-byte rows
     static constexpr int SCR = T + TS * BOX;
     static constexpr int SC = SCR + 2 * SCRATCH;
-    static constexpr int OUT = (SC + 4 * SC_BYTES + 1023) / 1024 * 1024;  // a chunk's output, [token][channel]
-    static constexpr int BAR = OUT + VT;
-    static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 8, SC_FULL = 10, T_FULL = 13, G_DONE = 35, KQ_FREE = 17,
+    static constexpr int BAR = SC + 4 * SC_BYTES;
+    static constexpr int KQ_FULL = 0, KQ_EMPTY = 3, V_FULL = 6, V_EMPTY = 7, SC_FULL = 10, T_FULL = 13, G_DONE = 35, KQ_FREE = 17,
                          KQ_ZERO = 18, SB_GO = 19, D1_DONE = 20, D1_GO = 21, N_DONE = 22, N_GO = 23, S_DONE = 24, O_DONE = 25,
                          SQ_DONE = 26, U_DONE = 27, OUT_RD = 28, FACT = 29, END = 32, END2 = 33, END3 = 34, T_EMPTY = 37, NBARS = 39;
     static constexpr int TMEMPTR = (BAR + NBARS * 8 + 15) / 16 * 16;
-    static constexpr int FLAGS = TMEMPTR + 16;
-    static constexpr int ALLOC = FLAGS + 16 + 1024;
+    static constexpr int FLAGS = TMEMPTR + 16;      // a wait ran out; groups of eight rows that hold no numbers at the end
+    static constexpr int OUT = (FLAGS + 16 + 1023) / 1024 * 1024;  // a chunk's output, [token][channel]
+    static constexpr int ALLOC = OUT + VT;          // all of it: the window starts on 1024 bytes, as nothing is static
     static_assert(ALLOC <= 227 * 1024, "shared memory budget");
-    static_assert(SC % 16 == 0 && SC_BYTES % 16 == 0 && BAR % 8 == 0, "alignment");
+    static_assert(SC % 16 == 0 && SC_BYTES % 16 == 0 && BAR % 8 == 0 && P % 1024 == 0 && T % 1024 == 0, "alignment");
 };
 
 // Place in the ring of KQS buffers and the parity of the round, of one chunk after another.
@@ -161,8 +170,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                       const __grid_constant__ CUtensorMap to, const __grid_constant__ GdnParams p)
 {
     using Lay = Layout;
-    extern __shared__ uint8_t smem_dyn[];
-    uint8_t *smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem_dyn_tiles[];
+    uint8_t *smem = smem_dyn_tiles;
     const uint32_t sb = smem_u32(smem);
 #define SM_AT(T, a) (*reinterpret_cast<T *>(smem + (smem_checked((a), sizeof(T), sb) - sb)))
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -175,16 +184,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!p.split) walk_groups(p, seq, h, sp, (1u << (DH / gdn::ROWS)) - 1u);
         return;
     }
-    // (the compiler is not told that there are chunks: with that it lays the loops out another way, 2.5 % slower)
-    asm volatile("" : "+r"(sp.len));
     const int nch = (sp.len + C - 1) / C;
 
     volatile int *flags = reinterpret_cast<volatile int *>(smem + Lay::FLAGS);
-    __shared__ uint32_t spoilt;  // groups of eight rows that hold no numbers at the end
+    uint32_t *const spoilt = reinterpret_cast<uint32_t *>(smem + Lay::FLAGS) + 1;
     auto bar = [&](int i) { return sb + Lay::BAR + 8 * i; };
     auto kq = [&](const Ring &g) { return sb + Lay::KQ + g.s * Lay::KQT; };
-    auto vt = [&](int n) { return sb + Lay::V + (n % Lay::VS) * Lay::VT; };
-    auto pt = [&](const Ring &g) { return sb + Lay::P + g.s * Lay::BOX; };
+    const uint32_t vt = sb + Lay::V;
+    auto pt = [&](const Ring &g) { return sb + Lay::P + g.s * Lay::PT; };
     auto tt = [&](int n) { return sb + Lay::T + (n & 1) * Lay::BOX; };
     auto sc = [&](int n) { return sb + Lay::SC + (n & 3) * SC_BYTES; };
     auto live_of = [&](int n) { return min(C, sp.len - n * C); };
@@ -201,29 +208,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(bar(Lay::T_FULL + i), 4);
             mbar_init(bar(Lay::FACT + i), 4);
         }
-        for (int i = 0; i < Lay::VS; ++i) {
-            mbar_init(bar(Lay::V_FULL + i), 1);
-            mbar_init(bar(Lay::V_EMPTY + i), 1);
-        }
-        for (int i : {Lay::G_DONE, Lay::G_DONE + 1, Lay::T_EMPTY, Lay::T_EMPTY + 1, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::SQ_DONE, Lay::U_DONE, Lay::END, Lay::END2, Lay::END3})
+        for (int i : {Lay::V_FULL, Lay::V_EMPTY, Lay::G_DONE, Lay::G_DONE + 1, Lay::T_EMPTY, Lay::T_EMPTY + 1, Lay::D1_DONE, Lay::N_DONE, Lay::S_DONE, Lay::O_DONE, Lay::SQ_DONE, Lay::U_DONE, Lay::END, Lay::END2, Lay::END3})
             mbar_init(bar(i), 1);
         mbar_init(bar(Lay::KQ_ZERO), 4);
         mbar_init(bar(Lay::OUT_RD), 4);
         mbar_init(bar(Lay::KQ_FREE), 4);
         for (int i : {Lay::SB_GO, Lay::D1_GO, Lay::N_GO}) mbar_init(bar(i), 8);
         flags[0] = 0;
-        spoilt = 0u;
+        *spoilt = 0u;
         fence_mbar_init();
     }
-    // the parts of P and T above their diagonal blocks are zero for good
-    for (int i = threadIdx.x; i < (Lay::KQS + Lay::TS) * Lay::BOX / 16; i += NTHREADS) SM_AT(uint4, sb + Lay::P + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    // the parts of T above its diagonal blocks are zero for good
+    for (int i = threadIdx.x; i < Lay::TS * Lay::BOX / 16; i += NTHREADS) SM_AT(uint4, sb + Lay::T + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     // the allocation is the whole tensor memory, so it starts at address 0
     constexpr uint32_t tmem = 0;
-    if (*reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR) != tmem && threadIdx.x == 0) flags[0] = 1;
+    if ((*reinterpret_cast<volatile uint32_t *>(smem + Lay::TMEMPTR) != tmem || (sb & 1023u)) && threadIdx.x == 0) flags[0] = 1;
     const uint32_t flag = sb + Lay::FLAGS;
     auto wait_w = [&](int b, uint32_t par) {
         wait_or_flag(bar(b), par, flag);
@@ -233,13 +236,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
     };
-    // operands: K step i of a K-major [K; Q] tile, of an MN-major tile (16 rows), of a tile of 128-byte rows, and of an
-    // operand in tensor memory that two warps have written halves of
+    // operands: K step i of a K-major [K; Q] tile, of an MN-major tile (16 rows), of a tile of 128-byte rows, of one of fp32, and
+    // of an operand in tensor memory that two warps have written halves of
     constexpr uint32_t HI = tc::sdesc_hi(1024, tc::SWZ_128B);
-    constexpr uint32_t id_n = tc::idesc(tc::BF16, 128, C, 0, 0), id_u = tc::idesc(tc::BF16, 128, C, 1, 0), id_s = tc::idesc(tc::BF16, 128, DH, 0, 1);
+    constexpr uint32_t id_n = tc::idesc(tc::BF16, 128, C, 0, 0), id_u = tc::idesc(tc::BF16, 128, C, 1, 0), id_s = tc::idesc(tc::BF16, 128, DH, 0, 1),
+                       id_o = tc::idesc(tc::TF32, 128, C, 0, 0);
     auto kmaj = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(((i >> 2) * 2 * Lay::BOX + (i & 3) * 32) >> 4)); };
     auto nmaj = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>((i * 16 * 128) >> 4)); };
     auto rows = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>((i * 32) >> 4)); };
+    auto rows32 = [](uint32_t lo, int i) { return tc::sdesc_of<HI>(lo + static_cast<uint32_t>(((i >> 2) * Lay::BOX + (i & 3) * 32) >> 4)); };
     auto halves = [](int i) { return static_cast<uint32_t>(32 * (i >> 1) + 8 * (i & 1)); };
     // a [K; Q] tile is there, with the rows past the sequence's end cleared
     auto wait_kq = [&](int n, const Ring &g) {
@@ -262,35 +267,40 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             Ring rg;
             int nk = 0, nv = 0;  // tiles issued
 #pragma unroll 1
-            for (int n = 0; n < nch; ++n, rg.next()) {
-                const int tok = sp.bos + n * C, full = Lay::KQ_FULL + rg.s, vfull = Lay::V_FULL + n % Lay::VS;
-                if (!wait_bar(bar(Lay::KQ_EMPTY + rg.s), rg.par ^ 1, flags)) break;
-                mbar_arrive_expect_tx(bar(full), Lay::KQT);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    tma_load_3d(kq(rg) + 2 * c * Lay::BOX, &tk, 64 * c, hk, tok, bar(full));
-                    tma_load_3d(kq(rg) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
-                }
-                ++nk;
-                // a tile's buffer is free late, so the next ones are on their way to L2 by then
-                if (n + Lay::KQS < nch) {
-                    const int ahead = tok + Lay::KQS * C;
+            for (int n = 0; n <= nch; ++n, rg.next()) {
+                if (n < nch) {
+                    const int tok = sp.bos + n * C, full = Lay::KQ_FULL + rg.s;
+                    if (!wait_bar(bar(Lay::KQ_EMPTY + rg.s), rg.par ^ 1, flags)) break;
+                    mbar_arrive_expect_tx(bar(full), Lay::KQT);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        tma_prefetch_3d(&tk, 64 * c, hk, ahead);
-                        tma_prefetch_3d(&tq, 64 * c, hk, ahead);
-                        tma_prefetch_3d(&tv, 64 * c, h, ahead);
+                        tma_load_3d(kq(rg) + 2 * c * Lay::BOX, &tk, 64 * c, hk, tok, bar(full));
+                        tma_load_3d(kq(rg) + (2 * c + 1) * Lay::BOX, &tq, 64 * c, hk, tok, bar(full));
+                    }
+                    ++nk;
+                    // a tile's buffer is free late, so the next ones are on their way to L2 by then
+                    if (n + Lay::KQS < nch) {
+                        const int ahead = tok + Lay::KQS * C;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            tma_prefetch_3d(&tk, 64 * c, hk, ahead);
+                            tma_prefetch_3d(&tq, 64 * c, hk, ahead);
+                            tma_prefetch_3d(&tv, 64 * c, h, ahead);
+                        }
                     }
                 }
-                if (!wait_bar(bar(Lay::V_EMPTY + n % Lay::VS), ((n / Lay::VS) & 1) ^ 1, flags)) break;
-                mbar_arrive_expect_tx(bar(vfull), Lay::VT);
+                // V's one buffer is free when the last V has met its T, most of a chunk before this one is wanted
+                if (n > 0) {
+                    if (!wait_bar(bar(Lay::V_EMPTY), n & 1, flags)) break;
+                    mbar_arrive_expect_tx(bar(Lay::V_FULL), Lay::VT);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) tma_load_3d(vt(n) + c * Lay::BOX, &tv, 64 * c, h, tok, bar(vfull));
-                ++nv;
+                    for (int c = 0; c < 2; ++c) tma_load_3d(vt + c * Lay::BOX, &tv, 64 * c, h, sp.bos + (n - 1) * C, bar(Lay::V_FULL));
+                    ++nv;
+                }
             }
             // no copy is in flight when the CTA ends, whichever way the loop was left
             for (int m = max(nk - Lay::KQS, 0); m < nk; ++m) drain_bar(bar(Lay::KQ_FULL + m % Lay::KQS), (m / Lay::KQS) & 1);
-            for (int m = max(nv - Lay::VS, 0); m < nv; ++m) drain_bar(bar(Lay::V_FULL + m % Lay::VS), (m / Lay::VS) & 1);
+            if (nv > 0) drain_bar(bar(Lay::V_FULL), (nv - 1) & 1);
             // and the watch over the others' waits lasts until the last chunk's output
             for (int m = max(nk - Lay::KQS, 0); m < nk; ++m) wait_bar(bar(Lay::KQ_EMPTY + m % Lay::KQS), (m / Lay::KQS) & 1, flags);
         }
@@ -310,7 +320,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             wait_w(Lay::D1_GO, n & 1);
             tc::fence_after();
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_D2, tmem + T_D1 + halves(i), rows(dt, i), id_n, 1);
+            for (int i = 0; i < 4; ++i)  // outputs from 16 i on: rows of T by 2048 bytes, columns of D2, N by 16
+                tc::mma_ts_w(tmem + T_D2 + 16 * i, tmem + T_D1 + halves(i), rows(dt + 128 * i, i), id_n - (i << 18), 1);
             tc::commit_w(bar(Lay::N_DONE));
             tc::commit_w(bar(Lay::T_EMPTY + (n & 1)));
             // (with the product of this state and Q done, S_DONE frees its copy too)
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             wait_w(Lay::N_GO, n & 1);
             tc::fence_after();
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_S, tmem + T_D2 + 16 * i + 8, nmaj(dkn, i), id_s, 1);
+            for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_S, tmem + T_D1 + halves(i), nmaj(dkn, i), id_s, 1);
             tc::commit_w(bar(Lay::S_DONE));
             tc::commit_w(bar(Lay::KQ_EMPTY + rg.s));
         }
@@ -335,27 +346,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::commit_w(bar(Lay::G_DONE + (n & 1)));  // either group sees every phase of its own
         };
         auto issue_u = [&](int n, const Ring &rg) {
-            wait_w(Lay::V_FULL + n % Lay::VS, (n / Lay::VS) & 1);
+            wait_w(Lay::V_FULL, n & 1);
             if (const int Lv = live_of(n); Lv < C) {  // as the rows of K and Q past the end, which other warps clear
                 for (int i = lane; i < (C - Lv) * 16; i += 32) {
                     const int r = Lv + (i >> 4), c = i & 15;
-                    SM_AT(uint4, vt(n) + (c >> 3) * Lay::BOX + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    SM_AT(uint4, vt + (c >> 3) * Lay::BOX + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 tc::fence_async_smem();
                 __syncwarp();
             }
-            // both products of the last chunk's N, whose columns these are, have been made
+            // the last chunk's N, whose columns these are, has been multiplied, and N' made of it
             if (n > 0) {
                 wait_w(Lay::O_DONE, (n - 1) & 1);
                 wait_w(Lay::S_DONE, (n - 1) & 1);
             }
             wait_w(Lay::T_FULL + rg.s, rg.par);
             tc::fence_after();
-            const uint32_t dv = tc::sdesc_lo(vt(n), Lay::BOX), dt = tc::sdesc_lo(tt(n), 16);
+            const uint32_t dv = tc::sdesc_lo(vt, Lay::BOX), dt = tc::sdesc_lo(tt(n), 16);
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) tc::mma_ss_w(tmem + T_D2, nmaj(dv, i), rows(dt, i), id_u, i > 0);
             tc::commit_w(bar(Lay::U_DONE));
-            tc::commit_w(bar(Lay::V_EMPTY + n % Lay::VS));
+            tc::commit_w(bar(Lay::V_EMPTY));
         };
         Ring rg, ru;
 #pragma unroll 1
@@ -397,10 +408,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 for (int i = 0; i < 8; ++i) tc::mma_ts_w(tmem + T_SQ, tmem + T_SB + 8 * i, kmaj(dq, i), id_n, i > 0);
                 tc::commit_w(bar(Lay::SQ_DONE));
                 wait_w(Lay::T_FULL + rg.s, rg.par);
-                wait_w(Lay::N_GO, n & 1);
+                wait_w(Lay::N_DONE, n & 1);
                 tc::fence_after();
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) tc::mma_ts_w(tmem + T_PV, tmem + T_D2 + 16 * i, rows(dp, i), id_n, i > 0);
+                for (int i = 0; i < 8; ++i)  // eight tokens j, outputs as above
+                    tc::mma_ts_tf32_w(tmem + T_PV + 16 * (i >> 1), tmem + T_D2 + 8 * i, rows32(dp + 128 * (i >> 1), i), id_o - ((i >> 1) << 18), i > 0);
                 tc::commit_w(bar(Lay::O_DONE));
                 tc::commit_w(bar(Lay::KQ_EMPTY + rg.s));
                 rg.next();
@@ -547,17 +559,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc::wait_st();
             tc::fence_before();
             arrive_w(Lay::D1_GO);
-            // N and N' over D2
+            // N' of N, over D1'
             wait_w(Lay::N_DONE, n & 1);
             tc::fence_after();
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
                 tc::ld16(l2 + 16 * g, r);
                 tc::wait_ld();
-                pack(r, o);
-                tc::st8(l2 + 16 * g, o);
                 pack_scaled(r, o, sc(n) + SC_N + 128 * hf + 64 * g);
-                tc::st8(l2 + 16 * g + 8, o);
+                tc::st8(l1 + 8 * g, o);
             }
             tc::wait_st();
             tc::fence_before();
@@ -574,10 +584,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) z = ffma2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(0.f, 0.f), z);
         }
-        if (!(z.x + z.y == 0.f)) atomicOr(&spoilt, 1u << (v / gdn::ROWS));
+        if (!(z.x + z.y == 0.f)) atomicOr(spoilt, 1u << (v / gdn::ROWS));
         named_bar_sync(4 + q, 64);  // both halves of these rows have been looked at
         if (p.fin) {
-            const bool number = !(*const_cast<volatile uint32_t *>(&spoilt) >> (v / gdn::ROWS) & 1u);  // else made again at the end
+            const bool number = !(*const_cast<volatile uint32_t *>(spoilt) >> (v / gdn::ROWS) & 1u);  // else made again at the end
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
                 uint32_t r[32];
@@ -770,9 +780,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; j += 4)
-                        SM_AT(uint4, pt(rg) + i0 * 128 + ((((b >> 3) + (j >> 2)) ^ (i0 & 7)) << 4)) =
-                            make_uint4(pack_bf16(w[j].x, w[j].y), pack_bf16(w[j + 1].x, w[j + 1].y), pack_bf16(w[j + 2].x, w[j + 2].y), pack_bf16(w[j + 3].x, w[j + 3].y));
+                    for (int j = 0; j < 8; j += 2)
+                        SM_AT(float4, pt(rg) + (b >> 5) * Lay::BOX + i0 * 128 + ((((b >> 2 & 4) + (j >> 1)) ^ (i0 & 7)) << 4)) = make_float4(w[j].x, w[j].y, w[j + 1].x, w[j + 1].y);
                 }
             }
             tc::fence_before();
@@ -866,7 +875,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     tc::fence_before();
     __syncthreads();
     if (*flags && threadIdx.x == 0) atomicOr(&g_dev_error, DEVERR_TIMEOUT);
-    const uint32_t groups = spoilt;
+    const uint32_t groups = *spoilt;
     if (groups) walk_groups(p, seq, h, sp, groups);
     if (warp == 0) {
         __syncwarp();

@@ -532,12 +532,23 @@ KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void
  *   flags    0 or KDA_FLAG_QK_L2NORM: q and k are used as
  *            x / sqrt(sum x^2 + 1e-6), formed in fp32.
  * Sequences of at most 8 tokens go token by token in fp32, beside longer ones of a
- * packed call as alone. Longer ones go 64 tokens at a time: operands of the products
- * (state, inverse, corrected values, scores) are bf16, sums, decays and the
- * carried state fp32; a head's outputs are off by about 3.1e-3 of their norm,
- * and a token's decay is held at 2^-160 at least. Where keys repeat, steps b are
- * near 1 and nothing decays, corrected values cancel and the rounding of the
- * inverse adds up, to .09 of the norm after 64 equal keys. A NaN or infinity
+ * packed call as alone. Longer ones go 64 tokens at a time: the state, the inverse
+ * and what the state is corrected by enter products as bf16, scores and corrected
+ * values as tf32; sums, decays and the carried state are fp32, a token's decay is
+ * held at 2^-160 at least. What these roundings make grows with what the keys have
+ * in common, with the steps b and with how little decays, for corrected values then
+ * take each other back. Errors of a head's outputs (rounded to bf16, 1.7e-3 by
+ * itself) and fp32 states, relative to their norm:
+ *   decays about .9, steps about .5: independent keys 1.9e-3, 1.7e-3; a cosine of .6
+ *     between them 2.4e-3, 2.6e-3; of .9 2.9e-3, 3.3e-3
+ *   decays about .99, steps about .5: independent 2.8e-3, 2.2e-3; .3 3.0e-3, 2.4e-3;
+ *     .6 4.3e-3, 2.5e-3; .9 6.0e-3, 4.3e-3
+ *   decays about .99, steps of .95: independent 3.2e-3, 2.7e-3; .3 3.9e-3, 3.1e-3; .6
+ *     7.5e-3, 3.6e-3; .9 8.2e-3, 4.4e-3
+ *   one key over and over, or two in turn: decays about .9 and steps of .73 4.8e-3,
+ *     7.5e-3; decays about .99 1.1e-2, 1.6e-2, and with steps of .95 2.4e-2, 3.3e-2; no
+ *     decay and steps of .9975 .05, .09
+ * A NaN or infinity
  * reaches what the recurrence lets it reach; a sequence that holds one is slow
  * (its state's rows are made again token by token). Keys are taken to be at most
  * about 1 long: longer ones may make the recurrence itself diverge.
