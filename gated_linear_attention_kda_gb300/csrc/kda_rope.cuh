@@ -5,8 +5,11 @@
 // where pair i is channels (i, i + R/2), or (2 i, 2 i + 1); channels from R on are not turned.
 // Angles: a float holds a far position's angle to no better than 2^-24 of it, which at position 100,000 is a hundredth of
 // a radian. The turn is therefore counted in whole turns, as a 64-bit fixed-point fraction: inv_freq / (2 pi) is an
-// integer F of 2^-64 turns, position F wraps as turns do, and its upper 32 bits are the angle. F is off by at most one
-// unit, so a position below 2^31 is off by less than 2^-33 turns; no 64-bit floating point is needed.
+// integer F of 2^-64 turns, position F wraps as turns do, and its upper 32 bits, rounded, are the angle. F is off by less than
+// 1 + inv_freq / 256 units (2 / pi has 64 bits, and F is cut off), so an angle is off by less than 2^-33 + |position| (1 +
+// inv_freq / 256) 2^-64 turns: 2^-31 below position 2^32 for frequencies up to 64. It is taken from the nearest quarter turn
+// before it becomes a float, whose 24 bits then hold it to 2^-28 turns at most and the smaller of cosine and sine to 2^-24 of
+// itself; no 64-bit floating point is needed.
 // Bound by HBM where there are many tokens: 32,768 of 20 heads of 128 take 63.5 us, 5.3 TB/s; 65,519 packed ones appended
 // with 8 key heads of 128, .54 GB, 92 us, 5.8 TB/s. For single tokens the launch and one chain of loads are all: 6 us.
 #pragma once
@@ -56,10 +59,12 @@ __device__ __forceinline__ uint64_t turns_per_step(float f)
 // cosine and sine of the angle at `position`
 __device__ __forceinline__ float2 turn_at(int64_t position, uint64_t F)
 {
-    const int32_t a = static_cast<int32_t>((static_cast<uint64_t>(position) * F) >> 32);  // 2^-32 turns, in [-1/2, 1/2)
+    const uint32_t a = static_cast<uint32_t>((static_cast<uint64_t>(position) * F + 0x80000000u) >> 32);  // 2^-32 turns
+    const uint32_t n = (a + 0x20000000u) >> 30;                                                           // the nearest quarter
     float s, c;
-    sincospif(static_cast<float>(a) * 0x1p-31f, &s, &c);
-    return make_float2(c, s);
+    sincospif(static_cast<float>(static_cast<int32_t>(a - (n << 30))) * 0x1p-31f, &s, &c);
+    const float x = n & 1 ? -s : c, y = n & 1 ? c : s;
+    return n & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
 // A head is held by D / 16 neighbouring lanes, two vectors of eight channels each, of the part that is turned both members

@@ -581,8 +581,9 @@ KDA_API kda_status kda_gdn_step(const void *q, int64_t q_stride, const void *k, 
  *   q, q_out  bf16 [M, H, D];  k, k_out  bf16 [M, HK, D] (HK == 0: no keys), token
  *             strides *_stride; D = 64, 128 or 256. q_out may be q, k_out may be k.
  *   positions int64 [M], any value;  inv_freq fp32 [R / 2] (R == 0: NULL allowed);
- *             R a multiple of 16, 0 .. D. Angles are exact to 2^-31 turns for
- *             positions below 2^32.
+ *             R a multiple of 16, 0 .. D. Angles are off by less than 2^-33 +
+ *             |position| (1 + inv_freq / 256) 2^-64 turns: 2^-31 for positions below
+ *             2^32 and frequencies up to 64.
  *   q_weight, k_weight  fp32 [D] or NULL, 16-byte aligned; read only with norm != 0.
  */
 KDA_API kda_status kda_qk_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, void *q_out, int64_t q_out_stride,
