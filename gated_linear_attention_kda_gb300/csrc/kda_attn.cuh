@@ -23,6 +23,7 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int SL = 16;          // tokens of a slice
 constexpr int CTAS = 2;         // per SM
 constexpr int JOIN_THREADS = 256;
+constexpr float LOWEST = -3.402823466e38f;  // the least number
 
 struct AttnParams {
     const uint16_t *q, *kc, *vc;
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) kda_attn_step_kernel(const Attn
     const float c2 = p.scale * LOG2E;
     uint32_t qa[D / 16][4];
     float acc[D / 8][4], top[2], sum[2];
+    unsigned seen;  // tokens that count, of the unit's slices so far
     auto begin = [&]() {  // queries of a unit's rows, and nothing seen so far
         const int hk = at.unit / p.tiles, r0 = (at.unit - hk * p.tiles) * 16;
         const uint16_t *qp = p.q + at.seq * p.qs + (static_cast<long long>(hk) * p.rows + r0) * D + 2 * t4;
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) kda_attn_step_kernel(const Attn
         for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         top[0] = top[1] = -INFINITY;
         sum[0] = sum[1] = 0.f;
+        seen = 0u;
     };
     begin();
     bool whole = at.slice == 0;  // the unit's first slice is in this run
@@ -262,6 +265,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) kda_attn_step_kernel(const Attn
         if (at.slice * SL + SL > at.tokens) live = (1u << static_cast<int>(at.tokens - at.slice * SL)) - 1u;
         const unsigned off = bad >> 2 * st & 3u;
         if (off) live &= (off & 1u ? 0u : 0x00ffu) | (off & 2u ? 0u : 0xff00u);
+        seen |= live;
         st = st + 1 == STAGES ? 0 : st + 1;
         float x[2][4] = {};
 #pragma unroll
@@ -328,6 +332,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) kda_attn_step_kernel(const Attn
             for (int j = 0; j < 2; ++j) {
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+                // a maximum of -infinity means that nothing counts, and an output of 0; scores of -infinity alone are 0 / 0
+                if (seen) top[j] = fmaxf(top[j], LOWEST);
             }
             const int hk = at.unit / p.tiles, r0 = (at.unit - hk * p.tiles) * 16;
 #pragma unroll
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) kda_attn_step_kernel(const Attn
                 if (r0 + r >= p.rows) continue;
                 const int h = hk * p.rows + r0 + r;
                 if (whole && ends) {
-                    const float f = sum[j] > 0.f || sum[j] != sum[j] ? 1.f / sum[j] : 0.f;
+                    const float f = top[j] == -INFINITY ? 0.f : 1.f / sum[j];
                     uint16_t *op = p.out + at.seq * p.os + static_cast<long long>(h) * D + 2 * t4;
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) *reinterpret_cast<uint32_t *>(op + 8 * n) = pack_bf16(f * acc[n][2 * j], f * acc[n][2 * j + 1]);
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) kda_attn_join_kernel(const AttnP
 #pragma unroll
                 for (int c = 0; c < CPL; ++c) acc[c] = acc[c] * f + mp[CPL * lane + c] * g;
             }
-            const float f = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+            const float f = top == -INFINITY ? 0.f : 1.f / sum;
             const int h = hk * p.rows + r0 + r;
             uint16_t *op = p.out + seq * p.os + static_cast<long long>(h) * D + CPL * lane;
 #pragma unroll

@@ -624,7 +624,8 @@ KDA_API kda_status kda_kv_append(const void *k, int64_t k_stride, const void *v,
  *             S at most 65,536.
  *   positions int64 [S], of the new tokens, which are in the cache already. Below
  *             0: the row sees nothing, its out is 0 and its lse -infinity.
- *   lse       fp32 [S, H] or NULL: log of the sum of exp(scale q . k_t).
+ *   lse       fp32 [S, H] or NULL: log of the sum of exp(scale q . k_t). Where all
+ *             of these are 0 (scores of -infinity), lse is -infinity and out no number.
  *   workspace 16-byte aligned device buffer or NULL. With at least the
  *             kda_attn_step_workspace_bytes bytes the caches of few sequences are
  *             read by many CTAs and their parts joined; without it one CTA reads
