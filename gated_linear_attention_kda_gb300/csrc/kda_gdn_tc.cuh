@@ -48,8 +48,8 @@
 // read 3,050 by the warps with four blocks of columns); and, over two chunks, a tile's way from its load over the norms and
 // the scores to T (inverse 3,500). The tensor pipe is busy 30 % of the time. Next to that, instruction supply: the
 // roles' loops hold some 40 KB of code (chain and its issuer 9, the other issuers and decays 9, output and norms 10, A, P
-// and T 13), which every chunk runs through once; the SM's own cache misses one fetch in seven and the
-// port of the one behind it runs at 83 % of its peak. 8 KB more straight-line code on the chain made the kernel 11 % slower,
+// and T 13), which every chunk runs through once; the SM's own cache misses one fetch in thirteen and
+// the port of the one behind it runs at 78 % of its peak. 8 KB more straight-line code on the chain made the kernel 11 % slower,
 // unrolling the eight products of one issuer 5 %, a call in place of an inlined wait costs 200 cycles more than the wait; so
 // loops over products stay rolled, waits are a few instructions, and masks are made only where they are read. Against 162 us
 // in one run: the inverse's products rolled as well 164 to 176; scores read a block ahead of their use, which frees the

@@ -173,8 +173,8 @@ def attn_step(q, k_cache, v_cache, page_table, positions, out, scale, lse=None, 
     """Softmax attention of one new token per sequence over a paged cache, ``kda_attn_step``: ``q``, ``out`` bf16
     [S, H, D] (D = 64, 128; the caches' HK heads divide H), caches and ``page_table`` as in ``kv_append``,
     ``positions`` int64 [S] of the new tokens, which see the cache up to themselves (below 0: out is 0), ``lse``
-    fp32 [S, H]. A CUDA uint8 ``workspace`` of ``attn_step_workspace_bytes`` bytes lets few sequences' caches be cut.
-    Returns ``(out, lse)``."""
+    fp32 [S, H]. Give a CUDA uint8 ``workspace`` of ``attn_step_workspace_bytes`` bytes: without it one warp reads all of a
+    sequence's keys and values of a key head, 10 to 80 times slower for one long sequence. Returns ``(out, lse)``."""
     dev = _device("q", q, (3,), "[S, H, D]")
     shape = q.shape
     S, H, D = shape
