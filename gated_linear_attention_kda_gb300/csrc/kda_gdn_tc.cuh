@@ -32,9 +32,11 @@
 // output's own rounding is 1.66e-3, and the rest mostly T's and the state's. That costs twice P's shared memory (V has one
 // buffer for it), and 3 % where one sequence's chain is all (4.42 to 4.57 ms for 131,072 tokens of 32 heads), 1 % for 8 x
 // 4096 tokens; packed prompts take 1 % less, as N is no longer converted. A second bf16 part of T would bring them to 2.5e-3
-// throughout, and one of N' states from 2.2e-3 to 4.3e-3 to below 2.4e-3 (by an emulation): 128 and 256 cycles of products on
-// the chain. Where all keys of a chunk are one, steps are near one and nothing decays, what T's rows sum to for
-// their rounding adds up: .09 after 64 tokens.
+// throughout (by an emulation). One of N' brings bf16 states of independent keys from 2.4e-3 to their own rounding, 1.7e-3, and
+// outputs from 2.1e-3 to 1.95e-3, and was not kept: four more products on the chain, 8 x 4096 tokens 164 to 178 us, packed prompts
+// 647 to 682, a long one 4,570 to 4,750 (of the last 32 tokens of a chunk alone: 1.8e-3 to 2.1e-3, 172, 686, 4,630). Where all keys
+// of a chunk are one, steps are near one and nothing decays, what T's rows sum to for their rounding adds up: .09 after 64
+// tokens.
 //
 // NaN: a product multiplies what a mask leaves out by zero, and 0 NaN is NaN, so a token that holds a NaN or infinity
 // would reach earlier ones of its chunk. What holds one leaves no number in the state's rows it reaches, up to the end of

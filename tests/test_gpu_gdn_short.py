@@ -49,3 +49,25 @@ def test_gdn_short_sequences_in_place_and_in_a_graph(kda):  # noqa: F811
     torch.cuda.synchronize()
     kda.check_device_status()
     assert torch.equal(o2.nan_to_num(5.0), out.nan_to_num(5.0)) and torch.equal(state.nan_to_num(5.0), fin.nan_to_num(5.0))
+
+
+def test_gdn_two_calls_at_once(kda):  # noqa: F811
+    """Calls of two streams that overlap in time, packed with short sequences and batched, give the bits of one after the other."""
+    lengths = [2, 700, 1, 8, 90, 1]
+    cu = torch.tensor([0] + lengths).cumsum(0).cuda()
+    one, two = make(1, sum(lengths), 8, 4, seed=60, nseq=len(lengths), init=F32), make(6, 500, 8, 8, seed=61)
+    want_one, want_two = run(kda, one, cu, nseq=len(lengths)), run(kda, two)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for st, d, c, n in ((streams[0], one, cu, len(lengths)), (streams[1], two, None, 6)):
+            with torch.cuda.stream(st):
+                out, fin = torch.empty_like(d["v"]), torch.empty(n, 8, 128, 128, device="cuda")
+                kda.gdn(d["q"], d["k"], d["v"], d["a"], d["beta"], SCALE, out, d["A_log"], d["dt_bias"], d["init"], fin, c, qk_l2norm=True)
+                got.append((out, fin))
+    torch.cuda.synchronize()
+    kda.check_device_status()
+    for i, (out, fin) in enumerate(got):
+        o, f = (want_one, want_two)[i % 2]
+        assert torch.equal(out, o) and torch.equal(fin, f)
