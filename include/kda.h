@@ -548,10 +548,9 @@ KDA_API kda_status kda_residual_norm(const void *x, int64_t x_stride, const void
  *   one key over and over, or two in turn: decays about .9 and steps of .73 4.8e-3,
  *     7.5e-3; decays about .99 1.1e-2, 1.6e-2, and with steps of .95 2.4e-2, 3.3e-2; no
  *     decay and steps of .9975 .05, .09
- * A NaN or infinity
- * reaches what the recurrence lets it reach; a sequence that holds one is slow
- * (its state's rows are made again token by token). Keys are taken to be at most
- * about 1 long: longer ones may make the recurrence itself diverge.
+ * A NaN or infinity reaches what the recurrence lets it reach; a sequence that
+ * holds one is slow (its state's rows are made again token by token). Keys are taken
+ * to be at most about 1 long: longer ones may make the recurrence itself diverge.
  */
 KDA_API kda_status kda_gdn(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                            const void *a, int64_t a_stride, const void *beta, int64_t beta_stride, float scale, void *out,
